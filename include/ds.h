@@ -19,6 +19,16 @@
  *   ds_compact_append     newly committed tokens appended to the compact
  *                         cache between retrievals.
  *
+ * and, for targets that keep their cache in 4 bits:
+ *
+ *   ds_qk_norm_rope       RMS norm of every query and key head and the position
+ *                         rotation, in one pass over the projection's rows;
+ *   ds_kv4_write          K/V rows quantised into the paged 4-bit cache (a
+ *                         prompt, a tree, or the accepted path of a tree);
+ *   ds_kv4_read           rows of the 4-bit cache read back as bf16;
+ *   ds_kv4_verify_attn    ds_verify_attn over the 4-bit cache; a tree of one
+ *                         node is plain decoding.
+ *
  * Conventions (all entry points):
  *   - Every pointer named in an args struct is a DEVICE pointer unless its
  *     comment says otherwise.  The caller owns every buffer, including the
@@ -77,6 +87,7 @@ typedef enum { DS_ACCEPT_GREEDY = 0, DS_ACCEPT_REJECT = 1 } ds_accept_mode;
 #define DS_DEV_BAD_PAGE     0x4u  /* a page id outside [0, num_pages)            */
 #define DS_DEV_BAD_TOKEN    0x8u  /* a draft token outside [0, vocab)            */
 #define DS_DEV_TIMEOUT      0x10u /* a bounded wait inside a kernel gave up      */
+#define DS_DEV_BAD_VALUE    0x20u /* a NaN or an infinity given to ds_kv4_write  */
 
 /* Name of the last failure on the calling thread ("" if none).  The string is
  * owned by the library and valid until the next call on this thread. */
@@ -86,8 +97,9 @@ const char* ds_last_error(void);
 int32_t ds_abi_version(void);
 
 /* sizeof() of each args struct as compiled into the library: 0 verify,
- * 1 gather, 2 accept, 3 commit, 4 append; -1 for anything else.  Bindings compare these with
- * their own struct layouts before the first call. */
+ * 1 gather, 2 accept, 3 commit, 4 append, 5 norm_rope, 6 kv4_rows, 8 kv4_attn; -1 for
+ * anything else (7 is not assigned).  Bindings compare these with their own struct layouts
+ * before the first call. */
 int64_t ds_struct_size(int32_t which);
 
 /* Zero the whole workspace: the status word (bytes 0..255 of any workspace)
@@ -430,6 +442,188 @@ typedef struct ds_commit_args {
 
 void ds_commit_args_default(ds_commit_args* args);
 ds_status ds_kv_commit(const ds_commit_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Norm of every query and key head with the position rotation, in one pass.
+ *
+ * For every row n (a token or a tree node) and every query and key head x of
+ * head_dim values:
+ *   y = x * w / sqrt(mean(x^2) + eps)      (w = q_weight / k_weight; y = x
+ *                                           when that weight is NULL)
+ *   out[j]       = y[j] cos(a_j) - y[j + D/2] sin(a_j)
+ *   out[j + D/2] = y[j] sin(a_j) + y[j + D/2] cos(a_j),   j < D/2,
+ * a_j = positions[n] * rope_base^(-2j/D), or positions[n] * inv_freq[j] when
+ * inv_freq is given (for scaled rotations).  Both 0 / NULL: no rotation.
+ * The sum of squares, the norm and the rotation are float32, the angle is
+ * reduced modulo one turn in 64-bit fixed point (as in ds_chunk_topk_gather),
+ * and each value is rounded to bf16 once.
+ *
+ * Rows may be slices of a wider buffer (the fused projection's output): the
+ * row strides are in elements, heads of a row are head_dim apart.  q_out may
+ * be q itself and k_out k itself, with the same stride; otherwise outputs
+ * must not overlap inputs.  num_q_heads or num_kv_heads may be 0.  A negative
+ * position sets DS_DEV_BAD_LENGTH and that row is not written.
+ *
+ * Refused: head_dim not 64 or 128; pointers not 16-byte aligned or strides
+ * not a multiple of 8 or shorter than a row; eps negative or not finite.
+ * ------------------------------------------------------------------------ */
+typedef struct ds_norm_rope_args {
+  const void*    q;             /* n_rows rows of num_q_heads x head_dim bf16    */
+  const void*    k;             /* n_rows rows of num_kv_heads x head_dim bf16   */
+  int64_t        q_row_stride;  /* elements from a row to the next               */
+  int64_t        k_row_stride;
+  const void*    q_weight;      /* [head_dim] bf16; NULL: queries not normed     */
+  const void*    k_weight;      /* [head_dim] bf16; NULL: keys not normed        */
+  const int32_t* positions;     /* [n_rows] absolute positions >= 0              */
+  int32_t n_rows;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128                                     */
+  float   eps;
+  float   rope_base;            /* 0: see inv_freq                               */
+  const double*  inv_freq;      /* HOST array [head_dim / 2] of radians per
+                                   position, or NULL; needs rope_base 0          */
+  void*   q_out;
+  void*   k_out;
+  int64_t q_out_row_stride;
+  int64_t k_out_row_stride;
+  void*   workspace;            /* >= 256 bytes: the status word                 */
+  size_t  workspace_bytes;
+} ds_norm_rope_args;
+
+void ds_norm_rope_args_default(ds_norm_rope_args* args);
+ds_status ds_qk_norm_rope(const ds_norm_rope_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The 4-bit paged cache.
+ *
+ * A value is  code * scale * 2^exp: an e2m1 code (magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), an e4m3 scale shared by 16 consecutive channels of one
+ * token's head, and one exponent per tensor (k_exp, v_exp; both are host
+ * integers that every call on the cache must repeat).  4.5 bits per value;
+ * code * scale has at most six significant bits, so bf16 holds it exactly.
+ *
+ * K and V are pools [num_pages, num_kv_heads, block] of bytes, block =
+ * DS_KV4_BLOCK_BYTES(page_size, head_dim): the codes [page_size][head_dim/2]
+ * (channel 2i in the low nibble of byte i, 2i + 1 in the high), then the
+ * scales [page_size][head_dim/16].  Slot t of sequence b lives in page
+ * page_table[b][t / page_size] at offset t % page_size, as in the bf16 cache.
+ *
+ * Quantising x (16 channels): y = x 2^-exp; scale = max|y| / 6 rounded to the
+ * nearest e4m3 (ties to even, at most 448); code = y / scale rounded to the
+ * nearest e2m1 (ties to even, at most 6); scale 0 gives codes 0.  All of it
+ * is exact but for these two roundings.  A NaN is stored as 0 and an
+ * infinity as the largest value; both set DS_DEV_BAD_VALUE.  Readers take
+ * the two e4m3 patterns that are no number (0x7f, 0xff) as 448, so no byte
+ * of a cache, written or not, ever reads as NaN or infinity.
+ * ------------------------------------------------------------------------ */
+#define DS_KV4_BLOCK_BYTES(page_size, head_dim) ((page_size) * (head_dim) * 9 / 16)
+
+/* Rows and slots: row row_offsets[b] + i of sequence b belongs to slot
+ * from_lens[b] + i.
+ *
+ * ds_kv4_write quantises the rows into their slots.  With `path` (and
+ * n_accepted, as ds_accept writes them) it commits a tree instead: the rows
+ * are the tree's (at most DS_MAX_TREE_NODES per sequence), and row
+ * row_offsets[b] + path[b, i] goes to slot from_lens[b] + 1 + i, i <
+ * n_accepted[b]; the root stays where the tree was written.  new_lens[b],
+ * when given, is the length that follows: from_lens[b] + rows of b, or
+ * from_lens[b] + 1 + n_accepted[b] with a path (from_lens[b] for an empty
+ * tree).  A path that is not strictly increasing inside (0, rows of b) sets
+ * DS_DEV_BAD_TREE and commits the root only.
+ *
+ * ds_kv4_read writes the rows from their slots, as bf16 (exactly; path,
+ * n_accepted and new_lens must be NULL).
+ *
+ * Both: a length below 0, past max_pages * page_size or row offsets that
+ * decrease or leave [0, n_rows] set DS_DEV_BAD_LENGTH and skip the sequence
+ * (new_lens[b] is from_lens[b] then);
+ * a page id outside [0, num_pages) sets DS_DEV_BAD_PAGE, and that slot is
+ * not written (its row reads as zeros).  Two rows must not share a slot.
+ * Refused: head_dim not 64 or 128; page_size not 16, 32, 64 or 128;
+ * exponents outside [-32, 32]; rows or caches not 16-byte aligned; strides
+ * not a multiple of 8 or shorter than a row; new_lens == from_lens. */
+typedef struct ds_kv4_rows_args {
+  void*   k_rows;               /* n_rows rows of num_kv_heads x head_dim bf16
+                                   (ds_kv4_write only reads them)                */
+  void*   v_rows;
+  int64_t k_row_stride;         /* elements from a row to the next               */
+  int64_t v_row_stride;
+  void*   k_cache;              /* 4-bit pools (ds_kv4_read only reads them)     */
+  void*   v_cache;
+  const int32_t* page_table;    /* [batch, max_pages]                            */
+  const int32_t* from_lens;     /* [batch] slot of each sequence's first row     */
+  const int32_t* row_offsets;   /* [batch + 1]                                   */
+  const int32_t* path;          /* [batch, DS_MAX_TREE_NODES] or NULL            */
+  const int32_t* n_accepted;    /* [batch]; NULL without a path                  */
+  int32_t batch;
+  int32_t n_rows;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t k_exp;
+  int32_t v_exp;
+  int32_t* new_lens;            /* [batch] out, or NULL                          */
+  void*   workspace;            /* >= 256 bytes: the status word                 */
+  size_t  workspace_bytes;
+} ds_kv4_rows_args;
+
+void ds_kv4_rows_args_default(ds_kv4_rows_args* args);
+ds_status ds_kv4_write(const ds_kv4_rows_args* args, void* stream);
+ds_status ds_kv4_read(const ds_kv4_rows_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Tree-verify attention over the 4-bit cache.
+ *
+ * ds_verify_attn (the same trees, masks, outputs, chunk salience, device-side
+ * checks and dependent launches) over K and V in the 4-bit cache.  The tree's
+ * own keys and values are in the cache too, at slots L + j (ds_kv4_write
+ * puts them there).  A batch whose trees have one node each is a decoding
+ * step.  Queries enter the product as float16: those beyond +-65504 are
+ * clamped to it (a NaN stays one), and the bits of a bf16 query below 2^-24
+ * are rounded off.
+ *
+ * chunk_scores NULL: no salience (chunk_size, max_chunks and
+ * accumulate_scores are then ignored).  A page id outside [0, num_pages)
+ * sets DS_DEV_BAD_PAGE and its slots read as zeros.  Refused by name: as
+ * ds_verify_attn, and exponents outside [-32, 32] and max_pages * page_size
+ * above 2^30. */
+typedef struct ds_kv4_attn_args {
+  const void*    q;             /* [n_nodes, num_q_heads, head_dim] bf16         */
+  const void*    k_cache;       /* 4-bit pools                                   */
+  const void*    v_cache;
+  const int32_t* page_table;    /* [batch, max_pages]                            */
+  const int32_t* ctx_lens;      /* [batch]                                       */
+  const int32_t* tree_offsets;  /* [batch + 1]                                   */
+  const int32_t* parents;       /* [n_nodes]                                     */
+  int32_t batch;
+  int32_t n_nodes;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t chunk_size;
+  float   scale;                /* softmax scale; 0 selects 1/sqrt(head_dim)     */
+  int32_t k_exp;
+  int32_t v_exp;
+  void*   out;                  /* [n_nodes, num_q_heads, head_dim]              */
+  int32_t out_dtype;            /* ds_out_dtype                                  */
+  float*  chunk_scores;         /* [batch, max_chunks] fp32, or NULL             */
+  int32_t max_chunks;
+  int32_t accumulate_scores;    /* as in ds_verify_args                          */
+  int32_t num_sms;              /* CTAs to plan for; 0 = the device's SM count   */
+  void*   workspace;            /* >= ds_kv4_verify_attn_workspace_size          */
+  size_t  workspace_bytes;
+} ds_kv4_attn_args;
+
+void ds_kv4_attn_args_default(ds_kv4_attn_args* args);
+ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* args,
+                                            size_t* bytes);
+ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* args, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

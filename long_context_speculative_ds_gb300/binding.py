@@ -23,6 +23,7 @@ DS_ACCEPT_GREEDY, DS_ACCEPT_REJECT = 0, 1
 DS_MAX_TREE_NODES = 64
 DS_DEV_BAD_LENGTH, DS_DEV_BAD_TREE, DS_DEV_BAD_PAGE, DS_DEV_BAD_TOKEN, \
     DS_DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+DS_DEV_BAD_VALUE = 0x20
 
 _p = C.c_void_p
 _i = C.c_int32
@@ -85,6 +86,42 @@ class AppendArgs(C.Structure):
                 ("workspace", _p), ("workspace_bytes", C.c_size_t)]
 
 
+class NormRopeArgs(C.Structure):
+    _fields_ = [("q", _p), ("k", _p), ("q_row_stride", C.c_int64),
+                ("k_row_stride", C.c_int64), ("q_weight", _p),
+                ("k_weight", _p), ("positions", _p), ("n_rows", _i),
+                ("num_q_heads", _i), ("num_kv_heads", _i), ("head_dim", _i),
+                ("eps", C.c_float), ("rope_base", C.c_float),
+                ("inv_freq", C.POINTER(C.c_double)), ("q_out", _p),
+                ("k_out", _p), ("q_out_row_stride", C.c_int64),
+                ("k_out_row_stride", C.c_int64), ("workspace", _p),
+                ("workspace_bytes", C.c_size_t)]
+
+
+class Kv4RowsArgs(C.Structure):
+    _fields_ = [("k_rows", _p), ("v_rows", _p), ("k_row_stride", C.c_int64),
+                ("v_row_stride", C.c_int64), ("k_cache", _p), ("v_cache", _p),
+                ("page_table", _p), ("from_lens", _p), ("row_offsets", _p),
+                ("path", _p), ("n_accepted", _p), ("batch", _i),
+                ("n_rows", _i), ("num_kv_heads", _i), ("head_dim", _i),
+                ("page_size", _i), ("num_pages", _i), ("max_pages", _i),
+                ("k_exp", _i), ("v_exp", _i), ("new_lens", _p),
+                ("workspace", _p), ("workspace_bytes", C.c_size_t)]
+
+
+class Kv4AttnArgs(C.Structure):
+    _fields_ = [("q", _p), ("k_cache", _p), ("v_cache", _p),
+                ("page_table", _p), ("ctx_lens", _p), ("tree_offsets", _p),
+                ("parents", _p), ("batch", _i), ("n_nodes", _i),
+                ("num_q_heads", _i), ("num_kv_heads", _i), ("head_dim", _i),
+                ("page_size", _i), ("num_pages", _i), ("max_pages", _i),
+                ("chunk_size", _i), ("scale", C.c_float), ("k_exp", _i),
+                ("v_exp", _i), ("out", _p), ("out_dtype", _i),
+                ("chunk_scores", _p), ("max_chunks", _i),
+                ("accumulate_scores", _i), ("num_sms", _i),
+                ("workspace", _p), ("workspace_bytes", C.c_size_t)]
+
+
 class DSError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"ds status {status}: {message}")
@@ -100,7 +137,11 @@ EXPORTS = ("ds_last_error", "ds_abi_version", "ds_struct_size",
            "ds_chunk_topk_gather_workspace_size", "ds_chunk_topk_gather",
            "ds_accept_args_default", "ds_accept_workspace_size", "ds_accept",
            "ds_accept_static", "ds_commit_args_default", "ds_kv_commit",
-           "ds_append_args_default", "ds_compact_append")
+           "ds_append_args_default", "ds_compact_append",
+           "ds_norm_rope_args_default", "ds_qk_norm_rope",
+           "ds_kv4_rows_args_default", "ds_kv4_write", "ds_kv4_read",
+           "ds_kv4_attn_args_default", "ds_kv4_verify_attn_workspace_size",
+           "ds_kv4_verify_attn")
 
 
 def lib_path() -> str:
@@ -126,10 +167,13 @@ def load(path: Optional[str] = None) -> C.CDLL:
                  "ds_verify_attn_workspace_size", "ds_verify_attn",
                  "ds_chunk_topk_gather_workspace_size", "ds_chunk_topk_gather",
                  "ds_accept_workspace_size", "ds_accept", "ds_accept_static",
-                 "ds_kv_commit", "ds_compact_append"):
+                 "ds_kv_commit", "ds_compact_append", "ds_qk_norm_rope",
+                 "ds_kv4_write", "ds_kv4_read",
+                 "ds_kv4_verify_attn_workspace_size", "ds_kv4_verify_attn"):
         getattr(lib, name).restype = C.c_int
-    for which, cls in enumerate((VerifyArgs, GatherArgs, AcceptArgs, CommitArgs,
-                                 AppendArgs)):
+    for which, cls in ((0, VerifyArgs), (1, GatherArgs), (2, AcceptArgs),
+                       (3, CommitArgs), (4, AppendArgs), (5, NormRopeArgs),
+                       (6, Kv4RowsArgs), (8, Kv4AttnArgs)):
         got = lib.ds_struct_size(which)
         if got != C.sizeof(cls):
             raise RuntimeError(f"struct {cls.__name__}: library has {got} bytes,"
@@ -352,6 +396,151 @@ def append_args(src_k, src_v, page_table, from_lens, to_lens, *, out_k, out_v,
 
 def ds_compact_append(args: AppendArgs, stream=None):
     _check(load().ds_compact_append(C.byref(args), _stream(stream)))
+
+
+def _rows(t: Optional[torch.Tensor]):
+    """Pointer, row stride (elements) and [rows, heads, head_dim] of bf16 rows
+    whose heads are packed; the rows may be slices of a wider buffer."""
+    if t is None:
+        return None, 0, (0, 0, 0)
+    if t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError("rows must be bfloat16 [rows, heads, head_dim]")
+    n, h, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError("the heads of a row must be contiguous")
+    stride = max(t.stride(0), h * d) if n <= 1 else t.stride(0)
+    return C.c_void_p(t.data_ptr()), stride, (n, h, d)
+
+
+def _set_workspace(a, workspace):
+    if workspace is not None:
+        a.workspace = _ptr(workspace)
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+
+
+def qk_norm_rope_args(q, k, positions, *, q_out, k_out, q_weight=None,
+                      k_weight=None, eps: float = 1e-6, rope_base: float = 0.0,
+                      inv_freq=None, workspace=None) -> NormRopeArgs:
+    """Arguments of ds_qk_norm_rope.  q [rows, H_q, D] and k [rows, H_kv, D]
+    (either may be None) and their outputs may be slices of wider rows;
+    inv_freq is a sequence of D / 2 radians per position."""
+    a = NormRopeArgs()
+    load().ds_norm_rope_args_default(C.byref(a))
+    a.q, a.q_row_stride, qs = _rows(q)
+    a.k, a.k_row_stride, ks = _rows(k)
+    a.q_out, a.q_out_row_stride, qo = _rows(q_out)
+    a.k_out, a.k_out_row_stride, ko = _rows(k_out)
+    if qs != qo or ks != ko or (q is not None and k is not None and
+                                (qs[0], qs[2]) != (ks[0], ks[2])):
+        raise ValueError("q, k and their outputs must agree in rows, heads and head_dim")
+    a.n_rows, a.head_dim = qs[0] if q is not None else ks[0], qs[2] or ks[2]
+    if positions.dtype != torch.int32 or positions.numel() != a.n_rows:
+        raise ValueError("positions must be int32, one per row")
+    a.num_q_heads, a.num_kv_heads = qs[1], ks[1]
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.bfloat16 or w.numel() != a.head_dim):
+            raise ValueError("weights must be bfloat16 [head_dim]")
+    a.q_weight, a.k_weight = _ptr(q_weight), _ptr(k_weight)
+    a.positions = _ptr(positions)
+    a.eps, a.rope_base = eps, rope_base
+    if inv_freq is not None:
+        if len(inv_freq) != a.head_dim // 2:
+            raise ValueError("inv_freq must hold head_dim / 2 values")
+        a._keep = (C.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
+        a.inv_freq = C.cast(a._keep, C.POINTER(C.c_double))
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_qk_norm_rope(args: NormRopeArgs, stream=None):
+    _check(load().ds_qk_norm_rope(C.byref(args), _stream(stream)))
+
+
+def kv4_block_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page of one kv head in a 4-bit pool: a pool is a uint8
+    tensor [num_pages, H_kv, kv4_block_bytes(page_size, head_dim)]."""
+    return page_size * head_dim * 9 // 16
+
+
+def _kv4_pool(pool: torch.Tensor, heads: int, page_size: int, head_dim: int) -> int:
+    if pool.dtype != torch.uint8 or tuple(pool.shape[1:]) != (
+            heads, kv4_block_bytes(page_size, head_dim)):
+        raise ValueError("a 4-bit pool is uint8 [num_pages, num_kv_heads, "
+                         "kv4_block_bytes(page_size, head_dim)]")
+    return pool.shape[0]
+
+
+def kv4_rows_args(k_rows, v_rows, k_cache, v_cache, page_table, from_lens,
+                  row_offsets, *, page_size: int, k_exp: int = 0, v_exp: int = 0,
+                  path=None, n_accepted=None, new_lens=None,
+                  workspace=None) -> Kv4RowsArgs:
+    """Arguments of ds_kv4_write and ds_kv4_read: rows [rows, H_kv, D] bf16
+    (slices of wider rows are fine) and 4-bit pools."""
+    a = Kv4RowsArgs()
+    load().ds_kv4_rows_args_default(C.byref(a))
+    a.k_rows, a.k_row_stride, ks = _rows(k_rows)
+    a.v_rows, a.v_row_stride, vs = _rows(v_rows)
+    if ks != vs:
+        raise ValueError("k_rows and v_rows must agree in shape")
+    a.n_rows, a.num_kv_heads, a.head_dim = ks
+    a.num_pages = min(_kv4_pool(c, ks[1], page_size, ks[2]) for c in (k_cache, v_cache))
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+    a.page_table, a.from_lens = _ptr(page_table), _ptr(from_lens)
+    a.row_offsets, a.path, a.n_accepted = _ptr(row_offsets), _ptr(path), _ptr(n_accepted)
+    a.batch, a.max_pages = page_table.shape
+    a.page_size, a.k_exp, a.v_exp = page_size, k_exp, v_exp
+    a.new_lens = _ptr(new_lens)
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_kv4_write(args: Kv4RowsArgs, stream=None):
+    _check(load().ds_kv4_write(C.byref(args), _stream(stream)))
+
+
+def ds_kv4_read(args: Kv4RowsArgs, stream=None):
+    _check(load().ds_kv4_read(C.byref(args), _stream(stream)))
+
+
+def kv4_attn_args(q, k_cache, v_cache, page_table, ctx_lens, tree_offsets,
+                  parents, *, page_size: int, chunk_size: int = 0, k_exp: int = 0,
+                  v_exp: int = 0, out=None, chunk_scores=None, workspace=None,
+                  scale: float = 0.0, accumulate: bool = False,
+                  num_sms: int = 0) -> Kv4AttnArgs:
+    """Arguments of ds_kv4_verify_attn; without chunk_scores no salience is
+    formed and chunk_size is not used."""
+    a = Kv4AttnArgs()
+    load().ds_kv4_attn_args_default(C.byref(a))
+    a.q, a.k_cache, a.v_cache = _ptr(q), _ptr(k_cache), _ptr(v_cache)
+    a.page_table, a.ctx_lens = _ptr(page_table), _ptr(ctx_lens)
+    a.tree_offsets, a.parents = _ptr(tree_offsets), _ptr(parents)
+    a.n_nodes, a.num_q_heads, a.head_dim = q.shape
+    a.num_kv_heads = k_cache.shape[1]
+    a.num_pages = min(_kv4_pool(c, a.num_kv_heads, page_size, a.head_dim)
+                      for c in (k_cache, v_cache))
+    a.batch, a.max_pages = page_table.shape
+    a.page_size, a.chunk_size, a.scale = page_size, chunk_size, scale
+    a.k_exp, a.v_exp = k_exp, v_exp
+    if out is not None:
+        a.out = _ptr(out)
+        a.out_dtype = DS_OUT_F32 if out.dtype == torch.float32 else DS_OUT_BF16
+    if chunk_scores is not None:
+        a.chunk_scores = _ptr(chunk_scores)
+        a.max_chunks = chunk_scores.shape[1]
+    a.accumulate_scores = 1 if accumulate else 0
+    a.num_sms = num_sms
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_kv4_verify_attn_workspace_size(args: Kv4AttnArgs) -> int:
+    n = C.c_size_t(0)
+    _check(load().ds_kv4_verify_attn_workspace_size(C.byref(args), C.byref(n)))
+    return n.value
+
+
+def ds_kv4_verify_attn(args: Kv4AttnArgs, stream=None):
+    _check(load().ds_kv4_verify_attn(C.byref(args), _stream(stream)))
 
 
 def ds_workspace_init(workspace: torch.Tensor, stream=None):

@@ -135,6 +135,34 @@ AcceptLayout accept_layout(const ds_accept_args& a) {
   return L;
 }
 
+ds_verify_args kv4_as_verify(const ds_kv4_attn_args& a) {
+  ds_verify_args v;
+  ds_verify_args_default(&v);
+  v.q = a.q;
+  v.page_table = a.page_table;
+  v.ctx_lens = a.ctx_lens;
+  v.tree_offsets = a.tree_offsets;
+  v.parents = a.parents;
+  v.batch = a.batch;
+  v.n_nodes = a.n_nodes;
+  v.num_q_heads = a.num_q_heads;
+  v.num_kv_heads = a.num_kv_heads;
+  v.head_dim = a.head_dim;
+  v.page_size = a.page_size;
+  v.num_pages = a.num_pages;
+  v.max_pages = a.max_pages;
+  v.kv_layout = DS_KV_HND;
+  v.scale = a.scale;
+  v.out = a.out;
+  v.out_dtype = a.out_dtype;
+  v.chunk_scores = a.chunk_scores;
+  v.chunk_size = a.chunk_scores ? a.chunk_size : 128;
+  v.max_chunks = a.chunk_scores ? a.max_chunks : 0;
+  v.accumulate_scores = a.chunk_scores ? a.accumulate_scores : 0;
+  v.num_sms = a.num_sms;
+  return v;
+}
+
 ds_status set_last_error(ds_status st, const char* msg) {
   g_err = msg;
   return st;
@@ -155,6 +183,9 @@ int64_t ds_struct_size(int32_t which) {
     case 2: return (int64_t)sizeof(ds_accept_args);
     case 3: return (int64_t)sizeof(ds_commit_args);
     case 4: return (int64_t)sizeof(ds_append_args);
+    case 5: return (int64_t)sizeof(ds_norm_rope_args);
+    case 6: return (int64_t)sizeof(ds_kv4_rows_args);
+    case 8: return (int64_t)sizeof(ds_kv4_attn_args);
     default: return -1;
   }
 }
@@ -418,6 +449,196 @@ ds_status ds_compact_append(const ds_append_args* a, void* stream) {
           "workspace_bytes %zu < %zu", a->workspace_bytes, ds::kStatusBytes);
   cudaError_t e = ds::launch_compact_append(*a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "ds_compact_append launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_norm_rope_args_default(ds_norm_rope_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+  a->eps = 1e-6f;
+}
+
+static ds_status check_heads(const char* name, const void* in, const void* out, int64_t is,
+                             int64_t os, int heads, int d) {
+  REQUIRE(in && out, DS_ERR_INVALID_ARG, "%s or %s_out is NULL", name, name);
+  REQUIRE(aligned16(in) && aligned16(out), DS_ERR_INVALID_ARG,
+          "%s and %s_out must be 16-byte aligned", name, name);
+  REQUIRE(is % 8 == 0 && os % 8 == 0 && is >= (int64_t)heads * d && os >= (int64_t)heads * d,
+          DS_ERR_INVALID_ARG,
+          "%s row strides (%lld, %lld) must be multiples of 8 of at least heads * head_dim",
+          name, (long long)is, (long long)os);
+  return DS_OK;
+}
+
+ds_status ds_qk_norm_rope(const ds_norm_rope_args* a, void* stream) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->n_rows >= 0, DS_ERR_INVALID_ARG, "n_rows must be >= 0 (got %d)", a->n_rows);
+  REQUIRE(a->num_q_heads >= 0 && a->num_kv_heads >= 0 &&
+              (int64_t)a->num_q_heads + a->num_kv_heads >= 1 &&
+              (int64_t)a->num_q_heads + a->num_kv_heads <= 1 << 20,
+          DS_ERR_INVALID_ARG, "num_q_heads (%d) and num_kv_heads (%d): at least one head",
+          a->num_q_heads, a->num_kv_heads);
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, DS_ERR_UNSUPPORTED,
+          "head_dim %d: only 64 and 128 are supported", a->head_dim);
+  REQUIRE(std::isfinite(a->eps) && a->eps >= 0.f, DS_ERR_INVALID_ARG,
+          "eps must be finite and >= 0");
+  REQUIRE(a->rope_base >= 0.f && a->rope_base < 3.0e38f, DS_ERR_INVALID_ARG,
+          "rope_base must be 0 or a finite positive base");
+  REQUIRE(!a->inv_freq || a->rope_base == 0.f, DS_ERR_INVALID_ARG,
+          "rope_base must be 0 when inv_freq is given");
+  if (a->inv_freq)
+    for (int j = 0; j < a->head_dim / 2; ++j)
+      REQUIRE(std::isfinite(a->inv_freq[j]), DS_ERR_INVALID_ARG, "inv_freq[%d] is not finite", j);
+  REQUIRE(a->workspace && a->workspace_bytes >= ds::kStatusBytes, DS_ERR_WORKSPACE,
+          "workspace must hold at least %zu bytes", ds::kStatusBytes);
+  if (a->n_rows == 0) return ok();
+  if (a->num_q_heads > 0) {
+    ds_status st = check_heads("q", a->q, a->q_out, a->q_row_stride, a->q_out_row_stride,
+                               a->num_q_heads, a->head_dim);
+    if (st != DS_OK) return st;
+  }
+  if (a->num_kv_heads > 0) {
+    ds_status st = check_heads("k", a->k, a->k_out, a->k_row_stride, a->k_out_row_stride,
+                               a->num_kv_heads, a->head_dim);
+    if (st != DS_OK) return st;
+  }
+  REQUIRE(aligned16(a->q_weight) && aligned16(a->k_weight), DS_ERR_INVALID_ARG,
+          "q_weight and k_weight must be 16-byte aligned");
+  REQUIRE(a->positions, DS_ERR_INVALID_ARG, "positions is NULL");
+  cudaError_t e = ds::launch_norm_rope(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_qk_norm_rope launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_kv4_rows_args_default(ds_kv4_rows_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+}
+
+static ds_status check_kv4(int head_dim, int page_size, int num_pages, int max_pages, int k_exp,
+                           int v_exp) {
+  REQUIRE(head_dim == 64 || head_dim == 128, DS_ERR_UNSUPPORTED, "head_dim %d (64 or 128)",
+          head_dim);
+  REQUIRE(page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128,
+          DS_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128)", page_size);
+  REQUIRE(num_pages >= 1 && max_pages >= 1, DS_ERR_INVALID_ARG,
+          "num_pages and max_pages must be >= 1");
+  REQUIRE((int64_t)max_pages * page_size <= ds::kKv4MaxSlots, DS_ERR_UNSUPPORTED,
+          "max_pages * page_size must not exceed 2^30");
+  REQUIRE(k_exp >= -32 && k_exp <= 32 && v_exp >= -32 && v_exp <= 32, DS_ERR_INVALID_ARG,
+          "k_exp (%d) and v_exp (%d) must lie in [-32, 32]", k_exp, v_exp);
+  return DS_OK;
+}
+
+static ds_status check_kv4_rows(const ds_kv4_rows_args* a) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->batch >= 1 && a->batch <= 1 << 24, DS_ERR_INVALID_ARG,
+          "batch must be >= 1 (got %d)", a->batch);
+  REQUIRE(a->n_rows >= 0, DS_ERR_INVALID_ARG, "n_rows must be >= 0 (got %d)", a->n_rows);
+  REQUIRE(a->num_kv_heads >= 1 && a->num_kv_heads <= 1024, DS_ERR_INVALID_ARG,
+          "num_kv_heads %d (1 to 1024)", a->num_kv_heads);
+  ds_status st = check_kv4(a->head_dim, a->page_size, a->num_pages, a->max_pages, a->k_exp,
+                           a->v_exp);
+  if (st != DS_OK) return st;
+  REQUIRE((a->k_rows && a->v_rows) || a->n_rows == 0, DS_ERR_INVALID_ARG,
+          "k_rows/v_rows is NULL");
+  REQUIRE(a->k_cache && a->v_cache, DS_ERR_INVALID_ARG, "k_cache/v_cache is NULL");
+  REQUIRE(aligned16(a->k_rows) && aligned16(a->v_rows) && aligned16(a->k_cache) &&
+              aligned16(a->v_cache),
+          DS_ERR_INVALID_ARG, "rows and caches must be 16-byte aligned");
+  const int64_t row = (int64_t)a->num_kv_heads * a->head_dim;
+  REQUIRE(a->k_row_stride % 8 == 0 && a->v_row_stride % 8 == 0 &&
+              ((a->k_row_stride >= row && a->v_row_stride >= row) || a->n_rows == 0),
+          DS_ERR_INVALID_ARG,
+          "row strides (%lld, %lld) must be multiples of 8 of at least %lld",
+          (long long)a->k_row_stride, (long long)a->v_row_stride, (long long)row);
+  REQUIRE(a->page_table && a->from_lens && a->row_offsets, DS_ERR_INVALID_ARG,
+          "page_table/from_lens/row_offsets is NULL");
+  REQUIRE(a->workspace, DS_ERR_WORKSPACE, "workspace is NULL");
+  REQUIRE(a->workspace_bytes >= ds::kStatusBytes, DS_ERR_WORKSPACE,
+          "workspace_bytes %zu < %zu", a->workspace_bytes, ds::kStatusBytes);
+  return DS_OK;
+}
+
+ds_status ds_kv4_write(const ds_kv4_rows_args* a, void* stream) {
+  ds_status st = check_kv4_rows(a);
+  if (st != DS_OK) return st;
+  REQUIRE((a->path == nullptr) == (a->n_accepted == nullptr), DS_ERR_INVALID_ARG,
+          "path and n_accepted go together");
+  REQUIRE(!a->new_lens || (const void*)a->new_lens != (const void*)a->from_lens,
+          DS_ERR_INVALID_ARG, "new_lens must not alias from_lens");
+  if (a->n_rows == 0 && !a->new_lens) return ok();
+  cudaError_t e = ds::launch_kv4_write(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_kv4_write launch");
+  return ok();
+}
+
+ds_status ds_kv4_read(const ds_kv4_rows_args* a, void* stream) {
+  ds_status st = check_kv4_rows(a);
+  if (st != DS_OK) return st;
+  REQUIRE(!a->path && !a->n_accepted && !a->new_lens, DS_ERR_INVALID_ARG,
+          "path, n_accepted and new_lens must be NULL when reading");
+  if (a->n_rows == 0) return ok();
+  cudaError_t e = ds::launch_kv4_read(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_kv4_read launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_kv4_attn_args_default(ds_kv4_attn_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+  a->out_dtype = DS_OUT_BF16;
+}
+
+static ds_status check_kv4_attn(const ds_kv4_attn_args* a, ds_verify_args* v) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  ds_status st = check_kv4(a->head_dim, a->page_size, a->num_pages, a->max_pages, a->k_exp,
+                           a->v_exp);
+  if (st != DS_OK) return st;
+  *v = ds::kv4_as_verify(*a);
+  return check_verify_sizes(v);
+}
+
+ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* a, size_t* bytes) {
+  ds_verify_args v;
+  ds_status st = check_kv4_attn(a, &v);
+  if (st != DS_OK) return st;
+  REQUIRE(bytes, DS_ERR_INVALID_ARG, "bytes is NULL");
+  int sms = v.num_sms;
+  if (sms == 0 && device_sms(&sms) != 0)
+    return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
+  *bytes = ds::verify_layout(v, sms).total;
+  return ok();
+}
+
+ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* a, void* stream) {
+  ds_verify_args v;
+  ds_status st = check_kv4_attn(a, &v);
+  if (st != DS_OK) return st;
+  REQUIRE(a->q || a->n_nodes == 0, DS_ERR_INVALID_ARG, "q is NULL");
+  REQUIRE(a->k_cache && a->v_cache, DS_ERR_INVALID_ARG, "k_cache/v_cache is NULL");
+  REQUIRE(a->page_table && a->ctx_lens && a->tree_offsets, DS_ERR_INVALID_ARG,
+          "page_table/ctx_lens/tree_offsets is NULL");
+  REQUIRE(a->parents || a->n_nodes == 0, DS_ERR_INVALID_ARG, "parents is NULL");
+  REQUIRE(a->out || a->n_nodes == 0, DS_ERR_INVALID_ARG, "out is NULL");
+  REQUIRE(aligned16(a->q) && aligned16(a->k_cache) && aligned16(a->v_cache) &&
+              aligned16(a->out),
+          DS_ERR_INVALID_ARG, "q, k_cache, v_cache and out must be 16-byte aligned");
+  REQUIRE(a->workspace, DS_ERR_WORKSPACE, "workspace is NULL");
+  REQUIRE((reinterpret_cast<uintptr_t>(a->workspace) & (ds::kAlign - 1)) == 0,
+          DS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  int sms = v.num_sms;
+  if (sms == 0 && device_sms(&sms) != 0)
+    return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
+  const ds::VerifyLayout L = ds::verify_layout(v, sms);
+  REQUIRE(a->workspace_bytes >= L.total, DS_ERR_WORKSPACE,
+          "workspace_bytes %zu < required %zu", a->workspace_bytes, L.total);
+  if (a->n_nodes == 0) return ok();
+  cudaError_t e = ds::launch_kv4_attn(*a, L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_kv4_verify_attn launch");
   return ok();
 }
 

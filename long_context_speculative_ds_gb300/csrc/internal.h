@@ -90,6 +90,18 @@ cudaError_t launch_accept(const ds_accept_args& a, const AcceptLayout& L,
 cudaError_t launch_kv_commit(const ds_commit_args& a, cudaStream_t stream);
 cudaError_t launch_compact_append(const ds_append_args& a, cudaStream_t stream);
 
+cudaError_t launch_norm_rope(const ds_norm_rope_args& a, cudaStream_t stream);
+cudaError_t launch_kv4_write(const ds_kv4_rows_args& a, cudaStream_t stream);
+cudaError_t launch_kv4_read(const ds_kv4_rows_args& a, cudaStream_t stream);
+cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
+                            cudaStream_t stream);
+
+// The sizes of a 4-bit attention call as those of a verify call: the work
+// plan and the workspace are the same.  Without salience there is one chunk
+// longer than any context, and no chunk masses.
+ds_verify_args kv4_as_verify(const ds_kv4_attn_args& a);
+constexpr int kKv4MaxSlots = 1 << 30;
+
 // Sets the message ds_last_error returns on this thread; returns st.
 ds_status set_last_error(ds_status st, const char* msg);
 
