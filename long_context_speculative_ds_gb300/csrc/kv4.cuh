@@ -10,6 +10,7 @@
 #include <stdint.h>
 
 #include "dev_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace ds {
 
@@ -49,18 +50,11 @@ DS_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// f16 pair of two f32 values, lo in the low half.
-DS_DEV uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A bf16 pair as an f16 pair: exact from 2^-14 up, rounded to 2^-24 below,
 // clamped to the largest f16 (a NaN stays one).
 DS_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
   auto clamp = [](float x) { return x > 65504.f ? 65504.f : (x < -65504.f ? -65504.f : x); };
-  return pack_f16x2(clamp(__uint_as_float(w << 16)), clamp(__uint_as_float(w & 0xffff0000u)));
+  return ptx::pack_f16x2(clamp(__uint_as_float(w << 16)), clamp(__uint_as_float(w & 0xffff0000u)));
 }
 
 // Sixteen values, already multiplied by 2^-exp, as one scale byte and eight

@@ -1,0 +1,594 @@
+// Split pass of ds_kv4_verify_attn for trees, on the 5th-generation tensor
+// cores (tcgen05) of sm_103a.
+//
+// The tree-verify split pass of the bf16 cache (verify_tc.cu: work items,
+// softmax groups, tensor-memory slots, P V / Q K order, split outputs) over
+// tiles that arrive in 4 bits and are brought to f16 in shared memory, where
+// code x scale is exact.  Rows of 72 bytes a key instead of 256 take the
+// stream of K and V off the critical path: with 256 query rows the tensor
+// pipe and the exponentials bound the kernel.
+//
+// 16 warps:
+//   warp 0      loader: page blocks (codes and scales of one page of one kv
+//               head, contiguous) into a ring of raw tiles by bulk copies;
+//               pages past the sequence end are not copied (no byte of the
+//               cache format reads as NaN or infinity, and their weights are
+//               zero), bad pages are marked and read as zeros.
+//   warp 1      tensor-memory allocator and ancestor masks.
+//   warps 2, 3  MMA issuers of softmax groups 0 and 1.
+//   warps 4-7, 8-11   softmax groups; at the start they also bring Q to f16.
+//   warps 12-15 converters: a key per thread.  Each thread reads its key's
+//               codes in 16-byte pieces, starting at a piece that depends on
+//               the lane so that eight lanes touch all banks, and writes
+//               16-byte chunks in the 128-byte-swizzled layout the MMA
+//               descriptors expect (eight lanes, eight bank groups).
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "dev_common.cuh"
+#include "internal.h"
+#include "kv4_common.cuh"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+#include "verify_common.cuh"
+#include "verify_softmax.cuh"
+
+namespace ds {
+namespace kv4tc {
+
+constexpr int kThreads = 512;
+constexpr uint32_t kHalfBytes = 128 * 128;
+constexpr int kTmemCols = 512;
+constexpr int kRawRow = 3;       // raw slots with two Q tiles
+constexpr int kRawKey = 6;       // three more in the second Q tile when it is unused
+
+enum Bar {
+  kQFull = 0,
+  kKFull = 1,      // 2 slots
+  kKEmpty = 3,
+  kVFull = 5,
+  kVEmpty = 7,
+  kRawFull = 9,    // 6 slots
+  kRawEmpty = 15,
+  kSFull = 21,     // [group][half]
+  kPFull = 25,     // [group][half]
+  kORdy = 29,      // [group]
+  kOFinal = 31,    // [group]
+  kAnc = 33,
+  kNumBars = 34
+};
+
+struct Ctrl {
+  uint64_t bar[kNumBars];
+  uint32_t tmem_base;
+  int abort;
+  Plan plan;
+  int32_t parents[DS_MAX_TREE_NODES];
+  uint64_t anc[DS_MAX_TREE_NODES];
+  uint32_t bad[kRawKey];         // bad pages of each raw tile, one bit a page
+  uint32_t where[6];             // last wait site of loader, issuers, softmax groups, converters
+  int last;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int TB = 128 * D * 2;            // bytes of one 128-row f16 tile
+  static constexpr int NH = D / 64;
+  static constexpr uint32_t RG = NH * 1024;
+  static constexpr int RAW = DS_KV4_BLOCK_BYTES(128, D);
+  // Q (2 tiles), K and V (2 slots each), raw tiles, control block
+  static constexpr size_t smem = 6 * TB + kRawRow * RAW + sizeof(Ctrl) + 1024;
+  static_assert(smem <= 232448, "dynamic shared memory above the 227 KB a block can have");
+  static_assert(4 * 32 * 32 * 4 <= TB, "output staging must fit in a Q tile");
+  static_assert((kRawKey - kRawRow) * RAW <= TB, "extra raw slots must fit in a Q tile");
+  static_assert(1024 <= kRawRow * RAW, "the merge's maxima and sums must fit in the raw ring");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
+  using namespace ptx;
+  using tc::softmax_unit;
+  const VerifyKArgs& a = ka.v;
+  constexpr int TB = Cfg<D>::TB;
+  constexpr uint32_t RG = Cfg<D>::RG;
+  constexpr int RAW = Cfg<D>::RAW;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t sQ = sbase;
+  const uint32_t sK = sbase + 2 * TB;
+  const uint32_t sV = sbase + 4 * TB;
+  const uint32_t sR = sbase + 6 * TB;
+  // key-mode merge scratch, used once all MMAs have completed: O of group 1
+  // over the V slots, its row maxima and sums over the raw ring
+  float* merge_buf = reinterpret_cast<float*>(smem + 4 * TB);
+  float* m1buf = reinterpret_cast<float*>(smem + 6 * TB);
+  float* l1buf = m1buf + 128;
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + 6 * TB + kRawRow * RAW);
+  volatile int* abort_flag = &ctrl->abort;
+  uint32_t* diag = a.plan.status + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return smem_addr(&ctrl->bar[i]); };
+
+  // ---------------------------------------------------------------- set-up
+  if (warp == 1 && lane == 0) {
+    mbar_init(bar(kQFull), 256);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kKFull + s), 4);      // one arrival per converter warp
+      mbar_init(bar(kVFull + s), 4);
+      mbar_init(bar(kKEmpty + s), 2);     // one commit per group (two in key mode)
+      mbar_init(bar(kVEmpty + s), 2);
+      mbar_init(bar(kORdy + s), 1);
+      mbar_init(bar(kOFinal + s), 1);
+    }
+    for (int s = 0; s < kRawKey; ++s) {
+      mbar_init(bar(kRawFull + s), 1);
+      mbar_init(bar(kRawEmpty + s), 4);
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(bar(kSFull + s), 1);
+    for (int s = 0; s < 4; ++s) mbar_init(bar(kPFull + s), 128);
+    mbar_init(bar(kAnc), 32);
+    ctrl->abort = 0;
+    for (int i = 0; i < 6; ++i) ctrl->where[i] = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&ctrl->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  const bool early_plan = a.accumulate != 0;
+  if (early_plan && warp == 0) {
+    Plan p = plan_find(a.plan, -1, blockIdx.x);
+    if (lane == 0) ctrl->plan = p;
+  }
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (!early_plan && warp == 0) {
+    Plan p = plan_find(a.plan, -1, blockIdx.x);
+    if (lane == 0) ctrl->plan = p;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctrl->tmem_base;
+  const Plan p = ctrl->plan;
+  const bool active = (int)blockIdx.x < p.total_items && p.b >= 0;
+
+  const SeqPlan& sq = p.seq;
+  const int G = a.plan.group;
+  int kvh = 0, rgi = 0, t0 = 0, t1 = 0, rows_here = 0;
+  if (active) {
+    const int local = blockIdx.x - sq.item_base;
+    const int per_h = sq.rg * sq.splits;
+    kvh = local / per_h;
+    rgi = (local % per_h) / sq.splits;
+    const int split = local % sq.splits;
+    const int base = sq.tiles / sq.splits, rem = sq.tiles % sq.splits;
+    t0 = split * base + min(split, rem);
+    t1 = t0 + base + (split < rem ? 1 : 0);
+    rows_here = min(kRowsPerGroup, sq.rows - rgi * kRowsPerGroup);
+  }
+  const int nt = t1 - t0;
+  const bool row_mode = rows_here > 128;
+  const int L = sq.L, T = sq.T;
+  const bool need_anc = active && t1 * kTileKeys > L;
+  const int nraw = row_mode ? kRawRow : kRawKey;
+  auto raw_addr = [&](int s) -> uint32_t {
+    return s < kRawRow ? sR + s * RAW : sQ + TB + (s - kRawRow) * RAW;
+  };
+  // Tiles are loaded and converted in the order the MMAs need them: K runs
+  // one tile ahead of V (two in key mode, where both groups start at once).
+  // Position i of that order: tensor and tile.
+  const int lead = row_mode ? 1 : 2;
+  auto order = [&](int i, int& is_v, int& n) {
+    const int head = min(lead, nt);
+    if (i < head) { is_v = 0; n = i; return; }
+    // V(m), K(m + lead) pairs while there are K tiles left, then V alone
+    const int j = i - head, pairs = max(0, nt - lead);
+    if (j < 2 * pairs) { is_v = (j & 1) ^ 1; n = (j >> 1) + (is_v ? 0 : lead); }
+    else { is_v = 1; n = j - pairs; }
+  };
+  // tiles of group g: row mode every tile, key mode every other tile (so
+  // slot n % 2 is then always group n % 2's)
+  auto ntiles = [&](int g) { return row_mode ? nt : (nt - g + 1) / 2; };
+  auto tile_of = [&](int g, int j) { return row_mode ? j : 2 * j + g; };
+
+  if (warp < 4) {
+    if (!(active && nt > 0)) {
+    } else if (warp == 0) {
+      // ------------------------------------------------------------ loader
+      const int P = a.plan.page_size;
+      const int npg = kTileKeys / P;
+      const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
+      const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
+      const uint64_t policy = l2_evict_first();
+      int issued = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < 2 * nt; ++i) {
+        int is_v, n;
+        order(i, is_v, n);
+        const int slot = i % nraw;
+        const int slot0 = (t0 + n) * kTileKeys + lane * P;
+        int pg = 0;
+        bool have = lane < npg && slot0 < L + T, bad = false;
+        if (have) {
+          pg = __ldg(ptab + slot0 / P);
+          bad = pg < 0 || pg >= a.num_pages;
+          if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
+        }
+        const uint32_t badm = __ballot_sync(0xffffffffu, bad);
+        have = have && !bad;
+        const uint32_t copies = __ballot_sync(0xffffffffu, have);
+        if (lane == 0) ctrl->where[0] = 10000 + i;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + slot), ((i / nraw) & 1) ^ 1,
+                                               abort_flag, diag, 10000 + i));
+        if (!ok) break;
+        if (lane == 0) {
+          ctrl->bad[slot] = badm;
+          mbar_arrive_expect_tx(bar(kRawFull + slot), __popc(copies) * blk);
+        }
+        __syncwarp();
+        if (have)
+          bulk_load_hint(raw_addr(slot) + lane * blk,
+                         (is_v ? ka.v4 : ka.k4) +
+                             ((int64_t)pg * a.plan.num_kv_heads + kvh) * blk,
+                         blk, bar(kRawFull + slot), policy);
+        issued = i + 1;
+      }
+      if (lane == 0) ctrl->where[0] = ok ? 19999 : 19998;
+      // copies still in flight must land before the CTA can exit
+      if (!ok && lane == 0)
+        for (int i = max(0, issued - nraw); i < issued; ++i)
+          drain_wait(bar(kRawFull + i % nraw), (i / nraw) & 1);
+    } else if (warp == 1) {
+      // ---------------------------------------------------- ancestor masks
+      if (need_anc) {
+        tc::tree_ancestors(a.parents + sq.node0, T, ctrl->parents, ctrl->anc, a.plan.status);
+        mbar_arrive(bar(kAnc));
+      }
+    } else {
+      // ------------------------------------------------------ MMA issuers
+      const int g = warp - 2;
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = idesc_f16_f32(128, 64, false);
+        constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, true);
+        const uint64_t qd0 = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t qb = (row_mode && g == 1) ? qd0 + (TB >> 4) : qd0;
+        const uint64_t kd0 = sdesc_sw128(sK, 16, RG);
+        const uint64_t vd0 = sdesc_sw128(sV, 1024, RG);
+        const uint32_t tG = tmem + (uint32_t)(256 * g);
+        const int rel = row_mode ? 1 : 2;
+        auto qk = [&](int t, int h) {
+          const uint64_t kb = kd0 + (uint64_t)((t & 1) * (TB >> 4) + h * ((8 * RG) >> 4));
+          const uint32_t d = tG + (uint32_t)(64 * h);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t qoff = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+            const uint32_t koff = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+            mma_ss(d, qb + qoff, kb + koff, idesc_qk, kk > 0);
+          }
+        };
+        auto pv = [&](int t, int h, bool acc) {
+          const uint64_t vb = vd0 + (uint64_t)((t & 1) * (TB >> 4) + h * ((8 * RG) >> 4));
+          const uint32_t pa = tG + (uint32_t)(64 * h);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tG + 128, pa + kk * 8, vb + (uint64_t)(kk * ((2 * RG) >> 4)), idesc_pv,
+                   (acc || kk > 0) ? 1u : 0u);
+        };
+        const int wi = 1 + g;
+        auto wait = [&](int b, uint32_t par, uint32_t tag) {
+          ctrl->where[wi] = tag;
+          return mbar_wait(bar(b), par, abort_flag, diag, tag);
+        };
+        auto wait_k = [&](int t) {
+          return wait(kKFull + (t & 1), (t >> 1) & 1, 20000 + kKFull * 100 + t);
+        };
+        auto wait_v = [&](int t) {
+          return wait(kVFull + (t & 1), (t >> 1) & 1, 20000 + kVFull * 100 + t);
+        };
+        const int my_nt = ntiles(g);
+        bool ok = wait(kQFull, 0, 20000 + kQFull * 100);
+        if (ok && my_nt > 0) {
+          const int t = tile_of(g, 0);
+          if ((ok = wait_k(t))) {
+            tc_fence_after();
+            for (int h = 0; h < 2; ++h) {
+              qk(t, h);
+              mma_commit(bar(kSFull + 2 * g + h));
+            }
+            for (int r = 0; r < rel; ++r) mma_commit(bar(kKEmpty + (t & 1)));
+          }
+        }
+        for (int j = 0; ok && j < my_nt; ++j) {
+          const int n = tile_of(g, j);
+          const bool more = j + 1 < my_nt;
+          const int tn = more ? tile_of(g, j + 1) : 0;
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait(kPFull + 2 * g + h, j & 1,
+                            20000 + (kPFull + 2 * g + h) * 100 + 2 * j + h)))
+              break;
+            if (h == 0 && !(ok = wait_v(n))) break;
+            tc_fence_after();
+            pv(n, h, j > 0 || h > 0);
+            mma_commit(bar(kORdy + g));
+            if (more) {
+              if (h == 0) {
+                if (!(ok = wait_k(tn))) break;
+                tc_fence_after();
+              }
+              qk(tn, h);
+              mma_commit(bar(kSFull + 2 * g + h));
+              if (h == 1)
+                for (int r = 0; r < rel; ++r) mma_commit(bar(kKEmpty + (tn & 1)));
+            }
+            if (h == 1)
+              for (int r = 0; r < rel; ++r) mma_commit(bar(kVEmpty + (n & 1)));
+          }
+        }
+        if (ok) ctrl->where[wi] = 29999;
+        mma_commit(bar(kOFinal + g));
+      }
+    }
+  } else if (warp < 12) {
+    if (active && nt > 0) {
+      // ------------------------------------------------------------ softmax
+      const int g = (warp - 4) >> 2;
+      const int q4 = warp & 3;
+      const int lrow = q4 * 32 + lane;
+      const int grow_local = row_mode ? g * 128 + lrow : lrow;
+      const bool row_ok = grow_local < rows_here;
+      const int grow = rgi * kRowsPerGroup + grow_local;
+      const int jn = grow / G;
+      // this thread's query row as f16 into its Q tile (key mode: one tile,
+      // group 0's)
+      if (row_mode || g == 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((int64_t)(sq.node0 + jn) * a.num_q_heads + kvh * G + grow % G) * D);
+        const uint32_t dst = sQ + (row_mode ? g * TB : 0) + lrow * 128;
+#pragma unroll
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = row_ok ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             dst + (c0 >> 3) * kHalfBytes + ((c ^ (lrow & 7)) << 4)),
+                         "r"(bf16x2_to_f16x2(x[c].x)), "r"(bf16x2_to_f16x2(x[c].y)),
+                         "r"(bf16x2_to_f16x2(x[c].z)), "r"(bf16x2_to_f16x2(x[c].w))
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(bar(kQFull));
+      uint64_t anc = 0ull;
+      bool anc_ready = !need_anc;
+      const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+      const uint32_t tG = tmem + lane_addr + 256 * g;
+      const uint32_t tO = tG + 128;
+      const float c2 = a.scale_log2;
+      const int C = a.plan.chunk_size;
+      const int cshift = __ffs(C) - 1;
+      const int n_ch = a.scores ? (L + C - 1) / C : 0;
+      float* clse_row = a.clse +
+                        (((int64_t)p.b * a.plan.num_kv_heads + kvh) * a.plan.rg_max + rgi) *
+                            a.plan.max_chunks * kRowsPerGroup +
+                        grow_local;
+      float m2 = -CUDART_INF_F, l = 0.f, cs = 0.f;
+      bool ok = true;
+      const int my_nt = ntiles(g);
+      const int wi = 3 + g;
+      for (int j = 0; ok && j < my_nt; ++j) {
+        const int n = tile_of(g, j);
+        const int tile_slot0 = (t0 + n) * kTileKeys;
+        for (int hb = 0; hb < 2; ++hb) {
+          const int u = 2 * j + hb;
+          if (lrow == 0) ctrl->where[wi] = 30000 + (kSFull + 2 * g + hb) * 100 + j;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + 2 * g + hb), j & 1, abort_flag,
+                                                 diag, 30000 + (kSFull + 2 * g + hb) * 100 + j));
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tS = tG + 64 * hb;
+          const int unit_slot0 = tile_slot0 + 64 * hb;
+          float alpha;
+          bool rescale;
+          if (unit_slot0 + 64 <= L) {
+            softmax_unit<false, true>(tS, tS, ~0u, ~0u, ~0u, ~0u, c2, u == 0, m2, l, cs, alpha,
+                                      rescale, tile_slot0, 4 * hb, cshift, n_ch, row_ok,
+                                      clse_row);
+          } else {
+            if (!anc_ready) {
+              if (lrow == 0) ctrl->where[wi] = 30000 + kAnc * 100;
+              ok = __all_sync(0xffffffffu, mbar_wait(bar(kAnc), 0, abort_flag, diag,
+                                                     30000 + kAnc * 100));
+              if (!ok) break;
+              anc = (row_ok && jn < T) ? ctrl->anc[jn] : 0ull;
+              anc_ready = true;
+            }
+            const int off = L - unit_slot0;
+            const uint64_t ctx = off >= 64 ? ~0ull : (off <= 0 ? 0ull : ((1ull << off) - 1));
+            const uint64_t tr = off >= 0 ? (off >= 64 ? 0ull : (anc << off))
+                                         : (-off >= 64 ? 0ull : (anc >> (-off)));
+            const uint64_t vis = ctx | tr;
+            softmax_unit<true, true>(tS, tS, (uint32_t)vis, (uint32_t)(vis >> 32),
+                                     (uint32_t)ctx, (uint32_t)(ctx >> 32), c2, u == 0, m2, l, cs,
+                                     alpha, rescale, tile_slot0, 4 * hb, cshift, n_ch, row_ok,
+                                     clse_row);
+          }
+          if (rescale) {
+            if (lrow == 0) ctrl->where[wi] = 30000 + (kORdy + g) * 100 + u;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kORdy + g), (u - 1) & 1, abort_flag,
+                                                   diag, 30000 + (kORdy + g) * 100 + u));
+            if (ok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int c4 = 0; c4 < D / 32; ++c4) {
+                uint32_t r[32];
+                tmem_ld32(tO + c4 * 32, r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+                tmem_st32(tO + c4 * 32, r);
+              }
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(kPFull + 2 * g + hb));
+          if (!ok) break;
+        }
+      }
+      // ------------------------------------------------------------ epilogue
+      if (lrow == 0) ctrl->where[wi] = 30000 + (kOFinal + g) * 100;
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFinal + g), 0, abort_flag, diag,
+                                               30000 + (kOFinal + g) * 100));
+      if (ok && !row_mode)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFinal + 1 - g), 0, abort_flag, diag,
+                                               30000 + (kOFinal + 1 - g) * 100));
+      else __syncwarp();
+      if (ok) tc_fence_after();
+      const int nt1 = row_mode ? 0 : ntiles(1);
+      float* stage = reinterpret_cast<float*>(smem + (row_mode ? g * TB : 0)) +
+                     q4 * 32 * tc::kStageStride;
+      const int warp_row0 = grow_local - lane;
+      const int64_t orow = ((int64_t)blockIdx.x * kRowsPerGroup + warp_row0) * D;
+      void* op_warp = a.out_f32 ? static_cast<void*>(a.o_part + orow)
+                                : static_cast<void*>(
+                                      reinterpret_cast<__nv_bfloat16*>(a.o_part) + orow);
+      tc::write_row_output<D>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l,
+                              merge_buf, m1buf, l1buf, stage, !a.out_f32, op_warp,
+                              a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
+                              ka.out_mult);
+    }
+  } else if (active && nt > 0) {
+    // ---------------------------------------------------------- converters
+    const int key = (warp - 12) * 32 + lane;
+    const int P = a.plan.page_size;
+    const int pidx = key / P, off = key % P;
+    // this key's codes and scales inside a raw tile
+    const uint32_t ccode = pidx * DS_KV4_BLOCK_BYTES(P, D) + off * (D / 2);
+    const uint32_t cscale = pidx * DS_KV4_BLOCK_BYTES(P, D) + P * (D / 2) + off * (D / 16);
+    const uint32_t drow = (key >> 3) * RG + (key & 7) * 128;
+    const bool rep = warp == 12 && lane == 0;
+    bool ok = true;
+    for (int i = 0; i < 2 * nt; ++i) {
+      int is_v, n;
+      order(i, is_v, n);
+      const int slot = i % nraw;
+      if (rep) ctrl->where[5] = 40000 + i;
+      ok = mbar_wait(bar(kRawFull + slot), (i / nraw) & 1, abort_flag, diag, 40000 + i) &&
+           mbar_wait(bar((is_v ? kVEmpty : kKEmpty) + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag,
+                     diag, 45000 + i);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const bool bad = (ctrl->bad[slot] >> pidx) & 1u;
+      const uint32_t raw = raw_addr(slot);
+      const uint32_t dst = (is_v ? sV : sK) + (n & 1) * TB + drow;
+      constexpr int NP = D / 32;           // 16-byte pieces of 32 channels
+      uint32_t s01, s23 = 0;
+      if constexpr (D == 128)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s01), "=r"(s23) : "r"(raw + cscale));
+      else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s01) : "r"(raw + cscale));
+      if (bad) s01 = s23 = 0u;             // scales of zero
+      const uint64_t sc = (uint64_t)s23 << 32 | s01;
+      uint4 c[NP];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint32_t pc = (j + (lane >> 1)) & (NP - 1);
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c[j].x), "=r"(c[j].y), "=r"(c[j].z), "=r"(c[j].w)
+                     : "r"(raw + ccode + pc * 16));
+      }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const uint32_t pc = (j + (lane >> 1)) & (NP - 1);
+        const uint32_t s2 = kv4_scales_f16((uint32_t)(sc >> (16 * pc)) & 0xffffu);
+        const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {      // 16-byte chunk 4 pc + k of the key
+          uint32_t v[4];
+          kv4_codes_f16(w[k], v);
+          const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
+          const uint32_t chunk = 4 * pc + k;
+          const uint32_t d = dst + (chunk >> 3) * 1024 + (((chunk & 7) ^ (key & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(hmul2(v[0], s)),
+                       "r"(hmul2(v[1], s)), "r"(hmul2(v[2], s)), "r"(hmul2(v[3], s))
+                       : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar((is_v ? kVFull : kKFull) + (n & 1)));
+        mbar_arrive(bar(kRawEmpty + slot));
+      }
+    }
+  }
+
+  // --------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && threadIdx.x == 0) {
+    flag(a.plan.status, DS_DEV_TIMEOUT);
+    if (diag[1] == blockIdx.x)
+      for (int i = 0; i < 6; ++i) diag[2 + i] = ctrl->where[i];
+  }
+  if (active && nt > 0) {
+    // the last split of the row group forms the rows' final log2-sum-exp
+    // (see verify_tc.cu)
+    const int64_t cidx = ((int64_t)p.b * a.plan.num_kv_heads + kvh) * a.plan.rg_max + rgi;
+    const int64_t base = (int64_t)sq.item_base + (kvh * sq.rg + rgi) * sq.splits;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      const uint32_t prev = atomicAdd(a.counters + cidx, 1u);
+      const int last = prev + 1 == (uint32_t)sq.splits;
+      if (last) {
+        a.counters[cidx] = 0u;
+        a.gdesc[cidx] = make_int4((int)base, sq.splits, 0, 0);
+        __threadfence();
+      }
+      ctrl->last = last;
+    }
+    __syncthreads();
+    if (ctrl->last)
+      for (int r = threadIdx.x; r < rows_here; r += kThreads)
+        a.row_lse[cidx * kRowsPerGroup + r] =
+            tc::row_lse_from_splits(a.lse_part + base * kRowsPerGroup + r, sq.splits);
+  }
+  if (warp == 1) {
+    if (active && nt > 0 && lane == 0) {
+      drain_wait(bar(kOFinal), 0);
+      drain_wait(bar(kOFinal + 1), 0);
+    }
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace kv4tc
+
+template <int D>
+static cudaError_t launch_tc(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t stream) {
+  const size_t smem = kv4tc::Cfg<D>::smem;
+  cudaError_t e = cudaFuncSetAttribute(kv4tc::kv4_split_tc<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kv4tc::kv4_split_tc<D>, dim3(L.max_items), dim3(kv4tc::kThreads), smem,
+                          stream, k);
+}
+
+cudaError_t launch_kv4_split_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
+                                cudaStream_t stream) {
+  return head_dim == 128 ? launch_tc<128>(k, L, stream) : launch_tc<64>(k, L, stream);
+}
+
+}  // namespace ds
