@@ -67,6 +67,7 @@ struct Ctrl {
   int32_t parents[DS_MAX_TREE_NODES];
   uint64_t anc[DS_MAX_TREE_NODES];
   uint32_t bad[kRawKey];         // bad pages of each raw tile, one bit a page
+  int32_t pages[2][32];          // page ids of two runs of tiles (the loader's)
   uint32_t where[6];             // last wait site of loader, issuers, softmax groups, converters
   int last;
 };
@@ -207,17 +208,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
       const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
       const uint64_t policy = l2_evict_first();
+      // Page ids come 32 at a time, a run of 32 / npg tiles, one run ahead of
+      // the K tiles (V is at most two tiles behind K, so two runs are kept):
+      // a load per tile would put its latency into every tile's turn.
+      const int run = 32 / npg, pend = (L + T + P - 1) / P;
+      auto ids_of = [&](int r) {
+        const int pi = (t0 + r * run) * npg + lane;
+        return pi < pend ? __ldg(ptab + pi) : 0;
+      };
+      int next_ids = ids_of(0);
       int issued = 0;
       bool ok = true;
       for (int i = 0; ok && i < 2 * nt; ++i) {
         int is_v, n;
         order(i, is_v, n);
+        const int r = n / run;
+        if (!is_v && n == r * run) {
+          ctrl->pages[r & 1][lane] = next_ids;
+          __syncwarp();
+          next_ids = ids_of(r + 1);
+        }
         const int slot = i % nraw;
         const int slot0 = (t0 + n) * kTileKeys + lane * P;
         int pg = 0;
         bool have = lane < npg && slot0 < L + T, bad = false;
         if (have) {
-          pg = __ldg(ptab + slot0 / P);
+          pg = ctrl->pages[r & 1][(n - r * run) * npg + lane];
           bad = pg < 0 || pg >= a.num_pages;
           if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
         }
