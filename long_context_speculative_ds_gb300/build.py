@@ -20,7 +20,8 @@ OUT_DIR = os.path.join(HERE, "lib")
 LIB_NAME = "libds_verify.so"
 SOURCES = ["abi.cpp", "verify_attn.cu", "verify_tc.cu", "topk_gather.cu",
            "accept.cu", "accept_static.cu", "kv_commit.cu",
-           "norm_rope.cu", "kv4_rows.cu", "kv4_attn.cu", "kv4_tc.cu"]
+           "norm_rope.cu", "kv4_rows.cu", "kv4_attn.cu", "kv4_tc.cu",
+           "kv4_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "-I" + INCLUDE, "-I" + CSRC]

@@ -55,6 +55,10 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
   ka.k4 = static_cast<const uint8_t*>(a.k_cache);
   ka.v4 = static_cast<const uint8_t*>(a.v_cache);
   ka.out_mult = ldexpf(1.f, a.v_exp);
+  // rows per sequence and kv head on average: the trees' sizes are on the
+  // device, and both passes handle any
+  const int64_t rows = ((int64_t)a.n_nodes + a.batch - 1) / a.batch * L.group;
+  if (rows <= 16) return launch_kv4_few(ka, a.head_dim, (int)rows, L, stream);
   cudaError_t e = launch_kv4_split_tc(ka, a.head_dim, L, stream);
   if (e != cudaSuccess) return e;
   return launch_finish(k, a.head_dim, L.rg_max, a.batch, stream);

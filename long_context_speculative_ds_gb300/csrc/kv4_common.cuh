@@ -17,4 +17,9 @@ struct Kv4KArgs {
 cudaError_t launch_kv4_split_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
                                 cudaStream_t stream);
 
+// The whole call for few query rows per sequence and kv head (kv4_few.cu);
+// `rows` is the number to plan for, any number is handled.
+cudaError_t launch_kv4_few(const Kv4KArgs& k, int head_dim, int rows, const VerifyLayout& L,
+                           cudaStream_t stream);
+
 }  // namespace ds
