@@ -168,16 +168,17 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
     tc::tree_ancestors(a.parents + sq.node0, T, ctrl.parents, ctrl.anc, a.plan.status);
   __syncthreads();
 
-  // this warp's blocks of 16 keys: units warp, warp + W, ... of the item
-  constexpr int bpu = 4;
+  // this warp's blocks of 16 keys: units warp, warp + W, ... of the item;
+  // block i is block i % 4 of its unit i / 4
+  constexpr int kUnit = 4;
   const int nb_item = (min(t1 * kTileKeys, L + T) - t0 * kTileKeys + 15) / 16;
-  const int n_units = (nb_item + bpu - 1) / bpu;
+  const int n_units = (nb_item + kUnit - 1) / kUnit;
   const int mine = n_units > warp ? (n_units - warp - 1) / W + 1 : 0;
   const int last_unit = warp + (mine - 1) * W;
-  const int nblk = mine > 0 ? (mine - 1) * bpu + min(bpu, nb_item - last_unit * bpu) : 0;
-  auto key_of = [&](int i) {
-    return t0 * kTileKeys + ((warp + i / bpu * W) * bpu + i % bpu) * 16;
-  };
+  const int nblk = mine > 0 ? (mine - 1) * kUnit + min(kUnit, nb_item - last_unit * kUnit) : 0;
+  const int first_key = t0 * kTileKeys + warp * kUnit * 16;
+  const int pshift = __ffs(P) - 1;
+  auto key_of = [&](int i) { return first_key + (i >> 2) * (W * kUnit * 16) + (i & 3) * 16; };
   const uint32_t ring = smem_addr(smem) + warp * C_::kRing;
   const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
   const uint8_t* k_head = ka.k4 + (int64_t)kvh * blk;
@@ -237,8 +238,18 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
     }
 
     // page ids of this warp's blocks, 32 at a time, the next 32 on their way
-    auto ids_of = [&](int i) { return i < nblk ? __ldg(ptab + key_of(i) / P) : 0; };
+    auto ids_of = [&](int i) { return i < nblk ? __ldg(ptab + (key_of(i) >> pshift)) : 0; };
     int ids = ids_of(lane), next_ids = ids_of(32 + lane);
+    // pieces this lane copies: one or two of the codes of each tensor, and
+    // for the first lanes one of the scales
+    constexpr int PPK = CB / 16;                    // 16-byte pieces of a key
+    constexpr int SP = SB;                          // pieces of 16 keys' scales
+    const int pk = lane / PPK;                      // key of the first piece
+    const uint32_t dcode =
+        ring + pk * CB + ((D == 128 ? lane % PPK ^ (((pk >> 2) & 1) << 1) : lane % PPK) << 4);
+    const uint32_t dscale = ring + (lane / SP) * C_::kTensor + 16 * CB + (lane % SP) * 16;
+    const uint8_t* const s_head =
+        (lane / SP ? v_head : k_head) + (P << (D == 128 ? 6 : 5)) + (lane % SP) * 16;
     auto issue = [&](int i) {
       if (i < nblk) {
         if (i > 0 && (i & 31) == 0) {
@@ -246,27 +257,19 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
           next_ids = ids_of(i + 32 + lane);
         }
         const int pg = __shfl_sync(0xffffffffu, ids, i & 31);
-        const bool ok = pg >= 0 && pg < a.num_pages;
+        const bool ok = (uint32_t)pg < (uint32_t)a.num_pages;
         if (!ok && lane == 0) flag(a.plan.status, DS_DEV_BAD_PAGE);
         const uint32_t n = ok ? 16u : 0u;
-        const int64_t at = ok ? (int64_t)pg * page_bytes : 0;
-        const int off = key_of(i) % P;
-        const uint32_t dst = ring + (i % kStages) * 2 * C_::kTensor;
-        constexpr int PPK = CB / 16;                // 16-byte pieces of a key
+        const int64_t at = (int64_t)(ok ? pg : 0) * page_bytes;
+        const int off = key_of(i) & (P - 1);
+        const uint32_t st = (i % kStages) * 2 * C_::kTensor;
+        const int64_t code = at + (off * CB + lane * 16);
 #pragma unroll
-        for (int c0 = 0; c0 < 16 * PPK; c0 += 32) {
-          const int c = c0 + lane, key = c / PPK, pc = c % PPK;
-          const uint32_t d =
-              dst + key * CB + ((D == 128 ? pc ^ (((key >> 2) & 1) << 1) : pc) << 4);
-          cp16(d, k_head + at + off * CB + c * 16, n);
-          cp16(d + C_::kTensor, v_head + at + off * CB + c * 16, n);
+        for (int c = 0; c < PPK / 2; ++c) {         // keys pk and, at 128, pk + 8
+          cp16(dcode + st + c * 512, k_head + code + c * 512, n);
+          cp16(dcode + st + C_::kTensor + c * 512, v_head + code + c * 512, n);
         }
-        constexpr int SP = 16 * SB / 16;            // pieces of 16 keys' scales
-        if (lane < 2 * SP) {
-          const int tensor = lane / SP, c = lane % SP;
-          cp16(dst + tensor * C_::kTensor + 16 * CB + c * 16,
-               (tensor ? v_head : k_head) + at + P * CB + off * SB + c * 16, n);
-        }
+        if (lane < 2 * SP) cp16(dscale + st, s_head + at + off * SB, n);
       }
       cp_commit();
     };
@@ -275,11 +278,23 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
 
     // fragment row g of a block, and the lane's four keys of the second product
     const int krow = g ^ ((g >> 1) & 1);
+    const uint32_t kcode =
+        ring + krow * CB + (D == 128 ? (t ^ (((krow >> 2) & 1) << 1)) << 4 : t * 8);
+    const uint32_t kscale = ring + 16 * CB + krow * SB + (D == 128 ? 2 * t : t);
+    uint32_t vcode[2], vscale[2];                   // keys of fragment rows 2t and 2t + 1
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int key = 2 * t + (e ^ (t & 1));
+      vcode[e] = ring + C_::kTensor + key * CB +
+                 (D == 128 ? (((g >> 1) ^ (((key >> 2) & 1) << 1)) << 4) + (g & 1) * 8 : g * 4);
+      vscale[e] = ring + C_::kTensor + 16 * CB + key * SB + (D == 128 ? g : g >> 1);
+    }
+#pragma unroll 1
     for (int i = 0; i < nblk; ++i) {
       cp_wait<kStages - 2>();
       __syncwarp();
       issue(i + kStages - 1);
-      const uint32_t sk = ring + (i % kStages) * 2 * C_::kTensor, sv = sk + C_::kTensor;
+      const uint32_t st = (i % kStages) * 2 * C_::kTensor;
       const int key0 = key_of(i);
       float s[NT][4];
 #pragma unroll
@@ -291,17 +306,16 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
         uint32_t w[2][D / 32], sc[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {               // keys krow and 8 + krow
-          const int key = 8 * h + krow;
           if constexpr (D == 128) {
-            const uint4 x = lds128(sk + key * CB + ((t ^ (((key >> 2) & 1) << 1)) << 4));
+            const uint4 x = lds128(kcode + st + h * 8 * CB);
             w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-            const uint32_t s2 = kv4_scales_f16(lds_u16(sk + 16 * CB + key * SB + 2 * t));
+            const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + st + h * 8 * SB));
             sc[h][0] = __byte_perm(s2, s2, 0x1010);
             sc[h][1] = __byte_perm(s2, s2, 0x3232);
           } else {
-            const uint2 x = lds64(sk + key * CB + t * 8);
+            const uint2 x = lds64(kcode + st + h * 8 * CB);
             w[h][0] = x.x; w[h][1] = x.y;
-            const uint32_t b = lds_u8(sk + 16 * CB + key * SB + t);
+            const uint32_t b = lds_u8(kscale + st + h * 8 * SB);
             sc[h][0] = sc[h][1] = kv4_scales_f16(b | b << 8);
           }
         }
@@ -327,26 +341,26 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
       // ---------------------------------------------------------- softmax
       // element 2h + e of tile n: key 8h + krow, row 8n + 2t + e
       const bool tail = key0 + 16 > L;
-      float mx[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      if (tail) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          s[n][x] *= c2;
-          if (tail) {
-            const int d = key0 + 8 * (x >> 1) + krow - L;      // tree slot when >= 0
+          const int d = key0 + 8 * (x >> 1) + krow - L;        // tree slot when >= 0
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
             if (d >= 0 && !(d < T && ((anc[n][x & 1] >> d) & 1))) s[n][x] = -CUDART_INF_F;
-          }
         }
-        mx[n][0] = fmaxf(s[n][0], s[n][2]);
-        mx[n][1] = fmaxf(s[n][1], s[n][3]);
       }
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mx[n][e] = fmaf(fmaxf(s[n][e], s[n][2 + e]), c2, -7.f);
       // lazy maximum, 2^7 above the reference so that P fills f16's range
       bool need = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) need |= mx[n][e] - 7.f > m[n][e] + 8.f;
+        for (int e = 0; e < 2; ++e) need |= mx[n][e] > m[n][e] + 8.f;
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -355,7 +369,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
             float x = mx[n][e];
 #pragma unroll
             for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-            x = fmaxf(m[n][e], x - 7.f);
+            x = fmaxf(m[n][e], x);
             const float al = x == -CUDART_INF_F ? 1.f : ex2(m[n][e] - x);
             m[n][e] = x;
             l[n][e] *= al;
@@ -373,13 +387,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
         float pr[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          // a row that has seen nothing: 2^(-inf - 0)
           const float mb = m[n][x & 1] == -CUDART_INF_F ? 0.f : m[n][x & 1];
-          pr[x] = ex2(s[n][x] - mb);
+          pr[x] = ex2(fmaf(s[n][x], c2, -mb));
         }
         l[n][0] += pr[0] + pr[2];
         l[n][1] += pr[1] + pr[3];
         if (C) {
-          const bool c0 = key0 + krow < L, c1 = key0 + 8 + krow < L;
+          const bool c0 = !tail || key0 + krow < L, c1 = !tail || key0 + 8 + krow < L;
           cs[n][0] += (c0 ? pr[0] : 0.f) + (c1 ? pr[2] : 0.f);
           cs[n][1] += (c0 ? pr[1] : 0.f) + (c1 ? pr[3] : 0.f);
         }
@@ -409,17 +424,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4
         uint32_t w[4][VW], b[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int key = 8 * (x >> 1) + 2 * t + ((x & 1) ^ (t & 1));
           if constexpr (D == 128) {
-            const uint2 y = lds64(sv + key * CB + (((g >> 1) ^ (((key >> 2) & 1) << 1)) << 4) +
-                                  (g & 1) * 8);
+            const uint2 y = lds64(vcode[x & 1] + st + (x >> 1) * 8 * CB);
             w[x][0] = y.x;
             w[x][VW - 1] = y.y;
-            b[x] = lds_u8(sv + 16 * CB + key * SB + g);
           } else {
-            w[x][0] = lds32(sv + key * CB + g * 4);
-            b[x] = lds_u8(sv + 16 * CB + key * SB + (g >> 1));
+            w[x][0] = lds32(vcode[x & 1] + st + (x >> 1) * 8 * CB);
           }
+          b[x] = lds_u8(vscale[x & 1] + st + (x >> 1) * 8 * SB);
         }
         const uint32_t s01 = kv4_scales_f16(b[0] | b[1] << 8);
         const uint32_t s23 = kv4_scales_f16(b[2] | b[3] << 8);
