@@ -99,7 +99,7 @@ ds_status check_verify_sizes(const ds_verify_args* a) {
 
 namespace ds {
 
-VerifyLayout verify_layout(const ds_verify_args& a, int num_sms) {
+VerifyLayout verify_layout(const ds_verify_args& a, int num_sms, size_t min_counters) {
   VerifyLayout L;
   L.group = a.num_q_heads / a.num_kv_heads;
   L.rg_max = (DS_MAX_TREE_NODES * L.group + kRowsPerItem - 1) / kRowsPerItem;
@@ -112,7 +112,8 @@ VerifyLayout verify_layout(const ds_verify_args& a, int num_sms) {
   L.max_items = (L.wave_ctas > 0 ? L.wave_ctas : num_sms) + a.batch * a.num_kv_heads * L.rg_max;
   size_t off = kStatusBytes;
   L.counters = off;
-  off = align_up(off + (size_t)a.batch * a.num_kv_heads * L.rg_max * sizeof(uint32_t));
+  const size_t groups = (size_t)a.batch * a.num_kv_heads * L.rg_max;
+  off = align_up(off + (groups > min_counters ? groups : min_counters) * sizeof(uint32_t));
   L.gdesc = off;
   off = align_up(off + (size_t)a.batch * a.num_kv_heads * L.rg_max * sizeof(int32_t) * 4);
   L.o_part = off;
@@ -610,7 +611,7 @@ ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* a, size_t* b
   int sms = v.num_sms;
   if (sms == 0 && device_sms(&sms) != 0)
     return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
-  *bytes = ds::verify_layout(v, sms).total;
+  *bytes = ds::verify_layout(v, sms, ds::kv4_few_segments(*a)).total;
   return ok();
 }
 
@@ -633,7 +634,7 @@ ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* a, void* stream) {
   int sms = v.num_sms;
   if (sms == 0 && device_sms(&sms) != 0)
     return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
-  const ds::VerifyLayout L = ds::verify_layout(v, sms);
+  const ds::VerifyLayout L = ds::verify_layout(v, sms, ds::kv4_few_segments(*a));
   REQUIRE(a->workspace_bytes >= L.total, DS_ERR_WORKSPACE,
           "workspace_bytes %zu < required %zu", a->workspace_bytes, L.total);
   if (a->n_nodes == 0) return ok();

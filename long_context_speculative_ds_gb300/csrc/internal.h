@@ -77,7 +77,8 @@ struct NodeStats {
 static_assert(sizeof(NodeStats) == 96, "the record size ds.h states for ds_accept_static");
 
 
-VerifyLayout verify_layout(const ds_verify_args& a, int num_sms);
+// min_counters: counters to make room for when they are more than the plan's
+VerifyLayout verify_layout(const ds_verify_args& a, int num_sms, size_t min_counters = 0);
 AcceptLayout accept_layout(const ds_accept_args& a);
 
 // Launchers (return cudaSuccess or the launch error).
@@ -101,6 +102,10 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
 // longer than any context, and no chunk masses.
 ds_verify_args kv4_as_verify(const ds_kv4_attn_args& a);
 constexpr int kKv4MaxSlots = 1 << 30;
+// Query rows per sequence and kv head, on average, when the few-row pass
+// takes the call (0: the tree pass does), and the segments it may need.
+int kv4_few_rows(const ds_kv4_attn_args& a);
+int kv4_few_segments(const ds_kv4_attn_args& a);
 
 // Sets the message ds_last_error returns on this thread; returns st.
 ds_status set_last_error(ds_status st, const char* msg);

@@ -14,6 +14,23 @@
 
 namespace ds {
 
+int kv4_few_rows(const ds_kv4_attn_args& a) {
+  // rows per sequence and kv head on average: the trees' sizes are on the
+  // device, and both passes handle any
+  const int64_t group = a.num_q_heads / a.num_kv_heads;
+  const int64_t rows = ((int64_t)a.n_nodes + a.batch - 1) / a.batch * group;
+  if (rows > 16) return 0;
+  // the few-row pass counts its work (64-key units, and segments) in 32 bits
+  const int64_t segs = a.num_kv_heads * (a.batch + a.n_nodes * group / 8 + 1);
+  const int64_t units = segs * ((int64_t)a.max_pages * a.page_size / 64 + 64);
+  return units < ((int64_t)1 << 31) ? (int)rows : 0;
+}
+
+int kv4_few_segments(const ds_kv4_attn_args& a) {
+  const int64_t group = a.num_q_heads / a.num_kv_heads;
+  return kv4_few_rows(a) ? (int)(a.num_kv_heads * (a.batch + a.n_nodes * group / 8 + 1)) : 0;
+}
+
 cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
                             cudaStream_t stream) {
   const ds_verify_args va = kv4_as_verify(a);
@@ -55,10 +72,7 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
   ka.k4 = static_cast<const uint8_t*>(a.k_cache);
   ka.v4 = static_cast<const uint8_t*>(a.v_cache);
   ka.out_mult = ldexpf(1.f, a.v_exp);
-  // rows per sequence and kv head on average: the trees' sizes are on the
-  // device, and both passes handle any
-  const int64_t rows = ((int64_t)a.n_nodes + a.batch - 1) / a.batch * L.group;
-  if (rows <= 16) return launch_kv4_few(ka, a.head_dim, (int)rows, L, stream);
+  if (const int rows = kv4_few_rows(a)) return launch_kv4_few(ka, a.head_dim, rows, L, stream);
   cudaError_t e = launch_kv4_split_tc(ka, a.head_dim, L, stream);
   if (e != cudaSuccess) return e;
   return launch_finish(k, a.head_dim, L.rg_max, a.batch, stream);

@@ -4,7 +4,7 @@
 // With few rows the pass is a stream of K and V, 72 bytes a key and head, and
 // a tcgen05 tile of 128 rows would convert every tile through shared memory
 // for products that are nearly all padding.  Here each warp works alone on
-// blocks of 16 keys, from its own ring of asynchronous copies, with
+// blocks of 32 keys, from its own ring of asynchronous copies, with
 // m16n8k16 products whose 16-row operand is the cache and whose 8-column
 // operand the queries, so that codes go from shared memory to registers to
 // the product:
@@ -21,17 +21,20 @@
 // yields the pairs over keys that the operand holds.  P^T is S^T's fragment
 // transposed (movmatrix).
 //
-// A block's 16 keys sit in fragment row i as key i ^ ((i >> 1) & 1), and the
-// 16-byte pieces of keys 4-7 and 12-15 with their halves exchanged: then
-// eight lanes of a 16-byte read and 16 lanes of an 8-byte read touch every
+// Of 16 keys, fragment row i holds key i ^ ((i >> 1) & 1), and keys 4-7 and
+// 12-15 have the halves of their 16-byte pieces exchanged: then eight lanes of a 16-byte read and 16 lanes of an 8-byte read touch every
 // bank once.
 //
-// A work item (the plan of the tree pass: sequence, kv head, row group, range
-// of 128-key tiles) is cut into units of 64 keys, dealt to the block's warps
-// in turn; the warps' outputs are merged in shared memory.  Rows beyond 8 NT
-// make the block go over its keys again.  The last split of a row group to
-// finish merges the splits into the output (with few rows that is less than
-// a launch); only the salience takes a second kernel.
+// Work: every (sequence, kv head, group of 8 NT query rows) is a segment of
+// 64-key units, and the units of all segments, in order, are dealt to the
+// blocks in equal contiguous ranges, each segment behind a lead-in that
+// stands for what its start and end cost, so that a ragged batch balances.
+// A block works its range segment by segment: the units of one go to
+// its warps in turn, whose outputs are merged in shared memory.  When a
+// segment was cut between blocks, the last of them to finish merges the
+// pieces into the output (with few rows that costs less than a launch); only
+// the salience takes a second kernel.  Each warp works the plan out by
+// itself, from the lengths, in one pass over the batch.
 //
 // Chunk masses are kept per 64 keys or less ("subchunks"), so that a unit
 // never shares one: [kv head][sequence's rows x subchunks][subchunk][row],
@@ -39,6 +42,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "dev_common.cuh"
 #include "internal.h"
@@ -51,24 +56,41 @@
 namespace ds {
 namespace kv4few {
 
-constexpr int kStages = 4;
+constexpr int kStages = 3;      // blocks of 32 keys in a warp's ring
+constexpr int kBlock = 32;
+// A piece's start (plan, page ids, first copies) and end (merge) take about
+// as long as 20 units do in a block: 5 us against 0.27 us a unit
+constexpr int kPieceUnits = 20;
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int W = NT == 1 ? 16 : 8;        // warps of a block
   static constexpr int R = 8 * NT;                  // query rows of one pass
-  static constexpr int kTensor = 16 * (D / 2 + D / 16);   // bytes of 16 keys
+  static constexpr int kTensor = kBlock * (D / 2 + D / 16);   // bytes of a block's K or V
   static constexpr int kRing = kStages * 2 * kTensor;     // bytes of a warp's ring
   static constexpr size_t smem = (size_t)W * kRing;
   static_assert(R * D * 4 <= kRing, "a warp's output must fit in its ring");
 };
 
+// One piece of a segment: units [u0, u1).
+struct Piece {
+  int L, T, node0, rows;         // the sequence's
+  int b, kvh, rgi;               // sequence, kv head, row group
+  int u0, u1;
+  int slot;                      // of this piece's partial output
+  int first_slot, n_slots;       // of the segment's pieces
+  int seg;                       // number of the segment in the batch
+  int next;                      // unit after the piece; -1 when the block's range ends
+};
+
 struct Ctrl {
-  Plan plan;
+  Piece piece[16];               // [warp]
   int32_t parents[DS_MAX_TREE_NODES];
   uint64_t anc[DS_MAX_TREE_NODES];
   float m[16][16], l[16][16];    // [warp][row]
-  int last;
+  Piece cut[2];                  // pieces of cut segments: at most the range's two ends
+  int n_cut, last[2];
+  float lse[32];                 // rows being merged
 };
 
 DS_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {   // bytes 0: zeros
@@ -119,421 +141,599 @@ DS_DEV uint32_t lds_u8(uint32_t a) {
   return r;
 }
 
+// The piece of this block's range that begins at unit x (x < 0: its first);
+// false when the block has none.  One warp, which writes *pc: the plan is
+// worked out again for every piece, so that nothing of it stays in registers.
+template <int R, int W>
+__device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc) {
+  const int lane = threadIdx.x & 31;
+  // units and segments of sequence b (lane-parallel)
+  struct Seq { int L, T, node0, rows, nu, segs; };
+  auto seq_of = [&](int b, bool report) {
+    Seq s = {0, 0, 0, 0, 0, 0};
+    if (b < pa.batch) {
+      const SeqPlan q = seq_sizes(pa, b, report);
+      s.L = q.L; s.T = q.T; s.node0 = q.node0; s.rows = q.rows;
+      s.nu = (q.L + q.T + 63) / 64;
+      s.segs = pa.num_kv_heads * ((q.rows + R - 1) / R);
+    }
+    return s;
+  };
+  const bool report = blockIdx.x == 0 && x < 0;
+  int U = 0, S = 0;
+  const Seq first = seq_of(lane, report);
+  for (int b0 = 0; b0 < pa.batch; b0 += 32) {
+    const Seq s = b0 == 0 ? first : seq_of(b0 + lane, report);
+    U += __reduce_add_sync(0xffffffffu, s.segs * s.nu);
+    S += __reduce_add_sync(0xffffffffu, s.segs);
+  }
+  // at most one block per segment or, for long segments, per W units
+  const int N = min((int)gridDim.x, max(S, (U + W - 1) / W));
+  const int i = blockIdx.x;
+  if (i >= N) return false;
+  U += S * kPieceUnits;                           // the axis: units behind their lead-ins
+  const int q = U / N, rem = U - q * N;           // the first rem blocks: q + 1 of it
+  const int lo = i * q + min(i, rem), hi = lo + q + (i < rem ? 1 : 0);
+  auto block_of = [&](int u) {
+    return u < rem * (q + 1) ? u / (q + 1) : rem + (u - rem * (q + 1)) / q;
+  };
+  if (x < 0) x = lo;
+  int ubase = 0, sbase = 0;                       // axis and segments before the 32
+  for (int b0 = 0; b0 < pa.batch; b0 += 32) {
+    const Seq s = b0 == 0 ? first : seq_of(b0 + lane, false);
+    const int len = s.nu + kPieceUnits;           // of a segment
+    int pu = s.segs * len, ps = s.segs;           // inclusive prefixes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, pu, o), v = __shfl_up_sync(0xffffffffu, ps, o);
+      if (lane >= o) { pu += u; ps += v; }
+    }
+    const int all_u = __shfl_sync(0xffffffffu, pu, 31), all_s = __shfl_sync(0xffffffffu, ps, 31);
+    pu += ubase - s.segs * len;                   // where the sequence begins
+    ps += sbase - s.segs;
+    if (x < ubase + all_u) {
+      if (s.segs > 0 && pu <= x && x < pu + s.segs * len) {             // one lane
+        const int rg = (s.rows + R - 1) / R;
+        const int seg = (x - pu) / len;
+        const int u = pu + seg * len + kPieceUnits;                     // its first unit
+        pc->L = s.L; pc->T = s.T; pc->node0 = s.node0; pc->rows = s.rows;
+        pc->b = b0 + lane;
+        pc->kvh = seg / rg;
+        pc->rgi = seg - pc->kvh * rg;
+        pc->u0 = max(x - u, 0);
+        pc->u1 = min(s.nu, hi - u);               // <= u0: only part of the lead-in
+        pc->seg = ps + seg;
+        // numbered by block and segment, which never both stand still, the
+        // pieces have slots of their own, a segment's in a row
+        pc->slot = i + ps + seg;
+        const int f = block_of(u);
+        pc->first_slot = f + ps + seg;
+        pc->n_slots = block_of(u + s.nu - 1) - f + 1;
+        pc->next = u + s.nu < hi ? u + s.nu : -1;
+      }
+      __syncwarp();
+      return true;
+    }
+    ubase += all_u;
+    sbase += all_s;
+  }
+  return false;
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const Kv4KArgs ka) {
+__device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, Ctrl& ctrl,
+                                           unsigned char* smem, const int warp) {
   using namespace ptx;
   using C_ = Cfg<D, NT>;
   constexpr int W = C_::W, R = C_::R;
   constexpr int NS = D / 16;              // product steps of Q K^T, dim tiles of O
   constexpr int CB = D / 2, SB = D / 16;  // bytes of a key's codes and scales
-  extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ Ctrl ctrl;
   const VerifyKArgs& a = ka.v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const bool early_plan = a.accumulate != 0;    // as in the tree pass
-  if (early_plan && warp == 0) {
-    const Plan p = plan_find(a.plan, -1, blockIdx.x);
-    if (lane == 0) ctrl.plan = p;
-  }
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  if (!early_plan && warp == 0) {
-    const Plan p = plan_find(a.plan, -1, blockIdx.x);
-    if (lane == 0) ctrl.plan = p;
-  }
-  __syncthreads();
-  const Plan p = ctrl.plan;
-  if ((int)blockIdx.x >= p.total_items || p.b < 0) return;
-  const SeqPlan& sq = p.seq;
-  const int G = a.plan.group;
-  const int local = blockIdx.x - sq.item_base;
-  const int kvh = local / (sq.rg * sq.splits);
-  const int rgi = local % (sq.rg * sq.splits) / sq.splits;
-  const int split = local % sq.splits;
-  const int tb = sq.tiles / sq.splits, rem = sq.tiles % sq.splits;
-  const int t0 = split * tb + min(split, rem), t1 = t0 + tb + (split < rem ? 1 : 0);
-  const int rows = min(kRowsPerGroup, sq.rows - rgi * kRowsPerGroup);
-  const int L = sq.L, T = sq.T, P = a.plan.page_size;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int G = a.plan.group, L = pc.L, T = pc.T, P = a.plan.page_size;
+  const int rows = min(R, pc.rows - pc.rgi * R);                // of this segment
   const int C = a.scores ? min(64, a.plan.chunk_size) : 0;      // keys of a subchunk
-  const int64_t row0 = (int64_t)sq.node0 * G;                    // first row of the sequence
+  const int64_t row0 = (int64_t)pc.node0 * G;                   // first row of the sequence
   const int64_t n_rows = (int64_t)a.plan.n_nodes * G;
   const int64_t n_sub = C ? (int64_t)a.plan.max_chunks * (a.plan.chunk_size / C) : 0;
-  float* const mass = a.clse + ((int64_t)kvh * n_rows + row0) * n_sub + rgi * kRowsPerGroup;
-  float* const row_lse = a.row_lse + (int64_t)kvh * n_rows + row0 + rgi * kRowsPerGroup;
-  const int64_t cidx = ((int64_t)p.b * a.plan.num_kv_heads + kvh) * a.plan.rg_max + rgi;
-  const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
-  const bool need_anc = t1 * kTileKeys > L;
-  if (need_anc && warp == 0)
-    tc::tree_ancestors(a.parents + sq.node0, T, ctrl.parents, ctrl.anc, a.plan.status);
-  __syncthreads();
+  float* const mass = a.clse + ((int64_t)pc.kvh * n_rows + row0) * n_sub + pc.rgi * R;
+  float* const row_lse = a.row_lse + (int64_t)pc.kvh * n_rows + row0 + pc.rgi * R;
+  const int32_t* ptab = a.page_table + (int64_t)pc.b * a.plan.max_pages;
 
-  // this warp's blocks of 16 keys: units warp, warp + W, ... of the item;
-  // block i is block i % 4 of its unit i / 4
-  constexpr int kUnit = 4;
-  const int nb_item = (min(t1 * kTileKeys, L + T) - t0 * kTileKeys + 15) / 16;
-  const int n_units = (nb_item + kUnit - 1) / kUnit;
+  // this warp's blocks: two for each of the piece's units u0 + warp, + W, ...;
+  // nh is their number of 16-key halves that hold keys of the sequence
+  const int nh_piece = (min(pc.u1 * 64, L + T) - pc.u0 * 64 + 15) / 16;
+  const int n_units = pc.u1 - pc.u0;
   const int mine = n_units > warp ? (n_units - warp - 1) / W + 1 : 0;
-  const int last_unit = warp + (mine - 1) * W;
-  const int nblk = mine > 0 ? (mine - 1) * kUnit + min(kUnit, nb_item - last_unit * kUnit) : 0;
-  const int first_key = t0 * kTileKeys + warp * kUnit * 16;
+  const int nh = mine > 0 ? (mine - 1) * 4 + min(4, nh_piece - (warp + (mine - 1) * W) * 4) : 0;
+  const int nblk = (nh + 1) / 2;
+  const int first_key = (pc.u0 + warp) * 64;
   const int pshift = __ffs(P) - 1;
-  auto key_of = [&](int i) { return first_key + (i >> 2) * (W * kUnit * 16) + (i & 3) * 16; };
+  // first key of half i (two to a block, four to a unit)
+  auto key_of = [&](int i) { return first_key + (i >> 2) * (W * 64) + (i & 3) * 16; };
+  // page ids of this warp's halves, 32 at a time, the next 32 on their way
+  auto ids_of = [&](int i) { return i < nh ? __ldg(ptab + (key_of(i) >> pshift)) : 0; };
+  int ids = ids_of(lane), next_ids = ids_of(32 + lane);
+  // output row of row r of this segment
+  auto out_row = [&](int r) {
+    const int grow = pc.rgi * R + r;
+    return ((int64_t)pc.node0 + grow / G) * a.num_q_heads + pc.kvh * G + grow % G;
+  };
+  // queries: column g of tile n is row 8 n + g
+  uint4 qx[NT][D / 32];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = 8 * n + g;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(r) * D + t * (D / 4));
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w)
+      qx[n][w] = r < rows ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+  }
+  // ancestor masks, when the piece holds tree keys; a tree of one node has
+  // only itself
+  const bool need_anc = pc.u1 * 64 > L;
+  uint64_t anc[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) anc[n][0] = anc[n][1] = 1ull;
+  if (need_anc && warp == 0) {
+    if (T > 1)
+      tc::tree_ancestors(a.parents + pc.node0, T, ctrl.parents, ctrl.anc, a.plan.status);
+    else if (lane == 0 && __ldg(a.parents + pc.node0) != -1)
+      flag(a.plan.status, DS_DEV_BAD_TREE);
+  }
+
   const uint32_t ring = smem_addr(smem) + warp * C_::kRing;
   const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
-  const uint8_t* k_head = ka.k4 + (int64_t)kvh * blk;
-  const uint8_t* v_head = ka.v4 + (int64_t)kvh * blk;
-  const int64_t page_bytes = (int64_t)a.plan.num_kv_heads * blk;
+  const uint32_t page_bytes = a.plan.num_kv_heads * blk;
+  const uint8_t* const k_head = ka.k4 + (int64_t)pc.kvh * blk;
+  const uint8_t* const v_head = ka.v4 + (int64_t)pc.kvh * blk;
   const float c2 = a.scale_log2;
-
-  // output row of row r of this row group
-  auto out_row = [&](int r) {
-    const int grow = rgi * kRowsPerGroup + r;
-    return ((int64_t)sq.node0 + grow / G) * a.num_q_heads + kvh * G + grow % G;
+  // pieces this lane copies: one or two of the codes of each tensor and
+  // half, and one of the scales (one of two lanes at head_dim 64)
+  constexpr int PPK = CB / 16;                      // 16-byte pieces of a key
+  constexpr int SP = SB;                            // pieces of 16 keys' scales
+  const int pk = lane / PPK;                        // key of the first piece
+  const uint32_t dcode =
+      ring + pk * CB + ((D == 128 ? lane % PPK ^ (((pk >> 2) & 1) << 1) : lane % PPK) << 4);
+  const int s_t = lane / SP & 1, s_h = lane / (2 * SP);        // tensor and half
+  const uint32_t dscale =
+      ring + s_t * C_::kTensor + kBlock * CB + s_h * 16 * SB + (lane % SP) * 16;
+  const uint8_t* const k_lane = k_head + lane * 16;
+  const uint8_t* const v_lane = v_head + lane * 16;
+  const uint8_t* const s_lane =
+      (s_t ? v_head : k_head) + (P << (D == 128 ? 6 : 5)) + (lane % SP) * 16;
+  // bad page ids among the 32 at hand: page 0 stands in, and copies nothing
+  auto check = [&]() {
+    const bool bad = (uint32_t)ids >= (uint32_t)a.num_pages;
+    if (bad) {
+      flag(a.plan.status, DS_DEV_BAD_PAGE);
+      ids = 0;
+    }
+    return __ballot_sync(0xffffffffu, bad);
   };
-  auto put = [&](void* dst, int64_t at, float x) {
-    if (a.out_f32) static_cast<float*>(dst)[at] = x;
-    else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(x);
+  uint32_t bad_ids = check();
+  uint32_t slot_in = 0;                             // ring offset of the next block
+  auto issue = [&](int i) {
+    if (i < nblk) {
+      if (i > 0 && (i & 15) == 0) {
+        ids = next_ids;
+        next_ids = ids_of(2 * i + 32 + lane);
+        bad_ids = check();
+      }
+      const int off = key_of(2 * i) & (P - 1);
+      const int off1 = (off + 16) & (P - 1);
+      const int j = (2 * i) & 31;
+      const uint32_t pg0 = __shfl_sync(0xffffffffu, ids, j);
+      const uint32_t pg1 = __shfl_sync(0xffffffffu, ids, j + 1);
+      const uint32_t n0 = (bad_ids >> j) & 1u ? 0u : 16u, n1 = (bad_ids >> j) & 2u ? 0u : 16u;
+      const uint32_t d = dcode + slot_in;
+      const uint8_t* kp = k_lane + ((uint64_t)pg0 * page_bytes + off * CB);
+      const uint8_t* vp = v_lane + ((uint64_t)pg0 * page_bytes + off * CB);
+#pragma unroll
+      for (int c = 0; c < PPK / 2; ++c) {           // keys pk and, at 128, pk + 8
+        cp16(d + c * 512, kp + c * 512, n0);
+        cp16(d + C_::kTensor + c * 512, vp + c * 512, n0);
+      }
+      const bool in1 = 2 * i + 1 < nh;   // past the end: whatever is there is masked
+      if (in1) {
+        kp = k_lane + ((uint64_t)pg1 * page_bytes + off1 * CB);
+        vp = v_lane + ((uint64_t)pg1 * page_bytes + off1 * CB);
+#pragma unroll
+        for (int c = 0; c < PPK / 2; ++c) {
+          cp16(d + 16 * CB + c * 512, kp + c * 512, n1);
+          cp16(d + 16 * CB + C_::kTensor + c * 512, vp + c * 512, n1);
+        }
+      }
+      if (lane < (in1 ? 4 * SP : 2 * SP))
+        cp16(dscale + slot_in,
+             s_lane + ((uint64_t)(s_h ? pg1 : pg0) * page_bytes + (s_h ? off1 : off) * SB),
+             s_h ? n1 : n0);
+    }
+    cp_commit();
+    slot_in = slot_in == (kStages - 1) * 2 * C_::kTensor ? 0u : slot_in + 2 * C_::kTensor;
   };
-
-  for (int r0 = 0; r0 < rows; r0 += R) {
-    // queries of rows r0 .. r0 + R - 1: column g of tile nt is row r0 + 8 nt + g
-    uint32_t q[NT][NS][2];
-    uint64_t anc[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = r0 + 8 * n + g;
-      const int grow = rgi * kRowsPerGroup + r;
-      const __nv_bfloat16* src =
-          a.q + (((int64_t)sq.node0 + grow / G) * a.num_q_heads + kvh * G + grow % G) * D +
-          t * (D / 4);
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  uint32_t q[NT][NS][2];
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {            // 8 channels: steps 2w, 2w + 1
-        const uint4 x = r < rows ? __ldg(reinterpret_cast<const uint4*>(src) + w)
-                                 : make_uint4(0, 0, 0, 0);
-        q[n][2 * w][0] = bf16x2_to_f16x2(x.x);
-        q[n][2 * w][1] = bf16x2_to_f16x2(x.y);
-        q[n][2 * w + 1][0] = bf16x2_to_f16x2(x.z);
-        q[n][2 * w + 1][1] = bf16x2_to_f16x2(x.w);
-      }
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = r0 + 8 * n + 2 * t + e;
-        anc[n][e] = need_anc && rr < rows ? ctrl.anc[(rgi * kRowsPerGroup + rr) / G] : 0ull;
-      }
+    for (int w = 0; w < D / 32; ++w) {              // 8 channels: steps 2w, 2w + 1
+      q[n][2 * w][0] = bf16x2_to_f16x2(qx[n][w].x);
+      q[n][2 * w][1] = bf16x2_to_f16x2(qx[n][w].y);
+      q[n][2 * w + 1][0] = bf16x2_to_f16x2(qx[n][w].z);
+      q[n][2 * w + 1][1] = bf16x2_to_f16x2(qx[n][w].w);
     }
-    float o[NT][NS][4];
-    float m[NT][2], l[NT][2], cs[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[n][e] = -CUDART_INF_F;
-        l[n][e] = cs[n][e] = 0.f;
-      }
-    }
-
-    // page ids of this warp's blocks, 32 at a time, the next 32 on their way
-    auto ids_of = [&](int i) { return i < nblk ? __ldg(ptab + (key_of(i) >> pshift)) : 0; };
-    int ids = ids_of(lane), next_ids = ids_of(32 + lane);
-    // pieces this lane copies: one or two of the codes of each tensor, and
-    // for the first lanes one of the scales
-    constexpr int PPK = CB / 16;                    // 16-byte pieces of a key
-    constexpr int SP = SB;                          // pieces of 16 keys' scales
-    const int pk = lane / PPK;                      // key of the first piece
-    const uint32_t dcode =
-        ring + pk * CB + ((D == 128 ? lane % PPK ^ (((pk >> 2) & 1) << 1) : lane % PPK) << 4);
-    const uint32_t dscale = ring + (lane / SP) * C_::kTensor + 16 * CB + (lane % SP) * 16;
-    const uint8_t* const s_head =
-        (lane / SP ? v_head : k_head) + (P << (D == 128 ? 6 : 5)) + (lane % SP) * 16;
-    auto issue = [&](int i) {
-      if (i < nblk) {
-        if (i > 0 && (i & 31) == 0) {
-          ids = next_ids;
-          next_ids = ids_of(i + 32 + lane);
-        }
-        const int pg = __shfl_sync(0xffffffffu, ids, i & 31);
-        const bool ok = (uint32_t)pg < (uint32_t)a.num_pages;
-        if (!ok && lane == 0) flag(a.plan.status, DS_DEV_BAD_PAGE);
-        const uint32_t n = ok ? 16u : 0u;
-        const int64_t at = (int64_t)(ok ? pg : 0) * page_bytes;
-        const int off = key_of(i) & (P - 1);
-        const uint32_t st = (i % kStages) * 2 * C_::kTensor;
-        const int64_t code = at + (off * CB + lane * 16);
-#pragma unroll
-        for (int c = 0; c < PPK / 2; ++c) {         // keys pk and, at 128, pk + 8
-          cp16(dcode + st + c * 512, k_head + code + c * 512, n);
-          cp16(dcode + st + C_::kTensor + c * 512, v_head + code + c * 512, n);
-        }
-        if (lane < 2 * SP) cp16(dscale + st, s_head + at + off * SB, n);
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-
-    // fragment row g of a block, and the lane's four keys of the second product
-    const int krow = g ^ ((g >> 1) & 1);
-    const uint32_t kcode =
-        ring + krow * CB + (D == 128 ? (t ^ (((krow >> 2) & 1) << 1)) << 4 : t * 8);
-    const uint32_t kscale = ring + 16 * CB + krow * SB + (D == 128 ? 2 * t : t);
-    uint32_t vcode[2], vscale[2];                   // keys of fragment rows 2t and 2t + 1
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int key = 2 * t + (e ^ (t & 1));
-      vcode[e] = ring + C_::kTensor + key * CB +
-                 (D == 128 ? (((g >> 1) ^ (((key >> 2) & 1) << 1)) << 4) + (g & 1) * 8 : g * 4);
-      vscale[e] = ring + C_::kTensor + 16 * CB + key * SB + (D == 128 ? g : g >> 1);
-    }
-#pragma unroll 1
-    for (int i = 0; i < nblk; ++i) {
-      cp_wait<kStages - 2>();
-      __syncwarp();
-      issue(i + kStages - 1);
-      const uint32_t st = (i % kStages) * 2 * C_::kTensor;
-      const int key0 = key_of(i);
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-      // ------------------------------------------------------------ Q K^T
-      {
-        uint32_t w[2][D / 32], sc[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {               // keys krow and 8 + krow
-          if constexpr (D == 128) {
-            const uint4 x = lds128(kcode + st + h * 8 * CB);
-            w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-            const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + st + h * 8 * SB));
-            sc[h][0] = __byte_perm(s2, s2, 0x1010);
-            sc[h][1] = __byte_perm(s2, s2, 0x3232);
-          } else {
-            const uint2 x = lds64(kcode + st + h * 8 * CB);
-            w[h][0] = x.x; w[h][1] = x.y;
-            const uint32_t b = lds_u8(kscale + st + h * 8 * SB);
-            sc[h][0] = sc[h][1] = kv4_scales_f16(b | b << 8);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {          // 8 channels of each key
-          uint32_t v0[4], v1[4];
-          kv4_codes_f16(w[0][k], v0);
-          kv4_codes_f16(w[1][k], v1);
-          const int si = D == 128 ? k >> 1 : 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v0[e] = hmul2(v0[e], sc[0][si]);
-            v1[e] = hmul2(v1[e], sc[1][si]);
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t fa[4] = {v0[2 * e], v1[2 * e], v0[2 * e + 1], v1[2 * e + 1]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(s[n], fa, q[n][2 * k + e][0], q[n][2 * k + e][1]);
-          }
-        }
-      }
-      // ---------------------------------------------------------- softmax
-      // element 2h + e of tile n: key 8h + krow, row 8n + 2t + e
-      const bool tail = key0 + 16 > L;
-      if (tail) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int d = key0 + 8 * (x >> 1) + krow - L;        // tree slot when >= 0
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (d >= 0 && !(d < T && ((anc[n][x & 1] >> d) & 1))) s[n][x] = -CUDART_INF_F;
-        }
-      }
-      float mx[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) mx[n][e] = fmaf(fmaxf(s[n][e], s[n][2 + e]), c2, -7.f);
-      // lazy maximum, 2^7 above the reference so that P fills f16's range
-      bool need = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) need |= mx[n][e] > m[n][e] + 8.f;
-      if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = mx[n][e];
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
-            x = fmaxf(m[n][e], x);
-            const float al = x == -CUDART_INF_F ? 1.f : ex2(m[n][e] - x);
-            m[n][e] = x;
-            l[n][e] *= al;
-            cs[n][e] *= al;
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-              o[n][j][e] *= al;
-              o[n][j][e + 2] *= al;
-            }
-          }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float pr[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          // a row that has seen nothing: 2^(-inf - 0)
-          const float mb = m[n][x & 1] == -CUDART_INF_F ? 0.f : m[n][x & 1];
-          pr[x] = ex2(fmaf(s[n][x], c2, -mb));
-        }
-        l[n][0] += pr[0] + pr[2];
-        l[n][1] += pr[1] + pr[3];
-        if (C) {
-          const bool c0 = !tail || key0 + krow < L, c1 = !tail || key0 + 8 + krow < L;
-          cs[n][0] += (c0 ? pr[0] : 0.f) + (c1 ? pr[2] : 0.f);
-          cs[n][1] += (c0 ? pr[1] : 0.f) + (c1 ? pr[3] : 0.f);
-        }
-        pb[n][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
-        pb[n][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
-      }
-      // log2 of the chunk's mass when this block ends the chunk or the context
-      if (C && key0 < L && (((key0 + 16) & (C - 1)) == 0 || key0 + 16 >= L)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = cs[n][e];
-            cs[n][e] = 0.f;
-#pragma unroll
-            for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-            const int r = r0 + 8 * n + 2 * t + e;
-            if (g == 0 && r < rows)
-              mass[(int64_t)(key0 / C) * sq.rows + r] =
-                  x > 0.f ? m[n][e] + __log2f(x) : -CUDART_INF_F;
-          }
-      }
-      // -------------------------------------------------------------- P V
-      // fragment rows 2t + e and 8 + 2t + e are keys 2t + (e ^ (t & 1))
-      {
-        constexpr int VW = D / 64;                  // words of 8 dims of a key
-        uint32_t w[4][VW], b[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if constexpr (D == 128) {
-            const uint2 y = lds64(vcode[x & 1] + st + (x >> 1) * 8 * CB);
-            w[x][0] = y.x;
-            w[x][VW - 1] = y.y;
-          } else {
-            w[x][0] = lds32(vcode[x & 1] + st + (x >> 1) * 8 * CB);
-          }
-          b[x] = lds_u8(vscale[x & 1] + st + (x >> 1) * 8 * SB);
-        }
-        const uint32_t s01 = kv4_scales_f16(b[0] | b[1] << 8);
-        const uint32_t s23 = kv4_scales_f16(b[2] | b[3] << 8);
-#pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          constexpr uint32_t M = 0x0f0f0f0fu;
-          uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, pairs over keys
-          kv4_codes_f16((w[0][k] & M) | ((w[1][k] << 4) & ~M), e01);
-          kv4_codes_f16(((w[0][k] >> 4) & M) | (w[1][k] & ~M), o01);
-          kv4_codes_f16((w[2][k] & M) | ((w[3][k] << 4) & ~M), e23);
-          kv4_codes_f16(((w[2][k] >> 4) & M) | (w[3][k] & ~M), o23);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t fa[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23),
-                                    hmul2(o23[j], s23)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][4 * k + j], fa, pb[n][0], pb[n][1]);
-          }
-        }
-      }
-    }
-    cp_wait<0>();
-    __syncwarp();
-
-    // ------------------------------------------- merge of the block's warps
-    float* ow = reinterpret_cast<float*>(smem + warp * C_::kRing);   // [row][D]
+  if (need_anc && T > 1) {
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 8 * n + 2 * t + e;
-        float x = l[n][e];
+        anc[n][e] = r < rows ? ctrl.anc[(pc.rgi * R + r) / G] : 0ull;
+      }
+  }
+  float o[NT][NS][4];
+  float m[NT][2], mb[NT][2], l[NT][2], cs[NT][2];
 #pragma unroll
-        for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-        if (g == 0) {
-          ctrl.m[warp][r] = m[n][e];
-          ctrl.l[warp][r] = x;
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[n][e] = -CUDART_INF_F;
+      l[n][e] = cs[n][e] = mb[n][e] = 0.f;
+    }
+  }
+
+  // fragment row g of a block, and the lane's four keys of the second product
+  const int krow = g ^ ((g >> 1) & 1);
+  const uint32_t kcode =
+      ring + krow * CB + (D == 128 ? (t ^ (((krow >> 2) & 1) << 1)) << 4 : t * 8);
+  const uint32_t kscale = ring + kBlock * CB + krow * SB + (D == 128 ? 2 * t : t);
+  uint32_t vcode[2], vscale[2];                   // keys of fragment rows 2t and 2t + 1
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int key = 2 * t + (e ^ (t & 1));
+    vcode[e] = ring + C_::kTensor + key * CB +
+               (D == 128 ? (((g >> 1) ^ (((key >> 2) & 1) << 1)) << 4) + (g & 1) * 8 : g * 4);
+    vscale[e] = ring + C_::kTensor + kBlock * CB + key * SB + (D == 128 ? g : g >> 1);
+  }
+  const int cshift = C ? __ffs(C) - 1 : 0;
+  uint32_t st = 0;
+#pragma unroll 1
+  for (int i = 0; i < nblk; ++i) {
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    issue(i + kStages - 1);
+    const int key0 = key_of(2 * i);
+    // ------------------------------------------------------------ Q K^T
+    // s[n][hf][2h + e]: key 16 hf + 8h + krow, row 8n + 2t + e
+    float s[NT][2][4];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t w[2][D / 32], sc[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k8 = 2 * hf + h;                // which eight keys
+        if constexpr (D == 128) {
+          const uint4 x = lds128(kcode + st + k8 * 8 * CB);
+          w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
+          const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + st + k8 * 8 * SB));
+          sc[h][0] = __byte_perm(s2, s2, 0x1010);
+          sc[h][1] = __byte_perm(s2, s2, 0x3232);
+        } else {
+          const uint2 x = lds64(kcode + st + k8 * 8 * CB);
+          w[h][0] = x.x; w[h][1] = x.y;
+          const uint32_t b = lds_u8(kscale + st + k8 * 8 * SB);
+          sc[h][0] = sc[h][1] = kv4_scales_f16(b | b << 8);
         }
-        // tile j: dims g D/8 + 2j (elements 0, 1) and the next (2, 3)
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][hf][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {          // 8 channels of each key
+        uint32_t v0[4], v1[4];
+        kv4_codes_f16(w[0][k], v0);
+        kv4_codes_f16(w[1][k], v1);
+        const int si = D == 128 ? k >> 1 : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v0[e] = hmul2(v0[e], sc[0][si]);
+          v1[e] = hmul2(v1[e], sc[1][si]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t fa[4] = {v0[2 * e], v1[2 * e], v0[2 * e + 1], v1[2 * e + 1]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816(s[n][hf], fa, q[n][2 * k + e][0], q[n][2 * k + e][1]);
+        }
+      }
+    }
+    // ---------------------------------------------------------- softmax
+    const bool tail = key0 + kBlock > L;
+    if (tail) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int d = key0 + 8 * (x >> 1) + krow - L;        // tree slot when >= 0
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          if (d >= 0 && !(d < T && ((anc[n][x & 1] >> d) & 1)))
+            s[n][x >> 2][x & 3] = -CUDART_INF_F;
+      }
+    }
+    // lazy maximum, 2^7 above the reference so that P fills f16's range
+    bool need = false;
+    float mx[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[n][e] = fmaf(fmax3(fmaxf(s[n][0][e], s[n][0][2 + e]), s[n][1][e], s[n][1][2 + e]),
+                        c2, -7.f);
+        need |= mx[n][e] > m[n][e] + 8.f;
+      }
+    if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = mx[n][e];
+#pragma unroll
+          for (int k = 4; k < 32; k <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+          x = fmaxf(m[n][e], x);
+          const float al = x == -CUDART_INF_F ? 1.f : ex2(m[n][e] - x);
+          m[n][e] = x;
+          mb[n][e] = x == -CUDART_INF_F ? 0.f : -x;      // a row that has seen nothing
+          l[n][e] *= al;
+          cs[n][e] *= al;
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            o[n][j][e] *= al;
+            o[n][j][e + 2] *= al;
+          }
+        }
+    }
+    uint32_t pb[NT][2][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float sum[2][2];                            // [half][e]
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        float pr[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) pr[x] = ex2(fmaf(s[n][hf][x], c2, mb[n][x & 1]));
+        sum[hf][0] = pr[0] + pr[2];
+        sum[hf][1] = pr[1] + pr[3];
+        pb[n][hf][0] = transpose8x8(pack_f16x2(pr[0], pr[1]));
+        pb[n][hf][1] = transpose8x8(pack_f16x2(pr[2], pr[3]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[n][e] += sum[hf][e];
+        if (C) {
+          if (tail) {                             // context keys only
+            const bool c0 = key0 + 16 * hf + krow < L, c1 = key0 + 16 * hf + 8 + krow < L;
+            sum[hf][0] = (c0 ? pr[0] : 0.f) + (c1 ? pr[2] : 0.f);
+            sum[hf][1] = (c0 ? pr[1] : 0.f) + (c1 ? pr[3] : 0.f);
+          }
+        }
+      }
+      // log2 of a chunk's mass at a half that ends the chunk or the context
+      if (C) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int k0 = key0 + 16 * hf;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) cs[n][e] += sum[hf][e];
+          if (k0 < L && (((k0 + 16) & (C - 1)) == 0 || k0 + 16 >= L)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = cs[n][e];
+              cs[n][e] = 0.f;
+#pragma unroll
+              for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+              const int r = 8 * n + 2 * t + e;
+              if (g == 0 && r < rows)
+                mass[(int64_t)(k0 >> cshift) * pc.rows + r] =
+                    x > 0.f ? m[n][e] + __log2f(x) : -CUDART_INF_F;
+            }
+          }
+        }
+      }
+    }
+    // -------------------------------------------------------------- P V
+    // fragment rows 2t + e and 8 + 2t + e are keys 2t + (e ^ (t & 1))
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      constexpr int VW = D / 64;                  // words of 8 dims of a key
+      uint32_t w[4][VW], b[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int k8 = 2 * hf + (x >> 1);
+        if constexpr (D == 128) {
+          const uint2 y = lds64(vcode[x & 1] + st + k8 * 8 * CB);
+          w[x][0] = y.x;
+          w[x][VW - 1] = y.y;
+        } else {
+          w[x][0] = lds32(vcode[x & 1] + st + k8 * 8 * CB);
+        }
+        b[x] = lds_u8(vscale[x & 1] + st + k8 * 8 * SB);
+      }
+      const uint32_t s01 = kv4_scales_f16(b[0] | b[1] << 8);
+      const uint32_t s23 = kv4_scales_f16(b[2] | b[3] << 8);
+#pragma unroll
+      for (int k = 0; k < VW; ++k) {
+        constexpr uint32_t M = 0x0f0f0f0fu;
+        uint32_t e01[4], o01[4], e23[4], o23[4];  // even and odd dims, pairs over keys
+        kv4_codes_f16((w[0][k] & M) | ((w[1][k] << 4) & ~M), e01);
+        kv4_codes_f16(((w[0][k] >> 4) & M) | (w[1][k] & ~M), o01);
+        kv4_codes_f16((w[2][k] & M) | ((w[3][k] << 4) & ~M), e23);
+        kv4_codes_f16(((w[2][k] >> 4) & M) | (w[3][k] & ~M), o23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t fa[4] = {hmul2(e01[j], s01), hmul2(o01[j], s01), hmul2(e23[j], s23),
+                                  hmul2(o23[j], s23)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            mma16816(o[n][4 * k + j], fa, pb[n][hf][0], pb[n][hf][1]);
+        }
+      }
+    }
+    st = st == (kStages - 1) * 2 * C_::kTensor ? 0u : st + 2 * C_::kTensor;
+  }
+  cp_wait<0>();
+  __syncwarp();
+
+  // --------------------------------------------- merge of the block's warps
+  float* ow = reinterpret_cast<float*>(smem + warp * C_::kRing);   // [row][D]
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * n + 2 * t + e;
+      float x = l[n][e];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+      if (g == 0) {
+        ctrl.m[warp][r] = m[n][e];
+        ctrl.l[warp][r] = x;
+      }
+      // tile j: dims g D/8 + 2j (elements 0, 1) and the next (2, 3)
+      if (r < rows) {
 #pragma unroll
         for (int j = 0; j < NS; ++j)
           *reinterpret_cast<float2*>(ow + r * D + g * (D / 8) + 2 * j) =
               make_float2(o[n][j][e], o[n][j][e + 2]);
       }
-    __syncthreads();
-    for (int x = threadIdx.x; x < R * D; x += 32 * W) {
-      const int r = x / D;
-      if (r0 + r >= rows) break;
-      float mm = -CUDART_INF_F;
-#pragma unroll
-      for (int w = 0; w < W; ++w) mm = fmaxf(mm, ctrl.m[w][r]);
-      const float mb = mm == -CUDART_INF_F ? 0.f : mm;
-      float sum = 0.f, acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = ex2(ctrl.m[w][r] - mb);
-        sum = fmaf(f, ctrl.l[w][r], sum);
-        acc = fmaf(f, reinterpret_cast<const float*>(smem + w * C_::kRing)[x], acc);
-      }
-      const float inv = sum > 0.f ? ka.out_mult / sum : 0.f;
-      const float lse = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
-      if (sq.splits == 1) {
-        put(a.out, out_row(r0 + r) * D + x % D, acc * inv);
-        if (x % D == 0) row_lse[r0 + r] = lse;
-      } else {
-        const int64_t row = (int64_t)blockIdx.x * kRowsPerGroup + r0 + r;
-        put(a.o_part, row * D + x % D, acc * inv);
-        if (x % D == 0) a.lse_part[row] = lse;
-      }
     }
-    __syncthreads();
+  __syncthreads();
+  auto put = [&](void* dst, int64_t at, float x) {
+    if (a.out_f32) static_cast<float*>(dst)[at] = x;
+    else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(x);
+  };
+  const int used = min(W, n_units);                 // warps that had a unit
+  for (int x = threadIdx.x; x < rows * D; x += 32 * W) {
+    const int r = x / D;
+    float mm = -CUDART_INF_F;
+    for (int w = 0; w < used; ++w) mm = fmaxf(mm, ctrl.m[w][r]);
+    const float mb0 = mm == -CUDART_INF_F ? 0.f : mm;
+    float sum = 0.f, acc = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < used; ++w) {
+      const float f = ex2(ctrl.m[w][r] - mb0);
+      sum = fmaf(f, ctrl.l[w][r], sum);
+      acc = fmaf(f, reinterpret_cast<const float*>(smem + w * C_::kRing)[x], acc);
+    }
+    const float inv = sum > 0.f ? ka.out_mult / sum : 0.f;
+    const float lse = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
+    if (pc.n_slots == 1) {
+      put(a.out, out_row(r) * D + x % D, acc * inv);
+      if (x % D == 0) row_lse[r] = lse;
+    } else {
+      const int64_t row = (int64_t)pc.slot * R + r;
+      put(a.o_part, row * D + x % D, acc * inv);
+      if (x % D == 0) a.lse_part[row] = lse;
+    }
   }
-  if (sq.splits == 1) return;
+  if (pc.n_slots > 1 && threadIdx.x == 0) ctrl.cut[ctrl.n_cut++] = pc;
+  __syncthreads();                 // the ring and ctrl are the next piece's
+}
 
-  // The last split to finish merges them: one warp per row, the log2-sum-exp
-  // of the row from its splits' (lane-parallel), then the outputs.
-  const int64_t base = (int64_t)sq.item_base + (kvh * sq.rg + rgi) * sq.splits;
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
+  constexpr int W = Cfg<D, NT>::W, R = Cfg<D, NT>::R;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ Ctrl ctrl;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);   // known uniform
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (threadIdx.x == 0) ctrl.n_cut = 0;
+  Piece& pc = ctrl.piece[warp];
+  bool more = find_piece<R, W>(ka.v.plan, -1, &pc);
+  while (more) {                   // the same for every warp of the block
+    if (pc.u1 > pc.u0) work_piece<D, NT>(ka, pc, ctrl, smem, warp);
+    const int next = pc.next;
+    __syncwarp();
+    more = next >= 0 && find_piece<R, W>(ka.v.plan, next, &pc);
+  }
+  // The last piece of a cut segment to finish merges them: a warp per row for
+  // the log2-sum-exp, then a thread per two columns for the output.
+  const int n_cut = ctrl.n_cut;
+  if (n_cut == 0) return;
+  const VerifyKArgs& a = ka.v;
+  __threadfence();                 // this block's pieces before its arrivals
+  __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    const uint32_t prev = atomicAdd(a.counters + cidx, 1u);
-    ctrl.last = prev + 1 == (uint32_t)sq.splits;
-    if (ctrl.last) {
-      a.counters[cidx] = 0u;
-      __threadfence();
+    for (int k = 0; k < n_cut; ++k) {
+      const int seg = ctrl.cut[k].seg;
+      ctrl.last[k] = atomicAdd(a.counters + seg, 1u) + 1 == (uint32_t)ctrl.cut[k].n_slots;
+      if (ctrl.last[k]) a.counters[seg] = 0u;
+    }
+    __threadfence();               // the others' pieces before reading them
+  }
+  __syncthreads();
+  // rows of the segments to merge, one after the other
+  auto rows_of = [&](int k) {
+    return k < n_cut && ctrl.last[k] ? min(R, ctrl.cut[k].rows - ctrl.cut[k].rgi * R) : 0;
+  };
+  const int n0 = rows_of(0), n1 = rows_of(1);
+  if (n0 + n1 == 0) return;
+  const int lane = threadIdx.x & 31, G = a.plan.group;
+  for (int x = warp; x < n0 + n1; x += W) {
+    const Piece& c = ctrl.cut[x >= n0];
+    const int r = x >= n0 ? x - n0 : x;
+    const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
+    float mm = -CUDART_INF_F, sum = 0.f;
+    for (int k = lane; k < c.n_slots; k += 32) {
+      const float v = __ldcg(lp + (int64_t)k * R);
+      const float nm = fmaxf(mm, v), mb = nm == -CUDART_INF_F ? 0.f : nm;
+      sum = sum * ptx::ex2(mm - mb) + ptx::ex2(v - mb);
+      mm = nm;
+    }
+    const float top = warp_max(mm), mb = top == -CUDART_INF_F ? 0.f : top;
+    sum = warp_sum(sum * ptx::ex2(mm - mb));
+    if (lane == 0) {
+      const float lse = sum > 0.f ? top + __log2f(sum) : -CUDART_INF_F;
+      ctrl.lse[x] = lse;
+      a.row_lse[((int64_t)c.kvh * a.plan.n_nodes + c.node0) * G + c.rgi * R + r] = lse;
     }
   }
   __syncthreads();
-  if (!ctrl.last) return;
-  for (int r = warp; r < rows; r += W) {
-    const float* lp = a.lse_part + base * kRowsPerGroup + r;
-    float mm = -CUDART_INF_F, sum = 0.f;
-    for (int k = lane; k < sq.splits; k += 32)
-      mm = fmaxf(mm, __ldcg(lp + (int64_t)k * kRowsPerGroup));
-    mm = warp_max(mm);
-    const float mb = mm == -CUDART_INF_F ? 0.f : mm;
-    for (int k = lane; k < sq.splits; k += 32)
-      sum += ex2(__ldcg(lp + (int64_t)k * kRowsPerGroup) - mb);
-    sum = warp_sum(sum);
-    const float lse = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
-    if (lane == 0) row_lse[r] = lse;
-    if (a.out_f32) combine_row_splits<D, false, 8>(a, base, sq.splits, r, lse, out_row(r));
-    else combine_row_splits<D, true, D == 128 ? 20 : 32>(a, base, sq.splits, r, lse, out_row(r));
+  for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
+    const int y = x / (D / 2), col = x % (D / 2) * 2;
+    const Piece& c = ctrl.cut[y >= n0];
+    const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r;
+    const float lse = ctrl.lse[y];
+    const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
+    const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 10
+    for (int k = 0; k < c.n_slots; ++k) {
+      // a row that saw nothing but NaN has log2-sum-exps of -inf: NaN stays
+      const float w = ptx::ex2(__ldcg(lp + (int64_t)k * R) - lse);
+      float2 v;
+      if (a.out_f32) {
+        v = __ldcg(reinterpret_cast<const float2*>(a.o_part + o + (int64_t)k * R * D));
+      } else {
+        const uint32_t u = __ldcg(reinterpret_cast<const uint32_t*>(
+            reinterpret_cast<const uint16_t*>(a.o_part) + o + (int64_t)k * R * D));
+        v = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      }
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+    }
+    const int64_t at =
+        (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
+    if (a.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = acc;
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+          ptx::pack_bf16x2(acc.x, acc.y);
   }
 }
 
@@ -575,11 +775,15 @@ __global__ void __launch_bounds__(256) kv4_scores_few(const VerifyKArgs a) {
 template <int D, int NT>
 static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t stream) {
   const size_t smem = Cfg<D, NT>::smem;
-  cudaError_t e = cudaFuncSetAttribute(kv4_split_few<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(kv4_split_few<D, NT>, dim3(L.max_items), dim3(32 * Cfg<D, NT>::W), smem,
-                       stream, k);
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(kv4_split_few<D, NT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  cudaError_t e = launch_dependent(kv4_split_few<D, NT>, dim3(L.target_ctas),
+                                   dim3(32 * Cfg<D, NT>::W), smem, stream, k);
   if (e != cudaSuccess || !k.v.scores || k.v.plan.max_chunks == 0) return e;
   return launch_dependent(kv4_scores_few,
                           dim3((k.v.plan.max_chunks + 31) / 32, k.v.plan.batch), dim3(256), 0,
