@@ -20,9 +20,9 @@ int kv4_few_rows(const ds_kv4_attn_args& a) {
   const int64_t group = a.num_q_heads / a.num_kv_heads;
   const int64_t rows = ((int64_t)a.n_nodes + a.batch - 1) / a.batch * group;
   if (rows > 16) return 0;
-  // the few-row pass counts its work (64-key units, and segments) in 32 bits
+  // the few-row pass counts its work (32-key units, and segments) in 32 bits
   const int64_t segs = a.num_kv_heads * (a.batch + a.n_nodes * group / 8 + 1);
-  const int64_t units = segs * ((int64_t)a.max_pages * a.page_size / 64 + 64);
+  const int64_t units = segs * ((int64_t)a.max_pages * a.page_size / 32 + 64);
   return units < ((int64_t)1 << 31) ? (int)rows : 0;
 }
 

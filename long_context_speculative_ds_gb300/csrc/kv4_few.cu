@@ -26,7 +26,7 @@
 // bank once.
 //
 // Work: every (sequence, kv head, group of 8 NT query rows) is a segment of
-// 64-key units, and the units of all segments, in order, are dealt to the
+// 32-key units, and the units of all segments, in order, are dealt to the
 // blocks in equal contiguous ranges, each segment behind a lead-in that
 // stands for what its start and end cost, so that a ragged batch balances.
 // A block works its range segment by segment: the units of one go to
@@ -36,14 +36,14 @@
 // the salience takes a second kernel.  Each warp works the plan out by
 // itself, from the lengths, in one pass over the batch.
 //
-// Chunk masses are kept per 64 keys or less ("subchunks"), so that a unit
+// Chunk masses are kept per 32 keys or less ("subchunks"), so that a unit
 // never shares one: [kv head][sequence's rows x subchunks][subchunk][row],
 // rows numbered through the batch.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
 
-#include <algorithm>
+#include <type_traits>
 
 #include "dev_common.cuh"
 #include "internal.h"
@@ -57,10 +57,10 @@ namespace ds {
 namespace kv4few {
 
 constexpr int kStages = 3;      // blocks of 32 keys in a warp's ring
-constexpr int kBlock = 32;
+constexpr int kBlock = 32;                       // keys of a block, and of a unit
 // A piece's start (plan, page ids, first copies) and end (merge) take about
-// as long as 20 units do in a block: 5 us against 0.27 us a unit
-constexpr int kPieceUnits = 20;
+// as long as 40 units do in a block of 16 warps: 5 us against 0.13 us a unit
+constexpr int kPieceUnits = 40;
 
 template <int D, int NT>
 struct Cfg {
@@ -154,7 +154,7 @@ __device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc) {
     if (b < pa.batch) {
       const SeqPlan q = seq_sizes(pa, b, report);
       s.L = q.L; s.T = q.T; s.node0 = q.node0; s.rows = q.rows;
-      s.nu = (q.L + q.T + 63) / 64;
+      s.nu = (q.L + q.T + kBlock - 1) / kBlock;
       s.segs = pa.num_kv_heads * ((q.rows + R - 1) / R);
     }
     return s;
@@ -167,8 +167,8 @@ __device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc) {
     U += __reduce_add_sync(0xffffffffu, s.segs * s.nu);
     S += __reduce_add_sync(0xffffffffu, s.segs);
   }
-  // at most one block per segment or, for long segments, per W units
-  const int N = min((int)gridDim.x, max(S, (U + W - 1) / W));
+  // at most one block per segment or, for long segments, per 2 W units
+  const int N = min((int)gridDim.x, max(S, (U + 2 * W - 1) / (2 * W)));
   const int i = blockIdx.x;
   if (i >= N) return false;
   U += S * kPieceUnits;                           // the axis: units behind their lead-ins
@@ -232,7 +232,7 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int G = a.plan.group, L = pc.L, T = pc.T, P = a.plan.page_size;
   const int rows = min(R, pc.rows - pc.rgi * R);                // of this segment
-  const int C = a.scores ? min(64, a.plan.chunk_size) : 0;      // keys of a subchunk
+  const int C = a.scores ? min(kBlock, a.plan.chunk_size) : 0;      // keys of a subchunk
   const int64_t row0 = (int64_t)pc.node0 * G;                   // first row of the sequence
   const int64_t n_rows = (int64_t)a.plan.n_nodes * G;
   const int64_t n_sub = C ? (int64_t)a.plan.max_chunks * (a.plan.chunk_size / C) : 0;
@@ -240,17 +240,16 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   float* const row_lse = a.row_lse + (int64_t)pc.kvh * n_rows + row0 + pc.rgi * R;
   const int32_t* ptab = a.page_table + (int64_t)pc.b * a.plan.max_pages;
 
-  // this warp's blocks: two for each of the piece's units u0 + warp, + W, ...;
-  // nh is their number of 16-key halves that hold keys of the sequence
-  const int nh_piece = (min(pc.u1 * 64, L + T) - pc.u0 * 64 + 15) / 16;
+  // this warp's units u0 + warp, + W, ... of the piece, a block each; nh is
+  // their number of 16-key halves that hold keys of the sequence
+  const int nh_piece = (min(pc.u1 * kBlock, L + T) - pc.u0 * kBlock + 15) / 16;
   const int n_units = pc.u1 - pc.u0;
-  const int mine = n_units > warp ? (n_units - warp - 1) / W + 1 : 0;
-  const int nh = mine > 0 ? (mine - 1) * 4 + min(4, nh_piece - (warp + (mine - 1) * W) * 4) : 0;
-  const int nblk = (nh + 1) / 2;
-  const int first_key = (pc.u0 + warp) * 64;
+  const int nblk = n_units > warp ? (n_units - warp - 1) / W + 1 : 0;
+  const int nh = nblk > 0 ? (nblk - 1) * 2 + min(2, nh_piece - (warp + (nblk - 1) * W) * 2) : 0;
+  const int first_key = (pc.u0 + warp) * kBlock;
   const int pshift = __ffs(P) - 1;
-  // first key of half i (two to a block, four to a unit)
-  auto key_of = [&](int i) { return first_key + (i >> 2) * (W * 64) + (i & 3) * 16; };
+  // first key of half i
+  auto key_of = [&](int i) { return first_key + (i >> 1) * (W * kBlock) + (i & 1) * 16; };
   // page ids of this warp's halves, 32 at a time, the next 32 on their way
   auto ids_of = [&](int i) { return i < nh ? __ldg(ptab + (key_of(i) >> pshift)) : 0; };
   int ids = ids_of(lane), next_ids = ids_of(32 + lane);
@@ -271,7 +270,7 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   }
   // ancestor masks, when the piece holds tree keys; a tree of one node has
   // only itself
-  const bool need_anc = pc.u1 * 64 > L;
+  const bool need_anc = pc.u1 * kBlock > L;
   uint64_t anc[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) anc[n][0] = anc[n][1] = 1ull;
@@ -704,37 +703,53 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
     }
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
-    const int y = x / (D / 2), col = x % (D / 2) * 2;
-    const Piece& c = ctrl.cut[y >= n0];
-    const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r;
-    const float lse = ctrl.lse[y];
-    const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
-    const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
-    float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 10
-    for (int k = 0; k < c.n_slots; ++k) {
-      // a row that saw nothing but NaN has log2-sum-exps of -inf: NaN stays
-      const float w = ptx::ex2(__ldcg(lp + (int64_t)k * R) - lse);
-      float2 v;
-      if (a.out_f32) {
-        v = __ldcg(reinterpret_cast<const float2*>(a.o_part + o + (int64_t)k * R * D));
-      } else {
-        const uint32_t u = __ldcg(reinterpret_cast<const uint32_t*>(
-            reinterpret_cast<const uint16_t*>(a.o_part) + o + (int64_t)k * R * D));
-        v = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  const auto columns = [&](auto f32) {
+    constexpr bool F32 = decltype(f32)::value;
+    constexpr int NB = 20;         // pieces on their way at once
+    for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
+      const int y = x / (D / 2), col = x % (D / 2) * 2;
+      const Piece& c = ctrl.cut[y >= n0];
+      const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r, ns = c.n_slots;
+      const float lse = ctrl.lse[y];
+      const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
+      const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
+      float2 acc = make_float2(0.f, 0.f);
+      for (int k0 = 0; k0 < ns; k0 += NB) {
+        float w[NB];
+        float2 v[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          if (k0 + k >= ns) continue;
+          const int64_t at = o + (int64_t)(k0 + k) * R * D;
+          w[k] = __ldcg(lp + (int64_t)(k0 + k) * R);
+          if constexpr (F32) {
+            v[k] = __ldcg(reinterpret_cast<const float2*>(a.o_part + at));
+          } else {
+            const uint32_t u = __ldcg(reinterpret_cast<const uint32_t*>(
+                reinterpret_cast<const uint16_t*>(a.o_part) + at));
+            v[k] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          if (k0 + k >= ns) continue;
+          // a row that saw nothing but NaN has log2-sum-exps of -inf: NaN stays
+          const float e = ptx::ex2(w[k] - lse);
+          acc.x = fmaf(e, v[k].x, acc.x);
+          acc.y = fmaf(e, v[k].y, acc.y);
+        }
       }
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
+      const int64_t at =
+          (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
+      if constexpr (F32)
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = acc;
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+            ptx::pack_bf16x2(acc.x, acc.y);
     }
-    const int64_t at =
-        (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
-    if (a.out_f32)
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = acc;
-    else
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
-          ptx::pack_bf16x2(acc.x, acc.y);
-  }
+  };
+  if (a.out_f32) columns(std::true_type{});
+  else columns(std::false_type{});
 }
 
 // Chunk scores: the sum over kv heads and rows of 2^(mass - the row's
@@ -742,12 +757,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
 // the kv heads w, w + 8, ..., whose sums are added in that order.
 __global__ void __launch_bounds__(256) kv4_scores_few(const VerifyKArgs a) {
   __shared__ float part[8][32];
-  grid_dep_wait();
-  grid_dep_launch_dependents();
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 32 + lane;
+  // the lengths are inputs of the call: the split pass, which this launch
+  // follows, has itself waited for whatever wrote them
   const SeqPlan sq = seq_sizes(a.plan, b, false);
-  const int sub = min(64, a.plan.chunk_size), per = a.plan.chunk_size / sub;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int sub = min(kBlock, a.plan.chunk_size), per = a.plan.chunk_size / sub;
   const int n_sub = (sq.L + sub - 1) / sub;       // of this sequence
   const int64_t n_rows = (int64_t)a.plan.n_nodes * a.plan.group;
   const int64_t row0 = (int64_t)sq.node0 * a.plan.group;

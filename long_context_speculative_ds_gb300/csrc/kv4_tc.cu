@@ -184,15 +184,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   };
   // Tiles are loaded and converted in the order the MMAs need them: K runs
   // one tile ahead of V (two in key mode, where both groups start at once).
-  // Position i of that order: tensor and tile.
-  const int lead = row_mode ? 1 : 2;
-  auto order = [&](int i, int& is_v, int& n) {
-    const int head = min(lead, nt);
-    if (i < head) { is_v = 0; n = i; return; }
-    // V(m), K(m + lead) pairs while there are K tiles left, then V alone
-    const int j = i - head, pairs = max(0, nt - lead);
-    if (j < 2 * pairs) { is_v = (j & 1) ^ 1; n = (j >> 1) + (is_v ? 0 : lead); }
-    else { is_v = 1; n = j - pairs; }
+  // The walk keeps counters instead of dividing: a single warp follows it,
+  // and every instruction adds its latency to each tile's turn.
+  struct Walk {
+    int lead, nt, nraw;
+    int k = 0, v = 0;              // K and V tiles taken so far
+    bool is_v = false;             // the tile at hand
+    int n = 0;
+    int slot = 0, phase = 0;       // its raw slot, and the parity of that slot's uses
+    __device__ bool take() {       // false at the end
+      if (v == nt) return false;
+      is_v = k >= nt || k >= v + lead;
+      n = is_v ? v++ : k++;
+      return true;
+    }
+    __device__ void release() {    // on to the next raw slot
+      if (++slot == nraw) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  };
+  auto walk = [&]() {
+    Walk w;
+    w.lead = row_mode ? 1 : 2;
+    w.nt = nt;
+    w.nraw = nraw;
+    return w;
   };
   // tiles of group g: row mode every tile, key mode every other tile (so
   // slot n % 2 is then always group n % 2's)
@@ -211,56 +229,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       // Page ids come 32 at a time, a run of 32 / npg tiles, one run ahead of
       // the K tiles (V is at most two tiles behind K, so two runs are kept):
       // a load per tile would put its latency into every tile's turn.
-      const int run = 32 / npg, pend = (L + T + P - 1) / P;
+      const int rshift = __ffs(P) - 1 - 2;       // log2 of the tiles of a run, P / 4
+      const int run = 1 << rshift, pend = (L + T + P - 1) / P;
       auto ids_of = [&](int r) {
         const int pi = (t0 + r * run) * npg + lane;
         return pi < pend ? __ldg(ptab + pi) : 0;
       };
       int next_ids = ids_of(0);
-      int issued = 0;
+      const uint8_t* const k_head = ka.k4 + (int64_t)kvh * blk;
+      const uint8_t* const v_head = ka.v4 + (int64_t)kvh * blk;
+      const uint32_t page_bytes = a.plan.num_kv_heads * blk;
       bool ok = true;
-      for (int i = 0; ok && i < 2 * nt; ++i) {
-        int is_v, n;
-        order(i, is_v, n);
-        const int r = n / run;
-        if (!is_v && n == r * run) {
+      Walk w = walk();
+      while (w.take()) {
+        const int r = w.n >> rshift, in_run = w.n & (run - 1);
+        if (!w.is_v && in_run == 0) {
           ctrl->pages[r & 1][lane] = next_ids;
           __syncwarp();
           next_ids = ids_of(r + 1);
         }
-        const int slot = i % nraw;
-        const int slot0 = (t0 + n) * kTileKeys + lane * P;
         int pg = 0;
-        bool have = lane < npg && slot0 < L + T, bad = false;
+        bool have = lane < npg && (t0 + w.n) * kTileKeys + lane * P < L + T, bad = false;
         if (have) {
-          pg = ctrl->pages[r & 1][(n - r * run) * npg + lane];
-          bad = pg < 0 || pg >= a.num_pages;
+          pg = ctrl->pages[r & 1][in_run * npg + lane];
+          bad = (uint32_t)pg >= (uint32_t)a.num_pages;
           if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
         }
         const uint32_t badm = __ballot_sync(0xffffffffu, bad);
         have = have && !bad;
         const uint32_t copies = __ballot_sync(0xffffffffu, have);
-        if (lane == 0) ctrl->where[0] = 10000 + i;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + slot), ((i / nraw) & 1) ^ 1,
-                                               abort_flag, diag, 10000 + i));
+        const uint32_t full = bar(kRawFull + w.slot);
+        const uint32_t tag = 10000 + 2 * w.n + (w.is_v ? 1 : 0);
+        if (lane == 0) ctrl->where[0] = tag;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
+                                               diag, tag));
         if (!ok) break;
         if (lane == 0) {
-          ctrl->bad[slot] = badm;
-          mbar_arrive_expect_tx(bar(kRawFull + slot), __popc(copies) * blk);
+          ctrl->bad[w.slot] = badm;
+          mbar_arrive_expect_tx(full, __popc(copies) * blk);
         }
         __syncwarp();
         if (have)
-          bulk_load_hint(raw_addr(slot) + lane * blk,
-                         (is_v ? ka.v4 : ka.k4) +
-                             ((int64_t)pg * a.plan.num_kv_heads + kvh) * blk,
-                         blk, bar(kRawFull + slot), policy);
-        issued = i + 1;
+          bulk_load_hint(raw_addr(w.slot) + lane * blk,
+                         (w.is_v ? v_head : k_head) + (uint64_t)(uint32_t)pg * page_bytes, blk,
+                         full, policy);
+        w.release();
       }
       if (lane == 0) ctrl->where[0] = ok ? 19999 : 19998;
-      // copies still in flight must land before the CTA can exit
+      // copies still in flight must land before the CTA can exit: each slot's
+      // last phase (a slot not used yet passes at once)
       if (!ok && lane == 0)
-        for (int i = max(0, issued - nraw); i < issued; ++i)
-          drain_wait(bar(kRawFull + i % nraw), (i / nraw) & 1);
+        for (int i = 0; i < nraw; ++i) {
+          const bool wrapped = i >= w.slot;        // last used one round ago
+          drain_wait(bar(kRawFull + i), wrapped ? w.phase ^ 1 : w.phase);
+        }
     } else if (warp == 1) {
       // ---------------------------------------------------- ancestor masks
       if (need_anc) {
@@ -495,14 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     const uint32_t drow = (key >> 3) * RG + (key & 7) * 128;
     const bool rep = warp == 12 && lane == 0;
     bool ok = true;
-    for (int i = 0; i < 2 * nt; ++i) {
-      int is_v, n;
-      order(i, is_v, n);
-      const int slot = i % nraw;
-      if (rep) ctrl->where[5] = 40000 + i;
-      ok = mbar_wait(bar(kRawFull + slot), (i / nraw) & 1, abort_flag, diag, 40000 + i) &&
+    Walk w = walk();
+    while (w.take()) {
+      const int slot = w.slot, n = w.n;
+      const bool is_v = w.is_v;
+      const uint32_t tag = 40000 + 2 * n + (is_v ? 1 : 0);
+      if (rep) ctrl->where[5] = tag;
+      ok = mbar_wait(bar(kRawFull + slot), w.phase, abort_flag, diag, tag) &&
            mbar_wait(bar((is_v ? kVEmpty : kKEmpty) + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag,
-                     diag, 45000 + i);
+                     diag, tag + 100000);
       if (!__all_sync(0xffffffffu, ok)) break;
       const bool bad = (ctrl->bad[slot] >> pidx) & 1u;
       const uint32_t raw = raw_addr(slot);
@@ -546,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         mbar_arrive(bar((is_v ? kVFull : kKFull) + (n & 1)));
         mbar_arrive(bar(kRawEmpty + slot));
       }
+      w.release();
     }
   }
 
