@@ -217,7 +217,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   auto ntiles = [&](int g) { return row_mode ? nt : (nt - g + 1) / 2; };
   auto tile_of = [&](int g, int j) { return row_mode ? j : 2 * j + g; };
 
+  // registers move from the loader's and the converters' warpgroups to the
+  // softmax groups: 128 (80 + 96) + 256 x 168 = the launch's 512 x 128
+  static_assert(128 * (80 + 96) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
+    regs_release<80>();
     if (!(active && nt > 0)) {
     } else if (warp == 0) {
       // ------------------------------------------------------------ loader
@@ -374,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       }
     }
   } else if (warp < 12) {
+    regs_claim<168>();
     if (active && nt > 0) {
       // ------------------------------------------------------------ softmax
       const int g = (warp - 4) >> 2;
@@ -506,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
                               a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
                               ka.out_mult);
     }
-  } else if (active && nt > 0) {
+  } else {
+    regs_release<96>();
+    if (active && nt > 0) {
     // ---------------------------------------------------------- converters
     const int key = (warp - 12) * 32 + lane;
     const int P = a.plan.page_size;
@@ -570,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         mbar_arrive(bar(kRawEmpty + slot));
       }
       w.release();
+    }
     }
   }
 

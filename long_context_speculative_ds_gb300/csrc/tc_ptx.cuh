@@ -224,6 +224,17 @@ DS_DEV void mma_commit(uint32_t bar) {
       : "memory");
 }
 
+// Registers per thread of the calling warpgroup, from here on (all four
+// warps execute it).  The sum over the block must stay within its launch's.
+template <int N>
+DS_DEV void regs_release() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+DS_DEV void regs_claim() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Packed pairs of fp32 (sm_100+ f32x2 arithmetic).
 DS_DEV uint64_t f2pack(float lo, float hi) {
   uint64_t r;
