@@ -69,6 +69,7 @@ struct Cfg {
   static constexpr int kTensor = kBlock * (D / 2 + D / 16);   // bytes of a block's K or V
   static constexpr int kRing = kStages * 2 * kTensor;     // bytes of a warp's ring
   static constexpr size_t smem = (size_t)W * kRing;
+  static_assert(kStages == 3, "a block in use, the next one's scores, one on its way");
   static_assert(R * D * 4 <= kRing, "a warp's output must fit in its ring");
 };
 
@@ -402,16 +403,9 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
     vscale[e] = ring + C_::kTensor + kBlock * CB + key * SB + (D == 128 ? g : g >> 1);
   }
   const int cshift = C ? __ffs(C) - 1 : 0;
-  uint32_t st = 0;
-#pragma unroll 1
-  for (int i = 0; i < nblk; ++i) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    issue(i + kStages - 1);
-    const int key0 = key_of(2 * i);
-    // ------------------------------------------------------------ Q K^T
-    // s[n][hf][2h + e]: key 16 hf + 8h + krow, row 8n + 2t + e
-    float s[NT][2][4];
+  // Scores of the block at ring offset `at`: s[n][hf][2h + e] is key 16 hf +
+  // 8h + krow, row 8n + 2t + e.
+  auto scores = [&](uint32_t at, float (&s)[NT][2][4]) {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t w[2][D / 32], sc[2][2];
@@ -419,15 +413,15 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
       for (int h = 0; h < 2; ++h) {
         const int k8 = 2 * hf + h;                // which eight keys
         if constexpr (D == 128) {
-          const uint4 x = lds128(kcode + st + k8 * 8 * CB);
+          const uint4 x = lds128(kcode + at + k8 * 8 * CB);
           w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-          const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + st + k8 * 8 * SB));
+          const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + at + k8 * 8 * SB));
           sc[h][0] = __byte_perm(s2, s2, 0x1010);
           sc[h][1] = __byte_perm(s2, s2, 0x3232);
         } else {
-          const uint2 x = lds64(kcode + st + k8 * 8 * CB);
+          const uint2 x = lds64(kcode + at + k8 * 8 * CB);
           w[h][0] = x.x; w[h][1] = x.y;
-          const uint32_t b = lds_u8(kscale + st + k8 * 8 * SB);
+          const uint32_t b = lds_u8(kscale + at + k8 * 8 * SB);
           sc[h][0] = sc[h][1] = kv4_scales_f16(b | b << 8);
         }
       }
@@ -455,6 +449,25 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
         }
       }
     }
+  };
+  // Software pipeline: the scores of block i + 1 are formed beside the
+  // softmax and the second product of block i, which depend on nothing of it,
+  // while block i + 2 is on its way.
+  cp_wait<kStages - 2>();
+  __syncwarp();
+  float s[NT][2][4];
+  scores(0, s);
+  uint32_t st = 0;
+#pragma unroll 1
+  for (int i = 0; i < nblk; ++i) {
+    __syncwarp();                  // all lanes are done with block i - 1
+    issue(i + kStages - 1);
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t st_next = st == (kStages - 1) * 2 * C_::kTensor ? 0u : st + 2 * C_::kTensor;
+    float s_next[NT][2][4];
+    scores(st_next, s_next);       // after the last block: not used
+    const int key0 = key_of(2 * i);
     // ---------------------------------------------------------- softmax
     const bool tail = key0 + kBlock > L;
     if (tail) {
@@ -583,7 +596,11 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
         }
       }
     }
-    st = st == (kStages - 1) * 2 * C_::kTensor ? 0u : st + 2 * C_::kTensor;
+    st = st_next;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s[n][x >> 2][x & 3] = s_next[n][x >> 2][x & 3];
   }
   cp_wait<0>();
   __syncwarp();
