@@ -196,8 +196,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return C.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without the Stream object around it, which takes
+# longer to make (3 us on a Grace core) than the call's own launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> C.c_void_p:
     if stream is None:
+        if _raw_stream is not None and _get_device is not None:
+            return C.c_void_p(_raw_stream(_get_device()))
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream")
                       else int(stream))

@@ -1,13 +1,17 @@
 // Rows of K and V into the paged 4-bit cache and back (include/ds.h,
 // ds_kv4_write and ds_kv4_read).
 //
-// One thread handles one scale group: 16 channels of one row's head, 32 bytes
-// of bf16 on one side, 8 bytes of codes and one scale byte on the other.
-// Nothing is shared between threads: the maximum over the group, the scale
-// and the codes are the thread's own.  A warp covers consecutive rows of one
-// head (4 rows at head_dim 128, 8 at 64), whose slots are consecutive in the
-// page block, so that its codes are one run of 256 bytes and its scales one
-// of 32.
+// Bound by memory when there are many rows, by latency when there are few.  A
+// warp takes a few consecutive rows and walks over (tensor, kv head) units,
+// several units' loads on their way at once; with few rows the units of a row
+// are spread over more warps.  Which sequence a row belongs to, its slot and
+// its page are looked up once per lane, for all units.
+//
+// Writing, a lane holds one scale group: 16 channels, whose maximum, scale and
+// codes are its own.  A warp covers 4 rows of one head (8 at head_dim 64),
+// whose slots follow each other in the page block: its codes are one run of
+// 256 bytes and its scales one of 32.  Reading, a lane makes 8 channels (one
+// 16-byte store), so that a store instruction covers whole sectors.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,11 +34,14 @@ struct Kv4RowsKArgs {
   const int32_t* row_offsets;
   const int32_t* path;
   const int32_t* n_accepted;
-  int32_t batch, n_rows, num_kv_heads, page_size, num_pages, max_pages;
+  int32_t batch, n_rows, num_kv_heads, page_size, page_shift, num_pages, max_pages;
+  int32_t slices;                 // warps that share a row group's units
   float mult[2];                  // write: 2^-exp, read: 2^exp
   int32_t* new_lens;
   uint32_t* status;
 };
+
+constexpr int64_t kRowWarps = 152 * 32;
 
 // The sequence that owns row r: the last b with row_offsets[b] <= r.
 DS_DEV int row_sequence(const int32_t* offs, int batch, int r) {
@@ -74,17 +81,17 @@ DS_DEV bool path_ok(const Kv4RowsKArgs& a, int b, int n, int acc) {
 
 template <int D, bool WRITE>
 __global__ void __launch_bounds__(256) kv4_rows(const Kv4RowsKArgs a) {
-  constexpr int NG = D / kKv4Group;       // scale groups of a head
-  constexpr int RW = 32 / NG;             // rows of a warp
+  constexpr int CH = WRITE ? 16 : 8;      // channels of a lane
+  constexpr int LPH = D / CH;             // lanes of a head
+  constexpr int RW = 32 / LPH;            // rows of a warp
+  constexpr int NB = WRITE ? 4 : 8;       // units on their way at once
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int units = 2 * a.num_kv_heads;   // (tensor, head) pairs
-  const int unit = (int)(w % units);
   // with a path, "rows" are the path's entries: DS_MAX_TREE_NODES a sequence
   const int total = a.path ? a.batch * DS_MAX_TREE_NODES : a.n_rows;
-  const int64_t e = w / units * RW + lane / NG;
+  const int64_t e = w / a.slices * RW + lane / LPH;
   // new lengths: the first thread of each sequence's number in the grid
   if (WRITE && a.new_lens) {
     const int64_t tid = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -120,54 +127,90 @@ __global__ void __launch_bounds__(256) kv4_rows(const Kv4RowsKArgs a) {
     if (!rows_of(a, b, n0, n, from) || row < n0 || row >= n0 + n) return;
     slot = from + (row - n0);
   }
-  const int P = a.page_size;
-  const int pg = __ldg(a.page_table + (int64_t)b * a.max_pages + slot / P);
-  const bool page_ok = pg >= 0 && pg < a.num_pages;
+  const int P = a.page_size, off = slot & (P - 1);
+  const int pg = __ldg(a.page_table + (int64_t)b * a.max_pages + (slot >> a.page_shift));
+  const bool page_ok = (uint32_t)pg < (uint32_t)a.num_pages;
   if (!page_ok) flag(a.status, DS_DEV_BAD_PAGE);
-  const int t = unit & 1, h = unit >> 1, g = lane % NG;
-  uint16_t* x = a.rows[t] + (int64_t)row * a.row_stride[t] + h * D + g * kKv4Group;
-  uint8_t* blk = a.cache[t] + ((int64_t)pg * a.num_kv_heads + h) * DS_KV4_BLOCK_BYTES(P, D);
-  const int off = slot % P;
-  uint8_t* cp = blk + off * kv4_code_bytes(D) + g * 8;
-  uint8_t* sp = blk + P * kv4_code_bytes(D) + off * kv4_scale_bytes(D) + g;
+  if (WRITE && !page_ok) return;
+  const int g = lane % LPH;
+  const int blk = DS_KV4_BLOCK_BYTES(P, D);
+  // this lane's codes and scale in head 0's block, and its channels in the row
+  const int64_t page0 = (int64_t)(page_ok ? pg : 0) * a.num_kv_heads * blk;
+  const int64_t code0 = page0 + off * kv4_code_bytes(D) + g * (CH / 2);
+  const int64_t scale0 =
+      page0 + P * kv4_code_bytes(D) + off * kv4_scale_bytes(D) + g * CH / kKv4Group;
+  const int units = 2 * a.num_kv_heads;   // unit u: tensor u % 2 of head u / 2
+  const int per = (units + a.slices - 1) / a.slices;
+  const int u0 = (int)(w % a.slices) * per, u1 = min(units, u0 + per);
+  uint16_t* const x0[2] = {a.rows[0] + (int64_t)row * a.row_stride[0] + g * CH,
+                           a.rows[1] + (int64_t)row * a.row_stride[1] + g * CH};
   if constexpr (WRITE) {
-    if (!page_ok) return;
-    const uint4 lo = __ldg(reinterpret_cast<const uint4*>(x));
-    const uint4 hi = __ldg(reinterpret_cast<const uint4*>(x) + 1);
-    const uint32_t r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    float y[16];
+    bool any_bad = false;
+    for (int u = u0; u < u1; u += NB) {
+      uint4 lo[NB], hi[NB];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[2 * i] = __uint_as_float(r[i] << 16) * a.mult[t];
-      y[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u) * a.mult[t];
+      for (int k = 0; k < NB; ++k)
+        if (u + k < u1) {
+          const int t = (u + k) & 1, h = (u + k) >> 1;
+          const uint4* x = reinterpret_cast<const uint4*>((t ? x0[1] : x0[0]) + h * D);
+          lo[k] = __ldg(x);
+          hi[k] = __ldg(x + 1);
+        }
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (u + k < u1) {
+          const int t = (u + k) & 1, h = (u + k) >> 1;
+          const uint32_t r[8] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w,
+                                 hi[k].x, hi[k].y, hi[k].z, hi[k].w};
+          const float mult = t ? a.mult[1] : a.mult[0];
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[2 * i] = __uint_as_float(r[i] << 16) * mult;
+            y[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u) * mult;
+          }
+          uint32_t sb;
+          uint2 codes;
+          bool bad;
+          kv4_quantise16(y, sb, codes, bad);
+          any_bad |= bad;
+          uint8_t* const c = (t ? a.cache[1] : a.cache[0]) + (int64_t)h * blk;
+          *reinterpret_cast<uint2*>(c + code0) = codes;
+          c[scale0] = (uint8_t)sb;
+        }
     }
-    uint32_t sb;
-    uint2 codes;
-    bool bad;
-    kv4_quantise16(y, sb, codes, bad);
-    if (bad) flag(a.status, DS_DEV_BAD_VALUE);
-    *reinterpret_cast<uint2*>(cp) = codes;
-    *sp = (uint8_t)sb;
+    if (any_bad) flag(a.status, DS_DEV_BAD_VALUE);
   } else {
-    uint32_t r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (page_ok) {
-      const uint2 codes = __ldg(reinterpret_cast<const uint2*>(cp));
-      const uint32_t s2 = kv4_scales_f16(__ldg(sp));
-      const float s = __half2float(__ushort_as_half((unsigned short)(s2 & 0xffffu))) * a.mult[t];
-      const uint32_t cw[2] = {codes.x, codes.y};
+    for (int u = u0; u < u1; u += NB) {
+      uint32_t codes[NB], sb[NB];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t v[4];
-        kv4_codes_f16(cw[k], v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r[4 * k + i]) : "f"(f.y * s), "f"(f.x * s));
+      for (int k = 0; k < NB; ++k) {
+        codes[k] = sb[k] = 0u;
+        if (u + k < u1 && page_ok) {
+          const int t = (u + k) & 1, h = (u + k) >> 1;
+          const uint8_t* const c = (t ? a.cache[1] : a.cache[0]) + (int64_t)h * blk;
+          codes[k] = __ldg(reinterpret_cast<const uint32_t*>(c + code0));
+          sb[k] = __ldg(c + scale0);
         }
       }
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (u + k < u1) {
+          const int t = (u + k) & 1, h = (u + k) >> 1;
+          const uint32_t s2 = kv4_scales_f16(sb[k]);
+          const float s = __half2float(__ushort_as_half((unsigned short)(s2 & 0xffffu))) *
+                          (t ? a.mult[1] : a.mult[0]);
+          uint32_t v[4], r[4];
+          kv4_codes_f16(codes[k], v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+            r[i] = ptx::pack_bf16x2(f.x * s, f.y * s);
+          }
+          *reinterpret_cast<uint4*>((t ? x0[1] : x0[0]) + h * D) =
+              make_uint4(r[0], r[1], r[2], r[3]);
+        }
     }
-    reinterpret_cast<uint4*>(x)[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    reinterpret_cast<uint4*>(x)[1] = make_uint4(r[4], r[5], r[6], r[7]);
   }
 }
 
@@ -189,16 +232,20 @@ static cudaError_t launch_rows(const ds_kv4_rows_args& g, cudaStream_t stream) {
   a.n_rows = g.n_rows;
   a.num_kv_heads = g.num_kv_heads;
   a.page_size = g.page_size;
+  a.page_shift = __builtin_ctz((unsigned)g.page_size);
   a.num_pages = g.num_pages;
   a.max_pages = g.max_pages;
   a.mult[0] = ldexpf(1.f, WRITE ? -g.k_exp : g.k_exp);
   a.mult[1] = ldexpf(1.f, WRITE ? -g.v_exp : g.v_exp);
   a.new_lens = g.new_lens;
   a.status = static_cast<uint32_t*>(g.workspace);
-  const int rw = 32 / (g.head_dim / kKv4Group);
+  const int rw = 32 / (g.head_dim / (WRITE ? 16 : 8));
   const int64_t total = g.path ? (int64_t)g.batch * DS_MAX_TREE_NODES : g.n_rows;
-  const int64_t warps = (total + rw - 1) / rw * 2 * g.num_kv_heads;
-  const dim3 grid((unsigned)std::max<int64_t>(1, (warps + 7) / 8));
+  const int64_t groups = (total + rw - 1) / rw;
+  // enough warps to fill the machine (152 SMs of 32), one unit a warp at least
+  const int units = 2 * g.num_kv_heads;
+  a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(units, kRowWarps / std::max<int64_t>(1, groups)));
+  const dim3 grid((unsigned)std::max<int64_t>(1, (groups * a.slices + 7) / 8));
   if (g.head_dim == 128)
     return launch_dependent(kv4_rows<128, WRITE>, grid, dim3(256), 0, stream, a);
   return launch_dependent(kv4_rows<64, WRITE>, grid, dim3(256), 0, stream, a);

@@ -1,12 +1,15 @@
 // RMS norm of every query and key head with the position rotation in the
 // same pass (include/ds.h, ds_qk_norm_rope).
 //
+// Bound by memory when there are many rows, by latency when there are few.
 // Eight lanes hold one head (head_dim 128; four at 64): lane l the eight
 // values from 8l of the head's first half and the eight opposite them in the
 // second, so that a lane owns whole rotation pairs, reads and writes 16-byte
 // vectors, and the sum of squares is a sum over the eight lanes.  A warp
-// takes four (eight) heads at a time.  A block works on one row, whose D / 2
-// sines and cosines it forms once.
+// takes a row and works on four (eight) heads at a time, the next ones' loads
+// on their way; the row's D / 2 sines and cosines are formed once, two a
+// lane, and shared through the warp's corner of shared memory.  With few rows
+// a row's heads are spread over more warps.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,6 +19,7 @@
 #include "dev_common.cuh"
 #include "internal.h"
 #include "pdl.cuh"
+#include "tc_ptx.cuh"
 
 namespace ds {
 
@@ -28,46 +32,97 @@ struct NormRopeKArgs {
   int32_t n_rows, hq, heads;      // heads = query + key heads
   float eps;
   int32_t rotate;
+  int32_t slices;                 // warps that share a row's heads
   uint32_t* status;
   // frequency j as a 64-bit fraction of a turn
   unsigned long long turn[64];
 };
 
+constexpr int kNormWarps = 8;             // warps of a block
+
 template <int D>
-__global__ void __launch_bounds__(256) qk_norm_rope(const NormRopeKArgs a) {
+__global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope(const NormRopeKArgs a) {
   constexpr int HALF = D / 2;
   constexpr int LPH = HALF / 8;           // lanes of a head
-  constexpr int HPW = 32 / LPH;           // heads of a warp
-  __shared__ __align__(16) float2 cs[HALF];
+  constexpr int HPW = 32 / LPH;           // heads of a warp at a time
+  constexpr int NB = 5;                   // head groups on their way at once
+  __shared__ __align__(16) float2 s_cs[kNormWarps][HALF];
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kNormWarps + warp;
+  const int row = (int)(w / a.slices);
+  if (row >= a.n_rows) return;
+  const int groups = (a.heads + HPW - 1) / HPW;
+  const int per = (groups + a.slices - 1) / a.slices;
+  const int g0 = (int)(w - (int64_t)row * a.slices) * per, g1 = min(groups, g0 + per);
+  if (g0 >= g1) return;
   const int pos = __ldg(a.positions + row);
+  const int l = lane % LPH, sub = lane / LPH;
+  // lane's part of head hh (query heads first, then key heads)
+  auto src = [&](int hh) {
+    const bool t = hh >= a.hq;
+    return (t ? a.x[1] + (int64_t)row * a.stride[1] - (int64_t)a.hq * D
+              : a.x[0] + (int64_t)row * a.stride[0]) + (int64_t)hh * D + l * 8;
+  };
+  auto dst = [&](int hh) {
+    const bool t = hh >= a.hq;
+    return (t ? a.out[1] + (int64_t)row * a.out_stride[1] - (int64_t)a.hq * D
+              : a.out[0] + (int64_t)row * a.out_stride[0]) + (int64_t)hh * D + l * 8;
+  };
+  uint4 u[NB], v[NB];
+  auto load = [&](int gr0) {
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int hh = (gr0 + k) * HPW + sub;
+      u[k] = v[k] = make_uint4(0, 0, 0, 0);
+      if (gr0 + k < g1 && hh < a.heads) {
+        // plain loads: with q_out = q the same bytes are written below
+        const uint16_t* p = src(hh);
+        u[k] = *reinterpret_cast<const uint4*>(p);
+        v[k] = *reinterpret_cast<const uint4*>(p + HALF);
+      }
+    }
+  };
+  load(g0);
   if (pos < 0) {
-    if (threadIdx.x == 0) flag(a.status, DS_DEV_BAD_LENGTH);
+    if (lane == 0) flag(a.status, DS_DEV_BAD_LENGTH);
     return;
   }
   // position * frequency wraps modulo one turn in 64 bits; its upper half,
   // read as a signed number, is the angle in units of pi / 2^31
-  for (int j = threadIdx.x; j < HALF; j += blockDim.x) {
+  float2* const cs = s_cs[warp];
+#pragma unroll
+  for (int k = 0; k < HALF / 32; ++k) {
+    const int j = lane + 32 * k;
     const unsigned long long t = (unsigned long long)pos * a.turn[j];
     float sn = 0.f, c = 1.f;
     if (a.rotate) sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &sn, &c);
     cs[j] = make_float2(c, sn);
   }
-  __syncthreads();
-  const int lane = threadIdx.x & 31, l = lane % LPH;
-  const int nw = blockDim.x >> 5;
-  for (int h0 = (threadIdx.x >> 5) * HPW; h0 < a.heads; h0 += nw * HPW) {
-    const int hh = h0 + lane / LPH;
-    const bool ok = hh < a.heads;
-    const int t = hh >= a.hq, h = t ? hh - a.hq : hh;
-    float x[8], y[8];
-    if (ok) {
-      const uint16_t* p = a.x[t] + (int64_t)row * a.stride[t] + h * D + l * 8;
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const uint4 v = *reinterpret_cast<const uint4*>(p + HALF);
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+  __syncwarp();
+  float4 rot[4];                          // cosine and sine of two pairs each
+#pragma unroll
+  for (int i = 0; i < 4; ++i) rot[i] = *reinterpret_cast<const float4*>(&cs[l * 8 + 2 * i]);
+  uint4 wq[2], wk[2];                     // the lane's weights
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    wq[h] = wk[h] = make_uint4(0, 0, 0, 0);
+    if (a.weight[0])
+      wq[h] = __ldg(reinterpret_cast<const uint4*>(a.weight[0] + h * HALF + l * 8));
+    if (a.weight[1])
+      wk[h] = __ldg(reinterpret_cast<const uint4*>(a.weight[1] + h * HALF + l * 8));
+  }
+  for (int gr = g0; gr < g1; gr += NB) {
+    if (gr > g0) load(gr);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      if (gr + k >= g1) break;
+      const int hh = (gr + k) * HPW + sub;
+      const bool is_k = hh >= a.hq;
+      const uint32_t uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      const uint32_t vw[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      float x[8], y[8], sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(uw[i] << 16);
@@ -75,42 +130,37 @@ __global__ void __launch_bounds__(256) qk_norm_rope(const NormRopeKArgs a) {
         y[2 * i] = __uint_as_float(vw[i] << 16);
         y[2 * i + 1] = __uint_as_float(vw[i] & 0xffff0000u);
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-    }
-    float sum = 0.f;
+      for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
+      for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (is_k ? a.weight[1] != nullptr : a.weight[0] != nullptr) {
+        const float r = 1.f / sqrtf(sum * (1.f / D) + a.eps);
+        const uint4 w0 = is_k ? wk[0] : wq[0], w1 = is_k ? wk[1] : wq[1];
+        const uint32_t p0[4] = {w0.x, w0.y, w0.z, w0.w}, p1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!ok) continue;
-    if (a.weight[t]) {
-      const float r = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(a.weight[t] + l * 8));
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.weight[t] + HALF + l * 8));
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] *= r * __uint_as_float(p0[i] << 16);
+          x[2 * i + 1] *= r * __uint_as_float(p0[i] & 0xffff0000u);
+          y[2 * i] *= r * __uint_as_float(p1[i] << 16);
+          y[2 * i + 1] *= r * __uint_as_float(p1[i] & 0xffff0000u);
+        }
+      }
+      uint32_t lo[4], hi[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[2 * i] *= r * __uint_as_float(uw[i] << 16);
-        x[2 * i + 1] *= r * __uint_as_float(uw[i] & 0xffff0000u);
-        y[2 * i] *= r * __uint_as_float(vw[i] << 16);
-        y[2 * i + 1] *= r * __uint_as_float(vw[i] & 0xffff0000u);
+        const float4 c = rot[i];
+        lo[i] = ptx::pack_bf16x2(x[2 * i] * c.x - y[2 * i] * c.y,
+                                 x[2 * i + 1] * c.z - y[2 * i + 1] * c.w);
+        hi[i] = ptx::pack_bf16x2(x[2 * i] * c.y + y[2 * i] * c.x,
+                                 x[2 * i + 1] * c.w + y[2 * i + 1] * c.z);
+      }
+      if (hh < a.heads) {
+        uint16_t* p = dst(hh);
+        *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(p + HALF) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       }
     }
-    uint32_t lo[4], hi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 c = *reinterpret_cast<const float4*>(&cs[l * 8 + 2 * i]);
-      const float a0 = x[2 * i], b0 = y[2 * i], a1 = x[2 * i + 1], b1 = y[2 * i + 1];
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-          : "=r"(lo[i]) : "f"(a1 * c.z - b1 * c.w), "f"(a0 * c.x - b0 * c.y));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-          : "=r"(hi[i]) : "f"(a1 * c.w + b1 * c.z), "f"(a0 * c.y + b0 * c.x));
-    }
-    uint16_t* p = a.out[t] + (int64_t)row * a.out_stride[t] + h * D + l * 8;
-    *reinterpret_cast<uint4*>(p) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(p + HALF) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
 }
 
@@ -134,21 +184,30 @@ cudaError_t launch_norm_rope(const ds_norm_rope_args& g, cudaStream_t stream) {
   a.rotate = g.rope_base > 0.f || g.inv_freq != nullptr;
   a.status = static_cast<uint32_t*>(g.workspace);
   // a double's 53 bits leave each frequency (at most a radian in use) off by
-  // less than 2^-54 of a turn, and the angle, at positions below 2^31, by
-  // less than 2^-23 of one; at 2^17 by less than 2^-37
+  // less than 2^-53 of a turn, and the angle, at positions below 2^31, by
+  // less than 2^-22 of one; at 2^17 by less than 2^-36
+  // (base^(-2j/D) as a product of two powers: sixteen calls of pow, not 64)
+  double lo[8], hi[8];
+  if (a.rotate && !g.inv_freq)
+    for (int k = 0; k < 8; ++k) {
+      lo[k] = std::pow((double)g.rope_base, -2.0 * k / g.head_dim);
+      hi[k] = std::pow((double)g.rope_base, -16.0 * k / g.head_dim) / 6.283185307179586;
+    }
   for (int j = 0; j < 64; ++j) {
     a.turn[j] = 0ull;
     if (a.rotate && j < g.head_dim / 2) {
-      const double f = g.inv_freq ? g.inv_freq[j]
-                                  : std::pow((double)g.rope_base, -2.0 * j / g.head_dim);
-      const double turns = f / 6.283185307179586;
+      const double turns =
+          g.inv_freq ? g.inv_freq[j] / 6.283185307179586 : lo[j & 7] * hi[j >> 3];
       const double frac = turns - std::floor(turns);   // whole turns drop out
-      a.turn[j] = frac < 1.0 ? (unsigned long long)std::ldexp(frac, 64) : 0ull;
+      a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
     }
   }
-  const int hpw = 32 / (g.head_dim / 16);
-  const int warps = std::max(1, std::min(8, (a.heads + hpw - 1) / hpw));
-  const dim3 grid(g.n_rows), block(32 * warps);
+  // enough warps to fill the machine (152 SMs of 24), a head group a warp at
+  // least
+  const int hpw = 32 / (g.head_dim / 16), groups = (a.heads + hpw - 1) / hpw;
+  a.slices = std::max(1, std::min(groups, 152 * 24 / g.n_rows));
+  const int64_t warps = (int64_t)g.n_rows * a.slices;
+  const dim3 grid((unsigned)((warps + kNormWarps - 1) / kNormWarps)), block(32 * kNormWarps);
   if (g.head_dim == 128) return launch_dependent(qk_norm_rope<128>, grid, block, 0, stream, a);
   return launch_dependent(qk_norm_rope<64>, grid, block, 0, stream, a);
 }
