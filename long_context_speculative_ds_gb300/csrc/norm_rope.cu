@@ -32,30 +32,29 @@ struct NormRopeKArgs {
   int32_t n_rows, hq, heads;      // heads = query + key heads
   float eps;
   int32_t rotate;
-  int32_t slices;                 // warps that share a row's heads
+  int32_t per;                    // head groups of a warp
   uint32_t* status;
   // frequency j as a 64-bit fraction of a turn
   unsigned long long turn[64];
 };
 
 constexpr int kNormWarps = 8;             // warps of a block
+constexpr int kNormBatch = 5;             // head groups of a warp, their loads together
 
 template <int D>
-__global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope(const NormRopeKArgs a) {
+__global__ void __launch_bounds__(32 * kNormWarps, 3) qk_norm_rope(const NormRopeKArgs a) {
   constexpr int HALF = D / 2;
   constexpr int LPH = HALF / 8;           // lanes of a head
   constexpr int HPW = 32 / LPH;           // heads of a warp at a time
-  constexpr int NB = 5;                   // head groups on their way at once
   __shared__ __align__(16) float2 s_cs[kNormWarps][HALF];
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kNormWarps + warp;
-  const int row = (int)(w / a.slices);
-  if (row >= a.n_rows) return;
+  const int64_t row64 = (int64_t)blockIdx.x * kNormWarps + warp;
+  if (row64 >= a.n_rows) return;
+  const int row = (int)row64;
   const int groups = (a.heads + HPW - 1) / HPW;
-  const int per = (groups + a.slices - 1) / a.slices;
-  const int g0 = (int)(w - (int64_t)row * a.slices) * per, g1 = min(groups, g0 + per);
+  const int g0 = blockIdx.y * a.per, g1 = min(groups, g0 + a.per);
   if (g0 >= g1) return;
   const int pos = __ldg(a.positions + row);
   const int l = lane % LPH, sub = lane / LPH;
@@ -70,21 +69,18 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope(const NormRopeKA
     return (t ? a.out[1] + (int64_t)row * a.out_stride[1] - (int64_t)a.hq * D
               : a.out[0] + (int64_t)row * a.out_stride[0]) + (int64_t)hh * D + l * 8;
   };
-  uint4 u[NB], v[NB];
-  auto load = [&](int gr0) {
+  uint4 u[kNormBatch], v[kNormBatch];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int hh = (gr0 + k) * HPW + sub;
-      u[k] = v[k] = make_uint4(0, 0, 0, 0);
-      if (gr0 + k < g1 && hh < a.heads) {
-        // plain loads: with q_out = q the same bytes are written below
-        const uint16_t* p = src(hh);
-        u[k] = *reinterpret_cast<const uint4*>(p);
-        v[k] = *reinterpret_cast<const uint4*>(p + HALF);
-      }
+  for (int k = 0; k < kNormBatch; ++k) {
+    const int hh = (g0 + k) * HPW + sub;
+    u[k] = v[k] = make_uint4(0, 0, 0, 0);
+    if (g0 + k < g1 && hh < a.heads) {
+      // plain loads: with q_out = q the same bytes are written below
+      const uint16_t* p = src(hh);
+      u[k] = *reinterpret_cast<const uint4*>(p);
+      v[k] = *reinterpret_cast<const uint4*>(p + HALF);
     }
-  };
-  load(g0);
+  }
   if (pos < 0) {
     if (lane == 0) flag(a.status, DS_DEV_BAD_LENGTH);
     return;
@@ -104,22 +100,10 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope(const NormRopeKA
   float4 rot[4];                          // cosine and sine of two pairs each
 #pragma unroll
   for (int i = 0; i < 4; ++i) rot[i] = *reinterpret_cast<const float4*>(&cs[l * 8 + 2 * i]);
-  uint4 wq[2], wk[2];                     // the lane's weights
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    wq[h] = wk[h] = make_uint4(0, 0, 0, 0);
-    if (a.weight[0])
-      wq[h] = __ldg(reinterpret_cast<const uint4*>(a.weight[0] + h * HALF + l * 8));
-    if (a.weight[1])
-      wk[h] = __ldg(reinterpret_cast<const uint4*>(a.weight[1] + h * HALF + l * 8));
-  }
-  for (int gr = g0; gr < g1; gr += NB) {
-    if (gr > g0) load(gr);
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      if (gr + k >= g1) break;
-      const int hh = (gr + k) * HPW + sub;
-      const bool is_k = hh >= a.hq;
+  for (int k = 0; k < kNormBatch; ++k) {
+    if (g0 + k < g1) {
+      const int hh = (g0 + k) * HPW + sub;
       const uint32_t uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
       const uint32_t vw[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       float x[8], y[8], sum = 0.f;
@@ -134,9 +118,11 @@ __global__ void __launch_bounds__(32 * kNormWarps) qk_norm_rope(const NormRopeKA
       for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], fmaf(y[i], y[i], sum));
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (is_k ? a.weight[1] != nullptr : a.weight[0] != nullptr) {
+      const uint16_t* const w = hh >= a.hq ? a.weight[1] : a.weight[0];
+      if (w) {
         const float r = 1.f / sqrtf(sum * (1.f / D) + a.eps);
-        const uint4 w0 = is_k ? wk[0] : wq[0], w1 = is_k ? wk[1] : wq[1];
+        const uint4 w0 = __ldg(reinterpret_cast<const uint4*>(w + l * 8));
+        const uint4 w1 = __ldg(reinterpret_cast<const uint4*>(w + HALF + l * 8));
         const uint32_t p0[4] = {w0.x, w0.y, w0.z, w0.w}, p1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -202,12 +188,15 @@ cudaError_t launch_norm_rope(const ds_norm_rope_args& g, cudaStream_t stream) {
       a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
     }
   }
-  // enough warps to fill the machine (152 SMs of 24), a head group a warp at
-  // least
+  // at most kNormBatch head groups a warp, fewer (down to one) while that
+  // fills the machine (152 SMs of 24 warps)
   const int hpw = 32 / (g.head_dim / 16), groups = (a.heads + hpw - 1) / hpw;
-  a.slices = std::max(1, std::min(groups, 152 * 24 / g.n_rows));
-  const int64_t warps = (int64_t)g.n_rows * a.slices;
-  const dim3 grid((unsigned)((warps + kNormWarps - 1) / kNormWarps)), block(32 * kNormWarps);
+  const int slices = std::max((groups + kNormBatch - 1) / kNormBatch,
+                              std::min(groups, 152 * 24 / g.n_rows));
+  a.per = (groups + slices - 1) / slices;
+  const dim3 grid((unsigned)(((int64_t)g.n_rows + kNormWarps - 1) / kNormWarps),
+                  (unsigned)((groups + a.per - 1) / a.per));
+  const dim3 block(32 * kNormWarps);
   if (g.head_dim == 128) return launch_dependent(qk_norm_rope<128>, grid, block, 0, stream, a);
   return launch_dependent(qk_norm_rope<64>, grid, block, 0, stream, a);
 }
