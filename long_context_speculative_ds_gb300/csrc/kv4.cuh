@@ -57,48 +57,65 @@ DS_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
   return ptx::pack_f16x2(clamp(__uint_as_float(w << 16)), clamp(__uint_as_float(w & 0xffff0000u)));
 }
 
-// Sixteen values, already multiplied by 2^-exp, as one scale byte and eight
-// bytes of codes.  `bad` is set when a value is a NaN (stored as 0) or an
-// infinity.
+// Sixteen bf16 values (eight words, in order) times `mult` = 2^-exp as one
+// scale byte and eight bytes of codes.  `bad` is set when a value is a NaN
+// (stored as 0) or an infinity.
 //
-// The quotients y / scale only decide between neighbouring e2m1 values, and
-// so does the scale's own rounding.  y has 8 significant bits and scale x
-// midpoint at most 7, so a quotient that is not exactly a midpoint is off it
-// by at least one part in 255: y times the rounded reciprocal, rounded once
-// more to f16 (11 bits), is the midpoint when the true quotient is, and on
-// its side of it otherwise.
-DS_DEV void kv4_quantise16(float (&y)[16], uint32_t& scale_byte, uint2& codes, bool& bad) {
-  float mx = 0.f;
-  bad = false;
+// Both roundings only decide between neighbouring values of a small format,
+// and an inexact quotient must not move one that lies on a midpoint.  x has 8
+// significant bits; a midpoint of the codes times a scale has at most 7, and
+// one of the scales times 6 at most 7 as well, so a quotient that is not a
+// midpoint is off it by at least one part in 255.  The quotients are formed
+// as products with a rounded reciprocal (off by 2^-23 of themselves) and then
+// rounded to a grid that holds every midpoint: the maximum's sixth to f16's
+// 11 bits, the others to multiples of 2^-11 by adding and subtracting 6144.
+// On the grid a midpoint is met exactly, and nothing else reaches one.
+DS_DEV void kv4_quantise16(uint32_t (&w)[8], float mult, uint32_t& scale_byte, uint2& codes,
+                           bool& bad) {
+  auto top = [&]() {               // the largest magnitude, NaN if there is one
+    uint32_t m = w[0] & 0x7fff7fffu;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (!(fabsf(y[i]) < INFINITY)) bad = true;
-    if (y[i] != y[i]) y[i] = 0.f;
-    mx = fmaxf(mx, fabsf(y[i]));
+    for (int i = 1; i < 8; ++i)
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i] & 0x7fff7fffu));
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(m >> 16 | m << 16));
+    return __uint_as_float(r << 16);
+  };
+  float mx = top();
+  bad = !(mx < INFINITY);
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((w[i] & 0x7fffu) > 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7fff0000u) > 0x7f800000u) w[i] &= 0xffffu;
+    }
+    mx = top();
   }
-  const float sf = fminf(__fdiv_rn(mx, 6.f), 448.f);
-  uint16_t sb;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sb) : "f"(0.f), "f"(sf));
-  scale_byte = sb & 0xffu;
+  const float sf = fminf(mx * mult * 0.16666667f, 448.f);
   uint32_t s2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"(sb));
+  uint16_t sb;
+  asm("{\n\t.reg .b32 h;\n\tcvt.rn.f16x2.f32 h, %2, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, %0;\n\t}"
+      : "=h"(sb), "=r"(s2)
+      : "f"(0.f), "f"(sf));
+  scale_byte = sb & 0xffu;
   const float s = __half2float(__ushort_as_half((unsigned short)(s2 & 0xffffu)));
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t w[2] = {0u, 0u};
+  const float inv = s > 0.f ? __frcp_rn(s) * mult : 0.f;
+  uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    // at most 6.4 unless the scale was cut at 448: clamped before f16
-    const float a = fminf(fmaxf(y[i] * inv, -8.f), 8.f);
-    const float b = fminf(fmaxf(y[i + 1] * inv, -8.f), 8.f);
-    const float2 q = __half22float2(__floats2half2_rn(a, b));
-    uint32_t byte;
+  for (int i = 0; i < 8; ++i) {
+    const float lo = fmaf(__uint_as_float(w[i] << 16), inv, 6144.f) - 6144.f;
+    const float hi = fmaf(__uint_as_float(w[i] & 0xffff0000u), inv, 6144.f) - 6144.f;
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
         "cvt.u32.u8 %0, t;\n\t}"
-        : "=r"(byte)
-        : "f"(q.y), "f"(q.x));
-    w[i >> 3] |= byte << (4 * (i & 7));
+        : "=r"(b[i])
+        : "f"(hi), "f"(lo));
   }
-  codes = make_uint2(w[0], w[1]);
+  auto pack = [](uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+    return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+  };
+  codes = make_uint2(pack(b[0], b[1], b[2], b[3]), pack(b[4], b[5], b[6], b[7]));
 }
 
 }  // namespace ds

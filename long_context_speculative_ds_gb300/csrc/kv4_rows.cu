@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(256) kv4_rows(const Kv4RowsKArgs a) {
   constexpr int CH = WRITE ? 16 : 8;      // channels of a lane
   constexpr int LPH = D / CH;             // lanes of a head
   constexpr int RW = 32 / LPH;            // rows of a warp
-  constexpr int NB = WRITE ? 4 : 8;       // units on their way at once
+  constexpr int NB = WRITE ? 3 : 8;       // units on their way at once
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -160,19 +160,12 @@ __global__ void __launch_bounds__(256) kv4_rows(const Kv4RowsKArgs a) {
       for (int k = 0; k < NB; ++k)
         if (u + k < u1) {
           const int t = (u + k) & 1, h = (u + k) >> 1;
-          const uint32_t r[8] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w,
-                                 hi[k].x, hi[k].y, hi[k].z, hi[k].w};
-          const float mult = t ? a.mult[1] : a.mult[0];
-          float y[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[2 * i] = __uint_as_float(r[i] << 16) * mult;
-            y[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u) * mult;
-          }
+          uint32_t r[8] = {lo[k].x, lo[k].y, lo[k].z, lo[k].w,
+                           hi[k].x, hi[k].y, hi[k].z, hi[k].w};
           uint32_t sb;
           uint2 codes;
           bool bad;
-          kv4_quantise16(y, sb, codes, bad);
+          kv4_quantise16(r, t ? a.mult[1] : a.mult[0], sb, codes, bad);
           any_bad |= bad;
           uint8_t* const c = (t ? a.cache[1] : a.cache[0]) + (int64_t)h * blk;
           *reinterpret_cast<uint2*>(c + code0) = codes;

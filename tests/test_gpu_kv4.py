@@ -263,6 +263,36 @@ def test_write_ties_nan_and_inf():
     np.testing.assert_array_equal(got[pg, :8], want[pg, :8])
 
 
+def test_write_every_pair_of_significands():
+    """Groups of a maximum and fifteen smaller values, over every pair of
+    bf16 significands: all quotients that can meet or miss a midpoint."""
+    P, d, heads = 128, 128, 8
+    sig = torch.arange(128, 256).double()
+    rel = 2.0 ** -torch.arange(7).double()
+    x = (sig.view(1, -1, 1) * rel.view(1, 1, -1)).expand(128, -1, -1).reshape(128, -1)
+    x = torch.where(x <= sig.view(-1, 1), x, x / 2)          # at most the maximum
+    n = -(-x.shape[1] // 15)
+    x = torch.nn.functional.pad(x, (0, 15 * n - x.shape[1])).view(128, n, 15)
+    sign = torch.where(torch.arange(15) % 2 == 0, 1.0, -1.0)
+    g = torch.cat([sig.view(128, 1, 1).expand(-1, n, 1), x * sign], -1).view(-1, 16)
+    rows = -(-g.shape[0] // (heads * d // 16))
+    g = torch.nn.functional.pad(g, (0, 0, 0, rows * heads * d // 16 - g.shape[0]))
+    for e in (-7, 0, 3):
+        rowsv = (g * 2.0 ** e).view(rows, heads, d).bfloat16()
+        c = Cache([rows], heads, d, P)
+        ws = status_word()
+        com = (c.k, c.v, c.dtable, i32([0]), i32([0, rows]))
+        r = rowsv.to(DEV)
+        B.ds_kv4_write(B.kv4_rows_args(r, r, *com, page_size=P, workspace=ws))
+        out = torch.empty(2, rows, heads, d, dtype=torch.bfloat16, device=DEV)
+        B.ds_kv4_read(B.kv4_rows_args(out[0], out[1], *com, page_size=P, workspace=ws))
+        assert B.ds_device_status(ws) == 0
+        code, sb = kv4.quantise(f64(rowsv), 0)
+        want = kv4.E2M1[code & 7] * np.where(code & 8, -1, 1) * kv4.E4M3[sb].repeat(16, -1)
+        np.testing.assert_array_equal(f64(out[0]), want)
+        np.testing.assert_array_equal(f64(out[1]), want)
+
+
 def test_commit_path():
     """Rows of accepted nodes go behind the root; bad paths commit the root."""
     heads, d, P = 2, 64, 16
