@@ -70,7 +70,8 @@ struct Cfg {
   static constexpr int kRing = kStages * 2 * kTensor;     // bytes of a warp's ring
   static constexpr size_t smem = (size_t)W * kRing;
   static_assert(kStages == 3, "a block in use, the next one's scores, one on its way");
-  static_assert(R * D * 4 <= kRing, "a warp's output must fit in its ring");
+  static constexpr int kOutStride = D + 8;          // floats of a row of a warp's output
+  static_assert(R * kOutStride * 4 <= kRing, "a warp's output must fit in its ring");
 };
 
 // One piece of a segment: units [u0, u1).
@@ -91,7 +92,6 @@ struct Ctrl {
   float m[16][16], l[16][16];    // [warp][row]
   Piece cut[2];                  // pieces of cut segments: at most the range's two ends
   int n_cut, last[2];
-  float lse[32];                 // rows being merged
 };
 
 DS_DEV void cp16(uint32_t dst, const void* src, uint32_t bytes) {   // bytes 0: zeros
@@ -606,7 +606,10 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   __syncwarp();
 
   // --------------------------------------------- merge of the block's warps
-  float* ow = reinterpret_cast<float*>(smem + warp * C_::kRing);   // [row][D]
+  // A warp's output in its ring: rows of D + 8 floats, dims 2j and 2j + 1 of
+  // lane group g at 16 j + 2 g, so that a store's 32 lanes touch all banks.
+  constexpr int ST = C_::kOutStride;
+  float* ow = reinterpret_cast<float*>(smem + warp * C_::kRing);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -620,41 +623,47 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
         ctrl.l[warp][r] = x;
       }
       // tile j: dims g D/8 + 2j (elements 0, 1) and the next (2, 3)
-      if (r < rows) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-          *reinterpret_cast<float2*>(ow + r * D + g * (D / 8) + 2 * j) =
-              make_float2(o[n][j][e], o[n][j][e + 2]);
-      }
+      for (int j = 0; j < NS; ++j)
+        *reinterpret_cast<float2*>(ow + r * ST + 16 * j + 2 * g) =
+            make_float2(o[n][j][e], o[n][j][e + 2]);
     }
   __syncthreads();
-  auto put = [&](void* dst, int64_t at, float x) {
-    if (a.out_f32) static_cast<float*>(dst)[at] = x;
-    else static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(x);
-  };
+  // a warp per row: the warps' weights (in place of their maxima) and the
+  // row's log2-sum-exp
   const int used = min(W, n_units);                 // warps that had a unit
-  for (int x = threadIdx.x; x < rows * D; x += 32 * W) {
-    const int r = x / D;
-    float mm = -CUDART_INF_F;
-    for (int w = 0; w < used; ++w) mm = fmaxf(mm, ctrl.m[w][r]);
-    const float mb0 = mm == -CUDART_INF_F ? 0.f : mm;
-    float sum = 0.f, acc = 0.f;
-#pragma unroll 4
+  for (int r = warp; r < rows; r += W) {
+    const float mw = lane < used ? ctrl.m[lane][r] : -CUDART_INF_F;
+    const float lw = lane < used ? ctrl.l[lane][r] : 0.f;
+    const float mm = warp_max(mw);
+    const float f = ex2(mw - (mm == -CUDART_INF_F ? 0.f : mm));
+    const float sum = warp_sum(f * lw);
+    if (lane < used) ctrl.m[lane][r] = f * (sum > 0.f ? ka.out_mult / sum : 0.f);
+    if (lane == 0) {
+      const float lse = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
+      if (pc.n_slots == 1) row_lse[r] = lse;
+      else a.lse_part[(int64_t)pc.slot * R + r] = lse;
+    }
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < rows * (D / 2); x += 32 * W) {
+    const int r = x / (D / 2), c = x % (D / 2);     // columns 2c and 2c + 1
+    const float* src = reinterpret_cast<const float*>(smem) + r * ST +
+                       c % (D / 16) * 16 + c / (D / 16) * 2;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 8
     for (int w = 0; w < used; ++w) {
-      const float f = ex2(ctrl.m[w][r] - mb0);
-      sum = fmaf(f, ctrl.l[w][r], sum);
-      acc = fmaf(f, reinterpret_cast<const float*>(smem + w * C_::kRing)[x], acc);
+      const float f = ctrl.m[w][r];
+      const float2 v = *reinterpret_cast<const float2*>(src + w * (C_::kRing / 4));
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
     }
-    const float inv = sum > 0.f ? ka.out_mult / sum : 0.f;
-    const float lse = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
-    if (pc.n_slots == 1) {
-      put(a.out, out_row(r) * D + x % D, acc * inv);
-      if (x % D == 0) row_lse[r] = lse;
-    } else {
-      const int64_t row = (int64_t)pc.slot * R + r;
-      put(a.o_part, row * D + x % D, acc * inv);
-      if (x % D == 0) a.lse_part[row] = lse;
-    }
+    void* const dst = pc.n_slots == 1 ? a.out : static_cast<void*>(a.o_part);
+    const int64_t at = (pc.n_slots == 1 ? out_row(r) : (int64_t)pc.slot * R + r) * D + 2 * c;
+    if (a.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(dst) + at) = acc;
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(dst) + at) = pack_bf16x2(acc.x, acc.y);
   }
   if (pc.n_slots > 1 && threadIdx.x == 0) ctrl.cut[ctrl.n_cut++] = pc;
   __syncthreads();                 // the ring and ctrl are the next piece's
@@ -677,8 +686,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
     __syncwarp();
     more = next >= 0 && find_piece<R, W>(ka.v.plan, next, &pc);
   }
-  // The last piece of a cut segment to finish merges them: a warp per row for
-  // the log2-sum-exp, then a thread per two columns for the output.
+  // The last piece of a cut segment to finish merges them.
   const int n_cut = ctrl.n_cut;
   if (n_cut == 0) return;
   const VerifyKArgs& a = ka.v;
@@ -699,43 +707,27 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
   };
   const int n0 = rows_of(0), n1 = rows_of(1);
   if (n0 + n1 == 0) return;
-  const int lane = threadIdx.x & 31, G = a.plan.group;
-  for (int x = warp; x < n0 + n1; x += W) {
-    const Piece& c = ctrl.cut[x >= n0];
-    const int r = x >= n0 ? x - n0 : x;
-    const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
-    float mm = -CUDART_INF_F, sum = 0.f;
-    for (int k = lane; k < c.n_slots; k += 32) {
-      const float v = __ldcg(lp + (int64_t)k * R);
-      const float nm = fmaxf(mm, v), mb = nm == -CUDART_INF_F ? 0.f : nm;
-      sum = sum * ptx::ex2(mm - mb) + ptx::ex2(v - mb);
-      mm = nm;
-    }
-    const float top = warp_max(mm), mb = top == -CUDART_INF_F ? 0.f : top;
-    sum = warp_sum(sum * ptx::ex2(mm - mb));
-    if (lane == 0) {
-      const float lse = sum > 0.f ? top + __log2f(sum) : -CUDART_INF_F;
-      ctrl.lse[x] = lse;
-      a.row_lse[((int64_t)c.kvh * a.plan.n_nodes + c.node0) * G + c.rgi * R + r] = lse;
-    }
-  }
-  __syncthreads();
+  // a thread per two columns of a row; the pieces' log2-sum-exps and outputs
+  // come in one round trip, NB at a time
+  const int G = a.plan.group;
   const auto columns = [&](auto f32) {
     constexpr bool F32 = decltype(f32)::value;
-    constexpr int NB = 20;         // pieces on their way at once
+    constexpr int NB = 20;
     for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
       const int y = x / (D / 2), col = x % (D / 2) * 2;
       const Piece& c = ctrl.cut[y >= n0];
       const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r, ns = c.n_slots;
-      const float lse = ctrl.lse[y];
       const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
       const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
+      float mm = -CUDART_INF_F, sum = 0.f;
       float2 acc = make_float2(0.f, 0.f);
       for (int k0 = 0; k0 < ns; k0 += NB) {
         float w[NB];
         float2 v[NB];
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
+          w[k] = -CUDART_INF_F;
+          v[k] = make_float2(0.f, 0.f);
           if (k0 + k >= ns) continue;
           const int64_t at = o + (int64_t)(k0 + k) * R * D;
           w[k] = __ldcg(lp + (int64_t)(k0 + k) * R);
@@ -747,22 +739,35 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
             v[k] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
           }
         }
+        float nm = mm;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) nm = fmaxf(nm, w[k]);
+        const float mb = nm == -CUDART_INF_F ? 0.f : nm, f = ptx::ex2(mm - mb);
+        mm = nm;
+        sum *= f;
+        acc.x *= f;
+        acc.y *= f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          if (k0 + k >= ns) continue;
-          // a row that saw nothing but NaN has log2-sum-exps of -inf: NaN stays
-          const float e = ptx::ex2(w[k] - lse);
+          const float e = ptx::ex2(w[k] - mb);
+          sum += e;
+          // a piece that saw nothing wrote zeros, or NaN for a query that is
+          // not a number; that stays
           acc.x = fmaf(e, v[k].x, acc.x);
           acc.y = fmaf(e, v[k].y, acc.y);
         }
       }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int64_t row = ((int64_t)c.kvh * a.plan.n_nodes + c.node0) * G + grow;
+      if (col == 0) a.row_lse[row] = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
       const int64_t at =
           (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
       if constexpr (F32)
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = acc;
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) =
+            make_float2(acc.x * inv, acc.y * inv);
       else
         *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
-            ptx::pack_bf16x2(acc.x, acc.y);
+            ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
     }
   };
   if (a.out_f32) columns(std::true_type{});
