@@ -64,11 +64,15 @@ constexpr int kPieceUnits = 40;
 
 template <int D, int NT>
 struct Cfg {
-  static constexpr int W = NT == 1 ? 16 : 8;        // warps of a block
+  static constexpr int W = NT == 1 ? 16 : 12;       // warps of a block
   static constexpr int R = 8 * NT;                  // query rows of one pass
   static constexpr int kTensor = kBlock * (D / 2 + D / 16);   // bytes of a block's K or V
   static constexpr int kRing = kStages * 2 * kTensor;     // bytes of a warp's ring
-  static constexpr size_t smem = (size_t)W * kRing;
+  // With two tiles of queries the fragments of both do not fit beside their
+  // outputs in the registers of 12 warps: the queries stay in shared memory,
+  // in fragment order, and the scores are not formed a block ahead.
+  static constexpr bool kQShared = NT > 1;
+  static constexpr size_t smem = (size_t)W * kRing + (kQShared ? R * D * 2 : 0);
   static_assert(kStages == 3, "a block in use, the next one's scores, one on its way");
   static constexpr int kOutStride = D + 8;          // floats of a row of a warp's output
   static_assert(R * kOutStride * 4 <= kRing, "a warp's output must fit in its ring");
@@ -259,15 +263,20 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
     const int grow = pc.rgi * R + r;
     return ((int64_t)pc.node0 + grow / G) * a.num_q_heads + pc.kvh * G + grow % G;
   };
-  // queries: column g of tile n is row 8 n + g
-  uint4 qx[NT][D / 32];
+  // queries: column g of tile n is row 8 n + g; the fragments of step s are
+  // channels t D/4 + 4 s .. + 3
+  constexpr bool QS = C_::kQShared;
+  constexpr int QT = QS ? 1 : NT;                   // tiles kept in registers
+  uint4 qx[QT][D / 32];
+  if constexpr (!QS) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = 8 * n + g;
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(r) * D + t * (D / 4));
+    for (int n = 0; n < QT; ++n) {
+      const int r = 8 * n + g;
+      const uint4* src = reinterpret_cast<const uint4*>(a.q + out_row(r) * D + t * (D / 4));
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w)
-      qx[n][w] = r < rows ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+      for (int w = 0; w < D / 32; ++w)
+        qx[n][w] = r < rows ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+    }
   }
   // ancestor masks, when the piece holds tree keys; a tree of one node has
   // only itself
@@ -354,16 +363,31 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
-  uint32_t q[NT][NS][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {              // 8 channels: steps 2w, 2w + 1
-      q[n][2 * w][0] = bf16x2_to_f16x2(qx[n][w].x);
-      q[n][2 * w][1] = bf16x2_to_f16x2(qx[n][w].y);
-      q[n][2 * w + 1][0] = bf16x2_to_f16x2(qx[n][w].z);
-      q[n][2 * w + 1][1] = bf16x2_to_f16x2(qx[n][w].w);
+  uint32_t q[QT][NS][2];
+  const uint32_t q_smem = smem_addr(smem) + W * C_::kRing + lane * 8;
+  if constexpr (QS) {
+    for (int x = threadIdx.x; x < NT * NS * 32; x += 32 * W) {      // (tile, step, lane)
+      const int r = 8 * (x / (NS * 32)) + ((x & 31) >> 2);
+      const int c = (x & 3) * (D / 4) + (x >> 5) % NS * 4;
+      uint2 v = make_uint2(0, 0);
+      if (r < rows) v = __ldg(reinterpret_cast<const uint2*>(a.q + out_row(r) * D + c));
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                       smem_addr(smem) + W * C_::kRing + x * 8),
+                   "r"(bf16x2_to_f16x2(v.x)), "r"(bf16x2_to_f16x2(v.y))
+                   : "memory");
     }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int n = 0; n < QT; ++n)
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {            // 8 channels: steps 2w, 2w + 1
+        q[n][2 * w][0] = bf16x2_to_f16x2(qx[n][w].x);
+        q[n][2 * w][1] = bf16x2_to_f16x2(qx[n][w].y);
+        q[n][2 * w + 1][0] = bf16x2_to_f16x2(qx[n][w].z);
+        q[n][2 * w + 1][1] = bf16x2_to_f16x2(qx[n][w].w);
+      }
+  }
   if (need_anc && T > 1) {
     __syncthreads();
 #pragma unroll
@@ -406,67 +430,81 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   // Scores of the block at ring offset `at`: s[n][hf][2h + e] is key 16 hf +
   // 8h + krow, row 8n + 2t + e.
   auto scores = [&](uint32_t at, float (&s)[NT][2][4]) {
+    uint32_t w[4][D / 32], sc[4][2];                // of the lane's four keys 8 x + krow
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t w[2][D / 32], sc[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k8 = 2 * hf + h;                // which eight keys
-        if constexpr (D == 128) {
-          const uint4 x = lds128(kcode + at + k8 * 8 * CB);
-          w[h][0] = x.x; w[h][1] = x.y; w[h][2] = x.z; w[h][3] = x.w;
-          const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + at + k8 * 8 * SB));
-          sc[h][0] = __byte_perm(s2, s2, 0x1010);
-          sc[h][1] = __byte_perm(s2, s2, 0x3232);
-        } else {
-          const uint2 x = lds64(kcode + at + k8 * 8 * CB);
-          w[h][0] = x.x; w[h][1] = x.y;
-          const uint32_t b = lds_u8(kscale + at + k8 * 8 * SB);
-          sc[h][0] = sc[h][1] = kv4_scales_f16(b | b << 8);
-        }
+    for (int x = 0; x < 4; ++x) {
+      if constexpr (D == 128) {
+        const uint4 y = lds128(kcode + at + x * 8 * CB);
+        w[x][0] = y.x; w[x][1] = y.y; w[x][2] = y.z; w[x][3] = y.w;
+        const uint32_t s2 = kv4_scales_f16(lds_u16(kscale + at + x * 8 * SB));
+        sc[x][0] = __byte_perm(s2, s2, 0x1010);
+        sc[x][1] = __byte_perm(s2, s2, 0x3232);
+      } else {
+        const uint2 y = lds64(kcode + at + x * 8 * CB);
+        w[x][0] = y.x; w[x][1] = y.y;
+        const uint32_t b = lds_u8(kscale + at + x * 8 * SB);
+        sc[x][0] = sc[x][1] = kv4_scales_f16(b | b << 8);
       }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s[n][x >> 2][x & 3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {              // 8 channels: steps 2k, 2k + 1
+      uint2 qs[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][hf][e] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (QS) qs[n][e] = lds64(q_smem + (n * NS + 2 * k + e) * 256);
+          else qs[n][e] = make_uint2(q[n][2 * k + e][0], q[n][2 * k + e][1]);
+        }
+      const int si = D == 128 ? k >> 1 : 0;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {          // 8 channels of each key
+      for (int hf = 0; hf < 2; ++hf) {
         uint32_t v0[4], v1[4];
-        kv4_codes_f16(w[0][k], v0);
-        kv4_codes_f16(w[1][k], v1);
-        const int si = D == 128 ? k >> 1 : 0;
+        kv4_codes_f16(w[2 * hf][k], v0);
+        kv4_codes_f16(w[2 * hf + 1][k], v1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v0[e] = hmul2(v0[e], sc[0][si]);
-          v1[e] = hmul2(v1[e], sc[1][si]);
+          v0[e] = hmul2(v0[e], sc[2 * hf][si]);
+          v1[e] = hmul2(v1[e], sc[2 * hf + 1][si]);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t fa[4] = {v0[2 * e], v1[2 * e], v0[2 * e + 1], v1[2 * e + 1]};
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(s[n][hf], fa, q[n][2 * k + e][0], q[n][2 * k + e][1]);
+          for (int n = 0; n < NT; ++n) mma16816(s[n][hf], fa, qs[n][e].x, qs[n][e].y);
         }
       }
     }
   };
-  // Software pipeline: the scores of block i + 1 are formed beside the
-  // softmax and the second product of block i, which depend on nothing of it,
-  // while block i + 2 is on its way.
-  cp_wait<kStages - 2>();
-  __syncwarp();
+  // Software pipeline (queries in registers): the scores of block i + 1 are
+  // formed beside the softmax and the second product of block i, which depend
+  // on nothing of it, while block i + 2 is on its way.
+  constexpr bool AHEAD = !QS;
   float s[NT][2][4];
-  scores(0, s);
+  if constexpr (AHEAD) {
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    scores(0, s);
+  }
   uint32_t st = 0;
 #pragma unroll 1
   for (int i = 0; i < nblk; ++i) {
+    if constexpr (!AHEAD) cp_wait<kStages - 2>();
     __syncwarp();                  // all lanes are done with block i - 1
     issue(i + kStages - 1);
-    cp_wait<kStages - 2>();
-    __syncwarp();
     const uint32_t st_next = st == (kStages - 1) * 2 * C_::kTensor ? 0u : st + 2 * C_::kTensor;
     float s_next[NT][2][4];
-    scores(st_next, s_next);       // after the last block: not used
+    if constexpr (AHEAD) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      scores(st_next, s_next);     // after the last block: not used
+    } else {
+      scores(st, s);
+    }
     const int key0 = key_of(2 * i);
     // ---------------------------------------------------------- softmax
     const bool tail = key0 + kBlock > L;
@@ -597,10 +635,12 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
       }
     }
     st = st_next;
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s[n][x >> 2][x & 3] = s_next[n][x >> 2][x & 3];
+        for (int x = 0; x < 8; ++x) s[n][x >> 2][x & 3] = s_next[n][x >> 2][x & 3];
+    }
   }
   cp_wait<0>();
   __syncwarp();
@@ -775,40 +815,47 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
 }
 
 // Chunk scores: the sum over kv heads and rows of 2^(mass - the row's
-// log2-sum-exp).  A block covers 32 chunks of a sequence, a lane each; warp w
-// the kv heads w, w + 8, ..., whose sums are added in that order.
+// log2-sum-exp).  A warp per chunk, lane-parallel over (kv head, subchunk,
+// row), NB loads of each kind on their way at once.
 __global__ void __launch_bounds__(256) kv4_scores_few(const VerifyKArgs a) {
-  __shared__ float part[8][32];
+  constexpr int NB = 4;
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * 8 + warp;
   // the lengths are inputs of the call: the split pass, which this launch
   // follows, has itself waited for whatever wrote them
   const SeqPlan sq = seq_sizes(a.plan, b, false);
-  grid_dep_wait();
-  grid_dep_launch_dependents();
   const int sub = min(kBlock, a.plan.chunk_size), per = a.plan.chunk_size / sub;
-  const int n_sub = (sq.L + sub - 1) / sub;       // of this sequence
+  const int k0 = c * per, n_k = min(per, (sq.L + sub - 1) / sub - k0);
+  const int per_head = n_k * sq.rows;             // a head's masses, consecutive
   const int64_t n_rows = (int64_t)a.plan.n_nodes * a.plan.group;
   const int64_t row0 = (int64_t)sq.node0 * a.plan.group;
-  const int64_t stride = (int64_t)a.plan.max_chunks * per;
+  const int64_t n_sub = (int64_t)a.plan.max_chunks * per;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (n_k <= 0 || c >= a.plan.max_chunks) return;
   float sum = 0.f;
-  for (int h = warp; h < a.plan.num_kv_heads; h += 8) {
-    const float* lse = a.row_lse + h * n_rows + row0;
-    const float* mass = a.clse + (h * n_rows + row0) * stride;
-    for (int k = c * per; k < min((c + 1) * per, n_sub); ++k) {
-      const float* mk = mass + (int64_t)k * sq.rows;
-#pragma unroll 4
-      for (int r = 0; r < sq.rows; ++r) sum += exp2f(__ldcg(mk + r) - __ldcg(lse + r));
-    }
-  }
-  part[warp][lane] = sum;
-  __syncthreads();
-  if (warp > 0 || c >= (sq.L + a.plan.chunk_size - 1) / a.plan.chunk_size) return;
-  sum = part[0][lane];
+  const int total = a.plan.num_kv_heads * per_head;
+  for (int x0 = lane; x0 < total; x0 += 32 * NB) {
+    float m[NB], l[NB];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) sum += part[w][lane];
-  float* dst = a.scores + (int64_t)b * a.plan.max_chunks + c;
-  *dst = a.accumulate ? *dst + sum : sum;
+    for (int k = 0; k < NB; ++k) {
+      const int x = x0 + 32 * k;
+      m[k] = l[k] = 0.f;
+      if (x < total) {
+        const int h = x / per_head, e = x - h * per_head;
+        m[k] = __ldcg(a.clse + (h * n_rows + row0) * n_sub + (int64_t)k0 * sq.rows + e);
+        l[k] = __ldcg(a.row_lse + h * n_rows + row0 + e % sq.rows);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+      if (x0 + 32 * k < total) sum += exp2f(m[k] - l[k]);
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) {
+    float* dst = a.scores + (int64_t)b * a.plan.max_chunks + c;
+    *dst = a.accumulate ? *dst + sum : sum;
+  }
 }
 
 template <int D, int NT>
@@ -825,7 +872,7 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
                                    dim3(32 * Cfg<D, NT>::W), smem, stream, k);
   if (e != cudaSuccess || !k.v.scores || k.v.plan.max_chunks == 0) return e;
   return launch_dependent(kv4_scores_few,
-                          dim3((k.v.plan.max_chunks + 31) / 32, k.v.plan.batch), dim3(256), 0,
+                          dim3((k.v.plan.max_chunks + 7) / 8, k.v.plan.batch), dim3(256), 0,
                           stream, k.v);
 }
 
