@@ -53,8 +53,11 @@ DS_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
 // A bf16 pair as an f16 pair: exact from 2^-14 up, rounded to 2^-24 below,
 // clamped to the largest f16 (a NaN stays one).
 DS_DEV uint32_t bf16x2_to_f16x2(uint32_t w) {
-  auto clamp = [](float x) { return x > 65504.f ? 65504.f : (x < -65504.f ? -65504.f : x); };
-  return ptx::pack_f16x2(clamp(__uint_as_float(w << 16)), clamp(__uint_as_float(w & 0xffff0000u)));
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;"
+      : "=r"(r)
+      : "f"(__uint_as_float(w & 0xffff0000u)), "f"(__uint_as_float(w << 16)));
+  return r;
 }
 
 // Sixteen bf16 values (eight words, in order) times `mult` = 2^-exp as one

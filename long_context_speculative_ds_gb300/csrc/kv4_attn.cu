@@ -73,9 +73,7 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
   ka.v4 = static_cast<const uint8_t*>(a.v_cache);
   ka.out_mult = ldexpf(1.f, a.v_exp);
   if (const int rows = kv4_few_rows(a)) return launch_kv4_few(ka, a.head_dim, rows, L, stream);
-  cudaError_t e = launch_kv4_split_tc(ka, a.head_dim, L, stream);
-  if (e != cudaSuccess) return e;
-  return launch_finish(k, a.head_dim, L.rg_max, a.batch, stream);
+  return launch_kv4_tc(ka, a.head_dim, L, stream);
 }
 
 }  // namespace ds

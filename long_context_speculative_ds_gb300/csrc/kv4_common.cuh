@@ -13,9 +13,9 @@ struct Kv4KArgs {
   float out_mult;                 // 2^v_exp
 };
 
-// Split pass for trees (kv4_tc.cu).
-cudaError_t launch_kv4_split_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
-                                cudaStream_t stream);
+// The whole call for trees (kv4_tc.cu).
+cudaError_t launch_kv4_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
+                          cudaStream_t stream);
 
 // The whole call for few query rows per sequence and kv head (kv4_few.cu);
 // `rows` is the number to plan for, any number is handled.

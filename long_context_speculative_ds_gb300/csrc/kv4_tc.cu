@@ -43,20 +43,23 @@ constexpr int kTmemCols = 512;
 constexpr int kRawRow = 3;       // raw slots with two Q tiles
 constexpr int kRawKey = 6;       // three more in the second Q tile when it is unused
 
+// A commit holds up the products behind it (about 0.1 us each here), so a
+// barrier is completed by few of them: one per 64-key unit of a group, when
+// its P V and the next tile's S are done, and one per tile, when with the
+// tile's last S its K and an earlier tile's V are free.
 enum Bar {
   kQFull = 0,
   kKFull = 1,      // 2 slots
-  kKEmpty = 3,
-  kVFull = 5,
-  kVEmpty = 7,
-  kRawFull = 9,    // 6 slots
-  kRawEmpty = 15,
-  kSFull = 21,     // [group][half]
-  kPFull = 25,     // [group][half]
-  kORdy = 29,      // [group]
-  kOFinal = 31,    // [group]
-  kAnc = 33,
-  kNumBars = 34
+  kVFull = 3,
+  kFree = 5,       // [t % 2]: S of tile t is done and with it, in row mode, P V
+                   // of tile t - 1 (in key mode, of the group's: t - 2)
+  kRawFull = 7,    // 6 slots
+  kRawEmpty = 13,
+  kSFull = 19,     // [group][half]: S is ready, and P V of the half before done
+  kPFull = 23,     // [group][half]
+  kOFinal = 27,    // [group]
+  kAnc = 29,
+  kNumBars = 30
 };
 
 struct Ctrl {
@@ -67,7 +70,6 @@ struct Ctrl {
   int32_t parents[DS_MAX_TREE_NODES];
   uint64_t anc[DS_MAX_TREE_NODES];
   uint32_t bad[kRawKey];         // bad pages of each raw tile, one bit a page
-  int32_t pages[2][32];          // page ids of two runs of tiles (the loader's)
   uint32_t where[6];             // last wait site of loader, issuers, softmax groups, converters
   int last;
 };
@@ -85,6 +87,51 @@ struct Cfg {
   static_assert((kRawKey - kRawRow) * RAW <= TB, "extra raw slots must fit in a Q tile");
   static_assert(1024 <= kRawRow * RAW, "the merge's maxima and sums must fit in the raw ring");
 };
+
+// The work item of this block, by one warp: the tree-verify plan (near-equal
+// ranges of tiles per row group, tiles per split t) with t found among 32
+// candidates at once, a lane each, instead of by bisection: the smallest of
+// them whose items fit one block per SM, or, when its rounding would cost
+// more than 15 % and the grid has room, two.
+__device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  int most = 1;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    SeqPlan s{0, 0, 0, 0, 0, 0, 0, 0};
+    if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, item == 0);
+    int64_t u = (int64_t)s.tiles * a.num_kv_heads * s.rg;
+    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+    total += u;
+    most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)s.tiles));
+  }
+  // items at t tiles per split, each lane its own t
+  auto items_at = [&](int t) {
+    int it = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      SeqPlan s{0, 0, 0, 0, 0, 0, 0, 0};
+      if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, false);
+      const int groups = a.num_kv_heads * s.rg, n = min(32, a.batch - b0);
+      for (int k = 0; k < n; ++k)
+        it += __shfl_sync(0xffffffffu, groups, k) *
+              ((__shfl_sync(0xffffffffu, s.tiles, k) + t - 1) / t);
+    }
+    return it;
+  };
+  // the smallest of 32 candidates from t0 up, in steps of a sixteenth, whose
+  // items fit; the longest sequence's tiles when none does
+  auto smallest = [&](int t0, int fit) {
+    const int t = min(most, t0 + (t0 * lane + 15) / 16);
+    const uint32_t ok = __ballot_sync(0xffffffffu, items_at(t) <= fit);
+    return ok ? __shfl_sync(0xffffffffu, t, __ffs(ok) - 1) : most;
+  };
+  const int ideal = (int)max((int64_t)1, min((int64_t)most, (total + a.target_ctas - 1) /
+                                                                 max(1, a.target_ctas)));
+  int t = smallest(ideal, a.target_ctas);
+  if (a.wave_ctas > a.target_ctas && (int64_t)t * 100 > (int64_t)ideal * 115)
+    t = min(t, smallest(max(1, ideal / 2), a.wave_ctas));
+  return plan_at(a, -1, item, t);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
@@ -121,9 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(kKFull + s), 4);      // one arrival per converter warp
       mbar_init(bar(kVFull + s), 4);
-      mbar_init(bar(kKEmpty + s), 2);     // one commit per group (two in key mode)
-      mbar_init(bar(kVEmpty + s), 2);
-      mbar_init(bar(kORdy + s), 1);
       mbar_init(bar(kOFinal + s), 1);
     }
     for (int s = 0; s < kRawKey; ++s) {
@@ -144,13 +188,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   }
   const bool early_plan = a.accumulate != 0;
   if (early_plan && warp == 0) {
-    Plan p = plan_find(a.plan, -1, blockIdx.x);
+    Plan p = kv4_plan(a.plan, blockIdx.x);
     if (lane == 0) ctrl->plan = p;
   }
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (!early_plan && warp == 0) {
-    Plan p = plan_find(a.plan, -1, blockIdx.x);
+    Plan p = kv4_plan(a.plan, blockIdx.x);
     if (lane == 0) ctrl->plan = p;
   }
   tc_fence_before();
@@ -176,6 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   }
   const int nt = t1 - t0;
   const bool row_mode = rows_here > 128;
+  // arrivals: both groups' in row mode, the tile's own group's in key mode
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) mbar_init(bar(kFree + s), row_mode ? 2 : 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
   const int L = sq.L, T = sq.T;
   const bool need_anc = active && t1 * kTileKeys > L;
   const int nraw = row_mode ? kRawRow : kRawKey;
@@ -230,63 +280,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
       const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
       const uint64_t policy = l2_evict_first();
-      // Page ids come 32 at a time, a run of 32 / npg tiles, one run ahead of
-      // the K tiles (V is at most two tiles behind K, so two runs are kept):
-      // a load per tile would put its latency into every tile's turn.
+      // Page ids come 32 at a time, a run of 32 / npg tiles, the next run on
+      // its way (a load per tile would put its latency into every tile's
+      // turn), and are checked together; lane r of a run holds page r of it.
+      // V is at most two tiles behind K and walks its own runs.
       const int rshift = __ffs(P) - 1 - 2;       // log2 of the tiles of a run, P / 4
       const int run = 1 << rshift, pend = (L + T + P - 1) / P;
+      const uint32_t page_bytes = a.plan.num_kv_heads * blk;
+      struct Side {                              // of K, of V
+        const uint8_t* head;
+        int ids, next;
+        uint32_t bad;
+      } side[2];
       auto ids_of = [&](int r) {
         const int pi = (t0 + r * run) * npg + lane;
         return pi < pend ? __ldg(ptab + pi) : 0;
       };
-      int next_ids = ids_of(0);
-      const uint8_t* const k_head = ka.k4 + (int64_t)kvh * blk;
-      const uint8_t* const v_head = ka.v4 + (int64_t)kvh * blk;
-      const uint32_t page_bytes = a.plan.num_kv_heads * blk;
+      auto check = [&](Side& x) {
+        const bool bad = (uint32_t)x.ids >= (uint32_t)a.num_pages;
+        if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
+        x.bad = __ballot_sync(0xffffffffu, bad);
+      };
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        side[v].head = (v ? ka.v4 : ka.k4) + (int64_t)kvh * blk;
+        side[v].ids = ids_of(0);
+        side[v].next = ids_of(1);
+        check(side[v]);
+      }
       bool ok = true;
+      const uint32_t pmask = npg == 8 ? 0xffu : (1u << npg) - 1u;
       Walk w = walk();
-      while (w.take()) {
-        const int r = w.n >> rshift, in_run = w.n & (run - 1);
-        if (!w.is_v && in_run == 0) {
-          ctrl->pages[r & 1][lane] = next_ids;
-          __syncwarp();
-          next_ids = ids_of(r + 1);
+      auto load = [&](Side& x) {
+        const int in_run = w.n & (run - 1);
+        if (w.n > 0 && in_run == 0) {
+          x.ids = x.next;
+          x.next = ids_of((w.n >> rshift) + 1);
+          check(x);
         }
-        int pg = 0;
-        bool have = lane < npg && (t0 + w.n) * kTileKeys + lane * P < L + T, bad = false;
-        if (have) {
-          pg = ctrl->pages[r & 1][in_run * npg + lane];
-          bad = (uint32_t)pg >= (uint32_t)a.num_pages;
-          if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
-        }
-        const uint32_t badm = __ballot_sync(0xffffffffu, bad);
-        have = have && !bad;
-        const uint32_t copies = __ballot_sync(0xffffffffu, have);
+        const uint32_t pg = __shfl_sync(0xffffffffu, x.ids, (in_run * npg + lane) & 31);
+        const uint32_t badm = (x.bad >> (in_run * npg)) & pmask;
+        const int left = pend - (t0 + w.n) * npg;          // pages of the sequence from here on
+        const bool have = lane < min(npg, left) && !((badm >> lane) & 1u);
+        const int n = min(npg, left) - __popc(badm);
         const uint32_t full = bar(kRawFull + w.slot);
         const uint32_t tag = 10000 + 2 * w.n + (w.is_v ? 1 : 0);
         if (lane == 0) ctrl->where[0] = tag;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
-                                               diag, tag));
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
+                                               diag, tag)))
+          return false;
         if (lane == 0) {
           ctrl->bad[w.slot] = badm;
-          mbar_arrive_expect_tx(full, __popc(copies) * blk);
+          mbar_arrive_expect_tx(full, n * blk);
         }
         __syncwarp();
         if (have)
-          bulk_load_hint(raw_addr(w.slot) + lane * blk,
-                         (w.is_v ? v_head : k_head) + (uint64_t)(uint32_t)pg * page_bytes, blk,
+          bulk_load_hint(raw_addr(w.slot) + lane * blk, x.head + (uint64_t)pg * page_bytes, blk,
                          full, policy);
+        return true;
+      };
+      while (w.take()) {
+        ok = w.is_v ? load(side[1]) : load(side[0]);
+        if (!ok) break;
         w.release();
       }
       if (lane == 0) ctrl->where[0] = ok ? 19999 : 19998;
       // copies still in flight must land before the CTA can exit: each slot's
       // last phase (a slot not used yet passes at once)
       if (!ok && lane == 0)
-        for (int i = 0; i < nraw; ++i) {
-          const bool wrapped = i >= w.slot;        // last used one round ago
-          drain_wait(bar(kRawFull + i), wrapped ? w.phase ^ 1 : w.phase);
-        }
+        for (int i = 0; i < nraw; ++i)
+          drain_wait(bar(kRawFull + i), i >= w.slot ? w.phase ^ 1 : w.phase);
     } else if (warp == 1) {
       // ---------------------------------------------------- ancestor masks
       if (need_anc) {
@@ -304,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         const uint64_t kd0 = sdesc_sw128(sK, 16, RG);
         const uint64_t vd0 = sdesc_sw128(sV, 1024, RG);
         const uint32_t tG = tmem + (uint32_t)(256 * g);
-        const int rel = row_mode ? 1 : 2;
         auto qk = [&](int t, int h) {
           const uint64_t kb = kd0 + (uint64_t)((t & 1) * (TB >> 4) + h * ((8 * RG) >> 4));
           const uint32_t d = tG + (uint32_t)(64 * h);
@@ -344,33 +406,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
               qk(t, h);
               mma_commit(bar(kSFull + 2 * g + h));
             }
-            for (int r = 0; r < rel; ++r) mma_commit(bar(kKEmpty + (t & 1)));
+            mma_commit(bar(kFree + (t & 1)));
           }
         }
         for (int j = 0; ok && j < my_nt; ++j) {
           const int n = tile_of(g, j);
+          const int tn = row_mode ? n + 1 : n + 2;
           const bool more = j + 1 < my_nt;
-          const int tn = more ? tile_of(g, j + 1) : 0;
           for (int h = 0; h < 2; ++h) {
             if (!(ok = wait(kPFull + 2 * g + h, j & 1,
                             20000 + (kPFull + 2 * g + h) * 100 + 2 * j + h)))
               break;
             if (h == 0 && !(ok = wait_v(n))) break;
+            // K is looked at before the products are issued: afterwards a
+            // look at a barrier waits until they have drained
+            const bool k_there =
+                h == 1 || !more || mbar_try_wait(bar(kKFull + (tn & 1)), (tn >> 1) & 1);
             tc_fence_after();
             pv(n, h, j > 0 || h > 0);
-            mma_commit(bar(kORdy + g));
             if (more) {
-              if (h == 0) {
+              if (!k_there) {
                 if (!(ok = wait_k(tn))) break;
                 tc_fence_after();
               }
               qk(tn, h);
-              mma_commit(bar(kSFull + 2 * g + h));
-              if (h == 1)
-                for (int r = 0; r < rel; ++r) mma_commit(bar(kKEmpty + (tn & 1)));
             }
-            if (h == 1)
-              for (int r = 0; r < rel; ++r) mma_commit(bar(kVEmpty + (n & 1)));
+            mma_commit(bar(kSFull + 2 * g + h));
+            if (h == 1) mma_commit(bar(kFree + (tn & 1)));
           }
         }
         if (ok) ctrl->where[wi] = 29999;
@@ -388,24 +450,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const bool row_ok = grow_local < rows_here;
       const int grow = rgi * kRowsPerGroup + grow_local;
       const int jn = grow / G;
-      // this thread's query row as f16 into its Q tile (key mode: one tile,
-      // group 0's)
+      // the group's query rows as f16 into its Q tile (key mode: one tile,
+      // group 0's): 16-byte chunks, a row's by consecutive lanes, all of a
+      // thread's on their way at once
       if (row_mode || g == 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.q + ((int64_t)(sq.node0 + jn) * a.num_q_heads + kvh * G + grow % G) * D);
-        const uint32_t dst = sQ + (row_mode ? g * TB : 0) + lrow * 128;
+        constexpr int CPR = D / 8;                   // chunks of a row
+        constexpr int RPI = 32 / CPR;                // rows of a warp's load
+        const int ch = lane % CPR;
+        const uint32_t dst = sQ + (row_mode ? g * TB : 0) + (ch >> 3) * kHalfBytes;
+        uint4 x[32 / RPI];
 #pragma unroll
-        for (int c0 = 0; c0 < D / 8; c0 += 8) {
-          uint4 x[8];
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int rl = q4 * 32 + i * RPI + lane / CPR;          // row of the tile
+          const int rr = (row_mode ? g * 128 : 0) + rl;
+          const int gr = rgi * kRowsPerGroup + rr;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (rr < rows_here)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(
+                             a.q + ((int64_t)(sq.node0 + gr / G) * a.num_q_heads + kvh * G +
+                                    gr % G) * D) + ch);
+        }
 #pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] = row_ok ? __ldg(src + c0 + c) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             dst + (c0 >> 3) * kHalfBytes + ((c ^ (lrow & 7)) << 4)),
-                         "r"(bf16x2_to_f16x2(x[c].x)), "r"(bf16x2_to_f16x2(x[c].y)),
-                         "r"(bf16x2_to_f16x2(x[c].z)), "r"(bf16x2_to_f16x2(x[c].w))
-                         : "memory");
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int rl = q4 * 32 + i * RPI + lane / CPR;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           dst + rl * 128 + (((ch & 7) ^ (rl & 7)) << 4)),
+                       "r"(bf16x2_to_f16x2(x[i].x)), "r"(bf16x2_to_f16x2(x[i].y)),
+                       "r"(bf16x2_to_f16x2(x[i].z)), "r"(bf16x2_to_f16x2(x[i].w))
+                       : "memory");
         }
         fence_proxy_async_smem();
       }
@@ -465,9 +537,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
                                      clse_row);
           }
           if (rescale) {
-            if (lrow == 0) ctrl->where[wi] = 30000 + (kORdy + g) * 100 + u;
-            ok = __all_sync(0xffffffffu, mbar_wait(bar(kORdy + g), (u - 1) & 1, abort_flag,
-                                                   diag, 30000 + (kORdy + g) * 100 + u));
+            // O must hold every earlier half: the half before this one is
+            // done with the other half's next S
+            if (lrow == 0) ctrl->where[wi] = 35000 + u;
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(bar(kSFull + 2 * g + 1 - hb), (hb ? j + 1 : j) & 1, abort_flag,
+                                      diag, 35000 + u));
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
@@ -530,9 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const bool is_v = w.is_v;
       const uint32_t tag = 40000 + 2 * n + (is_v ? 1 : 0);
       if (rep) ctrl->where[5] = tag;
-      ok = mbar_wait(bar(kRawFull + slot), w.phase, abort_flag, diag, tag) &&
-           mbar_wait(bar((is_v ? kVEmpty : kKEmpty) + (n & 1)), ((n >> 1) & 1) ^ 1, abort_flag,
-                     diag, tag + 100000);
+      ok = mbar_wait(bar(kRawFull + slot), w.phase, abort_flag, diag, tag);
+      if (ok && n >= 2) {                // the tile two before has been used
+        const int t = is_v ? (row_mode ? n - 1 : n) : n - 2;
+        ok = mbar_wait(bar(kFree + (t & 1)), (t >> 1) & 1, abort_flag, diag, tag + 100000);
+      }
       if (!__all_sync(0xffffffffu, ok)) break;
       const bool bad = (ctrl->bad[slot] >> pidx) & 1u;
       const uint32_t raw = raw_addr(slot);
@@ -622,20 +699,120 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   }
 }
 
+// Second launch: the first n_comb blocks merge the splits of the output rows,
+// a warp per (node, query head); the rest form the chunk scores, a warp per
+// (chunk, sequence), four rows a lane, kFinCombos (kv head, row group)
+// combinations per round trip.  What only depends on the call's inputs is
+// worked out before the wait for the split pass, which has itself waited for
+// whatever wrote them.
+constexpr int kFinCombos = 2;
+
+template <int D, bool HALF>
+DS_DEV void merge_row(const VerifyKArgs& a, int blk) {
+  const int lane = threadIdx.x & 31;
+  const int64_t x = (int64_t)blk * 8 + (threadIdx.x >> 5);
+  const int node = (int)(x / a.num_q_heads), qh = (int)(x - (int64_t)node * a.num_q_heads);
+  const int G = a.plan.group, kvh = qh / G;
+  // the sequence that owns the node: the last whose offset is at most it
+  int b = -1;
+  for (int b0 = 0; b0 < a.plan.batch; b0 += 32) {
+    const bool in = b0 + lane < a.plan.batch && __ldg(a.plan.tree_offsets + b0 + lane) <= node;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (m) b = b0 + 31 - __clz(m);
+  }
+  SeqPlan sq{0, 0, 0, 0, 0, 0, 0, 0};
+  if (b >= 0 && node < a.plan.n_nodes) sq = seq_sizes(a.plan, b, false);
+  const int row = (node - sq.node0) * G + qh % G;
+  const int rgi = row / kRowsPerGroup, r = row % kRowsPerGroup;
+  const int64_t grp = ((int64_t)max(b, 0) * a.plan.num_kv_heads + kvh) * a.plan.rg_max + rgi;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (row < 0 || row >= sq.rows) return;          // not a row of a usable sequence
+  const int4 gd = __ldcg(a.gdesc + grp);
+  const float lse = __ldcg(a.row_lse + grp * kRowsPerGroup + r);
+  combine_row_splits<D, HALF, HALF ? (D == 128 ? 20 : 32) : 8>(a, gd.x, gd.y, r, lse, x);
+}
+
+DS_DEV void chunk_score(const VerifyKArgs& a, int blk) {
+  const int per_b = (a.plan.max_chunks + 7) / 8;
+  const int b = blk / per_b, c = blk % per_b * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const SeqPlan sq = seq_sizes(a.plan, b, false);
+  const int rg = sq.rg, combos = a.plan.num_kv_heads * rg;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (c >= (sq.L + a.plan.chunk_size - 1) / a.plan.chunk_size) return;
+  float sum = 0.f;
+  for (int cb0 = 0; cb0 < combos; cb0 += kFinCombos) {
+    float4 v[kFinCombos][2], w[kFinCombos][2];
+    int n[kFinCombos];                             // rows from this lane's first on
+#pragma unroll
+    for (int k = 0; k < kFinCombos; ++k) {
+      const int h = (cb0 + k) / max(rg, 1), rgi = (cb0 + k) - h * rg;
+      const int64_t g =
+          ((int64_t)b * a.plan.num_kv_heads + h) * a.plan.rg_max + rgi;
+      n[k] = cb0 + k < combos ? min(kRowsPerGroup, sq.rows - rgi * kRowsPerGroup) - 4 * lane : 0;
+      const float4* m =
+          reinterpret_cast<const float4*>(a.clse + (g * a.plan.max_chunks + c) * kRowsPerGroup);
+      const float4* l = reinterpret_cast<const float4*>(a.row_lse + g * kRowsPerGroup);
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        if (n[k] > 128 * q) {
+          v[k][q] = __ldcg(m + lane + 32 * q);
+          w[k][q] = __ldcg(l + lane + 32 * q);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kFinCombos; ++k)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int left = n[k] - 128 * q;
+        if (left > 0) sum += exp2f(v[k][q].x - w[k][q].x);
+        if (left > 1) sum += exp2f(v[k][q].y - w[k][q].y);
+        if (left > 2) sum += exp2f(v[k][q].z - w[k][q].z);
+        if (left > 3) sum += exp2f(v[k][q].w - w[k][q].w);
+      }
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) {
+    float* dst = a.scores + (int64_t)b * a.plan.max_chunks + c;
+    *dst = a.accumulate ? *dst + sum : sum;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 4) kv4_finish(const __grid_constant__ VerifyKArgs a,
+                                                     int n_comb) {
+  if ((int)blockIdx.x >= n_comb) chunk_score(a, blockIdx.x - n_comb);
+  else if (a.out_f32) merge_row<D, false>(a, blockIdx.x);
+  else merge_row<D, true>(a, blockIdx.x);
+}
+
 }  // namespace kv4tc
 
 template <int D>
 static cudaError_t launch_tc(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t stream) {
   const size_t smem = kv4tc::Cfg<D>::smem;
-  cudaError_t e = cudaFuncSetAttribute(kv4tc::kv4_split_tc<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static bool attr = false;
+  if (!attr) {
+    cudaError_t e = cudaFuncSetAttribute(kv4tc::kv4_split_tc<D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  cudaError_t e = launch_dependent(kv4tc::kv4_split_tc<D>, dim3(L.max_items),
+                                   dim3(kv4tc::kThreads), smem, stream, k);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kv4tc::kv4_split_tc<D>, dim3(L.max_items), dim3(kv4tc::kThreads), smem,
-                          stream, k);
+  const VerifyKArgs& v = k.v;
+  const int64_t n_comb = ((int64_t)v.plan.n_nodes * v.num_q_heads + 7) / 8;
+  const int64_t n_fin = v.scores ? (int64_t)v.plan.batch * ((v.plan.max_chunks + 7) / 8) : 0;
+  return launch_dependent(kv4tc::kv4_finish<D>, dim3((unsigned)(n_comb + n_fin)), dim3(256), 0,
+                          stream, v, (int)n_comb);
 }
 
-cudaError_t launch_kv4_split_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
-                                cudaStream_t stream) {
+// The whole call for trees.
+cudaError_t launch_kv4_tc(const Kv4KArgs& k, int head_dim, const VerifyLayout& L,
+                          cudaStream_t stream) {
   return head_dim == 128 ? launch_tc<128>(k, L, stream) : launch_tc<64>(k, L, stream);
 }
 

@@ -169,18 +169,6 @@ __global__ void __launch_bounds__(kFinishThreads, 4) verify_finish(VerifyKArgs a
 cudaError_t launch_split_tc(const VerifyKArgs& k, const ds_verify_args& a,
                             const VerifyLayout& L, cudaStream_t stream);
 
-cudaError_t launch_finish(const VerifyKArgs& k, int head_dim, int rg_max, int batch,
-                          cudaStream_t stream) {
-  const int n_comb = batch * k.plan.num_kv_heads * rg_max * (kRowsPerGroup / kFinishWarps);
-  const int n_fin = k.scores != nullptr && k.plan.max_chunks > 0
-                        ? batch * ((k.plan.max_chunks + kFinishWarps - 1) / kFinishWarps)
-                        : 0;
-  const dim3 grid(n_comb + n_fin), block(kFinishThreads);
-  if (head_dim == 128)
-    return launch_dependent(verify_finish<128>, grid, block, 0, stream, k, n_comb);
-  return launch_dependent(verify_finish<64>, grid, block, 0, stream, k, n_comb);
-}
-
 template <int D>
 static cudaError_t launch_d(const VerifyKArgs& k, const ds_verify_args& a,
                             const VerifyLayout& L, int batch, cudaStream_t stream,
@@ -189,7 +177,12 @@ static cudaError_t launch_d(const VerifyKArgs& k, const ds_verify_args& a,
   cudaError_t e = launch_split_tc(k, a, L, stream);
   if (e != cudaSuccess) return e;
   if (ev1) cudaEventRecord(ev1, stream);
-  return launch_finish(k, D, L.rg_max, batch, stream);
+  const int n_comb = batch * k.plan.num_kv_heads * L.rg_max * (kRowsPerGroup / kFinishWarps);
+  const int n_fin = k.plan.max_chunks > 0
+                        ? batch * ((k.plan.max_chunks + kFinishWarps - 1) / kFinishWarps)
+                        : 0;
+  return launch_dependent(verify_finish<D>, dim3(n_comb + n_fin), dim3(kFinishThreads), 0,
+                          stream, k, n_comb);
 }
 
 cudaError_t launch_verify(const ds_verify_args& a, const VerifyLayout& L,

@@ -30,11 +30,6 @@ struct VerifyKArgs {
   int32_t accumulate;
 };
 
-// Second launch of a verify call (verify_attn.cu): merges the splits into
-// `out` and, when scores is not NULL, forms the chunk scores.
-cudaError_t launch_finish(const VerifyKArgs& k, int head_dim, int rg_max, int batch,
-                          cudaStream_t stream);
-
 // Output row r of a row group merged over the group's ns splits (items
 // base .. base + ns - 1): sum over s of 2^{lse_s - lse} O_s, the split
 // outputs O_s being normalised and lse the row's final log2-sum-exp.  One
