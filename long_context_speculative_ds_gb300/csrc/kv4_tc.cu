@@ -89,28 +89,44 @@ struct Cfg {
 };
 
 // The work item of this block, by one warp: the tree-verify plan (near-equal
-// ranges of tiles per row group, tiles per split t) with t found among 32
-// candidates at once, a lane each, instead of by bisection: the smallest of
-// them whose items fit one block per SM, or, when its rounding would cost
-// more than 15 % and the grid has room, two.
+// ranges of tiles per row group, t tiles per split).  t is the even share when
+// its items fit one block per SM; else the smallest of 32 candidates that
+// does, tried at once, a lane each; and when that would cost more than 15 %
+// and the grid has room, the smallest that fits two.
 __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
   const int lane = threadIdx.x & 31;
+  // tiles and row groups over all heads of the first 32 sequences, a lane each
+  SeqPlan s0{0, 0, 0, 0, 0, 0, 0, 0};
+  if (lane < a.batch) s0 = seq_sizes(a, lane, item == 0);
+  auto seq = [&](int b0) {
+    if (b0 == 0) return s0;
+    SeqPlan s{0, 0, 0, 0, 0, 0, 0, 0};
+    if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, item == 0);
+    return s;
+  };
   int64_t total = 0;
   int most = 1;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    SeqPlan s{0, 0, 0, 0, 0, 0, 0, 0};
-    if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, item == 0);
+    const SeqPlan s = seq(b0);
     int64_t u = (int64_t)s.tiles * a.num_kv_heads * s.rg;
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     total += u;
     most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)s.tiles));
   }
+  const int ctas = max(1, a.target_ctas);
+  const int ideal = (int)max((int64_t)1, min((int64_t)most, (total + ctas - 1) / ctas));
+  int fits = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const SeqPlan s = seq(b0);
+    fits += (int)__reduce_add_sync(
+        0xffffffffu, (unsigned)(a.num_kv_heads * s.rg * ((s.tiles + ideal - 1) / ideal)));
+  }
+  if (fits <= a.target_ctas) return plan_at(a, -1, item, ideal);
   // items at t tiles per split, each lane its own t
   auto items_at = [&](int t) {
     int it = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      SeqPlan s{0, 0, 0, 0, 0, 0, 0, 0};
-      if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, false);
+      const SeqPlan s = seq(b0);
       const int groups = a.num_kv_heads * s.rg, n = min(32, a.batch - b0);
       for (int k = 0; k < n; ++k)
         it += __shfl_sync(0xffffffffu, groups, k) *
@@ -125,8 +141,6 @@ __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
     const uint32_t ok = __ballot_sync(0xffffffffu, items_at(t) <= fit);
     return ok ? __shfl_sync(0xffffffffu, t, __ffs(ok) - 1) : most;
   };
-  const int ideal = (int)max((int64_t)1, min((int64_t)most, (total + a.target_ctas - 1) /
-                                                                 max(1, a.target_ctas)));
   int t = smallest(ideal, a.target_ctas);
   if (a.wave_ctas > a.target_ctas && (int64_t)t * 100 > (int64_t)ideal * 115)
     t = min(t, smallest(max(1, ideal / 2), a.wave_ctas));
