@@ -40,8 +40,8 @@ namespace kv4tc {
 constexpr int kThreads = 512;
 constexpr uint32_t kHalfBytes = 128 * 128;
 constexpr int kTmemCols = 512;
-constexpr int kRawRow = 3;       // raw slots with two Q tiles
-constexpr int kRawKey = 6;       // three more in the second Q tile when it is unused
+constexpr int kRing = 3;         // raw slots of a ring: one for K and V in row mode, one
+                                 // for each in key mode (V's in the unused second Q tile)
 
 // A commit holds up the products behind it (about 0.1 us each here), so a
 // barrier is completed by few of them: one per 64-key unit of a group, when
@@ -69,7 +69,7 @@ struct Ctrl {
   Plan plan;
   int32_t parents[DS_MAX_TREE_NODES];
   uint64_t anc[DS_MAX_TREE_NODES];
-  uint32_t bad[kRawKey];         // bad pages of each raw tile, one bit a page
+  uint32_t bad[2 * kRing];       // bad pages of each raw tile, one bit a page
   uint32_t where[6];             // last wait site of loader, issuers, softmax groups, converters
   int last;
 };
@@ -81,21 +81,24 @@ struct Cfg {
   static constexpr uint32_t RG = NH * 1024;
   static constexpr int RAW = DS_KV4_BLOCK_BYTES(128, D);
   // Q (2 tiles), K and V (2 slots each), raw tiles, control block
-  static constexpr size_t smem = 6 * TB + kRawRow * RAW + sizeof(Ctrl) + 1024;
+  static constexpr size_t smem = 6 * TB + kRing * RAW + sizeof(Ctrl) + 1024;
   static_assert(smem <= 232448, "dynamic shared memory above the 227 KB a block can have");
   static_assert(4 * 32 * 32 * 4 <= TB, "output staging must fit in a Q tile");
-  static_assert((kRawKey - kRawRow) * RAW <= TB, "extra raw slots must fit in a Q tile");
-  static_assert(1024 <= kRawRow * RAW, "the merge's maxima and sums must fit in the raw ring");
+  static_assert(kRing * RAW <= TB, "extra raw slots must fit in a Q tile");
+  static_assert(1024 <= kRing * RAW, "the merge's maxima and sums must fit in the raw ring");
 };
 
-// The work item of this block, by one warp: the tree-verify plan (near-equal
-// ranges of tiles per row group, t tiles per split).  t is the even share when
-// its items fit one block per SM; else the smallest of 32 candidates that
-// does, tried at once, a lane each; and when that would cost more than 15 %
-// and the grid has room, the smallest that fits two.
+// Cost of a tile: 1.28 us in key mode, 1.87 us in row mode (128K, 32 heads)
+DS_DEV int tile_cost(const SeqPlan& s) { return s.rows <= 128 ? 5 : 7; }
+
+// The work item of this block, by one warp: near-equal ranges of tiles per
+// row group, of a cost of at most q (but for the rounding to tiles) each.  q
+// is the even share when its items fit one block per SM; else the smallest of
+// 32 candidates that does, tried at once, a lane each; and when that would
+// cost more than 15 % and the grid has room, the smallest that fits two.
 __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
   const int lane = threadIdx.x & 31;
-  // tiles and row groups over all heads of the first 32 sequences, a lane each
+  // tiles and row groups of the first 32 sequences, a lane each
   SeqPlan s0{0, 0, 0, 0, 0, 0, 0, 0};
   if (lane < a.batch) s0 = seq_sizes(a, lane, item == 0);
   auto seq = [&](int b0) {
@@ -104,47 +107,87 @@ __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
     if (b0 + lane < a.batch) s = seq_sizes(a, b0 + lane, item == 0);
     return s;
   };
+  auto splits = [](int tiles, int cost, int q) {
+    const int t = (q + cost - 1) / cost;
+    return (tiles + t - 1) / t;
+  };
   int64_t total = 0;
   int most = 1;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const SeqPlan s = seq(b0);
-    int64_t u = (int64_t)s.tiles * a.num_kv_heads * s.rg;
+    const int cost = s.tiles * tile_cost(s);
+    int64_t u = (int64_t)cost * a.num_kv_heads * s.rg;
     for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     total += u;
-    most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)s.tiles));
+    most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)cost));
   }
   const int ctas = max(1, a.target_ctas);
-  const int ideal = (int)max((int64_t)1, min((int64_t)most, (total + ctas - 1) / ctas));
+  int q = (int)max((int64_t)1, min((int64_t)most, (total + ctas - 1) / ctas));
   int fits = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const SeqPlan s = seq(b0);
     fits += (int)__reduce_add_sync(
-        0xffffffffu, (unsigned)(a.num_kv_heads * s.rg * ((s.tiles + ideal - 1) / ideal)));
+        0xffffffffu, (unsigned)(a.num_kv_heads * s.rg * splits(s.tiles, tile_cost(s), q)));
   }
-  if (fits <= a.target_ctas) return plan_at(a, -1, item, ideal);
-  // items at t tiles per split, each lane its own t
-  auto items_at = [&](int t) {
-    int it = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const SeqPlan s = seq(b0);
-      const int groups = a.num_kv_heads * s.rg, n = min(32, a.batch - b0);
-      for (int k = 0; k < n; ++k)
-        it += __shfl_sync(0xffffffffu, groups, k) *
-              ((__shfl_sync(0xffffffffu, s.tiles, k) + t - 1) / t);
+  if (fits > a.target_ctas) {
+    // items at q, each lane its own q
+    auto items_at = [&](int q) {
+      int it = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const SeqPlan s = seq(b0);
+        const int groups = a.num_kv_heads * s.rg, cost = tile_cost(s), n = min(32, a.batch - b0);
+        for (int k = 0; k < n; ++k)
+          it += __shfl_sync(0xffffffffu, groups, k) *
+                splits(__shfl_sync(0xffffffffu, s.tiles, k), __shfl_sync(0xffffffffu, cost, k), q);
+      }
+      return it;
+    };
+    // the smallest of 32 candidates from q0 up, in steps of a sixteenth, whose
+    // items fit; the longest sequence's cost when none does
+    auto smallest = [&](int q0, int fit) {
+      const int x = (int)min((int64_t)most, q0 + ((int64_t)q0 * lane + 15) / 16);
+      const uint32_t ok = __ballot_sync(0xffffffffu, items_at(x) <= fit);
+      return ok ? __shfl_sync(0xffffffffu, x, __ffs(ok) - 1) : most;
+    };
+    const int even = q;
+    q = smallest(even, a.target_ctas);
+    if (a.wave_ctas > a.target_ctas && (int64_t)q * 100 > (int64_t)even * 115)
+      q = min(q, smallest(max(1, even / 2), a.wave_ctas));
+  }
+  // the sequence that owns the item
+  Plan p;
+  p.tps = q;
+  p.b = -1;
+  p.seq = SeqPlan{0, 0, 0, 0, 0, 0, 0, 0};
+  int base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    SeqPlan s = seq(b0);
+    s.splits = splits(s.tiles, tile_cost(s), q);
+    const int items = a.num_kv_heads * s.rg * s.splits;
+    int incl = items;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
     }
-    return it;
-  };
-  // the smallest of 32 candidates from t0 up, in steps of a sixteenth, whose
-  // items fit; the longest sequence's tiles when none does
-  auto smallest = [&](int t0, int fit) {
-    const int t = min(most, t0 + (t0 * lane + 15) / 16);
-    const uint32_t ok = __ballot_sync(0xffffffffu, items_at(t) <= fit);
-    return ok ? __shfl_sync(0xffffffffu, t, __ffs(ok) - 1) : most;
-  };
-  int t = smallest(ideal, a.target_ctas);
-  if (a.wave_ctas > a.target_ctas && (int64_t)t * 100 > (int64_t)ideal * 115)
-    t = min(t, smallest(max(1, ideal / 2), a.wave_ctas));
-  return plan_at(a, -1, item, t);
+    s.item_base = base + incl - items;
+    const uint32_t m =
+        __ballot_sync(0xffffffffu, item >= s.item_base && item < s.item_base + items);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      p.b = b0 + src;
+      p.seq.L = __shfl_sync(0xffffffffu, s.L, src);
+      p.seq.T = __shfl_sync(0xffffffffu, s.T, src);
+      p.seq.node0 = __shfl_sync(0xffffffffu, s.node0, src);
+      p.seq.tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+      p.seq.rows = __shfl_sync(0xffffffffu, s.rows, src);
+      p.seq.rg = __shfl_sync(0xffffffffu, s.rg, src);
+      p.seq.splits = __shfl_sync(0xffffffffu, s.splits, src);
+      p.seq.item_base = __shfl_sync(0xffffffffu, s.item_base, src);
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  p.total_items = base;
+  return p;
 }
 
 template <int D>
@@ -168,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   float* merge_buf = reinterpret_cast<float*>(smem + 4 * TB);
   float* m1buf = reinterpret_cast<float*>(smem + 6 * TB);
   float* l1buf = m1buf + 128;
-  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + 6 * TB + kRawRow * RAW);
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + 6 * TB + kRing * RAW);
   volatile int* abort_flag = &ctrl->abort;
   uint32_t* diag = a.plan.status + 1;
 
@@ -184,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       mbar_init(bar(kVFull + s), 4);
       mbar_init(bar(kOFinal + s), 1);
     }
-    for (int s = 0; s < kRawKey; ++s) {
+    for (int s = 0; s < 2 * kRing; ++s) {
       mbar_init(bar(kRawFull + s), 1);
       mbar_init(bar(kRawEmpty + s), 4);
     }
@@ -215,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
-  const Plan p = ctrl->plan;
+  const Plan& p = ctrl->plan;           // stays in shared memory: registers are scarce
   const bool active = (int)blockIdx.x < p.total_items && p.b >= 0;
 
   const SeqPlan& sq = p.seq;
@@ -242,38 +285,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   __syncthreads();
   const int L = sq.L, T = sq.T;
   const bool need_anc = active && t1 * kTileKeys > L;
-  const int nraw = row_mode ? kRawRow : kRawKey;
   auto raw_addr = [&](int s) -> uint32_t {
-    return s < kRawRow ? sR + s * RAW : sQ + TB + (s - kRawRow) * RAW;
+    return s < kRing ? sR + s * RAW : sQ + TB + (s - kRing) * RAW;
   };
   // Tiles are loaded and converted in the order the MMAs need them: K runs
   // one tile ahead of V (two in key mode, where both groups start at once).
-  // The walk keeps counters instead of dividing: a single warp follows it,
-  // and every instruction adds its latency to each tile's turn.
+  // In row mode K and V share a ring of raw slots; in key mode each has one,
+  // and a loader.  The walk keeps counters instead of dividing: a single warp
+  // follows it, and every instruction adds its latency to each tile's turn.
+  enum { kAll = 0, kOnlyK = 1, kOnlyV = 2 };
   struct Walk {
-    int lead, nt, nraw;
+    int what, lead, nt;
     int k = 0, v = 0;              // K and V tiles taken so far
     bool is_v = false;             // the tile at hand
     int n = 0;
     int slot = 0, phase = 0;       // its raw slot, and the parity of that slot's uses
+    int other_slot, other_phase = 0;             // of the ring that is not at hand
+    bool other_v = true, two;
     __device__ bool take() {       // false at the end
-      if (v == nt) return false;
-      is_v = k >= nt || k >= v + lead;
+      if ((what == kOnlyK ? k : v) == nt) return false;
+      is_v = what == kOnlyV || (what == kAll && (k >= nt || k >= v + lead));
       n = is_v ? v++ : k++;
+      if (two && is_v == other_v) {
+        const int s = slot, p = phase;
+        slot = other_slot; phase = other_phase;
+        other_slot = s; other_phase = p;
+        other_v = !other_v;
+      }
       return true;
     }
-    __device__ void release() {    // on to the next raw slot
-      if (++slot == nraw) {
-        slot = 0;
+    __device__ void release() {    // on to the next raw slot of the ring
+      if (++slot == kRing || slot == 2 * kRing) {
+        slot -= kRing;
         phase ^= 1;
       }
     }
   };
-  auto walk = [&]() {
+  auto walk = [&](int what) {
     Walk w;
+    w.what = what;
     w.lead = row_mode ? 1 : 2;
     w.nt = nt;
-    w.nraw = nraw;
+    w.two = !row_mode;
+    w.other_slot = kRing;
     return w;
   };
   // tiles of group g: row mode every tile, key mode every other tile (so
@@ -282,12 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   auto tile_of = [&](int g, int j) { return row_mode ? j : 2 * j + g; };
 
   // registers move from the loader's and the converters' warpgroups to the
-  // softmax groups: 128 (80 + 96) + 256 x 168 = the launch's 512 x 128
-  static_assert(128 * (80 + 96) + 256 * 168 <= kThreads * 128, "more than the launch has");
+  // softmax groups: 128 (88 + 88) + 256 x 168 = the launch's 512 x 128
+  static_assert(128 * (88 + 88) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
-    regs_release<80>();
+    regs_release<88>();
     if (!(active && nt > 0)) {
-    } else if (warp == 0) {
+    } else if (warp < 2) {
+      // ---------------------------------------------------- ancestor masks
+      if (warp == 1 && need_anc) {
+        tc::tree_ancestors(a.parents + sq.node0, T, ctrl->parents, ctrl->anc, a.plan.status);
+        mbar_arrive(bar(kAnc));
+      }
+      if (warp == 0 || !row_mode) {
       // ------------------------------------------------------------ loader
       const int P = a.plan.page_size;
       const int npg = kTileKeys / P;
@@ -324,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       }
       bool ok = true;
       const uint32_t pmask = npg == 8 ? 0xffu : (1u << npg) - 1u;
-      Walk w = walk();
+      Walk w = walk(row_mode ? kAll : warp == 0 ? kOnlyK : kOnlyV);
       auto load = [&](Side& x) {
         const int in_run = w.n & (run - 1);
         if (w.n > 0 && in_run == 0) {
@@ -339,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         const int n = min(npg, left) - __popc(badm);
         const uint32_t full = bar(kRawFull + w.slot);
         const uint32_t tag = 10000 + 2 * w.n + (w.is_v ? 1 : 0);
-        if (lane == 0) ctrl->where[0] = tag;
+        if (lane == 0 && warp == 0) ctrl->where[0] = tag;
         if (!__all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
                                                diag, tag)))
           return false;
@@ -358,17 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         if (!ok) break;
         w.release();
       }
-      if (lane == 0) ctrl->where[0] = ok ? 19999 : 19998;
+      if (lane == 0 && warp == 0) ctrl->where[0] = ok ? 19999 : 19998;
       // copies still in flight must land before the CTA can exit: each slot's
       // last phase (a slot not used yet passes at once)
       if (!ok && lane == 0)
-        for (int i = 0; i < nraw; ++i)
+        for (int s0 = w.slot < kRing ? 0 : kRing, i = s0; i < s0 + kRing; ++i)
           drain_wait(bar(kRawFull + i), i >= w.slot ? w.phase ^ 1 : w.phase);
-    } else if (warp == 1) {
-      // ---------------------------------------------------- ancestor masks
-      if (need_anc) {
-        tc::tree_ancestors(a.parents + sq.node0, T, ctrl->parents, ctrl->anc, a.plan.status);
-        mbar_arrive(bar(kAnc));
       }
     } else {
       // ------------------------------------------------------ MMA issuers
@@ -462,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const int lrow = q4 * 32 + lane;
       const int grow_local = row_mode ? g * 128 + lrow : lrow;
       const bool row_ok = grow_local < rows_here;
+      const bool idle = grow_local - lane >= rows_here;        // a warp without rows
       const int grow = rgi * kRowsPerGroup + grow_local;
       const int jn = grow / G;
       // the group's query rows as f16 into its Q tile (key mode: one tile,
@@ -522,6 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
           ok = __all_sync(0xffffffffu, mbar_wait(bar(kSFull + 2 * g + hb), j & 1, abort_flag,
                                                  diag, 30000 + (kSFull + 2 * g + hb) * 100 + j));
           if (!ok) break;
+          if (idle) {                    // its part of P is never read back
+            mbar_arrive(bar(kPFull + 2 * g + hb));
+            continue;
+          }
           tc_fence_after();
           const uint32_t tS = tG + 64 * hb;
           const int unit_slot0 = tile_slot0 + 64 * hb;
@@ -601,19 +661,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
                               ka.out_mult);
     }
   } else {
-    regs_release<96>();
+    regs_release<88>();
     if (active && nt > 0) {
     // ---------------------------------------------------------- converters
-    const int key = (warp - 12) * 32 + lane;
+    // A lane takes one 16-byte piece pc (32 channels) of a key per round, a
+    // warp 8 keys (16 at head_dim 64), and the rounds of a warp's 32 keys are
+    // a constant apart but for a page's end.  Of eight lanes, four keys with
+    // the low bits r, the reads (piece pc of key r) and the writes (chunk
+    // 4 pc + k in place of chunk (4 pc + k) ^ key % 8) touch all banks once.
+    constexpr int NJ = D / 32;                       // rounds
+    constexpr int KPR = 32 / NJ;                     // keys of a round
     const int P = a.plan.page_size;
+    const int r = (lane >> 1) & 3, ph = lane >> 3;
+    const int pc = D == 128 ? (lane & 1) + 2 * (((lane >> 2) ^ ph) & 1) : lane & 1;
+    const int key = (warp - 12) * 32 + r + 4 * (D == 128 ? ph >> 1 : ph);
     const int pidx = key / P, off = key % P;
-    // this key's codes and scales inside a raw tile
-    const uint32_t ccode = pidx * DS_KV4_BLOCK_BYTES(P, D) + off * (D / 2);
-    const uint32_t cscale = pidx * DS_KV4_BLOCK_BYTES(P, D) + P * (D / 2) + off * (D / 16);
-    const uint32_t drow = (key >> 3) * RG + (key & 7) * 128;
+    // the first key's piece and scales inside a raw tile; the second half of
+    // the rounds is a page further on when pages have 16 keys
+    const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
+    const uint32_t ccode = pidx * blk + off * (D / 2) + pc * 16;
+    const uint32_t cscale = pidx * blk + P * (D / 2) + off * (D / 16) + pc * 2;
+    const uint32_t code_hop = P == 16 ? blk - 16 * (D / 2) : 0;
+    const uint32_t scale_hop = P == 16 ? blk - 16 * (D / 16) : 0;
+    const int bad_hop = P == 16 ? 1 : 0;
+    // chunk 4 pc + k of key % 8 is at drow ^ 16 k
+    const uint32_t drow = (key >> 3) * RG + (key & 7) * 128 + (pc >> 1) * 1024 +
+                          ((((pc & 1) * 4) ^ (key & 7)) << 4);
     const bool rep = warp == 12 && lane == 0;
     bool ok = true;
-    Walk w = walk();
+    Walk w = walk(kAll);
     while (w.take()) {
       const int slot = w.slot, n = w.n;
       const bool is_v = w.is_v;
@@ -625,39 +701,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         ok = mbar_wait(bar(kFree + (t & 1)), (t >> 1) & 1, abort_flag, diag, tag + 100000);
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      const bool bad = (ctrl->bad[slot] >> pidx) & 1u;
+      const uint32_t badm = ctrl->bad[slot] >> pidx;
       const uint32_t raw = raw_addr(slot);
       const uint32_t dst = (is_v ? sV : sK) + (n & 1) * TB + drow;
-      constexpr int NP = D / 32;           // 16-byte pieces of 32 channels
-      uint32_t s01, s23 = 0;
-      if constexpr (D == 128)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s01), "=r"(s23) : "r"(raw + cscale));
-      else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s01) : "r"(raw + cscale));
-      if (bad) s01 = s23 = 0u;             // scales of zero
-      const uint64_t sc = (uint64_t)s23 << 32 | s01;
-      uint4 c[NP];
+      uint4 c[NJ];
+      uint32_t sb[NJ];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const uint32_t pc = (j + (lane >> 1)) & (NP - 1);
+      for (int j = 0; j < NJ; ++j) {
+        const bool far = j >= NJ / 2;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(c[j].x), "=r"(c[j].y), "=r"(c[j].z), "=r"(c[j].w)
-                     : "r"(raw + ccode + pc * 16));
+                     : "r"(raw + ccode + j * KPR * (D / 2) + (far ? code_hop : 0)));
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];"
+                     : "=h"(h)
+                     : "r"(raw + cscale + j * KPR * (D / 16) + (far ? scale_hop : 0)));
+        sb[j] = (badm >> (far ? bad_hop : 0)) & 1u ? 0u : h;     // a bad page: scales of zero
       }
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const uint32_t pc = (j + (lane >> 1)) & (NP - 1);
-        const uint32_t s2 = kv4_scales_f16((uint32_t)(sc >> (16 * pc)) & 0xffffu);
+      for (int j = 0; j < NJ; ++j) {
+        const uint32_t s2 = kv4_scales_f16(sb[j]);
         const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {      // 16-byte chunk 4 pc + k of the key
           uint32_t v[4];
           kv4_codes_f16(w[k], v);
           const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
-          const uint32_t chunk = 4 * pc + k;
-          const uint32_t d = dst + (chunk >> 3) * 1024 + (((chunk & 7) ^ (key & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(hmul2(v[0], s)),
-                       "r"(hmul2(v[1], s)), "r"(hmul2(v[2], s)), "r"(hmul2(v[3], s))
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           (dst ^ (16 * k)) + j * (KPR / 8) * RG),
+                       "r"(hmul2(v[0], s)), "r"(hmul2(v[1], s)), "r"(hmul2(v[2], s)),
+                       "r"(hmul2(v[3], s))
                        : "memory");
         }
       }
