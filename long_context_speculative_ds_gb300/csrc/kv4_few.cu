@@ -43,8 +43,6 @@
 #include <math_constants.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 #include "dev_common.cuh"
 #include "internal.h"
 #include "kv4_common.cuh"
@@ -698,12 +696,15 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
       acc.x = fmaf(f, v.x, acc.x);
       acc.y = fmaf(f, v.y, acc.y);
     }
-    void* const dst = pc.n_slots == 1 ? a.out : static_cast<void*>(a.o_part);
-    const int64_t at = (pc.n_slots == 1 ? out_row(r) : (int64_t)pc.slot * R + r) * D + 2 * c;
-    if (a.out_f32)
-      *reinterpret_cast<float2*>(static_cast<float*>(dst) + at) = acc;
+    const bool whole = pc.n_slots == 1;
+    const int64_t at = (whole ? out_row(r) : (int64_t)pc.slot * R + r) * D + 2 * c;
+    if (!whole)
+      *reinterpret_cast<float2*>(a.o_part + at) = acc;
+    else if (a.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) = acc;
     else
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(dst) + at) = pack_bf16x2(acc.x, acc.y);
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+          pack_bf16x2(acc.x, acc.y);
   }
   if (pc.n_slots > 1 && threadIdx.x == 0) ctrl.cut[ctrl.n_cut++] = pc;
   __syncthreads();                 // the ring and ctrl are the next piece's
@@ -750,68 +751,57 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __g
   // a thread per two columns of a row; the pieces' log2-sum-exps and outputs
   // come in one round trip, NB at a time
   const int G = a.plan.group;
-  const auto columns = [&](auto f32) {
-    constexpr bool F32 = decltype(f32)::value;
-    constexpr int NB = 20;
-    for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
-      const int y = x / (D / 2), col = x % (D / 2) * 2;
-      const Piece& c = ctrl.cut[y >= n0];
-      const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r, ns = c.n_slots;
-      const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
-      const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
-      float mm = -CUDART_INF_F, sum = 0.f;
-      float2 acc = make_float2(0.f, 0.f);
-      for (int k0 = 0; k0 < ns; k0 += NB) {
-        float w[NB];
-        float2 v[NB];
+  constexpr int NB = 20;
+  for (int x = threadIdx.x; x < (n0 + n1) * (D / 2); x += 32 * W) {
+    const int y = x / (D / 2), col = x % (D / 2) * 2;
+    const Piece& c = ctrl.cut[y >= n0];
+    const int r = y >= n0 ? y - n0 : y, grow = c.rgi * R + r, ns = c.n_slots;
+    const float* lp = a.lse_part + (int64_t)c.first_slot * R + r;
+    const int64_t o = ((int64_t)c.first_slot * R + r) * D + col;
+    float mm = -CUDART_INF_F, sum = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int k0 = 0; k0 < ns; k0 += NB) {
+      float w[NB];
+      float2 v[NB];
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          w[k] = -CUDART_INF_F;
-          v[k] = make_float2(0.f, 0.f);
-          if (k0 + k >= ns) continue;
-          const int64_t at = o + (int64_t)(k0 + k) * R * D;
-          w[k] = __ldcg(lp + (int64_t)(k0 + k) * R);
-          if constexpr (F32) {
-            v[k] = __ldcg(reinterpret_cast<const float2*>(a.o_part + at));
-          } else {
-            const uint32_t u = __ldcg(reinterpret_cast<const uint32_t*>(
-                reinterpret_cast<const uint16_t*>(a.o_part) + at));
-            v[k] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-          }
-        }
-        float nm = mm;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) nm = fmaxf(nm, w[k]);
-        const float mb = nm == -CUDART_INF_F ? 0.f : nm, f = ptx::ex2(mm - mb);
-        mm = nm;
-        sum *= f;
-        acc.x *= f;
-        acc.y *= f;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          const float e = ptx::ex2(w[k] - mb);
-          sum += e;
-          // a piece that saw nothing wrote zeros, or NaN for a query that is
-          // not a number; that stays
-          acc.x = fmaf(e, v[k].x, acc.x);
-          acc.y = fmaf(e, v[k].y, acc.y);
-        }
+      for (int k = 0; k < NB; ++k) {
+        w[k] = -CUDART_INF_F;
+        v[k] = make_float2(0.f, 0.f);
+        if (k0 + k >= ns) continue;
+        const int64_t at = o + (int64_t)(k0 + k) * R * D;
+        w[k] = __ldcg(lp + (int64_t)(k0 + k) * R);
+        v[k] = __ldcg(reinterpret_cast<const float2*>(a.o_part + at));
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-      const int64_t row = ((int64_t)c.kvh * a.plan.n_nodes + c.node0) * G + grow;
-      if (col == 0) a.row_lse[row] = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
-      const int64_t at =
-          (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
-      if constexpr (F32)
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) =
-            make_float2(acc.x * inv, acc.y * inv);
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
-            ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+      float nm = mm;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) nm = fmaxf(nm, w[k]);
+      const float mb = nm == -CUDART_INF_F ? 0.f : nm, f = ptx::ex2(mm - mb);
+      mm = nm;
+      sum *= f;
+      acc.x *= f;
+      acc.y *= f;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const float e = ptx::ex2(w[k] - mb);
+        sum += e;
+        // a piece that saw nothing wrote zeros, or NaN for a query that is
+        // not a number; that stays
+        acc.x = fmaf(e, v[k].x, acc.x);
+        acc.y = fmaf(e, v[k].y, acc.y);
+      }
     }
-  };
-  if (a.out_f32) columns(std::true_type{});
-  else columns(std::false_type{});
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t row = ((int64_t)c.kvh * a.plan.n_nodes + c.node0) * G + grow;
+    if (col == 0) a.row_lse[row] = sum > 0.f ? mm + __log2f(sum) : -CUDART_INF_F;
+    const int64_t at =
+        (((int64_t)c.node0 + grow / G) * a.num_q_heads + c.kvh * G + grow % G) * D + col;
+    if (a.out_f32)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at) =
+          make_float2(acc.x * inv, acc.y * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at) =
+          ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+  }
 }
 
 // Chunk scores: the sum over kv heads and rows of 2^(mass - the row's

@@ -654,11 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       const int64_t orow = ((int64_t)blockIdx.x * kRowsPerGroup + warp_row0) * D;
       void* op_warp = a.out_f32 ? static_cast<void*>(a.o_part + orow)
                                 : static_cast<void*>(
-                                      reinterpret_cast<__nv_bfloat16*>(a.o_part) + orow);
-      tc::write_row_output<D>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l,
+                                      reinterpret_cast<uint16_t*>(a.o_part) + orow);
+      // A split's output is a weighted mean of code x scale, at most 2688: f16
+      // holds it with three more bits than bf16, to 2^-25 at worst; the
+      // cache's exponent is applied where the splits meet.
+      tc::write_row_output<D, true>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l,
                               merge_buf, m1buf, l1buf, stage, !a.out_f32, op_warp,
                               a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
-                              ka.out_mult);
+                              a.out_f32 ? ka.out_mult : 1.f);
     }
   } else {
     regs_release<88>();
@@ -795,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
 constexpr int kFinCombos = 2;
 
 template <int D, bool HALF>
-DS_DEV void merge_row(const VerifyKArgs& a, int blk) {
+DS_DEV void merge_row(const VerifyKArgs& a, int blk, float out_mult) {
   const int lane = threadIdx.x & 31;
   const int64_t x = (int64_t)blk * 8 + (threadIdx.x >> 5);
   const int node = (int)(x / a.num_q_heads), qh = (int)(x - (int64_t)node * a.num_q_heads);
@@ -817,7 +820,8 @@ DS_DEV void merge_row(const VerifyKArgs& a, int blk) {
   if (row < 0 || row >= sq.rows) return;          // not a row of a usable sequence
   const int4 gd = __ldcg(a.gdesc + grp);
   const float lse = __ldcg(a.row_lse + grp * kRowsPerGroup + r);
-  combine_row_splits<D, HALF, HALF ? (D == 128 ? 20 : 32) : 8>(a, gd.x, gd.y, r, lse, x);
+  combine_row_splits<D, HALF, HALF ? (D == 128 ? 20 : 32) : 8, HALF>(a, gd.x, gd.y, r, lse, x,
+                                                                     out_mult);
 }
 
 DS_DEV void chunk_score(const VerifyKArgs& a, int blk) {
@@ -869,10 +873,10 @@ DS_DEV void chunk_score(const VerifyKArgs& a, int blk) {
 
 template <int D>
 __global__ void __launch_bounds__(256, 4) kv4_finish(const __grid_constant__ VerifyKArgs a,
-                                                     int n_comb) {
+                                                     int n_comb, float out_mult) {
   if ((int)blockIdx.x >= n_comb) chunk_score(a, blockIdx.x - n_comb);
-  else if (a.out_f32) merge_row<D, false>(a, blockIdx.x);
-  else merge_row<D, true>(a, blockIdx.x);
+  else if (a.out_f32) merge_row<D, false>(a, blockIdx.x, out_mult);
+  else merge_row<D, true>(a, blockIdx.x, out_mult);
 }
 
 }  // namespace kv4tc
@@ -894,7 +898,7 @@ static cudaError_t launch_tc(const Kv4KArgs& k, const VerifyLayout& L, cudaStrea
   const int64_t n_comb = ((int64_t)v.plan.n_nodes * v.num_q_heads + 7) / 8;
   const int64_t n_fin = v.scores ? (int64_t)v.plan.batch * ((v.plan.max_chunks + 7) / 8) : 0;
   return launch_dependent(kv4tc::kv4_finish<D>, dim3((unsigned)(n_comb + n_fin)), dim3(256), 0,
-                          stream, v, (int)n_comb);
+                          stream, v, (int)n_comb, k.out_mult);
 }
 
 // The whole call for trees.

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "dev_common.cuh"
@@ -37,10 +38,11 @@ struct VerifyKArgs {
 // lane-parallel over splits and the weights broadcast from the lane that
 // holds split s.  NB splits per round trip.  Split outputs are bf16 (HALF)
 // or f32; the result goes to out row out_row ([n_nodes * num_q_heads] rows
-// of head_dim) in the output dtype.
-template <int D, bool HALF, int NB>
+// of head_dim) in the output dtype.  F16: HALF outputs are f16, and the sum
+// is multiplied by mult.
+template <int D, bool HALF, int NB, bool F16 = false>
 DS_DEV void combine_row_splits(const VerifyKArgs& a, int64_t base, int ns, int r, float lse,
-                               int64_t out_row) {
+                               int64_t out_row, float mult = 1.f) {
   static_assert(NB <= 32, "split weights are held one per lane");
   const int lane = threadIdx.x & 31;
   const float* lp = a.lse_part + base * kRowsPerGroup + r;
@@ -80,7 +82,9 @@ DS_DEV void combine_row_splits(const VerifyKArgs& a, int64_t base, int ns, int r
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           float xv;
-          if constexpr (HALF)   // bf16 pair: element 2i in the low half
+          if constexpr (HALF && F16)
+            xv = __half2float(__ushort_as_half((unsigned short)(x[k][e >> 1] >> (16 * (e & 1)))));
+          else if constexpr (HALF)   // bf16 pair: element 2i in the low half
             xv = __uint_as_float((e & 1) ? (x[k][e >> 1] & 0xffff0000u) : (x[k][e >> 1] << 16));
           else
             xv = __uint_as_float(x[k][e]);
@@ -89,6 +93,9 @@ DS_DEV void combine_row_splits(const VerifyKArgs& a, int64_t base, int ns, int r
       }
     }
   }
+  if constexpr (F16)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= mult;
   const int64_t obase = out_row * D + lane * E;
   if (a.out_f32) {
     float* out = reinterpret_cast<float*>(a.out) + obase;
