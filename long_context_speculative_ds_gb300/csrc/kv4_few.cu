@@ -12,6 +12,13 @@
 //   S^T[16 keys, 8 rows] += K[16 keys, 16 channels] Q^T[16 channels, 8 rows]
 //   O^T[16 dims, 8 rows] += V^T[16 dims, 16 keys]  P^T[16 keys, 8 rows]
 //
+// One token over 128K (32 query heads on 8 of the cache, 151 MB) takes 48.6
+// us, 3.1 TB/s of the 6.78 a copy reaches; without the products it takes 39,
+// without the loads 44: conversions and products (26.6 M warp instructions,
+// the issue slots 46 % busy) and the stream overlap, and some 15 us go into
+// the start, the merge, the join and the salience.  A ragged batch of eight
+// (4K to 128K, no salience) takes 89 us, 4.5 TB/s.
+//
 // Which channels make up a step of the first product, and which dims a tile
 // of the second, is free as long as both operands agree.  Lane 4g + t takes
 // the channels from 32t on of its two keys (two scale groups), and dims 16g
@@ -22,8 +29,8 @@
 // transposed (movmatrix).
 //
 // Of 16 keys, fragment row i holds key i ^ ((i >> 1) & 1), and keys 4-7 and
-// 12-15 have the halves of their 16-byte pieces exchanged: then eight lanes of a 16-byte read and 16 lanes of an 8-byte read touch every
-// bank once.
+// 12-15 have the halves of their 16-byte pieces exchanged: then eight lanes
+// of a 16-byte read and 16 lanes of an 8-byte read touch every bank once.
 //
 // Work: every (sequence, kv head, group of 8 NT query rows) is a segment of
 // 32-key units, and the units of all segments, in order, are dealt to the
@@ -868,8 +875,12 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
 
 }  // namespace kv4few
 
+// Up to 8 rows a segment the queries stay in registers beside 16 warps (2
+// nodes of 4 rows over 128K: 60 us); above, two tiles of 8 need the shared
+// memory and leave room for 12 (3 nodes: 74 us; with 16 warps and the queries
+// in registers, spilled, 4 nodes took 99 instead of 76).
 cudaError_t launch_kv4_few(const Kv4KArgs& k, int head_dim, int rows, const VerifyLayout& L,
-                                 cudaStream_t stream) {
+                           cudaStream_t stream) {
   using kv4few::launch;
   if (rows <= 8) return head_dim == 128 ? launch<128, 1>(k, L, stream) : launch<64, 1>(k, L, stream);
   return head_dim == 128 ? launch<128, 2>(k, L, stream) : launch<64, 2>(k, L, stream);

@@ -1,12 +1,25 @@
 // Split pass of ds_kv4_verify_attn for trees, on the 5th-generation tensor
-// cores (tcgen05) of sm_103a.
+// cores (tcgen05) of sm_103a, and the pass that joins the splits.
 //
-// The tree-verify split pass of the bf16 cache (verify_tc.cu: work items,
-// softmax groups, tensor-memory slots, P V / Q K order, split outputs) over
-// tiles that arrive in 4 bits and are brought to f16 in shared memory, where
-// code x scale is exact.  Rows of 72 bytes a key instead of 256 take the
-// stream of K and V off the critical path: with 256 query rows the tensor
-// pipe and the exponentials bound the kernel.
+// softmax(scale Q K^T) V by one pass over the keys with a running reference
+// point and sum per row, as in the bf16 cache's split pass (verify_tc.cu:
+// work items, softmax groups, P V / Q K order, split outputs), over tiles of
+// 128 keys that arrive in 4 bits and are brought to f16 in shared memory,
+// where code x scale is exact.  P is f16 too, with a reference point 2^7
+// below the row's maximum (verify_softmax.cuh).
+//
+// The two products of 256 query rows with 128K keys of eight heads (137
+// GFLOP) are 72 us of the tensor pipe at its measured rate; the 151 MB of the
+// cache are 22 us.  A call over 64 nodes and 32 query heads takes 124 us, 1.11
+// PFLOP/s or 58 %: about 25 us go into the start (plan, Q, first tiles), the
+// split outputs and the join, and in between a tile takes 1.8 us: 1.2 of
+// products, 1.2 of softmax (0.9 with nothing beside it) and 0.7 of conversion
+// share issue slots and wait for one another.
+//
+// More than 128 rows ("row mode"): each of two softmax groups has a tile of
+// 128 rows and goes through all keys.  Up to 128 rows ("key mode"): both
+// groups have the same rows and take every other tile of keys; their outputs
+// are merged in the end.  A tile takes 1.2 us in key mode, 1.8 in row mode.
 //
 // 16 warps:
 //   warp 0      loader: page blocks (codes and scales of one page of one kv
@@ -14,14 +27,17 @@
 //               pages past the sequence end are not copied (no byte of the
 //               cache format reads as NaN or infinity, and their weights are
 //               zero), bad pages are marked and read as zeros.
-//   warp 1      tensor-memory allocator and ancestor masks.
+//   warp 1      tensor-memory allocator and ancestor masks; in key mode then
+//               V's loader, with a ring of its own (one loader for both was
+//               the slowest part there: 106 us against 99 for 8 nodes over
+//               128K).  In row mode one keeps up, and there is no room.
 //   warps 2, 3  MMA issuers of softmax groups 0 and 1.
 //   warps 4-7, 8-11   softmax groups; at the start they also bring Q to f16.
-//   warps 12-15 converters: a key per thread.  Each thread reads its key's
-//               codes in 16-byte pieces, starting at a piece that depends on
-//               the lane so that eight lanes touch all banks, and writes
-//               16-byte chunks in the 128-byte-swizzled layout the MMA
-//               descriptors expect (eight lanes, eight bank groups).
+//   warps 12-15 converters, 32 keys of a tile a warp.  Four warps do: a
+//               second team, with 20 warps and fewer registers each, made a
+//               row-mode call 152 us instead of 125, and reading the cache
+//               into registers without the raw ring a key-mode call 148
+//               instead of 106.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -43,9 +59,8 @@ constexpr int kTmemCols = 512;
 constexpr int kRing = 3;         // raw slots of a ring: one for K and V in row mode, one
                                  // for each in key mode (V's in the unused second Q tile)
 
-// A commit holds up the products behind it (about 0.1 us each here), so a
-// barrier is completed by few of them: one per 64-key unit of a group, when
-// its P V and the next tile's S are done, and one per tile, when with the
+// The products complete two kinds of barrier: one per 64-key unit of a group,
+// when its P V and the next tile's S are done, and one per tile, when with the
 // tile's last S its K and an earlier tile's V are free.
 enum Bar {
   kQFull = 0,
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   auto ntiles = [&](int g) { return row_mode ? nt : (nt - g + 1) / 2; };
   auto tile_of = [&](int g, int j) { return row_mode ? j : 2 * j + g; };
 
-  // registers move from the loader's and the converters' warpgroups to the
+  // registers (all of them in use) move from the loader's and the converters' warpgroups to the
   // softmax groups: 128 (88 + 88) + 256 x 168 = the launch's 512 x 128
   static_assert(128 * (88 + 88) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
@@ -789,7 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   }
 }
 
-// Second launch: the first n_comb blocks merge the splits of the output rows,
+// Second launch, bound by the round trips to the L2 (8 us of a 64-node call):
+// the first n_comb blocks merge the splits of the output rows,
 // a warp per (node, query head); the rest form the chunk scores, a warp per
 // (chunk, sequence), four rows a lane, kFinCombos (kv head, row group)
 // combinations per round trip.  What only depends on the call's inputs is

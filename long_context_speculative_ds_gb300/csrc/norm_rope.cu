@@ -1,7 +1,14 @@
 // RMS norm of every query and key head with the position rotation in the
 // same pass (include/ds.h, ds_qk_norm_rope).
 //
-// Bound by memory when there are many rows, by latency when there are few.
+// y = x w / sqrt(mean(x^2) + eps), then each pair (a, b) half a head apart to
+// (a cos - b sin, a sin + b cos), in float32 with one rounding to bf16.
+//
+// Bound by memory when there are many rows, by latency when there are few:
+// with 32 + 8 heads of 128, 32,768 rows take 112 us, 6.0 TB/s of the 6.78 a
+// copy reaches; 331 rows 4.5 us and one row 3.5 us, a launch and two round
+// trips.  (A warp per row and one head at a time took 161, 10 and 9 us.)
+//
 // Eight lanes hold one head (head_dim 128; four at 64): lane l the eight
 // values from 8l of the head's first half and the eight opposite them in the
 // second, so that a lane owns whole rotation pairs, reads and writes 16-byte
