@@ -42,6 +42,8 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dev_common.cuh"
 #include "internal.h"
 #include "kv4_common.cuh"
@@ -907,10 +909,15 @@ static cudaError_t launch_tc(const Kv4KArgs& k, const VerifyLayout& L, cudaStrea
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  cudaError_t e = launch_dependent(kv4tc::kv4_split_tc<D>, dim3(L.max_items),
+  const VerifyKArgs& v = k.v;
+  // The plan makes at most one item per SM, two in its two-wave form, or one
+  // per row group.  No blocks beyond that: one without work still takes an
+  // SM's turn, behind the last items when those end together.
+  const int64_t groups = (int64_t)v.plan.batch * v.plan.num_kv_heads * v.plan.rg_max;
+  const int64_t blocks = std::max<int64_t>(groups, std::max(L.target_ctas, L.wave_ctas));
+  cudaError_t e = launch_dependent(kv4tc::kv4_split_tc<D>, dim3((unsigned)blocks),
                                    dim3(kv4tc::kThreads), smem, stream, k);
   if (e != cudaSuccess) return e;
-  const VerifyKArgs& v = k.v;
   const int64_t n_comb = ((int64_t)v.plan.n_nodes * v.num_q_heads + 7) / 8;
   const int64_t n_fin = v.scores ? (int64_t)v.plan.batch * ((v.plan.max_chunks + 7) / 8) : 0;
   return launch_dependent(kv4tc::kv4_finish<D>, dim3((unsigned)(n_comb + n_fin)), dim3(256), 0,
