@@ -668,3 +668,23 @@ def test_attention_other_stream_and_graph():
     o, A, sr = _oracle_attn(c, q, [899, 29], offs, par, 64)
     torch.cuda.synchronize()
     _check_attn(out, None, o, A, None, lens, None)
+
+
+@pytest.mark.parametrize("trees,page,d", [([20, 50], 16, 128), ([9, 32], 128, 128),
+                                          ([33, 5], 32, 64), ([2, 3], 16, 128)])
+@pytest.mark.parametrize("num_sms", [1, 9, 0])
+def test_attention_rows_above_and_below_a_tile(trees, page, d, num_sms):
+    # 4 query heads on a kv head: up to 32 nodes share one tile of 128 rows.
+    # Splits are f16 or wider: 2^-11 A instead of a bf16 split's 2^-8 A, and
+    # the bf16 output's own rounding of a value that is that far off already
+    lens = [3001, 1500]
+    c, q, offs, par = _attn_case(lens, trees, 8, 2, d, page, seed=11)
+    o, A, s = _oracle_attn(c, q, lens, offs, par, 128)
+    out, sc, st, _ = _run_attn(c, q, lens, offs, par, 128, torch.bfloat16, num_sms=num_sms)
+    assert st == 0
+    err = np.abs(f64(out) - o)
+    bound = (2 * 2.0 ** -11 + 2.0 ** -12) * A + 2.0 ** -8 * np.abs(o) + 2.0 ** -17 * A
+    assert (err <= bound).all(), (err / bound).max()
+    for b, L in enumerate(lens):
+        n = -(-L // 128)
+        assert (np.abs(f64(sc)[b, :n] - s[b, :n]) <= 2.5e-4 * s[b, :n]).all()
