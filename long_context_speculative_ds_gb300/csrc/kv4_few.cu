@@ -718,7 +718,8 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1) kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
+__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 1)
+kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
   constexpr int W = Cfg<D, NT>::W, R = Cfg<D, NT>::R;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ Ctrl ctrl;
@@ -882,7 +883,8 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
 cudaError_t launch_kv4_few(const Kv4KArgs& k, int head_dim, int rows, const VerifyLayout& L,
                            cudaStream_t stream) {
   using kv4few::launch;
-  if (rows <= 8) return head_dim == 128 ? launch<128, 1>(k, L, stream) : launch<64, 1>(k, L, stream);
+  if (rows <= 8)
+    return head_dim == 128 ? launch<128, 1>(k, L, stream) : launch<64, 1>(k, L, stream);
   return head_dim == 128 ? launch<128, 2>(k, L, stream) : launch<64, 2>(k, L, stream);
 }
 

@@ -242,7 +242,8 @@ static cudaError_t launch_rows(const ds_kv4_rows_args& g, cudaStream_t stream) {
   const int64_t groups = (total + rw - 1) / rw;
   // enough warps to fill the machine (152 SMs of 32), one unit a warp at least
   const int units = 2 * g.num_kv_heads;
-  a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(units, kRowWarps / std::max<int64_t>(1, groups)));
+  const int64_t spread = kRowWarps / std::max<int64_t>(1, groups);
+  a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(units, spread));
   const dim3 grid((unsigned)std::max<int64_t>(1, (groups * a.slices + 7) / 8));
   if (g.head_dim == 128)
     return launch_dependent(kv4_rows<128, WRITE>, grid, dim3(256), 0, stream, a);

@@ -352,8 +352,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   auto ntiles = [&](int g) { return row_mode ? nt : (nt - g + 1) / 2; };
   auto tile_of = [&](int g, int j) { return row_mode ? j : 2 * j + g; };
 
-  // registers (all of them in use) move from the loader's and the converters' warpgroups to the
-  // softmax groups: 128 (88 + 88) + 256 x 168 = the launch's 512 x 128
+  // registers move from the loader's and the converters' warpgroups to the
+  // softmax groups: 128 (88 + 88) + 256 x 168 = the launch's 512 x 128.  At 80
+  // the issuers spill.
   static_assert(128 * (88 + 88) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
     regs_release<88>();
@@ -365,82 +366,82 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         mbar_arrive(bar(kAnc));
       }
       if (warp == 0 || !row_mode) {
-      // ------------------------------------------------------------ loader
-      const int P = a.plan.page_size;
-      const int npg = kTileKeys / P;
-      const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
-      const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
-      const uint64_t policy = l2_evict_first();
-      // Page ids come 32 at a time, a run of 32 / npg tiles, the next run on
-      // its way (a load per tile would put its latency into every tile's
-      // turn), and are checked together; lane r of a run holds page r of it.
-      // V is at most two tiles behind K and walks its own runs.
-      const int rshift = __ffs(P) - 1 - 2;       // log2 of the tiles of a run, P / 4
-      const int run = 1 << rshift, pend = (L + T + P - 1) / P;
-      const uint32_t page_bytes = a.plan.num_kv_heads * blk;
-      struct Side {                              // of K, of V
-        const uint8_t* head;
-        int ids, next;
-        uint32_t bad;
-      } side[2];
-      auto ids_of = [&](int r) {
-        const int pi = (t0 + r * run) * npg + lane;
-        return pi < pend ? __ldg(ptab + pi) : 0;
-      };
-      auto check = [&](Side& x) {
-        const bool bad = (uint32_t)x.ids >= (uint32_t)a.num_pages;
-        if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
-        x.bad = __ballot_sync(0xffffffffu, bad);
-      };
+        // ------------------------------------------------------------ loader
+        const int P = a.plan.page_size;
+        const int npg = kTileKeys / P;
+        const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
+        const int32_t* ptab = a.page_table + (int64_t)p.b * a.plan.max_pages;
+        const uint64_t policy = l2_evict_first();
+        // Page ids come 32 at a time, a run of 32 / npg tiles, the next run on
+        // its way (a load per tile would put its latency into every tile's
+        // turn), and are checked together; lane r of a run holds page r of it.
+        // K and V walk their own runs.
+        const int rshift = __ffs(P) - 1 - 2;       // log2 of the tiles of a run, P / 4
+        const int run = 1 << rshift, pend = (L + T + P - 1) / P;
+        const uint32_t page_bytes = a.plan.num_kv_heads * blk;
+        struct Side {                              // of K, of V
+          const uint8_t* head;
+          int ids, next;
+          uint32_t bad;
+        } side[2];
+        auto ids_of = [&](int r) {
+          const int pi = (t0 + r * run) * npg + lane;
+          return pi < pend ? __ldg(ptab + pi) : 0;
+        };
+        auto check = [&](Side& x) {
+          const bool bad = (uint32_t)x.ids >= (uint32_t)a.num_pages;
+          if (bad) flag(a.plan.status, DS_DEV_BAD_PAGE);
+          x.bad = __ballot_sync(0xffffffffu, bad);
+        };
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        side[v].head = (v ? ka.v4 : ka.k4) + (int64_t)kvh * blk;
-        side[v].ids = ids_of(0);
-        side[v].next = ids_of(1);
-        check(side[v]);
-      }
-      bool ok = true;
-      const uint32_t pmask = npg == 8 ? 0xffu : (1u << npg) - 1u;
-      Walk w = walk(row_mode ? kAll : warp == 0 ? kOnlyK : kOnlyV);
-      auto load = [&](Side& x) {
-        const int in_run = w.n & (run - 1);
-        if (w.n > 0 && in_run == 0) {
-          x.ids = x.next;
-          x.next = ids_of((w.n >> rshift) + 1);
-          check(x);
+        for (int v = 0; v < 2; ++v) {
+          side[v].head = (v ? ka.v4 : ka.k4) + (int64_t)kvh * blk;
+          side[v].ids = ids_of(0);
+          side[v].next = ids_of(1);
+          check(side[v]);
         }
-        const uint32_t pg = __shfl_sync(0xffffffffu, x.ids, (in_run * npg + lane) & 31);
-        const uint32_t badm = (x.bad >> (in_run * npg)) & pmask;
-        const int left = pend - (t0 + w.n) * npg;          // pages of the sequence from here on
-        const bool have = lane < min(npg, left) && !((badm >> lane) & 1u);
-        const int n = min(npg, left) - __popc(badm);
-        const uint32_t full = bar(kRawFull + w.slot);
-        const uint32_t tag = 10000 + 2 * w.n + (w.is_v ? 1 : 0);
-        if (lane == 0 && warp == 0) ctrl->where[0] = tag;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
-                                               diag, tag)))
-          return false;
-        if (lane == 0) {
-          ctrl->bad[w.slot] = badm;
-          mbar_arrive_expect_tx(full, n * blk);
+        bool ok = true;
+        const uint32_t pmask = npg == 8 ? 0xffu : (1u << npg) - 1u;
+        Walk w = walk(row_mode ? kAll : warp == 0 ? kOnlyK : kOnlyV);
+        auto load = [&](Side& x) {
+          const int in_run = w.n & (run - 1);
+          if (w.n > 0 && in_run == 0) {
+            x.ids = x.next;
+            x.next = ids_of((w.n >> rshift) + 1);
+            check(x);
+          }
+          const uint32_t pg = __shfl_sync(0xffffffffu, x.ids, (in_run * npg + lane) & 31);
+          const uint32_t badm = (x.bad >> (in_run * npg)) & pmask;
+          const int left = pend - (t0 + w.n) * npg;          // pages of the sequence from here on
+          const bool have = lane < min(npg, left) && !((badm >> lane) & 1u);
+          const int n = min(npg, left) - __popc(badm);
+          const uint32_t full = bar(kRawFull + w.slot);
+          const uint32_t tag = 10000 + 2 * w.n + (w.is_v ? 1 : 0);
+          if (lane == 0 && warp == 0) ctrl->where[0] = tag;
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(kRawEmpty + w.slot), w.phase ^ 1, abort_flag,
+                                                 diag, tag)))
+            return false;
+          if (lane == 0) {
+            ctrl->bad[w.slot] = badm;
+            mbar_arrive_expect_tx(full, n * blk);
+          }
+          __syncwarp();
+          if (have)
+            bulk_load_hint(raw_addr(w.slot) + lane * blk, x.head + (uint64_t)pg * page_bytes, blk,
+                           full, policy);
+          return true;
+        };
+        while (w.take()) {
+          ok = w.is_v ? load(side[1]) : load(side[0]);
+          if (!ok) break;
+          w.release();
         }
-        __syncwarp();
-        if (have)
-          bulk_load_hint(raw_addr(w.slot) + lane * blk, x.head + (uint64_t)pg * page_bytes, blk,
-                         full, policy);
-        return true;
-      };
-      while (w.take()) {
-        ok = w.is_v ? load(side[1]) : load(side[0]);
-        if (!ok) break;
-        w.release();
-      }
-      if (lane == 0 && warp == 0) ctrl->where[0] = ok ? 19999 : 19998;
-      // copies still in flight must land before the CTA can exit: each slot's
-      // last phase (a slot not used yet passes at once)
-      if (!ok && lane == 0)
-        for (int s0 = w.slot < kRing ? 0 : kRing, i = s0; i < s0 + kRing; ++i)
-          drain_wait(bar(kRawFull + i), i >= w.slot ? w.phase ^ 1 : w.phase);
+        if (lane == 0 && warp == 0) ctrl->where[0] = ok ? 19999 : 19998;
+        // copies still in flight must land before the CTA can exit: each slot's
+        // last phase (a slot not used yet passes at once)
+        if (!ok && lane == 0)
+          for (int s0 = w.slot < kRing ? 0 : kRing, i = s0; i < s0 + kRing; ++i)
+            drain_wait(bar(kRawFull + i), i >= w.slot ? w.phase ^ 1 : w.phase);
       }
     } else {
       // ------------------------------------------------------ MMA issuers
@@ -632,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
             // done with the other half's next S
             if (lrow == 0) ctrl->where[wi] = 35000 + u;
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(bar(kSFull + 2 * g + 1 - hb), (hb ? j + 1 : j) & 1, abort_flag,
-                                      diag, 35000 + u));
+                            mbar_wait(bar(kSFull + 2 * g + 1 - hb), (hb ? j + 1 : j) & 1,
+                                      abort_flag, diag, 35000 + u));
             if (ok) {
               tc_fence_after();
 #pragma unroll 1
@@ -676,92 +677,92 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       // holds it with three more bits than bf16, to 2^-25 at worst; the
       // cache's exponent is applied where the splits meet.
       tc::write_row_output<D, true>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l,
-                              merge_buf, m1buf, l1buf, stage, !a.out_f32, op_warp,
-                              a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
-                              a.out_f32 ? ka.out_mult : 1.f);
+                                    merge_buf, m1buf, l1buf, stage, !a.out_f32, op_warp,
+                                    a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
+                                    a.out_f32 ? ka.out_mult : 1.f);
     }
   } else {
     regs_release<88>();
     if (active && nt > 0) {
-    // ---------------------------------------------------------- converters
-    // A lane takes one 16-byte piece pc (32 channels) of a key per round, a
-    // warp 8 keys (16 at head_dim 64), and the rounds of a warp's 32 keys are
-    // a constant apart but for a page's end.  Of eight lanes, four keys with
-    // the low bits r, the reads (piece pc of key r) and the writes (chunk
-    // 4 pc + k in place of chunk (4 pc + k) ^ key % 8) touch all banks once.
-    constexpr int NJ = D / 32;                       // rounds
-    constexpr int KPR = 32 / NJ;                     // keys of a round
-    const int P = a.plan.page_size;
-    const int r = (lane >> 1) & 3, ph = lane >> 3;
-    const int pc = D == 128 ? (lane & 1) + 2 * (((lane >> 2) ^ ph) & 1) : lane & 1;
-    const int key = (warp - 12) * 32 + r + 4 * (D == 128 ? ph >> 1 : ph);
-    const int pidx = key / P, off = key % P;
-    // the first key's piece and scales inside a raw tile; the second half of
-    // the rounds is a page further on when pages have 16 keys
-    const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
-    const uint32_t ccode = pidx * blk + off * (D / 2) + pc * 16;
-    const uint32_t cscale = pidx * blk + P * (D / 2) + off * (D / 16) + pc * 2;
-    const uint32_t code_hop = P == 16 ? blk - 16 * (D / 2) : 0;
-    const uint32_t scale_hop = P == 16 ? blk - 16 * (D / 16) : 0;
-    const int bad_hop = P == 16 ? 1 : 0;
-    // chunk 4 pc + k of key % 8 is at drow ^ 16 k
-    const uint32_t drow = (key >> 3) * RG + (key & 7) * 128 + (pc >> 1) * 1024 +
-                          ((((pc & 1) * 4) ^ (key & 7)) << 4);
-    const bool rep = warp == 12 && lane == 0;
-    bool ok = true;
-    Walk w = walk(kAll);
-    while (w.take()) {
-      const int slot = w.slot, n = w.n;
-      const bool is_v = w.is_v;
-      const uint32_t tag = 40000 + 2 * n + (is_v ? 1 : 0);
-      if (rep) ctrl->where[5] = tag;
-      ok = mbar_wait(bar(kRawFull + slot), w.phase, abort_flag, diag, tag);
-      if (ok && n >= 2) {                // the tile two before has been used
-        const int t = is_v ? (row_mode ? n - 1 : n) : n - 2;
-        ok = mbar_wait(bar(kFree + (t & 1)), (t >> 1) & 1, abort_flag, diag, tag + 100000);
-      }
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t badm = ctrl->bad[slot] >> pidx;
-      const uint32_t raw = raw_addr(slot);
-      const uint32_t dst = (is_v ? sV : sK) + (n & 1) * TB + drow;
-      uint4 c[NJ];
-      uint32_t sb[NJ];
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const bool far = j >= NJ / 2;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(c[j].x), "=r"(c[j].y), "=r"(c[j].z), "=r"(c[j].w)
-                     : "r"(raw + ccode + j * KPR * (D / 2) + (far ? code_hop : 0)));
-        uint16_t h;
-        asm volatile("ld.shared.u16 %0, [%1];"
-                     : "=h"(h)
-                     : "r"(raw + cscale + j * KPR * (D / 16) + (far ? scale_hop : 0)));
-        sb[j] = (badm >> (far ? bad_hop : 0)) & 1u ? 0u : h;     // a bad page: scales of zero
-      }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint32_t s2 = kv4_scales_f16(sb[j]);
-        const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {      // 16-byte chunk 4 pc + k of the key
-          uint32_t v[4];
-          kv4_codes_f16(w[k], v);
-          const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           (dst ^ (16 * k)) + j * (KPR / 8) * RG),
-                       "r"(hmul2(v[0], s)), "r"(hmul2(v[1], s)), "r"(hmul2(v[2], s)),
-                       "r"(hmul2(v[3], s))
-                       : "memory");
+      // ---------------------------------------------------------- converters
+      // A lane takes one 16-byte piece pc (32 channels) of a key per round, a
+      // warp 8 keys (16 at head_dim 64), and the rounds of a warp's 32 keys are
+      // a constant apart but for a page's end.  Of eight lanes, four keys with
+      // the low bits r, the reads (piece pc of key r) and the writes (chunk
+      // 4 pc + k in place of chunk (4 pc + k) ^ key % 8) touch all banks once.
+      constexpr int NJ = D / 32;                       // rounds
+      constexpr int KPR = 32 / NJ;                     // keys of a round
+      const int P = a.plan.page_size;
+      const int r = (lane >> 1) & 3, ph = lane >> 3;
+      const int pc = D == 128 ? (lane & 1) + 2 * (((lane >> 2) ^ ph) & 1) : lane & 1;
+      const int key = (warp - 12) * 32 + r + 4 * (D == 128 ? ph >> 1 : ph);
+      const int pidx = key / P, off = key % P;
+      // the first key's piece and scales inside a raw tile; the second half of
+      // the rounds is a page further on when pages have 16 keys
+      const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
+      const uint32_t ccode = pidx * blk + off * (D / 2) + pc * 16;
+      const uint32_t cscale = pidx * blk + P * (D / 2) + off * (D / 16) + pc * 2;
+      const uint32_t code_hop = P == 16 ? blk - 16 * (D / 2) : 0;
+      const uint32_t scale_hop = P == 16 ? blk - 16 * (D / 16) : 0;
+      const int bad_hop = P == 16 ? 1 : 0;
+      // chunk 4 pc + k of key % 8 is at drow ^ 16 k
+      const uint32_t drow = (key >> 3) * RG + (key & 7) * 128 + (pc >> 1) * 1024 +
+                            ((((pc & 1) * 4) ^ (key & 7)) << 4);
+      const bool rep = warp == 12 && lane == 0;
+      bool ok = true;
+      Walk w = walk(kAll);
+      while (w.take()) {
+        const int slot = w.slot, n = w.n;
+        const bool is_v = w.is_v;
+        const uint32_t tag = 40000 + 2 * n + (is_v ? 1 : 0);
+        if (rep) ctrl->where[5] = tag;
+        ok = mbar_wait(bar(kRawFull + slot), w.phase, abort_flag, diag, tag);
+        if (ok && n >= 2) {                // the tile two before has been used
+          const int t = is_v ? (row_mode ? n - 1 : n) : n - 2;
+          ok = mbar_wait(bar(kFree + (t & 1)), (t >> 1) & 1, abort_flag, diag, tag + 100000);
         }
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t badm = ctrl->bad[slot] >> pidx;
+        const uint32_t raw = raw_addr(slot);
+        const uint32_t dst = (is_v ? sV : sK) + (n & 1) * TB + drow;
+        uint4 c[NJ];
+        uint32_t sb[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const bool far = j >= NJ / 2;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(c[j].x), "=r"(c[j].y), "=r"(c[j].z), "=r"(c[j].w)
+                       : "r"(raw + ccode + j * KPR * (D / 2) + (far ? code_hop : 0)));
+          uint16_t h;
+          asm volatile("ld.shared.u16 %0, [%1];"
+                       : "=h"(h)
+                       : "r"(raw + cscale + j * KPR * (D / 16) + (far ? scale_hop : 0)));
+          sb[j] = (badm >> (far ? bad_hop : 0)) & 1u ? 0u : h;     // a bad page: scales of zero
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint32_t s2 = kv4_scales_f16(sb[j]);
+          const uint32_t w[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {      // 16-byte chunk 4 pc + k of the key
+            uint32_t v[4];
+            kv4_codes_f16(w[k], v);
+            const uint32_t s = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             (dst ^ (16 * k)) + j * (KPR / 8) * RG),
+                         "r"(hmul2(v[0], s)), "r"(hmul2(v[1], s)), "r"(hmul2(v[2], s)),
+                         "r"(hmul2(v[3], s))
+                         : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar((is_v ? kVFull : kKFull) + (n & 1)));
+          mbar_arrive(bar(kRawEmpty + slot));
+        }
+        w.release();
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar((is_v ? kVFull : kKFull) + (n & 1)));
-        mbar_arrive(bar(kRawEmpty + slot));
-      }
-      w.release();
-    }
     }
   }
 
