@@ -856,47 +856,55 @@ kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
 }
 
 // Chunk scores: the sum over kv heads and rows of 2^(mass - the row's
-// log2-sum-exp).  A warp per chunk, lane-parallel over (kv head, subchunk,
-// row), NB loads of each kind on their way at once.
-__global__ void __launch_bounds__(256) kv4_scores_few(const VerifyKArgs a) {
-  constexpr int NB = 4;
+// log2-sum-exp).  A warp per chunk; a lane has one (subchunk, row) of several
+// heads, whose loads are on their way together: the launch is bound by one
+// round trip (2 to 4 us behind the split pass).
+__global__ void __launch_bounds__(256) kv4_scores_few(const __grid_constant__ VerifyKArgs a) {
+  constexpr int NB = 8;
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c = blockIdx.x * 8 + warp;
-  // the lengths are inputs of the call: the split pass, which this launch
-  // follows, has itself waited for whatever wrote them
+  // the lengths (and the sums so far) are inputs of the call: the split pass,
+  // which this launch follows, has itself waited for whatever wrote them
   const SeqPlan sq = seq_sizes(a.plan, b, false);
   const int sub = min(kBlock, a.plan.chunk_size), per = a.plan.chunk_size / sub;
   const int k0 = c * per, n_k = min(per, (sq.L + sub - 1) / sub - k0);
-  const int per_head = n_k * sq.rows;             // a head's masses, consecutive
+  const bool work = n_k > 0 && c < a.plan.max_chunks;
+  const int per_head = work ? n_k * sq.rows : 0;  // a head's masses, consecutive
+  const int span = min(32, max(1, per_head));     // lanes of a head
+  const int hp = 32 / span;                       // heads side by side in the warp
+  const int hl = per_head < 32 ? lane / span : 0;
+  const int e0 = lane - hl * span;
   const int64_t n_rows = (int64_t)a.plan.n_nodes * a.plan.group;
-  const int64_t row0 = (int64_t)sq.node0 * a.plan.group;
   const int64_t n_sub = (int64_t)a.plan.max_chunks * per;
+  const float* const mass = a.clse + (int64_t)sq.node0 * a.plan.group * n_sub +
+                            (int64_t)k0 * sq.rows;
+  const float* const lse = a.row_lse + (int64_t)sq.node0 * a.plan.group;
+  float* const dst = a.scores + (int64_t)b * a.plan.max_chunks + c;
+  const float before = work && a.accumulate && lane == 0 ? *dst : 0.f;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  if (n_k <= 0 || c >= a.plan.max_chunks) return;
+  if (!work) return;
   float sum = 0.f;
-  const int total = a.plan.num_kv_heads * per_head;
-  for (int x0 = lane; x0 < total; x0 += 32 * NB) {
-    float m[NB], l[NB];
+  for (int e = hl < hp ? e0 : per_head; e < per_head; e += 32) {
+    const int r = e % sq.rows;
+    for (int h0 = hl; h0 < a.plan.num_kv_heads; h0 += hp * NB) {
+      float m[NB], l[NB];
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int x = x0 + 32 * k;
-      m[k] = l[k] = 0.f;
-      if (x < total) {
-        const int h = x / per_head, e = x - h * per_head;
-        m[k] = __ldcg(a.clse + (h * n_rows + row0) * n_sub + (int64_t)k0 * sq.rows + e);
-        l[k] = __ldcg(a.row_lse + h * n_rows + row0 + e % sq.rows);
+      for (int k = 0; k < NB; ++k) {
+        const int h = h0 + k * hp;
+        m[k] = -CUDART_INF_F;
+        l[k] = 0.f;
+        if (h < a.plan.num_kv_heads) {
+          m[k] = __ldcg(mass + h * n_rows * n_sub + e);
+          l[k] = __ldcg(lse + h * n_rows + r);
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (x0 + 32 * k < total) sum += exp2f(m[k] - l[k]);
+      for (int k = 0; k < NB; ++k) sum += ptx::ex2(m[k] - l[k]);
+    }
   }
   sum = warp_sum(sum);
-  if (lane == 0) {
-    float* dst = a.scores + (int64_t)b * a.plan.max_chunks + c;
-    *dst = a.accumulate ? *dst + sum : sum;
-  }
+  if (lane == 0) *dst = before + sum;
 }
 
 template <int D, int NT>
