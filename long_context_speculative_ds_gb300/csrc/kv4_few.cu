@@ -332,12 +332,6 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   uint64_t anc[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) anc[n][0] = anc[n][1] = 1ull;
-  if (need_anc && warp == 0) {
-    if (T > 1)
-      tc::tree_ancestors(a.parents + pc.node0, T, ctrl.parents, ctrl.anc, a.plan.status);
-    else if (lane == 0 && __ldg(a.parents + pc.node0) != -1)
-      flag(a.plan.status, DS_DEV_BAD_TREE);
-  }
 
   const uint32_t ring = smem_addr(smem) + warp * C_::kRing;
   const uint32_t blk = DS_KV4_BLOCK_BYTES(P, D);
@@ -411,6 +405,12 @@ __device__ __forceinline__ void work_piece(const Kv4KArgs& ka, const Piece& pc, 
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i);
+  if (need_anc && warp == 0) {
+    if (T > 1)
+      tc::tree_ancestors(a.parents + pc.node0, T, ctrl.parents, ctrl.anc, a.plan.status);
+    else if (lane == 0 && __ldg(a.parents + pc.node0) != -1)
+      flag(a.plan.status, DS_DEV_BAD_TREE);
+  }
   uint32_t q[QT][NS][2];
   const uint32_t q_smem = smem_addr(smem) + W * C_::kRing + lane * 8;
   if constexpr (QS) {
