@@ -84,6 +84,7 @@ struct Ctrl {
   uint32_t tmem_base;
   int abort;
   Plan plan;
+  int kvh, rgi, t0, t1, rows;    // of the item: kv head, row group, tiles, rows; 0 without one
   int32_t parents[DS_MAX_TREE_NODES];
   uint64_t anc[DS_MAX_TREE_NODES];
   uint32_t bad[2 * kRing];       // bad pages of each raw tile, one bit a page
@@ -133,13 +134,15 @@ __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const SeqPlan s = seq(b0);
     const int cost = s.tiles * tile_cost(s);
-    int64_t u = (int64_t)cost * a.num_kv_heads * s.rg;
-    for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-    total += u;
+    const int64_t u = (int64_t)cost * a.num_kv_heads * s.rg;
+    total += ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)(u >> 24)) << 24) +
+             __reduce_add_sync(0xffffffffu, (unsigned)u & 0xffffffu);
     most = max(most, (int)__reduce_max_sync(0xffffffffu, (unsigned)cost));
   }
   const int ctas = max(1, a.target_ctas);
-  int q = (int)max((int64_t)1, min((int64_t)most, (total + ctas - 1) / ctas));
+  const int64_t up = total + ctas - 1;
+  const int64_t share = up >> 32 ? up / ctas : (int64_t)((uint32_t)up / (uint32_t)ctas);
+  int q = (int)max((int64_t)1, min((int64_t)most, share));
   int fits = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const SeqPlan s = seq(b0);
@@ -260,48 +263,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     tmem_alloc(smem_addr(&ctrl->tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  // the item, and the barriers whose arrivals depend on it
+  auto find_item = [&]() {
+    const Plan p = kv4_plan(a.plan, blockIdx.x);
+    int kvh = 0, rgi = 0, t0 = 0, t1 = 0, rows = 0;
+    if ((int)blockIdx.x < p.total_items && p.b >= 0) {
+      const SeqPlan& sq = p.seq;
+      const int local = blockIdx.x - sq.item_base;
+      const int grp = local / sq.splits, split = local - grp * sq.splits;
+      kvh = grp / sq.rg;
+      rgi = grp - kvh * sq.rg;
+      const int base = sq.tiles / sq.splits, rem = sq.tiles - base * sq.splits;
+      t0 = split * base + min(split, rem);
+      t1 = t0 + base + (split < rem ? 1 : 0);
+      rows = min(kRowsPerGroup, sq.rows - rgi * kRowsPerGroup);
+    }
+    if (lane == 0) {
+      ctrl->plan = p;
+      ctrl->kvh = kvh; ctrl->rgi = rgi; ctrl->t0 = t0; ctrl->t1 = t1; ctrl->rows = rows;
+      // both groups' arrivals in row mode, the tile's own group's in key mode
+      for (int s = 0; s < 2; ++s) mbar_init(bar(kFree + s), rows > 128 ? 2 : 1);
+      fence_mbar_init();
+    }
+  };
   const bool early_plan = a.accumulate != 0;
-  if (early_plan && warp == 0) {
-    Plan p = kv4_plan(a.plan, blockIdx.x);
-    if (lane == 0) ctrl->plan = p;
-  }
+  if (early_plan && warp == 0) find_item();
   grid_dep_wait();
   grid_dep_launch_dependents();
-  if (!early_plan && warp == 0) {
-    Plan p = kv4_plan(a.plan, blockIdx.x);
-    if (lane == 0) ctrl->plan = p;
-  }
+  if (!early_plan && warp == 0) find_item();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem_base;
   const Plan& p = ctrl->plan;           // stays in shared memory: registers are scarce
-  const bool active = (int)blockIdx.x < p.total_items && p.b >= 0;
-
   const SeqPlan& sq = p.seq;
-  const int G = a.plan.group;
-  int kvh = 0, rgi = 0, t0 = 0, t1 = 0, rows_here = 0;
-  if (active) {
-    const int local = blockIdx.x - sq.item_base;
-    const int per_h = sq.rg * sq.splits;
-    kvh = local / per_h;
-    rgi = (local % per_h) / sq.splits;
-    const int split = local % sq.splits;
-    const int base = sq.tiles / sq.splits, rem = sq.tiles % sq.splits;
-    t0 = split * base + min(split, rem);
-    t1 = t0 + base + (split < rem ? 1 : 0);
-    rows_here = min(kRowsPerGroup, sq.rows - rgi * kRowsPerGroup);
-  }
-  const int nt = t1 - t0;
-  const bool row_mode = rows_here > 128;
-  // arrivals: both groups' in row mode, the tile's own group's in key mode
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) mbar_init(bar(kFree + s), row_mode ? 2 : 1);
-    fence_mbar_init();
-  }
-  __syncthreads();
+  const int kvh = ctrl->kvh, rgi = ctrl->rgi, t0 = ctrl->t0, rows_here = ctrl->rows;
+  const int G = a.plan.group, nt = ctrl->t1 - t0;
+  const bool active = nt > 0, row_mode = rows_here > 128;
   const int L = sq.L, T = sq.T;
-  const bool need_anc = active && t1 * kTileKeys > L;
+  const bool need_anc = active && (t0 + nt) * kTileKeys > L;
   auto raw_addr = [&](int s) -> uint32_t {
     return s < kRing ? sR + s * RAW : sQ + TB + (s - kRing) * RAW;
   };
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   static_assert(128 * (88 + 88) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
     regs_release<88>();
-    if (!(active && nt > 0)) {
+    if (!active) {
     } else if (warp < 2) {
       // ---------------------------------------------------- ancestor masks
       if (warp == 1 && need_anc) {
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     }
   } else if (warp < 12) {
     regs_claim<168>();
-    if (active && nt > 0) {
+    if (active) {
       // ------------------------------------------------------------ softmax
       const int g = (warp - 4) >> 2;
       const int q4 = warp & 3;
@@ -546,6 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
         constexpr int RPI = 32 / CPR;                // rows of a warp's load
         const int ch = lane % CPR;
         const uint32_t dst = sQ + (row_mode ? g * TB : 0) + (ch >> 3) * kHalfBytes;
+        // row / G as a product: exact, as rows times G stay below 2^32
+        const uint32_t inv = G > 1 ? 0xffffffffu / G + 1u : 0u;
         uint4 x[32 / RPI];
 #pragma unroll
         for (int i = 0; i < 32 / RPI; ++i) {
@@ -553,10 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
           const int rr = (row_mode ? g * 128 : 0) + rl;
           const int gr = rgi * kRowsPerGroup + rr;
           x[i] = make_uint4(0, 0, 0, 0);
+          const int node = G > 1 ? (int)__umulhi((uint32_t)gr, inv) : gr;
           if (rr < rows_here)
             x[i] = __ldg(reinterpret_cast<const uint4*>(
-                             a.q + ((int64_t)(sq.node0 + gr / G) * a.num_q_heads + kvh * G +
-                                    gr % G) * D) + ch);
+                             a.q + ((int64_t)(sq.node0 + node) * a.num_q_heads + kvh * G +
+                                    (gr - node * G)) * D) + ch);
         }
 #pragma unroll
         for (int i = 0; i < 32 / RPI; ++i) {
@@ -609,6 +612,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
             softmax_unit<false, true>(tS, tS, ~0u, ~0u, ~0u, ~0u, c2, u == 0, m2, l, cs, alpha,
                                       rescale, tile_slot0, 4 * hb, cshift, n_ch, row_ok,
                                       clse_row);
+          } else if (unit_slot0 >= L + T && u > 0) {
+            // past the end: zero weights; a chunk of the context may end here
+            alpha = 1.f;
+            rescale = false;
+            const int c = unit_slot0 >> cshift;
+            if (row_ok && c < n_ch)
+              clse_row[(int64_t)c * kRowsPerGroup] = cs > 0.f ? m2 + __log2f(cs) : -CUDART_INF_F;
+            cs = 0.f;
+            uint32_t zero[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) zero[i] = 0u;
+            tmem_st32(tS, zero);
           } else {
             if (!anc_ready) {
               if (lrow == 0) ctrl->where[wi] = 30000 + kAnc * 100;
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     }
   } else {
     regs_release<88>();
-    if (active && nt > 0) {
+    if (active) {
       // ---------------------------------------------------------- converters
       // A lane takes one 16-byte piece pc (32 channels) of a key per round, a
       // warp 8 keys (16 at head_dim 64), and the rounds of a warp's 32 keys are
@@ -774,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
     if (diag[1] == blockIdx.x)
       for (int i = 0; i < 6; ++i) diag[2 + i] = ctrl->where[i];
   }
-  if (active && nt > 0) {
+  if (active) {
     // the last split of the row group forms the rows' final log2-sum-exp
     // (see verify_tc.cu)
     const int64_t cidx = ((int64_t)p.b * a.plan.num_kv_heads + kvh) * a.plan.rg_max + rgi;
@@ -797,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
             tc::row_lse_from_splits(a.lse_part + base * kRowsPerGroup + r, sq.splits);
   }
   if (warp == 1) {
-    if (active && nt > 0 && lane == 0) {
+    if (active && lane == 0) {
       drain_wait(bar(kOFinal), 0);
       drain_wait(bar(kOFinal + 1), 0);
     }
