@@ -210,6 +210,112 @@ __device__ __noinline__ Plan kv4_plan(const PlanArgs& a, int item) {
   return p;
 }
 
+// Output of one softmax thread after its last tile: O / l and the row's
+// log2-sum-exp.  In key mode group 1 leaves its O, maximum and sum in shared
+// memory and group 0 merges them.  A warp's rows go through a staging tile of
+// 32 rows x 32 columns (idle by then), so that a store instruction covers
+// whole sectors; 16-byte chunk c of row r is staged where eight lanes of an
+// access, eight rows' or a row's, touch all banks.
+template <int D>
+__device__ __noinline__ void write_split(const bool row_mode, const int g, const bool ok,
+                                         const int nt1, const uint32_t tO, const int lrow,
+                                         const int rows_left, const float m2, const float l,
+                                         float* __restrict__ merge_buf, float* m1buf,
+                                         float* l1buf, unsigned char* __restrict__ stage,
+                                         const bool f32, void* __restrict__ dst,
+                                         float* __restrict__ lse_out, const float out_mult) {
+  using namespace ptx;
+  const int lane = threadIdx.x & 31;
+  const bool merge = !row_mode && nt1 > 0;
+  if (!row_mode && g == 1) {
+    if (ok && merge) {
+#pragma unroll 1
+      for (int c4 = 0; c4 < D / 32; ++c4) {
+        uint32_t r[32];
+        tmem_ld32(tO + c4 * 32, r);
+        tmem_ld_wait(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) merge_buf[(c4 * 32 + i) * 128 + lrow] = __uint_as_float(r[i]);
+      }
+      m1buf[lrow] = m2;
+      l1buf[lrow] = l;
+    }
+    if (merge) asm volatile("bar.sync 1, 256;" ::: "memory");
+    return;
+  }
+  float k0 = 1.f, k1 = 0.f, lt = l, mt = m2;
+  if (merge) {
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float m1 = m1buf[lrow], l1 = l1buf[lrow];
+    mt = fmaxf(m2, m1);
+    const float mb = mt == -CUDART_INF_F ? 0.f : mt;
+    k0 = l > 0.f ? ex2(m2 - mb) : 0.f;
+    k1 = l1 > 0.f ? ex2(m1 - mb) : 0.f;
+    lt = l * k0 + l1 * k1;
+  }
+  if (lane < rows_left) *lse_out = lt > 0.f ? mt + __log2f(lt) : -CUDART_INF_F;
+  const float inv = lt > 0.f ? __fdividef(out_mult, lt) : 0.f;
+  k0 *= inv;
+  k1 *= inv;
+#pragma unroll 1
+  for (int c4 = 0; c4 < D / 32; ++c4) {
+    uint32_t r[32];
+    if (ok) {
+      tmem_ld32(tO + c4 * 32, r);
+      tmem_ld_wait(r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * k0);
+    if (merge && k1 != 0.f) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        r[i] = __float_as_uint(
+            fmaf(merge_buf[(c4 * 32 + i) * 128 + lrow], k1, __uint_as_float(r[i])));
+    }
+    if (!f32) {
+      // four 16-byte chunks a row, chunk c in place c ^ ((row / 2) % 4)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = pack_f16x2(__uint_as_float(r[8 * c + 2 * e]),
+                            __uint_as_float(r[8 * c + 2 * e + 1]));
+        *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = 8 * k + (lane >> 2), cc = lane & 3;
+        if (rr < rows_left)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + (int64_t)rr * D + c4 * 32 +
+                                    cc * 8) =
+              *reinterpret_cast<const uint4*>(stage + rr * 64 + 16 * (cc ^ ((rr >> 1) & 3)));
+      }
+    } else {
+      // eight chunks a row, chunk c in place c ^ (row % 8)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + 16 * (c ^ (lane & 7))) =
+            make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rr = 4 * k + (lane >> 3), cc = lane & 7;
+        if (rr < rows_left)
+          *reinterpret_cast<uint4*>(static_cast<float*>(dst) + (int64_t)rr * D + c4 * 32 +
+                                    cc * 4) =
+              *reinterpret_cast<const uint4*>(stage + rr * 128 + 16 * (cc ^ (rr & 7)));
+      }
+    }
+    __syncwarp();
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
   using namespace ptx;
@@ -681,8 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       else __syncwarp();
       if (ok) tc_fence_after();
       const int nt1 = row_mode ? 0 : ntiles(1);
-      float* stage = reinterpret_cast<float*>(smem + (row_mode ? g * TB : 0)) +
-                     q4 * 32 * tc::kStageStride;
+      unsigned char* stage = smem + (row_mode ? g * TB : 0) + q4 * 4096;
       const int warp_row0 = grow_local - lane;
       const int64_t orow = ((int64_t)blockIdx.x * kRowsPerGroup + warp_row0) * D;
       void* op_warp = a.out_f32 ? static_cast<void*>(a.o_part + orow)
@@ -691,10 +796,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
       // A split's output is a weighted mean of code x scale, at most 2688: f16
       // holds it with three more bits than bf16, to 2^-25 at worst; the
       // cache's exponent is applied where the splits meet.
-      tc::write_row_output<D, true>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l,
-                                    merge_buf, m1buf, l1buf, stage, !a.out_f32, op_warp,
-                                    a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
-                                    a.out_f32 ? ka.out_mult : 1.f);
+      write_split<D>(row_mode, g, ok, nt1, tO, lrow, rows_here - warp_row0, m2, l, merge_buf,
+                     m1buf, l1buf, stage, a.out_f32, op_warp,
+                     a.lse_part + (int64_t)blockIdx.x * kRowsPerGroup + grow_local,
+                     a.out_f32 ? ka.out_mult : 1.f);
     }
   } else {
     regs_release<88>();

@@ -147,7 +147,7 @@ DS_DEV void softmax_unit(const uint32_t tS, const uint32_t tP, const uint32_t vw
   tmem_st32(tP, pk);
 }
 
-// Output of one softmax thread after its last tile: O out_mult / l (merged with the
+// Output of one softmax thread after its last tile: O / l (merged with the
 // other group's partial result in key mode) and the row's log2-sum-exp.
 // The rows are written through a per-warp staging tile in shared memory
 // (`stage`, 32 rows x 32 floats = 4 KB, idle by then; 16-byte chunk c of row
@@ -158,18 +158,16 @@ DS_DEV void softmax_unit(const uint32_t tS, const uint32_t tP, const uint32_t vw
 // segments instead of 32 rows' scattered 16 bytes.
 constexpr int kStageStride = 32;   // floats per staged row
 
-// F16: half-width outputs (part_half) are f16 instead of bf16.
-template <int D, bool F16 = false>
+template <int D>
 __device__ __noinline__ void write_row_output(const bool row_mode, const int g, const bool ok,
                                               const int nt1, const uint32_t tO, const int lrow,
                                               const int rows_left, const float m2,
                                               const float l, float* __restrict__ merge_buf,
                                               float* m1buf, float* l1buf,
                                               float* __restrict__ stage,
-                                              const bool part_half,
+                                              const bool part_bf16,
                                               void* __restrict__ op_warp,
-                                              float* __restrict__ lse_out,
-                                              const float out_mult = 1.f) {
+                                              float* __restrict__ lse_out) {
   using namespace ptx;
   const int lane = threadIdx.x & 31;
   const bool row_ok = (lrow & 31) < rows_left;
@@ -201,7 +199,7 @@ __device__ __noinline__ void write_row_output(const bool row_mode, const int g, 
       lt = l * sc0 + l1 * sc1;
     }
   }
-  const float inv = lt > 0.f ? out_mult / lt : 0.f;
+  const float inv = lt > 0.f ? 1.f / lt : 0.f;
 #pragma unroll 1
   for (int c4 = 0; c4 < D / 32; ++c4) {
     uint32_t r[32];
@@ -218,8 +216,8 @@ __device__ __noinline__ void write_row_output(const bool row_mode, const int g, 
       if (sc1 != 0.f) o += merge_buf[(c4 * 32 + i) * 128 + lrow] * sc1;
       r[i] = __float_as_uint(o * inv);
     }
-    if (part_half) {
-      // pairs: a row's 32 columns are 64 bytes, four 16-byte chunks;
+    if (part_bf16) {
+      // bf16 pairs: a row's 32 columns are 64 bytes, four 16-byte chunks;
       // chunk c of row q sits in the row's slot c ^ ((q / 2) % 4), so that
       // eight lanes of one access (eight rows, or two rows' four chunks)
       // touch distinct 16-byte bank groups
@@ -229,10 +227,8 @@ __device__ __noinline__ void write_row_output(const bool row_mode, const int g, 
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          w[e] = F16 ? pack_f16x2(__uint_as_float(r[8 * c + 2 * e]),
-                                  __uint_as_float(r[8 * c + 2 * e + 1]))
-                     : pack_bf16x2(__uint_as_float(r[8 * c + 2 * e]),
-                                   __uint_as_float(r[8 * c + 2 * e + 1]));
+          w[e] = pack_bf16x2(__uint_as_float(r[8 * c + 2 * e]),
+                             __uint_as_float(r[8 * c + 2 * e + 1]));
         *reinterpret_cast<uint4*>(st + 4 * (c ^ ((lane >> 1) & 3))) =
             make_uint4(w[0], w[1], w[2], w[3]);
       }
