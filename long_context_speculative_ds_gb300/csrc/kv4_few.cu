@@ -12,12 +12,13 @@
 //   S^T[16 keys, 8 rows] += K[16 keys, 16 channels] Q^T[16 channels, 8 rows]
 //   O^T[16 dims, 8 rows] += V^T[16 dims, 16 keys]  P^T[16 keys, 8 rows]
 //
-// One token over 128K (32 query heads on 8 of the cache, 151 MB) takes 48.6
-// us, 3.1 TB/s of the 6.78 a copy reaches; without the products it takes 39,
-// without the loads 44: conversions and products (26.6 M warp instructions,
-// the issue slots 46 % busy) and the stream overlap, and some 15 us go into
-// the start, the merge, the join and the salience.  A ragged batch of eight
-// (4K to 128K, no salience) takes 89 us, 4.5 TB/s.
+// One token over 128K (32 query heads on 8 of the cache, 151 MB) takes 44.8
+// us, 3.4 TB/s of the 6.78 a copy reaches.  An earlier form of 48 took 39
+// without the products and 44 without the loads: conversions and products
+// (issue slots 57 % busy) and the stream overlap, and some 12 us go into the
+// start, the merge, the join and the salience.  A ragged batch of eight (4K to
+// 128K, no salience) takes 86 us, 4.6 TB/s; one token over 512 keys, with 4
+// heads of 64 on 2, 8.8 us.
 //
 // Which channels make up a step of the first product, and which dims a tile
 // of the second, is free as long as both operands agree.  Lane 4g + t takes
@@ -927,10 +928,11 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
 
 }  // namespace kv4few
 
-// Up to 8 rows a segment the queries stay in registers beside 16 warps (2
-// nodes of 4 rows over 128K: 60 us); above, two tiles of 8 need the shared
-// memory and leave room for 12 (3 nodes: 74 us; with 16 warps and the queries
-// in registers, spilled, 4 nodes took 99 instead of 76).
+// Up to 8 rows a segment the queries stay in registers beside 16 warps (a
+// single call of 2 nodes of 4 rows over 128K: 56 us); above, two tiles of 8
+// need the shared memory and leave room for 12 (3 nodes: 70; with 16 warps and
+// the queries in registers, spilled, an earlier form of 4 nodes took 99
+// instead of 76).
 cudaError_t launch_kv4_few(const Kv4KArgs& k, int head_dim, int rows, const VerifyLayout& L,
                            cudaStream_t stream) {
   using kv4few::launch;

@@ -10,11 +10,11 @@
 //
 // The two products of 256 query rows with 128K keys of eight heads (137
 // GFLOP) are 72 us of the tensor pipe at its measured rate; the 151 MB of the
-// cache are 22 us.  A call over 64 nodes and 32 query heads takes 124 us, 1.11
-// PFLOP/s or 58 %: about 25 us go into the start (plan, Q, first tiles), the
-// split outputs and the join, and in between a tile takes 1.8 us: 1.2 of
-// products, 1.2 of softmax (0.9 with nothing beside it) and 0.7 of conversion
-// share issue slots and wait for one another.
+// cache are 22 us.  A call over 64 nodes and 32 query heads takes 122 us, 1.12
+// PFLOP/s or 59 %: about 22 us go into the start (plan 2.5, Q 2.5, first
+// tile), the split outputs (2.5) and the join (8), and in between a tile takes
+// 1.8 us: 1.2 of products, 1.2 of softmax (0.9 with nothing beside it) and 0.7
+// of conversion share issue slots and wait for one another.
 //
 // More than 128 rows ("row mode"): each of two softmax groups has a tile of
 // 128 rows and goes through all keys.  Up to 128 rows ("key mode"): both
