@@ -583,7 +583,9 @@ ds_status ds_kv4_read(const ds_kv4_rows_args* args, void* stream);
  * puts them there).  A batch whose trees have one node each is a decoding
  * step.  Queries enter the product as float16: those beyond +-65504 are
  * clamped to it (a NaN stays one), and the bits of a bf16 query below 2^-24
- * are rounded off.
+ * are rounded off.  Weights enter the second product as float16 too; maxima,
+ * sums and outputs in progress are float32, and outputs that splits exchange
+ * float16 or float32.
  *
  * chunk_scores NULL: no salience (chunk_size, max_chunks and
  * accumulate_scores are then ignored).  A page id outside [0, num_pages)
