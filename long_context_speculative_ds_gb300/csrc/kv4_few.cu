@@ -772,13 +772,19 @@ kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
   grid_dep_launch_dependents();
   if (threadIdx.x == 0) ctrl.n_cut = 0;
   Piece& pc = ctrl.piece[warp];
-  bool more = find_piece<R, W>(ka.v.plan, -1, &pc);
+  bool more = find_piece<R, W>(ka.v.plan, -1, &pc), worked = false;
   while (more) {                   // the same for every warp of the block
-    if (pc.u1 > pc.u0) work_piece<D, NT>(ka, pc, ctrl, smem, warp);
+    if (pc.u1 > pc.u0) {
+      work_piece<D, NT>(ka, pc, ctrl, smem, warp);
+      worked = true;
+    }
     const int next = pc.next;
     __syncwarp();
     more = next >= 0 && find_piece<R, W>(ka.v.plan, next, &pc);
   }
+  // Only the barriers of a piece order n_cut's first value before its read by
+  // the other warps: a block without a piece leaves here, in every warp.
+  if (!worked) return;
   // The last piece of a cut segment to finish merges them.
   const int n_cut = ctrl.n_cut;
   if (n_cut == 0) return;

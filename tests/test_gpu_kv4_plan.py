@@ -1,0 +1,47 @@
+"""How ds_kv4_verify_attn divides its work, against the float64 oracle: blocks
+without a piece of it, one workspace for calls of different trees, batches of
+more than one warp's lanes.
+
+The bounds are those of test_gpu_kv4.py: with A = sum p |v|, 2^-11 A for
+weights in f16 and 2^-12 A for the f32 logits and sums."""
+import numpy as np
+import pytest
+import torch
+
+from long_context_speculative_ds_gb300 import binding as B
+import test_gpu_kv4 as K
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.mark.parametrize("trees", [[1, 1], [3, 3]])
+def test_blocks_without_a_piece(trees):
+    """Short contexts leave most blocks without a piece, right after a call
+    that cut segments between all of them: such blocks touch nothing."""
+    hq, hkv, d = 8, 2, 128
+    long_lens, short_lens = [9000, 7001], [40, 7]
+    c, q, offs, par = K._attn_case(long_lens, trees, hq, hkv, d, 16, seed=31)
+    o, A, s = K._oracle_attn(c, q, short_lens, offs, par, 64)
+    n = q.shape[0]
+    wide = torch.full((n + 8, hq, d), 9.0, device=DEV)
+    out = wide[4:4 + n]
+    score = torch.full((2, 150), -5.0, device=DEV)
+    ctx = K.i32(long_lens)
+    base = dict(q=q, k_cache=c.k, v_cache=c.v, page_table=c.dtable, ctx_lens=ctx,
+                tree_offsets=K.i32(offs), parents=K.i32(par), page_size=16, chunk_size=64,
+                out=out, chunk_scores=score)
+    ws = torch.zeros(B.ds_kv4_verify_attn_workspace_size(B.kv4_attn_args(**base)),
+                     dtype=torch.uint8, device=DEV)
+    args = B.kv4_attn_args(workspace=ws, **base)
+    lens = [K.i32(long_lens), K.i32(short_lens)]
+    for _ in range(20):
+        for x in lens:                   # cut segments, then mostly idle blocks
+            ctx.copy_(x)
+            out.fill_(9.0)
+            score.fill_(-5.0)
+            B.ds_kv4_verify_attn(args)
+        torch.cuda.synchronize()
+        K._check_attn(out, score, o, A, s, short_lens, 64)
+        assert bool((wide[:4] == 9.0).all()) and bool((wide[4 + n:] == 9.0).all())
+    assert B.ds_device_status(ws) == 0
