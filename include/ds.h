@@ -103,10 +103,14 @@ int32_t ds_abi_version(void);
 int64_t ds_struct_size(int32_t which);
 
 /* Zero the whole workspace: the status word (bytes 0..255 of any workspace)
- * and the verify call's split counters behind it (which every completed
+ * and the attention calls' split counters behind it (which every completed
  * call leaves at zero).  Call once after allocating a workspace, whenever the
- * sticky bits should be cleared, and after a call that set DS_DEV_TIMEOUT (an
- * aborted call can leave counters behind).  Enqueued on `stream`. */
+ * sticky bits should be cleared, after a call that set DS_DEV_TIMEOUT (an
+ * aborted call can leave counters behind), and before calls of another batch
+ * size, of other head counts or of the other cache's attention on the same
+ * workspace: the counters' number goes by these.  Everything else (nodes,
+ * lengths, chunks, num_sms) may change from call to call.  Enqueued on
+ * `stream`. */
 ds_status ds_workspace_init(void* workspace, size_t workspace_bytes,
                             void* stream);
 
@@ -589,7 +593,8 @@ ds_status ds_kv4_read(const ds_kv4_rows_args* args, void* stream);
  *
  * chunk_scores NULL: no salience (chunk_size, max_chunks and
  * accumulate_scores are then ignored).  A page id outside [0, num_pages)
- * sets DS_DEV_BAD_PAGE and its slots read as zeros.  Refused by name: as
+ * sets DS_DEV_BAD_PAGE and its slots read as zeros.  The workspace's size does
+ * not depend on n_nodes.  Refused by name: as
  * ds_verify_attn, and exponents outside [-32, 32] and max_pages * page_size
  * above 2^30. */
 typedef struct ds_kv4_attn_args {

@@ -611,7 +611,7 @@ ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* a, size_t* b
   int sms = v.num_sms;
   if (sms == 0 && device_sms(&sms) != 0)
     return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
-  *bytes = ds::verify_layout(v, sms, ds::kv4_few_segments(*a)).total;
+  *bytes = ds::verify_layout(v, sms, ds::kv4_counters(*a)).total;
   return ok();
 }
 
@@ -634,7 +634,7 @@ ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* a, void* stream) {
   int sms = v.num_sms;
   if (sms == 0 && device_sms(&sms) != 0)
     return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
-  const ds::VerifyLayout L = ds::verify_layout(v, sms, ds::kv4_few_segments(*a));
+  const ds::VerifyLayout L = ds::verify_layout(v, sms, ds::kv4_counters(*a));
   REQUIRE(a->workspace_bytes >= L.total, DS_ERR_WORKSPACE,
           "workspace_bytes %zu < required %zu", a->workspace_bytes, L.total);
   if (a->n_nodes == 0) return ok();

@@ -98,14 +98,14 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
                             cudaStream_t stream);
 
 // The sizes of a 4-bit attention call as those of a verify call: the work
-// plan and the workspace are the same.  Without salience there is one chunk
-// longer than any context, and no chunk masses.
+// plan and the workspace are the same.  Without salience the plan's chunks are
+// of 128 keys, as many as any context has, and there are no chunk masses.
 ds_verify_args kv4_as_verify(const ds_kv4_attn_args& a);
 constexpr int kKv4MaxSlots = 1 << 30;
 // Query rows per sequence and kv head, on average, when the few-row pass
-// takes the call (0: the tree pass does), and the segments it may need.
+// takes the call (0: the tree pass does), and the arrival counters of a call.
 int kv4_few_rows(const ds_kv4_attn_args& a);
-int kv4_few_segments(const ds_kv4_attn_args& a);
+size_t kv4_counters(const ds_kv4_attn_args& a);
 
 // Sets the message ds_last_error returns on this thread; returns st.
 ds_status set_last_error(ds_status st, const char* msg);

@@ -30,9 +30,14 @@ int kv4_few_rows(const ds_kv4_attn_args& a) {
   return units < ((int64_t)1 << 31) ? (int)rows : 0;
 }
 
-int kv4_few_segments(const ds_kv4_attn_args& a) {
-  const int64_t group = a.num_q_heads / a.num_kv_heads;
-  return kv4_few_rows(a) ? (int)(a.num_kv_heads * (a.batch + a.n_nodes * group / 8 + 1)) : 0;
+size_t kv4_counters(const ds_kv4_attn_args& a) {
+  // The few-row pass counts arrivals by segment: at most 8 rows each but for
+  // a sequence's last, and it takes calls of at most 16 rows a sequence and kv
+  // head on average, so 3 a sequence and kv head.  Neither the number of
+  // nodes nor the pass goes into it: what lies behind the counters stays where
+  // it is when a workspace serves calls of other trees, and no call finds
+  // anything but the zeros that the last one left in them.
+  return (size_t)a.num_kv_heads * (3 * (size_t)a.batch + 1);
 }
 
 cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,

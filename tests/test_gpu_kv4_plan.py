@@ -45,3 +45,31 @@ def test_blocks_without_a_piece(trees):
         K._check_attn(out, score, o, A, s, short_lens, 64)
         assert bool((wide[:4] == 9.0).all()) and bool((wide[4 + n:] == 9.0).all())
     assert B.ds_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 2, 64)])
+def test_one_workspace_for_any_trees(hq, hkv, d):
+    """Large trees, ragged small ones and single nodes by turns over one
+    workspace, zeroed once: each finds its arrival counters at zero."""
+    lens = [700, 3000, 40, 1999, 512, 5000, 0, 333]
+    sizes = ([64, 40, 33, 64, 50, 64, 64, 20], [3, 1, 3, 1, 3, 1, 3, 1], [1] * 8,
+             [2, 4, 1, 3, 0, 4, 2, 2])
+    calls = []
+    for i, trees in enumerate(sizes):
+        c, q, offs, par = K._attn_case(lens, trees, hq, hkv, d, 16, seed=40 + i)
+        calls.append((c, q, offs, par, K._oracle_attn(c, q, lens, offs, par, 64)))
+    ws = None
+    for i in (0, 1, 0, 2, 1, 3, 0, 3, 2, 0):
+        c, q, offs, par, (o, A, s) = calls[i]
+        out = torch.full(q.shape, 9.0, device=DEV)
+        score = torch.full((8, 90), -5.0, device=DEV)
+        base = dict(q=q, k_cache=c.k, v_cache=c.v, page_table=c.dtable, ctx_lens=K.i32(lens),
+                    tree_offsets=K.i32(offs), parents=K.i32(par), page_size=16, chunk_size=64,
+                    out=out, chunk_scores=score)
+        size = B.ds_kv4_verify_attn_workspace_size(B.kv4_attn_args(**base))
+        if ws is None:
+            ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+        assert size == ws.numel()
+        B.ds_kv4_verify_attn(B.kv4_attn_args(workspace=ws, **base))
+        assert B.ds_device_status(ws) == 0
+        K._check_attn(out, score, o, A, s, lens, 64, i)

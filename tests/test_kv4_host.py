@@ -206,3 +206,22 @@ def test_binding_refuses_wrong_tensors(lib):
         B.kv4_rows_args(x, x[:2], pool, pool, table, i32, i32, page_size=16)
     a = B.kv4_rows_args(x, x, pool, pool, table, i32, i32, page_size=16)
     assert (a.n_rows, a.num_kv_heads, a.head_dim, a.k_row_stride) == (3, 4, 64, 256)
+
+
+def _size(lib, **kw):
+    n = C.c_size_t(0)
+    a = _attn(**kw)
+    assert lib.ds_kv4_verify_attn_workspace_size(C.byref(a), C.byref(n)) == B.DS_OK
+    return n.value
+
+
+@pytest.mark.parametrize("batch,hq,hkv,d", [(1, 32, 8, 128), (8, 32, 8, 128), (3, 16, 1, 64),
+                                            (40, 8, 8, 64), (5, 6, 3, 128)])
+@pytest.mark.parametrize("scores", [4096, None])
+def test_attn_workspace_does_not_depend_on_the_trees(lib, batch, hq, hkv, d, scores):
+    """One workspace serves calls of any tree sizes, by either pass: nothing
+    behind the arrival counters may move with n_nodes."""
+    kw = dict(batch=batch, num_q_heads=hq, num_kv_heads=hkv, head_dim=d, chunk_scores=scores)
+    sizes = {_size(lib, n_nodes=n, **kw) for n in (0, 1, batch, 2 * batch, 3 * batch + 1,
+                                                   4 * batch, 5 * batch, 16 * batch, 64 * batch)}
+    assert len(sizes) == 1, sizes
