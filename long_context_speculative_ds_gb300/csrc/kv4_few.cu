@@ -155,8 +155,11 @@ DS_DEV uint32_t lds_u8(uint32_t a) {
 // The piece of this block's range that begins at unit x (x < 0: its first);
 // false when the block has none.  One warp, which writes *pc: the plan is
 // worked out again for every piece, so that nothing of it stays in registers.
+// Offsets that go up and down can describe more nodes than there are, and
+// more segments than there are counters: then there is no work (*overlap).
 template <int R, int W>
-__device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc) {
+__device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc,
+                                        int32_t* overlap) {
   const int lane = threadIdx.x & 31;
   // units and segments of sequence b (lane-parallel)
   struct Seq { int L, T, node0, rows, nu, segs; };
@@ -171,16 +174,19 @@ __device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc) {
     return s;
   };
   const bool report = blockIdx.x == 0 && x < 0;
-  int U = 0, S = 0;
+  int U = 0, S = 0, nodes = 0;
   unsigned most = 0, least = ~0u;                 // units of a segment
   const Seq first = seq_of(lane, report);
   for (int b0 = 0; b0 < pa.batch; b0 += 32) {
     const Seq s = b0 == 0 ? first : seq_of(b0 + lane, report);
     U += __reduce_add_sync(0xffffffffu, s.segs * s.nu);
     S += __reduce_add_sync(0xffffffffu, s.segs);
+    nodes += __reduce_add_sync(0xffffffffu, s.T);
     most = max(most, __reduce_max_sync(0xffffffffu, s.segs ? (unsigned)s.nu : 0u));
     least = min(least, __reduce_min_sync(0xffffffffu, s.segs ? (unsigned)s.nu : ~0u));
   }
+  if (report && lane == 0) *overlap = nodes > pa.n_nodes;
+  if (nodes > pa.n_nodes) return false;
   // at most one block per segment or, for long segments, per 2 W units
   const int N = min((int)gridDim.x, max(S, (U + 2 * W - 1) / (2 * W)));
   const int i = blockIdx.x;
@@ -772,7 +778,10 @@ kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
   grid_dep_launch_dependents();
   if (threadIdx.x == 0) ctrl.n_cut = 0;
   Piece& pc = ctrl.piece[warp];
-  bool more = find_piece<R, W>(ka.v.plan, -1, &pc), worked = false;
+  // the row groups' table is the tree pass's: its first word tells the
+  // salience's launch that there is nothing to sum
+  int32_t* const overlap = reinterpret_cast<int32_t*>(ka.v.gdesc);
+  bool more = find_piece<R, W>(ka.v.plan, -1, &pc, overlap), worked = false;
   while (more) {                   // the same for every warp of the block
     if (pc.u1 > pc.u0) {
       work_piece<D, NT>(ka, pc, ctrl, smem, warp);
@@ -780,7 +789,7 @@ kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
     }
     const int next = pc.next;
     __syncwarp();
-    more = next >= 0 && find_piece<R, W>(ka.v.plan, next, &pc);
+    more = next >= 0 && find_piece<R, W>(ka.v.plan, next, &pc, overlap);
   }
   // Only the barriers of a piece order n_cut's first value before its read by
   // the other warps: a block without a piece leaves here, in every warp.
@@ -891,6 +900,7 @@ __global__ void __launch_bounds__(256) kv4_scores_few(const __grid_constant__ Ve
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (!work) return;
+  const int overlap = __ldcg(reinterpret_cast<const int32_t*>(a.gdesc));
   float sum = 0.f;
   for (int e = hl < hp ? e0 : per_head; e < per_head; e += 32) {
     const int r = e % sq.rows;
@@ -911,7 +921,7 @@ __global__ void __launch_bounds__(256) kv4_scores_few(const __grid_constant__ Ve
     }
   }
   sum = warp_sum(sum);
-  if (lane == 0) *dst = before + sum;
+  if (lane == 0 && !overlap) *dst = before + sum;
 }
 
 template <int D, int NT>

@@ -73,3 +73,32 @@ def test_one_workspace_for_any_trees(hq, hkv, d):
         B.ds_kv4_verify_attn(B.kv4_attn_args(workspace=ws, **base))
         assert B.ds_device_status(ws) == 0
         K._check_attn(out, score, o, A, s, lens, 64, i)
+
+
+def test_offsets_that_go_up_and_down():
+    """Offsets under which sequences share nodes: more segments than a call of
+    that many nodes has.  Nothing is written, the bit is set, and the workspace
+    serves the next call."""
+    hq, hkv, d, batch = 8, 2, 64, 16
+    lens = [600, 45] * (batch // 2)
+    trees = [4] * batch                                   # 16 rows a sequence and kv head
+    c, q, offs, par = K._attn_case(lens, trees, hq, hkv, d, 16, seed=50)
+    o, A, s = K._oracle_attn(c, q, lens, offs, par, 32)
+    out = torch.full(q.shape, 9.0, device=DEV)
+    score = torch.full((batch, 30), -5.0, device=DEV)
+    offsets = K.i32([0, 64] * (batch // 2) + [0])
+    base = dict(q=q, k_cache=c.k, v_cache=c.v, page_table=c.dtable, ctx_lens=K.i32([500] * batch),
+                tree_offsets=offsets, parents=K.i32(par), page_size=16, chunk_size=32, out=out,
+                chunk_scores=score)
+    ws = torch.zeros(B.ds_kv4_verify_attn_workspace_size(B.kv4_attn_args(**base)),
+                     dtype=torch.uint8, device=DEV)
+    args = B.kv4_attn_args(workspace=ws, **base)
+    B.ds_kv4_verify_attn(args)
+    assert B.ds_device_status(ws) & B.DS_DEV_BAD_TREE
+    assert bool((out == 9.0).all()) and bool((score == -5.0).all())
+    assert bool((ws[256:256 + 4 * 98] == 0).all())        # the counters: 2 (3 batch + 1)
+    offsets.copy_(K.i32(offs))
+    base["ctx_lens"].copy_(K.i32(lens))
+    B.ds_kv4_verify_attn(args)
+    torch.cuda.synchronize()
+    K._check_attn(out, score, o, A, s, lens, 32)
