@@ -541,7 +541,8 @@ ds_status ds_qk_norm_rope(const ds_norm_rope_args* args, void* stream);
  *
  * Both: a length below 0, past max_pages * page_size or row offsets that
  * decrease or leave [0, n_rows] set DS_DEV_BAD_LENGTH and skip the sequence
- * (new_lens[b] is from_lens[b] then);
+ * (new_lens[b] is from_lens[b] then; with n_rows 0 and no new_lens there is
+ * nothing to do and nothing is looked at);
  * a page id outside [0, num_pages) sets DS_DEV_BAD_PAGE, and that slot is
  * not written (its row reads as zeros).  Two rows must not share a slot.
  * Refused: head_dim not 64 or 128; page_size not 16, 32, 64 or 128;

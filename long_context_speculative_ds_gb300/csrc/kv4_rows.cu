@@ -41,6 +41,7 @@ struct Kv4RowsKArgs {
   const int32_t* n_accepted;
   int32_t batch, n_rows, num_kv_heads, page_size, page_shift, num_pages, max_pages;
   int32_t slices;                 // warps that share a row group's units
+  int32_t row_blocks;             // the blocks behind these look at the sequences
   float mult[2];                  // write: 2^-exp, read: 2^exp
   int32_t* new_lens;
   uint32_t* status;
@@ -94,24 +95,29 @@ __global__ void __launch_bounds__(256) kv4_rows(const Kv4RowsKArgs a) {
   grid_dep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  // with a path, "rows" are the path's entries: DS_MAX_TREE_NODES a sequence
-  const int total = a.path ? a.batch * DS_MAX_TREE_NODES : a.n_rows;
-  const int64_t e = w / a.slices * RW + lane / LPH;
-  // new lengths: the first thread of each sequence's number in the grid
-  if (WRITE && a.new_lens) {
-    const int64_t tid = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (int64_t b = tid; b < a.batch; b += (int64_t)gridDim.x * 256) {
-      int n0, n, from, add = 0;
-      if (rows_of(a, (int)b, n0, n, from)) {
+  // The last blocks have a thread per sequence, which checks its offsets and
+  // length even when no row is mapped to it (offsets that decrease or leave
+  // the rows), and writes the length that follows.
+  if ((int)blockIdx.x >= a.row_blocks) {
+    const int b = (blockIdx.x - a.row_blocks) * 256 + threadIdx.x;
+    if (b >= a.batch) return;
+    int n0, n, from, add = 0;
+    const bool usable = rows_of(a, b, n0, n, from);
+    if (WRITE && a.new_lens) {
+      if (usable) {
         add = n;
         if (a.path && n > 0) {
           const int acc = __ldg(a.n_accepted + b);
-          add = 1 + (path_ok(a, (int)b, n, acc) ? acc : 0);
+          add = 1 + (path_ok(a, b, n, acc) ? acc : 0);
         }
       }
       a.new_lens[b] = from + add;
     }
+    return;
   }
+  // with a path, "rows" are the path's entries: DS_MAX_TREE_NODES a sequence
+  const int total = a.path ? a.batch * DS_MAX_TREE_NODES : a.n_rows;
+  const int64_t e = w / a.slices * RW + lane / LPH;
   if (e >= total) return;
   int row, slot, b, n0, n, from;
   if (WRITE && a.path) {
@@ -244,7 +250,8 @@ static cudaError_t launch_rows(const ds_kv4_rows_args& g, cudaStream_t stream) {
   const int units = 2 * g.num_kv_heads;
   const int64_t spread = kRowWarps / std::max<int64_t>(1, groups);
   a.slices = (int)std::max<int64_t>(1, std::min<int64_t>(units, spread));
-  const dim3 grid((unsigned)std::max<int64_t>(1, (groups * a.slices + 7) / 8));
+  a.row_blocks = (int)((groups * a.slices + 7) / 8);
+  const dim3 grid((unsigned)(a.row_blocks + (g.batch + 255) / 256));
   if (g.head_dim == 128)
     return launch_dependent(kv4_rows<128, WRITE>, grid, dim3(256), 0, stream, a);
   return launch_dependent(kv4_rows<64, WRITE>, grid, dim3(256), 0, stream, a);
