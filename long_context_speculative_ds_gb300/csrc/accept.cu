@@ -1254,20 +1254,13 @@ accept_finish(AcceptKArgs a) {
 
 template <int G>
 cudaError_t launch_reject_g(const AcceptKArgs& a, int per, cudaStream_t stream) {
-  static bool attr_set = false;   // the attribute is per device function
-  const int max_smem = G * kAccThreads * (int)sizeof(float4);
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(accept_reject_node<G>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(accept_finish<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               max_smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  const size_t max_smem = G * kAccThreads * sizeof(float4);
+  cudaError_t e = allow_smem(accept_reject_node<G>, max_smem);
+  if (e == cudaSuccess) e = allow_smem(accept_finish<G>, max_smem);
+  if (e != cudaSuccess) return e;
   const size_t smem = (size_t)per * sizeof(float);
-  cudaError_t e = launch_dependent(accept_reject_node<G>, dim3(a.n_nodes * kAccCluster),
-                                   dim3(kAccThreads), smem, stream, a);
+  e = launch_dependent(accept_reject_node<G>, dim3(a.n_nodes * kAccCluster), dim3(kAccThreads),
+                       smem, stream, a);
   if (e != cudaSuccess) return e;
   return launch_dependent(accept_finish<G>, dim3(a.batch * kAccCluster), dim3(kAccThreads),
                           smem, stream, a);

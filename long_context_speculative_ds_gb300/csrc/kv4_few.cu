@@ -927,15 +927,10 @@ __global__ void __launch_bounds__(256) kv4_scores_few(const __grid_constant__ Ve
 template <int D, int NT>
 static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t stream) {
   const size_t smem = Cfg<D, NT>::smem;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(kv4_split_few<D, NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
-  cudaError_t e = launch_dependent(kv4_split_few<D, NT>, dim3(L.target_ctas),
-                                   dim3(32 * Cfg<D, NT>::W), smem, stream, k);
+  cudaError_t e = allow_smem(kv4_split_few<D, NT>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kv4_split_few<D, NT>, dim3(L.target_ctas), dim3(32 * Cfg<D, NT>::W), smem,
+                       stream, k);
   if (e != cudaSuccess || !k.v.scores || k.v.plan.max_chunks == 0) return e;
   return launch_dependent(kv4_scores_few,
                           dim3((k.v.plan.max_chunks + 7) / 8, k.v.plan.batch), dim3(256), 0,

@@ -1051,21 +1051,16 @@ __global__ void __launch_bounds__(256, 4) kv4_finish(const __grid_constant__ Ver
 template <int D>
 static cudaError_t launch_tc(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t stream) {
   const size_t smem = kv4tc::Cfg<D>::smem;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(kv4tc::kv4_split_tc<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  cudaError_t e = allow_smem(kv4tc::kv4_split_tc<D>, smem);
+  if (e != cudaSuccess) return e;
   const VerifyKArgs& v = k.v;
   // The plan makes at most one item per SM, two in its two-wave form, or one
   // per row group.  No blocks beyond that: one without work still takes an
   // SM's turn, behind the last items when those end together.
   const int64_t groups = (int64_t)v.plan.batch * v.plan.num_kv_heads * v.plan.rg_max;
   const int64_t blocks = std::max<int64_t>(groups, std::max(L.target_ctas, L.wave_ctas));
-  cudaError_t e = launch_dependent(kv4tc::kv4_split_tc<D>, dim3((unsigned)blocks),
-                                   dim3(kv4tc::kThreads), smem, stream, k);
+  e = launch_dependent(kv4tc::kv4_split_tc<D>, dim3((unsigned)blocks), dim3(kv4tc::kThreads),
+                       smem, stream, k);
   if (e != cudaSuccess) return e;
   const int64_t n_comb = ((int64_t)v.plan.n_nodes * v.num_q_heads + 7) / 8;
   const int64_t n_fin = v.scores ? (int64_t)v.plan.batch * ((v.plan.max_chunks + 7) / 8) : 0;

@@ -743,13 +743,8 @@ cudaError_t launch_tc(const VerifyKArgs& k, const ds_verify_args& a, const Verif
   if (!encode(&tk, a.k_cache, 5, dims, strides, box)) return cudaErrorInvalidValue;
   if (!encode(&tv, a.v_cache, 5, dims, strides, box)) return cudaErrorInvalidValue;
   const size_t smem = tc::Cfg<D>::smem;
-  static bool attr = false;
-  if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(tc::verify_split_tc<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  const cudaError_t e = allow_smem(tc::verify_split_tc<D>, smem);
+  if (e != cudaSuccess) return e;
   return launch_dependent(tc::verify_split_tc<D>, dim3(L.max_items), dim3(tc::kThreads), smem,
                           stream, tq, tk, tv, k, hnd ? 1 : 0);
 }
