@@ -877,8 +877,10 @@ kv4_split_few(const __grid_constant__ Kv4KArgs ka) {
 // round trip (2 to 4 us behind the split pass).
 __global__ void __launch_bounds__(256) kv4_scores_few(const __grid_constant__ VerifyKArgs a) {
   constexpr int NB = 8;
-  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = blockIdx.x * 8 + warp;
+  // sequences and chunks share the grid's long axis: the others end at 65,535
+  const int per_b = (a.plan.max_chunks + 7) / 8;
+  const int b = blockIdx.x / per_b, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = (blockIdx.x - b * per_b) * 8 + warp;
   // the lengths (and the sums so far) are inputs of the call: the split pass,
   // which this launch follows, has itself waited for whatever wrote them
   const SeqPlan sq = seq_sizes(a.plan, b, false);
@@ -932,9 +934,8 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
   e = launch_dependent(kv4_split_few<D, NT>, dim3(L.target_ctas), dim3(32 * Cfg<D, NT>::W), smem,
                        stream, k);
   if (e != cudaSuccess || !k.v.scores || k.v.plan.max_chunks == 0) return e;
-  return launch_dependent(kv4_scores_few,
-                          dim3((k.v.plan.max_chunks + 7) / 8, k.v.plan.batch), dim3(256), 0,
-                          stream, k.v);
+  const int64_t blocks = (int64_t)k.v.plan.batch * ((k.v.plan.max_chunks + 7) / 8);
+  return launch_dependent(kv4_scores_few, dim3((unsigned)blocks), dim3(256), 0, stream, k.v);
 }
 
 }  // namespace kv4few

@@ -1,7 +1,8 @@
 // A CUDA runtime of two devices, as far as the library's launches see it, and
 // the library's own entry points over it: a launch is refused unless its
-// kernel may use as much dynamic shared memory on the current device.  Nothing
-// runs; the pointers are never read.
+// kernel may use as much dynamic shared memory on the current device, and its
+// grid has sizes that a grid can have.  Nothing runs; the pointers are never
+// read.  With the argument "batches": calls of batches up to 200,000.
 #include <cuda.h>
 #include <cuda_runtime_api.h>
 
@@ -28,6 +29,9 @@ cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute attr, int valu
   return cudaSuccess;
 }
 cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t* cfg, const void* f, void**) {
+  const dim3 g = cfg->gridDim;
+  if (g.x < 1 || g.x > 0x7fffffffu || g.y < 1 || g.y > 65535 || g.z < 1 || g.z > 65535)
+    return cudaErrorInvalidConfiguration;
   if (cfg->dynamicSmemBytes > 48 * 1024) {
     ++g_large;
     auto it = g_allowed.find({g_device, f});
@@ -51,13 +55,16 @@ static T* at(uintptr_t x) {
   return reinterpret_cast<T*>(x);
 }
 
-static ds_status kv4(int nodes, int d) {
+static ds_status kv4(int nodes, int d, int batch = 1, bool scores = false) {
   ds_kv4_attn_args a;
   ds_kv4_attn_args_default(&a);
   a.q = at<void>(4096); a.k_cache = at<void>(8192); a.v_cache = at<void>(12288);
   a.page_table = at<int32_t>(64); a.ctx_lens = at<int32_t>(64);
   a.tree_offsets = at<int32_t>(64); a.parents = at<int32_t>(64);
-  a.batch = 1; a.n_nodes = nodes; a.num_q_heads = 8; a.num_kv_heads = 2; a.head_dim = d;
+  a.batch = batch; a.n_nodes = nodes; a.num_q_heads = 8; a.num_kv_heads = 2; a.head_dim = d;
+  if (scores) {
+    a.chunk_scores = at<float>(16384); a.chunk_size = 64; a.max_chunks = 9;
+  }
   a.page_size = 16; a.num_pages = 9; a.max_pages = 9; a.num_sms = 152;
   a.out = at<void>(16384); a.workspace = at<void>(65536); a.workspace_bytes = (size_t)1 << 40;
   return ds_kv4_verify_attn(&a, nullptr);
@@ -89,7 +96,21 @@ static ds_status reject(int vocab) {
   return ds_accept(&a, nullptr);
 }
 
-int main() {
+static int batches() {
+  int bad = 0;
+  for (int batch : {1, 33, 65535, 65536, 200000})
+    for (int nodes : {1, 4, 9})
+      for (bool scores : {false, true}) {
+        if (kv4(nodes * batch, 64, batch, scores) == DS_OK) continue;
+        ++bad;
+        std::printf("batch %d, %d nodes each, salience %d: %s\n", batch, nodes, scores,
+                    ds_last_error());
+      }
+  return bad;
+}
+
+int main(int argc, char** argv) {
+  if (argc > 1 && !std::strcmp(argv[1], "batches")) return batches() != 0;
   int bad = 0;
   for (int turn = 0; turn < 4; ++turn) {
     g_device = turn & 1;
