@@ -597,8 +597,8 @@ ds_status ds_kv4_read(const ds_kv4_rows_args* args, void* stream);
  * sets DS_DEV_BAD_PAGE and its slots read as zeros.  Offsets that are not
  * monotone set DS_DEV_BAD_TREE; when they describe more nodes than n_nodes, the
  * call may write nothing.  The workspace's size does not depend on n_nodes.
- * Refused by name: as ds_verify_attn, and exponents outside [-32, 32] and
- * max_pages * page_size above 2^30. */
+ * Refused by name: as ds_verify_attn, and exponents outside [-32, 32],
+ * scale * 2^k_exp beyond float32 and max_pages * page_size above 2^30. */
 typedef struct ds_kv4_attn_args {
   const void*    q;             /* [n_nodes, num_q_heads, head_dim] bf16         */
   const void*    k_cache;       /* 4-bit pools                                   */

@@ -600,7 +600,12 @@ static ds_status check_kv4_attn(const ds_kv4_attn_args* a, ds_verify_args* v) {
                            a->v_exp);
   if (st != DS_OK) return st;
   *v = ds::kv4_as_verify(*a);
-  return check_verify_sizes(v);
+  st = check_verify_sizes(v);
+  if (st != DS_OK) return st;
+  // (the kernels' factor is log2(e) of it)
+  REQUIRE(std::isfinite(std::ldexp(a->scale, a->k_exp + 1)), DS_ERR_INVALID_ARG,
+          "scale %g times 2^k_exp (%d) must stay within float32", a->scale, a->k_exp);
+  return DS_OK;
 }
 
 ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* a, size_t* bytes) {

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "dev_common.cuh"
@@ -67,7 +68,9 @@ cudaError_t launch_kv4_attn(const ds_kv4_attn_args& a, const VerifyLayout& L,
   k.num_q_heads = a.num_q_heads;
   k.num_pages = a.num_pages;
   const float scale = a.scale != 0.f ? a.scale : 1.0f / sqrtf((float)a.head_dim);
-  k.scale_log2 = ldexpf(scale * kLog2e, a.k_exp);
+  // never zero: a hidden slot's score is -inf, and -inf times zero no number.
+  // Products with the keys stay below 2^35, so that every weight is the same either way.
+  k.scale_log2 = fmaxf(ldexpf(scale * kLog2e, a.k_exp), FLT_MIN);
   k.counters = reinterpret_cast<uint32_t*>(ws + L.counters);
   k.gdesc = reinterpret_cast<int4*>(ws + L.gdesc);
   k.o_part = reinterpret_cast<float*>(ws + L.o_part);

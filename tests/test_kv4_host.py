@@ -225,3 +225,13 @@ def test_attn_workspace_does_not_depend_on_the_trees(lib, batch, hq, hkv, d, sco
     sizes = {_size(lib, n_nodes=n, **kw) for n in (0, 1, batch, 2 * batch, 3 * batch + 1,
                                                    4 * batch, 5 * batch, 16 * batch, 64 * batch)}
     assert len(sizes) == 1, sizes
+
+
+@pytest.mark.parametrize("scale,k_exp", [(3e38, 1), (1e30, 32), (3.3e38, 0)])
+def test_attn_refuses_a_scale_beyond_float32(lib, scale, k_exp):
+    n = C.c_size_t(0)
+    a = _attn(scale=scale, k_exp=k_exp)
+    assert lib.ds_kv4_verify_attn_workspace_size(C.byref(a), C.byref(n)) == B.DS_ERR_INVALID_ARG
+    assert "scale" in lib.ds_last_error().decode()
+    assert lib.ds_kv4_verify_attn(C.byref(a), None) == B.DS_ERR_INVALID_ARG
+    assert _size(lib, scale=scale, k_exp=-4) > 0
