@@ -6,9 +6,12 @@ committed behind the root.
 
 `Kv4Step` owns the step's buffers (4-bit pools, normed rows, outputs,
 workspaces) for fixed sizes; every computation is a call into the library.
-Retrieval and acceptance are the entry points the bf16 cache uses:
-`scores` feeds ds_chunk_topk_gather, and ds_accept's path and count feed
-`commit`.
+Acceptance and retrieval are the entry points the bf16 cache uses: ds_accept's
+path and count feed `commit`, and `scores` feeds ds_chunk_topk_gather.  That
+gathers from bf16 pools, so retrieval is for a draft model that keeps a bf16
+cache of its own on the same page table (before rotation, when it asks for
+local positions); the rows of this cache, which are rotated at their absolute
+positions, come back as bf16 with `read`.
 """
 from __future__ import annotations
 
@@ -39,7 +42,10 @@ class Kv4Step:
     heads, key heads, value heads.  All device-side inputs (page_table,
     ctx_lens, tree_offsets, parents, positions, qkv) are read at call time, so
     the same object serves the following steps when they are written in
-    place."""
+    place.  `commit` reads the value heads of qkv[l] once more (the key heads
+    it has in k_rows): layers of trees with more than one node need a buffer
+    each, and the next step's rows may only be written behind the commit on
+    its stream."""
 
     def __init__(self, qkv: List[torch.Tensor], page_table: torch.Tensor,
                  ctx_lens: torch.Tensor, tree_offsets: torch.Tensor,
@@ -113,7 +119,8 @@ class Kv4Step:
 
     def commit(self, path, n_accepted, stream=None):
         """The accepted nodes' rows behind the root in every layer, and
-        new_ctx_lens."""
+        new_ctx_lens.  Reads k_rows[l] and the value heads of qkv[l], which
+        must still be those that verify_layer(l) has seen."""
         for l in range(self.layers):
             a = self._rows(l, self.k_rows[l], self.v_rows[l], self.ctx_lens, self.tree_offsets,
                            path=path, n_accepted=n_accepted,
