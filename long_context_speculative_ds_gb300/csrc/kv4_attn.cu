@@ -19,9 +19,10 @@ int kv4_few_rows(const ds_kv4_attn_args& a) {
   // device, and both passes handle any.  The tree pass takes as long for any
   // number up to its tile of 128, this one in proportion to tiles of 8 from
   // the second on.  Single calls with the cache not in the L2, 8 kv heads, 4
-  // rows a node, 128K keys: 2 nodes 56 us, 4 nodes 68, 5 to 32 nodes in the
-  // tree pass 97 to 101.  8 sequences of 2K: 4 nodes 32, 5 nodes there 45;
-  // head_dim 64, 128K: 50 and 85.
+  // rows a node, 128K keys: 2 nodes 54 us, 4 nodes 68, 5 to 32 nodes in the
+  // tree pass 95 to 99.  8 sequences of 2K: 4 nodes 31, 5 nodes there 44;
+  // head_dim 64, 128K: 50 and 80.  All trees of these batches are alike: in a
+  // mixed one the rule may give some sequences the slower pass.
   const int64_t group = a.num_q_heads / a.num_kv_heads;
   const int64_t rows = ((int64_t)a.n_nodes + a.batch - 1) / a.batch * group;
   if (rows > 16) return 0;

@@ -12,13 +12,13 @@
 //   S^T[16 keys, 8 rows] += K[16 keys, 16 channels] Q^T[16 channels, 8 rows]
 //   O^T[16 dims, 8 rows] += V^T[16 dims, 16 keys]  P^T[16 keys, 8 rows]
 //
-// One token over 128K (32 query heads on 8 of the cache, 151 MB) takes 44.8
-// us, 3.4 TB/s of the 6.78 a copy reaches.  An earlier form of 48 took 39
+// One token over 128K (32 query heads on 8 of the cache, 151 MB) takes 43.8
+// us, 3.4 TB/s of the 6.70 a copy reaches.  An earlier form of 48 took 39
 // without the products and 44 without the loads: conversions and products
-// (issue slots 57 % busy) and the stream overlap, and some 12 us go into the
+// (issue slots 58 % busy) and the stream overlap, and some 12 us go into the
 // start, the merge, the join and the salience.  A ragged batch of eight (4K to
-// 128K, no salience) takes 86 us, 4.6 TB/s; one token over 512 keys, with 4
-// heads of 64 on 2, 8.8 us.
+// 128K, no salience) takes 84 us, 4.7 TB/s; one token over 512 keys, with 4
+// heads of 64 on 2, 9.0 us.
 //
 // Which channels make up a step of the first product, and which dims a tile
 // of the second, is free as long as both operands agree.  Lane 4g + t takes
@@ -42,7 +42,9 @@
 // segment was cut between blocks, the last of them to finish merges the
 // pieces into the output (with few rows that costs less than a launch); only
 // the salience takes a second kernel.  Each warp works the plan out by
-// itself, from the lengths, in one pass over the batch.
+// itself, from the lengths, in one pass over the batch, and again for every
+// piece: with a thousand sequences that is what takes the time (8 heads over
+// 1K keys each: 64 sequences 55 us, 256 264, 1,024 2,450).
 //
 // Chunk masses are kept per 32 keys or less ("subchunks"), so that a unit
 // never shares one: [kv head][sequence's rows x subchunks][subchunk][row],
@@ -66,6 +68,7 @@ constexpr int kStages = 3;      // blocks of 32 keys in a warp's ring
 constexpr int kBlock = 32;                       // keys of a block, and of a unit
 // A piece's start (plan, page ids, first copies) and end (merge) take about
 // as long as 40 units do in a block of 16 warps: 5 us against 0.13 us a unit
+// (heads of 128; the other forms were not measured for it and share it)
 constexpr int kPieceUnits = 40;
 
 template <int D, int NT>
@@ -193,7 +196,7 @@ __device__ __noinline__ bool find_piece(const PlanArgs& pa, int x, Piece* pc,
   // Segments of one length: cut evenly, a piece a block, down to a unit a
   // warp (but not for the second unit: the join costs as much), unless that
   // leaves more blocks idle than the cuts of the general way cost.  One token
-  // over 1K, 2K, 8K: 12, 13 and 16 us against 20, 18 and 18.
+  // over 1K, 2K, 8K: 12, 12 and 14 us; the general way had 20, 18 and 18.
   const int each =
       S > 0 ? min((int)gridDim.x / S, (int)most <= 2 * W ? 1 : ((int)most + W - 1) / W) : 0;
   const bool even = each > 0 && most == least &&
@@ -941,8 +944,9 @@ static cudaError_t launch(const Kv4KArgs& k, const VerifyLayout& L, cudaStream_t
 }  // namespace kv4few
 
 // Up to 8 rows a segment the queries stay in registers beside 16 warps (a
-// single call of 2 nodes of 4 rows over 128K: 56 us); above, two tiles of 8
-// need the shared memory and leave room for 12 (3 nodes: 70; with 16 warps and
+// single call of 2 nodes of 4 rows over 128K: 54 us); above, two tiles of 8
+// need the shared memory and leave room for 12 (3 nodes: 68, with 52 bytes a
+// thread spilled and 64 loaded at head_dim 128; with 16 warps and
 // the queries in registers, spilled, an earlier form of 4 nodes took 99
 // instead of 76).
 cudaError_t launch_kv4_few(const Kv4KArgs& k, int head_dim, int rows, const VerifyLayout& L,

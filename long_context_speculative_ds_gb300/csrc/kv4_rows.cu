@@ -2,12 +2,12 @@
 // ds_kv4_write and ds_kv4_read).
 //
 // Bound by memory when there are many rows, by latency when there are few:
-// with 8 heads of 128, 131,072 rows read back in 108.5 us, 6.3 TB/s of the
-// 6.78 a copy reaches; a ragged batch of eight prompts (88,518 rows) is written
-// and read back in 157 us, 5.9 TB/s (writing alone was 128 us before the
-// quantiser worked in packed maxima and products with a reciprocal, 81 after:
-// its arithmetic overlaps the loads only in part); 64 rows written and read
-// back 5.4 us.  A warp takes a few consecutive rows and walks over (tensor, kv head) units,
+// with 8 heads of 128, 131,072 rows read back in 108.7 us, 6.3 TB/s of the
+// 6.70 a copy reaches; a ragged batch of eight prompts (88,518 rows) is written
+// and read back in 158 us, 5.9 TB/s (writing alone was 128 us before the
+// quantiser worked in packed maxima and products with a reciprocal, 79 after,
+// 10 above its bytes: its arithmetic overlaps the loads only in part); 64 rows
+// written and read back 5.3 us.  A warp takes a few consecutive rows and walks over (tensor, kv head) units,
 // several units' loads on their way at once; with few rows the units of a row
 // are spread over more warps.  Which sequence a row belongs to, its slot and
 // its page are looked up once per lane, for all units.

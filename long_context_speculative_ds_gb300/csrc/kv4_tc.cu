@@ -9,9 +9,9 @@
 // below the row's maximum (verify_softmax.cuh).
 //
 // The two products of 256 query rows with 128K keys of eight heads (137
-// GFLOP) are 72 us of the tensor pipe at its measured rate; the 151 MB of the
-// cache are 22 us.  A call over 64 nodes and 32 query heads takes 122 us, 1.12
-// PFLOP/s or 59 %: about 22 us go into the start (plan 2.5, Q 2.5, first
+// GFLOP) are 70 us of the tensor pipe at its measured rate; the 151 MB of the
+// cache are 23 us.  A call over 64 nodes and 32 query heads takes 122 us, 1.13
+// PFLOP/s or 57 %: about 22 us go into the start (plan 2.5, Q 2.5, first
 // tile), the split outputs (2.5) and the join (8), and in between a tile takes
 // 1.8 us: 1.2 of products, 1.2 of softmax (0.9 with nothing beside it) and 0.7
 // of conversion share issue slots and wait for one another.
@@ -106,7 +106,8 @@ struct Cfg {
   static_assert(1024 <= kRing * RAW, "the merge's maxima and sums must fit in the raw ring");
 };
 
-// Cost of a tile: 1.28 us in key mode, 1.87 us in row mode (128K, 32 heads)
+// Cost of a tile: 1.28 us in key mode, 1.87 us in row mode (128K, 32 heads of
+// 128; calls over heads of 64 take 70 and 117 us there, 5 : 8, with the same)
 DS_DEV int tile_cost(const SeqPlan& s) { return s.rows <= 128 ? 5 : 7; }
 
 // The work item of this block, by one warp: near-equal ranges of tiles per
@@ -460,7 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_split_tc(const Kv4KArgs ka) {
 
   // registers move from the loader's and the converters' warpgroups to the
   // softmax groups: 128 (88 + 88) + 256 x 168 = the launch's 512 x 128.  At 80
-  // the issuers spill.
+  // the issuers spill.  With 128-wide heads nothing spills then; with 64-wide
+  // ones the paired conversion does (48 bytes stored, 296 loaded), and is
+  // faster all the same.
   static_assert(128 * (88 + 88) + 256 * 168 <= kThreads * 128, "more than the launch has");
   if (warp < 4) {
     regs_release<88>();
@@ -1038,6 +1041,8 @@ DS_DEV void chunk_score(const VerifyKArgs& a, int blk) {
   }
 }
 
+// Four blocks an SM leave 64 registers: 72 bytes spilled and 100 loaded at
+// head_dim 128, 28 and 32 at 64.
 template <int D>
 __global__ void __launch_bounds__(256, 4) kv4_finish(const __grid_constant__ VerifyKArgs a,
                                                      int n_comb, float out_mult) {

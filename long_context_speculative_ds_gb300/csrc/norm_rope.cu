@@ -5,8 +5,8 @@
 // (a cos - b sin, a sin + b cos), in float32 with one rounding to bf16.
 //
 // Bound by memory when there are many rows, by latency when there are few:
-// with 32 + 8 heads of 128, 32,768 rows take 112 us, 6.0 TB/s of the 6.78 a
-// copy reaches; 331 rows 4.5 us and one row 3.5 us, a launch and two round
+// with 32 + 8 heads of 128, 32,768 rows take 112 us, 6.0 TB/s of the 6.70 a
+// copy reaches; 331 rows 4.5 us and one row 3.3 us, a launch and two round
 // trips.  (A warp per row and one head at a time took 161, 10 and 9 us.)
 //
 // Eight lanes hold one head (head_dim 128; four at 64): lane l the eight
@@ -46,7 +46,9 @@ struct NormRopeKArgs {
 };
 
 constexpr int kNormWarps = 8;             // warps of a block
-constexpr int kNormBatch = 5;             // head groups of a warp, their loads together
+// Head groups of a warp, their loads together; at three blocks an SM (80
+// registers) a few words spill, 16 bytes stored and 48 loaded a thread.
+constexpr int kNormBatch = 5;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kNormWarps, 3) qk_norm_rope(const NormRopeKArgs a) {
