@@ -1,6 +1,5 @@
 """The library's launches, on the CPU: its own objects linked against a
 runtime of two devices that only keeps account (native/two_devices.cpp)."""
-import glob
 import os
 import shutil
 import subprocess
@@ -14,13 +13,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 @pytest.fixture(scope="module")
 def exe(tmp_path_factory):
-    build.build()
+    objs = [os.path.join(build.OUT_DIR, "_obj", s + ".o") for s in build.SOURCES]
+    build.build(force=not all(os.path.exists(o) for o in objs))
     cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
     libs = os.path.join(cuda, "lib64")
     if not os.path.exists(os.path.join(libs, "libcudart.so")):
         pytest.skip("no shared CUDA runtime to take the kernels' registration")
     out = str(tmp_path_factory.mktemp("native") / "two_devices")
-    objs = glob.glob(os.path.join(build.OUT_DIR, "_obj", "*.o"))
     r = subprocess.run(["g++", "-std=c++17", "-O1", "-I" + build.INCLUDE,
                         "-I" + os.path.join(cuda, "include"),
                         os.path.join(HERE, "native", "two_devices.cpp"), *objs, "-o", out,
