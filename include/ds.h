@@ -27,7 +27,20 @@
  *                         prompt, a tree, or the accepted path of a tree);
  *   ds_kv4_read           rows of the 4-bit cache read back as bf16;
  *   ds_kv4_verify_attn    ds_verify_attn over the 4-bit cache; a tree of one
- *                         node is plain decoding.
+ *                         node is plain decoding;
+ *
+ * and, for the draft model that decodes over the compact cache (or over a
+ * paged one of its own):
+ *
+ *   ds_rope_frequencies   the rotation's frequencies, scaled for long contexts
+ *                         (host only);
+ *   ds_rope_append        queries and keys rotated, keys and values written
+ *                         behind the cache's last slots (or the rotation alone,
+ *                         or its inverse);
+ *   ds_decode_attn        attention of one new token per sequence, every key's
+ *                         weight added to its running sum;
+ *   ds_cache_evict        a cache over its budget keeps its first and recent
+ *                         tokens and the heaviest of the others.
  *
  * Conventions (all entry points):
  *   - Every pointer named in an args struct is a DEVICE pointer unless its
@@ -87,7 +100,8 @@ typedef enum { DS_ACCEPT_GREEDY = 0, DS_ACCEPT_REJECT = 1 } ds_accept_mode;
 #define DS_DEV_BAD_PAGE     0x4u  /* a page id outside [0, num_pages)            */
 #define DS_DEV_BAD_TOKEN    0x8u  /* a draft token outside [0, vocab)            */
 #define DS_DEV_TIMEOUT      0x10u /* a bounded wait inside a kernel gave up      */
-#define DS_DEV_BAD_VALUE    0x20u /* a NaN or an infinity given to ds_kv4_write  */
+#define DS_DEV_BAD_VALUE    0x20u /* a NaN or an infinity given to ds_kv4_write, a
+                                     NaN among the weights of ds_cache_evict     */
 
 /* Name of the last failure on the calling thread ("" if none).  The string is
  * owned by the library and valid until the next call on this thread. */
@@ -97,8 +111,8 @@ const char* ds_last_error(void);
 int32_t ds_abi_version(void);
 
 /* sizeof() of each args struct as compiled into the library: 0 verify,
- * 1 gather, 2 accept, 3 commit, 4 append, 5 norm_rope, 6 kv4_rows, 8 kv4_attn; -1 for
- * anything else (7 is not assigned).  Bindings compare these with their own struct layouts
+ * 1 gather, 2 accept, 3 commit, 4 append, 5 norm_rope, 6 kv4_rows, 8 kv4_attn,
+ * 9 rope_scaling, 10 rope, 11 decode, 12 evict; -1 for anything else (7 is not assigned).  Bindings compare these with their own struct layouts
  * before the first call. */
 int64_t ds_struct_size(int32_t which);
 
@@ -633,6 +647,287 @@ void ds_kv4_attn_args_default(ds_kv4_attn_args* args);
 ds_status ds_kv4_verify_attn_workspace_size(const ds_kv4_attn_args* args,
                                             size_t* bytes);
 ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The draft's cache.
+ *
+ * The three calls below work on one layer's K/V cache of bf16 or f16 values,
+ * in one of two forms:
+ *   paged    (page_table given) as in ds_verify_attn: slot t of sequence b is
+ *            at offset t % page_size of page page_table[b][t / page_size];
+ *            page_size 16, 32, 64 or 128;
+ *   compact  (page_table NULL) as ds_chunk_topk_gather writes it: sequence b's
+ *            slots are page b, [batch, page_size, num_kv_heads, head_dim] (or
+ *            heads before slots with DS_KV_HND), page_size any capacity >= 1,
+ *            num_pages >= batch; max_pages is ignored.
+ * A sequence has max_pages * page_size slots (page_size when compact), at
+ * most 2^30.  Beside the cache a program may keep, per slot, the token's
+ * position (int32) and the sum of the attention weight it has received (f32),
+ * both [batch, slot_heads, slot_stride]: slot_heads 1 when all kv heads keep
+ * the same tokens, num_kv_heads when each keeps its own; slot_stride at least
+ * the slots of a sequence.  Slots need not be in order of position.
+ *
+ * Caches must be 16-byte aligned; head_dim 64 or 128.
+ * ------------------------------------------------------------------------ */
+typedef enum { DS_KV_BF16 = 0, DS_KV_F16 = 1 } ds_kv_dtype;
+
+/* Which two values of a head's first rotary_dim = r are rotated together:
+ * (j, j + r/2) or (2j, 2j + 1), j < r/2. */
+typedef enum { DS_ROPE_HALF = 0, DS_ROPE_INTERLEAVED = 1 } ds_rope_layout;
+
+/* Frequencies scaled for contexts longer than those of training.  Pair j has
+ * th = base^(-2j/r) radians per position; o = original_len, f = factor, and
+ * turns = o th / (2 pi), the pair's turns over the original length:
+ *   NONE    th
+ *   LINEAR  th / f
+ *   BANDS   th (s + (1 - s) / f), s = (turns - low) / (high - low) clamped to
+ *           [0, 1]: pairs of more than `high` turns as they are, those of
+ *           fewer than `low` divided by f
+ *   RAMP    th (1 - g + g / f), g = (j - lo) / (hi - lo) clamped to [0, 1],
+ *           d(n) = r ln(o / (2 pi n)) / (2 ln base), lo = max(0, floor
+ *           d(high)), hi = min(r - 1, ceil d(low)) (a denominator of zero or
+ *           less counts as 0.001); magnitude 0.1 ln f + 1
+ * The magnitude (1 but for RAMP) multiplies cosines and sines. */
+typedef enum {
+  DS_ROPE_SCALE_NONE = 0,
+  DS_ROPE_SCALE_LINEAR = 1,
+  DS_ROPE_SCALE_BANDS = 2,
+  DS_ROPE_SCALE_RAMP = 3
+} ds_rope_scale;
+
+typedef struct ds_rope_scaling {
+  int32_t kind;                 /* ds_rope_scale                                 */
+  int32_t rotary_dim;           /* r: even, 2 to 128                             */
+  double  base;                 /* > 1                                           */
+  double  factor;               /* f >= 1 (all but NONE)                         */
+  double  original_len;         /* o > 0 (BANDS, RAMP)                           */
+  double  low;                  /* turns, 0 < low < high (BANDS, RAMP)           */
+  double  high;
+} ds_rope_scaling;
+
+/* Zeros, kind NONE, factor 1. */
+void ds_rope_scaling_default(ds_rope_scaling* scaling);
+
+/* inv_freq[rotary_dim / 2] (HOST) in radians per position, for inv_freq of
+ * ds_rope_append and ds_qk_norm_rope, and *magnitude (HOST).  Host only.
+ * Refused: a value outside the ranges above, or not finite. */
+ds_status ds_rope_frequencies(const ds_rope_scaling* scaling, double* inv_freq,
+                              float* magnitude);
+
+/* ------------------------------------------------------------------------ *
+ * Rotation by position, and the new tokens' rows into the cache.
+ *
+ * For every row n (a token) and every query and key head x, with
+ * a_j = positions[n] * inv_freq[j] (or * rope_base^(-2j/r)) and m = magnitude:
+ *   (x_j, x_j') -> m (x_j cos a_j - x_j' sin a_j, x_j sin a_j + x_j' cos a_j)
+ * for the r/2 pairs (j, j') of `layout`; the values from r on are copied.
+ * With inverse = 1 the angles are -a_j: m times the transpose of the matrix
+ * without it, so that dL/dx = the inverse rotation of dL/dy (with the same m).
+ * Angles are reduced modulo one turn in 64-bit fixed point, sines, cosines and
+ * products are float32, and each value is rounded once.
+ *
+ * k_cache NULL: the rotation alone, q into q_out and k into k_out; v and the
+ * fields of the cache are ignored.
+ *
+ * With a cache, row row_offsets[b] + i of sequence b belongs to slot
+ * from_lens[b] + i: the rotated key and the value go there (and the key into
+ * k_out too when that is not NULL), slot_positions[b, :, slot] = positions[n]
+ * and slot_weights[b, :, slot] = 0 when given, and new_lens[b] = from_lens[b]
+ * + rows of b when given.  Rows that belong to no sequence, or to one that is
+ * refused, are left out altogether, q_out included.  Two rows must not share
+ * a slot.
+ *
+ * Rows may be slices of a wider buffer, as in ds_qk_norm_rope.  q_out may be q
+ * and k_out may be k, with the same stride; outputs must not overlap inputs
+ * otherwise.  num_q_heads 0 (no queries) or, without a cache, num_kv_heads 0
+ * is allowed.
+ *
+ * Checked on the device: a negative position sets DS_DEV_BAD_LENGTH and that
+ * row is left out (its slot keeps what it holds; new_lens counts it); a
+ * from_lens below 0, rows beyond the sequence's slots, or row offsets that
+ * decrease or leave [0, n_rows] set DS_DEV_BAD_LENGTH and leave the sequence
+ * out (new_lens[b] is from_lens[b] then); a page id outside [0, num_pages)
+ * sets DS_DEV_BAD_PAGE, and that slot's key and value are not written.
+ *
+ * Refused: head_dim not 64 or 128; rotary_dim not a multiple of 16 up to
+ * head_dim; pointers not 16-byte aligned or strides not a multiple of 8 or
+ * shorter than a row; new_lens == from_lens; enums out of range; magnitude,
+ * inv_freq or rope_base not finite, or neither or both of the last two given.
+ * ------------------------------------------------------------------------ */
+typedef struct ds_rope_args {
+  const void*    q;             /* n_rows rows of num_q_heads x head_dim         */
+  const void*    k;             /* n_rows rows of num_kv_heads x head_dim        */
+  const void*    v;             /* the same; only with a cache                   */
+  int64_t        q_row_stride;  /* elements from a row to the next               */
+  int64_t        k_row_stride;
+  int64_t        v_row_stride;
+  const int32_t* positions;     /* [n_rows] >= 0                                 */
+  int32_t n_rows;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128                                     */
+  int32_t dtype;                /* ds_kv_dtype of rows, outputs and cache        */
+  int32_t layout;               /* ds_rope_layout                                */
+  int32_t rotary_dim;           /* r; 0 selects head_dim                         */
+  int32_t inverse;              /* 0 or 1                                        */
+  float   rope_base;            /* > 0, or 0 with inv_freq                       */
+  float   magnitude;            /* m; default 1                                  */
+  const double*  inv_freq;      /* HOST array [r / 2], or NULL with rope_base    */
+  void*   q_out;
+  void*   k_out;                /* NULL: none (with a cache)                     */
+  int64_t q_out_row_stride;
+  int64_t k_out_row_stride;
+  void*   k_cache;              /* NULL: rotation alone                          */
+  void*   v_cache;
+  const int32_t* page_table;    /* [batch, max_pages]; NULL: compact             */
+  const int32_t* from_lens;     /* [batch] slot of each sequence's first row     */
+  const int32_t* row_offsets;   /* [batch + 1]                                   */
+  int32_t batch;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t kv_layout;            /* ds_kv_layout                                  */
+  int32_t slot_heads;           /* 1 or num_kv_heads; of the next two            */
+  int64_t slot_stride;
+  int32_t* slot_positions;      /* [batch, slot_heads, slot_stride] or NULL      */
+  float*   slot_weights;        /* the same, or NULL                             */
+  int32_t* new_lens;            /* [batch] out, or NULL                          */
+  void*   workspace;            /* >= 256 bytes: the status word                 */
+  size_t  workspace_bytes;
+} ds_rope_args;
+
+void ds_rope_args_default(ds_rope_args* args);
+ds_status ds_rope_append(const ds_rope_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Attention of one new token per sequence.
+ *
+ * Sequence b has n = lens[b] slots (the new token's own among them, when it
+ * was appended).  Query head h attends, under kv head h / (Hq/Hkv), to the
+ * slots t < n, with window > 0 only to t >= n - window and to t < sinks:
+ *   s_t = scale * <q[b, h, :], k_t>,  p = softmax(s),
+ *   out[b, h, :] = sum_t p_t v_t,  lse[b, h] = ln sum_t exp(s_t).
+ * A sequence without slots gets out 0 and lse -inf.
+ *
+ * With weights_out every slot t < n gets
+ *   weights_out[b, w, t] = decay * weights_in[b, w, t] + sum of p_t
+ * over the query heads of kv head w (slot_heads = num_kv_heads) or over all
+ * query heads (slot_heads = 1); p_t is 0 for slots that are not attended to.
+ * weights_in NULL counts as zeros; it may be weights_out.  Slots from n on
+ * are left as they were.
+ *
+ * Products are float32 sums of exact products; each weight enters the second
+ * product as the sum of two values of the cache's type, which is exact to
+ * 2^-16 of it (bf16; f16: 2^-22, or 2^-25 of the row's largest); maxima, sums,
+ * and what splits exchange are float32.
+ * What lies in slots that are not attended to (NaN included) has no effect.
+ * No state is kept in the workspace from call to call.
+ *
+ * Checked on the device: a length below 0 or beyond the sequence's slots sets
+ * DS_DEV_BAD_LENGTH and counts as 0; a page id outside [0, num_pages) sets
+ * DS_DEV_BAD_PAGE and its slots read as zeros.  Pages of which no slot is
+ * attended to are not looked up.
+ * Refused: head_dim not 64 or 128; num_q_heads not a multiple of
+ * num_kv_heads, or more than 16 query heads to a kv head; pointers not 16-byte
+ * aligned; q_row_stride not a multiple of 8 or shorter than a row; window,
+ * sinks, decay or scale negative or not finite; batch above 65,536.
+ * ------------------------------------------------------------------------ */
+typedef struct ds_decode_args {
+  const void*    q;             /* [batch] rows of num_q_heads x head_dim        */
+  int64_t        q_row_stride;  /* elements from a row to the next               */
+  const void*    k_cache;
+  const void*    v_cache;
+  const int32_t* page_table;    /* [batch, max_pages]; NULL: compact             */
+  const int32_t* lens;          /* [batch]                                       */
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128                                     */
+  int32_t dtype;                /* ds_kv_dtype of q and the cache                */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t kv_layout;            /* ds_kv_layout                                  */
+  float   scale;                /* softmax scale; 0 selects 1/sqrt(head_dim)     */
+  int32_t window;               /* 0: all slots                                  */
+  int32_t sinks;
+  void*   out;                  /* [batch, num_q_heads, head_dim]                */
+  int32_t out_f32;              /* 0: out has dtype, 1: float32                  */
+  float*  lse;                  /* [batch, num_q_heads], or NULL                 */
+  const float* weights_in;      /* [batch, slot_heads, slot_stride], or NULL     */
+  float*  weights_out;          /* the same, or NULL: no weights are formed      */
+  float   decay;                /* default 1                                     */
+  int32_t slot_heads;           /* 1 or num_kv_heads                             */
+  int64_t slot_stride;
+  int32_t num_sms;              /* CTAs to plan for; 0 = the device's SM count   */
+  void*   workspace;            /* >= ds_decode_attn_workspace_size              */
+  size_t  workspace_bytes;
+} ds_decode_args;
+
+void ds_decode_args_default(ds_decode_args* args);
+/* Depends on the sizes, on num_sms and on whether weights_out is given (then
+ * it holds a float32 per query head and slot). */
+ds_status ds_decode_attn_workspace_size(const ds_decode_args* args, size_t* bytes);
+ds_status ds_decode_attn(const ds_decode_args* args, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Eviction by accumulated attention weight, in place.
+ *
+ * A sequence of n = lens[b] slots is cut when n > max(budget, trigger), to
+ * `budget` slots, per slot head w (all kv heads together when slot_heads is
+ * 1): slots whose position is below `sinks`, or at least next_positions[b] -
+ * recent, come first, then those of the larger weight, of equal ones (-0 is
+ * 0) the lower slot; a NaN counts as lighter than any weight and sets
+ * DS_DEV_BAD_VALUE.  The first `budget` in this order are kept.  Kept slots
+ * below `budget` stay where they are; the kept slots from `budget` on move, in
+ * ascending order, into the slots below `budget` that are given up, ascending:
+ * K, V, position and weight.  new_lens[b] = budget.  Slots from `budget` on
+ * keep what they hold.  A sequence that is not cut keeps its n slots, and
+ * new_lens[b] = n.
+ *
+ * weights_out and positions_out, when given, receive the slots below new_lens
+ * and leave the inputs as they were (they must not overlap them, or be the
+ * inputs themselves, which is the same as NULL: in place).
+ *
+ * Checked on the device: a length below 0 or beyond the sequence's slots sets
+ * DS_DEV_BAD_LENGTH and the sequence is left alone (new_lens[b] = lens[b]); a
+ * page id outside [0, num_pages) sets DS_DEV_BAD_PAGE, and that token's key and
+ * value are not moved.  No state is kept in the workspace from call to call.
+ * Refused: budget below 1; recent + sinks above it; trigger, recent or sinks
+ * negative; new_lens == lens; sizes as in the calls above; batch *
+ * slot_heads above 65,536.
+ * ------------------------------------------------------------------------ */
+typedef struct ds_evict_args {
+  void*   k_cache;
+  void*   v_cache;
+  const int32_t* page_table;    /* [batch, max_pages]; NULL: compact             */
+  const int32_t* lens;          /* [batch]                                       */
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128 (values of two bytes of any type)   */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t kv_layout;            /* ds_kv_layout                                  */
+  int32_t slot_heads;           /* 1 or num_kv_heads                             */
+  int64_t slot_stride;
+  float*   weights;             /* [batch, slot_heads, slot_stride]              */
+  int32_t* positions;
+  float*   weights_out;         /* the same, or NULL: in place                   */
+  int32_t* positions_out;
+  const int32_t* next_positions; /* [batch] position of the next token           */
+  int32_t budget;
+  int32_t trigger;              /* 0: budget                                     */
+  int32_t recent;
+  int32_t sinks;
+  int32_t* new_lens;            /* [batch] out                                   */
+  void*   workspace;            /* >= ds_cache_evict_workspace_size              */
+  size_t  workspace_bytes;
+} ds_evict_args;
+
+void ds_evict_args_default(ds_evict_args* args);
+ds_status ds_cache_evict_workspace_size(const ds_evict_args* args, size_t* bytes);
+ds_status ds_cache_evict(const ds_evict_args* args, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

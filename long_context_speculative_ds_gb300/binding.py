@@ -24,6 +24,10 @@ DS_MAX_TREE_NODES = 64
 DS_DEV_BAD_LENGTH, DS_DEV_BAD_TREE, DS_DEV_BAD_PAGE, DS_DEV_BAD_TOKEN, \
     DS_DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
 DS_DEV_BAD_VALUE = 0x20
+DS_KV_BF16, DS_KV_F16 = 0, 1
+DS_ROPE_HALF, DS_ROPE_INTERLEAVED = 0, 1
+DS_ROPE_SCALE_NONE, DS_ROPE_SCALE_LINEAR, DS_ROPE_SCALE_BANDS, \
+    DS_ROPE_SCALE_RAMP = range(4)
 
 _p = C.c_void_p
 _i = C.c_int32
@@ -122,6 +126,58 @@ class Kv4AttnArgs(C.Structure):
                 ("workspace", _p), ("workspace_bytes", C.c_size_t)]
 
 
+class RopeScaling(C.Structure):
+    _fields_ = [("kind", _i), ("rotary_dim", _i), ("base", C.c_double),
+                ("factor", C.c_double), ("original_len", C.c_double),
+                ("low", C.c_double), ("high", C.c_double)]
+
+
+class RopeArgs(C.Structure):
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("q_row_stride", C.c_int64),
+                ("k_row_stride", C.c_int64), ("v_row_stride", C.c_int64),
+                ("positions", _p), ("n_rows", _i), ("num_q_heads", _i),
+                ("num_kv_heads", _i), ("head_dim", _i), ("dtype", _i),
+                ("layout", _i), ("rotary_dim", _i), ("inverse", _i),
+                ("rope_base", C.c_float), ("magnitude", C.c_float),
+                ("inv_freq", C.POINTER(C.c_double)), ("q_out", _p),
+                ("k_out", _p), ("q_out_row_stride", C.c_int64),
+                ("k_out_row_stride", C.c_int64), ("k_cache", _p),
+                ("v_cache", _p), ("page_table", _p), ("from_lens", _p),
+                ("row_offsets", _p), ("batch", _i), ("page_size", _i),
+                ("num_pages", _i), ("max_pages", _i), ("kv_layout", _i),
+                ("slot_heads", _i), ("slot_stride", C.c_int64),
+                ("slot_positions", _p), ("slot_weights", _p),
+                ("new_lens", _p), ("workspace", _p),
+                ("workspace_bytes", C.c_size_t)]
+
+
+class DecodeArgs(C.Structure):
+    _fields_ = [("q", _p), ("q_row_stride", C.c_int64), ("k_cache", _p),
+                ("v_cache", _p), ("page_table", _p), ("lens", _p),
+                ("batch", _i), ("num_q_heads", _i), ("num_kv_heads", _i),
+                ("head_dim", _i), ("dtype", _i), ("page_size", _i),
+                ("num_pages", _i), ("max_pages", _i), ("kv_layout", _i),
+                ("scale", C.c_float), ("window", _i), ("sinks", _i),
+                ("out", _p), ("out_f32", _i), ("lse", _p),
+                ("weights_in", _p), ("weights_out", _p),
+                ("decay", C.c_float), ("slot_heads", _i),
+                ("slot_stride", C.c_int64), ("num_sms", _i),
+                ("workspace", _p), ("workspace_bytes", C.c_size_t)]
+
+
+class EvictArgs(C.Structure):
+    _fields_ = [("k_cache", _p), ("v_cache", _p), ("page_table", _p),
+                ("lens", _p), ("batch", _i), ("num_kv_heads", _i),
+                ("head_dim", _i), ("page_size", _i), ("num_pages", _i),
+                ("max_pages", _i), ("kv_layout", _i), ("slot_heads", _i),
+                ("slot_stride", C.c_int64), ("weights", _p),
+                ("positions", _p), ("weights_out", _p),
+                ("positions_out", _p), ("next_positions", _p),
+                ("budget", _i), ("trigger", _i), ("recent", _i),
+                ("sinks", _i), ("new_lens", _p), ("workspace", _p),
+                ("workspace_bytes", C.c_size_t)]
+
+
 class DSError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"ds status {status}: {message}")
@@ -141,7 +197,11 @@ EXPORTS = ("ds_last_error", "ds_abi_version", "ds_struct_size",
            "ds_norm_rope_args_default", "ds_qk_norm_rope",
            "ds_kv4_rows_args_default", "ds_kv4_write", "ds_kv4_read",
            "ds_kv4_attn_args_default", "ds_kv4_verify_attn_workspace_size",
-           "ds_kv4_verify_attn")
+           "ds_kv4_verify_attn", "ds_rope_scaling_default",
+           "ds_rope_frequencies", "ds_rope_args_default", "ds_rope_append",
+           "ds_decode_args_default", "ds_decode_attn_workspace_size",
+           "ds_decode_attn", "ds_evict_args_default",
+           "ds_cache_evict_workspace_size", "ds_cache_evict")
 
 
 def lib_path() -> str:
@@ -169,11 +229,15 @@ def load(path: Optional[str] = None) -> C.CDLL:
                  "ds_accept_workspace_size", "ds_accept", "ds_accept_static",
                  "ds_kv_commit", "ds_compact_append", "ds_qk_norm_rope",
                  "ds_kv4_write", "ds_kv4_read",
-                 "ds_kv4_verify_attn_workspace_size", "ds_kv4_verify_attn"):
+                 "ds_kv4_verify_attn_workspace_size", "ds_kv4_verify_attn",
+                 "ds_rope_frequencies", "ds_rope_append",
+                 "ds_decode_attn_workspace_size", "ds_decode_attn",
+                 "ds_cache_evict_workspace_size", "ds_cache_evict"):
         getattr(lib, name).restype = C.c_int
     for which, cls in ((0, VerifyArgs), (1, GatherArgs), (2, AcceptArgs),
                        (3, CommitArgs), (4, AppendArgs), (5, NormRopeArgs),
-                       (6, Kv4RowsArgs), (8, Kv4AttnArgs)):
+                       (6, Kv4RowsArgs), (8, Kv4AttnArgs), (9, RopeScaling),
+                       (10, RopeArgs), (11, DecodeArgs), (12, EvictArgs)):
         got = lib.ds_struct_size(which)
         if got != C.sizeof(cls):
             raise RuntimeError(f"struct {cls.__name__}: library has {got} bytes,"
@@ -549,6 +613,210 @@ def ds_kv4_verify_attn_workspace_size(args: Kv4AttnArgs) -> int:
 
 def ds_kv4_verify_attn(args: Kv4AttnArgs, stream=None):
     _check(load().ds_kv4_verify_attn(C.byref(args), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+_SCALES = {"none": DS_ROPE_SCALE_NONE, "linear": DS_ROPE_SCALE_LINEAR,
+           "bands": DS_ROPE_SCALE_BANDS, "ramp": DS_ROPE_SCALE_RAMP}
+_ROPE_LAYOUT = {"half": DS_ROPE_HALF, "interleaved": DS_ROPE_INTERLEAVED}
+_KV_DTYPE = {torch.bfloat16: DS_KV_BF16, torch.float16: DS_KV_F16}
+
+
+def rope_frequencies(rotary_dim: int, base: float, *, scaling: str = "none",
+                     factor: float = 1.0, original_len: float = 0.0,
+                     low: float = 0.0, high: float = 0.0):
+    """(inv_freq, magnitude) for `inv_freq` and `magnitude` of
+    rope_append_args (inv_freq serves qk_norm_rope_args too): radians per
+    position of every pair, scaled as the name says (ds_rope_scaling)."""
+    s = RopeScaling()
+    lib = load()
+    lib.ds_rope_scaling_default(C.byref(s))
+    s.kind, s.rotary_dim, s.base, s.factor = _SCALES[scaling], rotary_dim, base, factor
+    s.original_len, s.low, s.high = original_len, low, high
+    inv, mag = (C.c_double * max(rotary_dim // 2, 1))(), C.c_float(0)
+    _check(lib.ds_rope_frequencies(C.byref(s), inv, C.byref(mag)))
+    return list(inv), mag.value
+
+
+def _typed_rows(t: Optional[torch.Tensor], dtype, what: str):
+    """Pointer, row stride and [rows, heads, head_dim] of 16-bit rows whose
+    heads are packed; the rows may be slices of a wider buffer."""
+    if t is None:
+        return None, 0, (0, 0, 0)
+    if t.dim() != 3 or t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype} [rows, heads, head_dim]")
+    n, h, d = t.shape
+    if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"the heads of a row of {what} must be contiguous")
+    return C.c_void_p(t.data_ptr()), max(t.stride(0), h * d) if n <= 1 else t.stride(0), (n, h, d)
+
+
+def _int32(t: Optional[torch.Tensor], n: Optional[int], what: str):
+    if t is not None and (t.dtype != torch.int32 or (n is not None and t.numel() != n)):
+        raise ValueError(f"{what} must be int32" + ("" if n is None else f" of {n} values"))
+    return _ptr(t)
+
+
+def _draft_cache(a, k_cache, v_cache, page_table, kv_layout: str, batch: int):
+    """The cache's part of an argument struct: paged with a page_table, else
+    compact ([batch, capacity, ...])."""
+    if k_cache.dtype not in _KV_DTYPE or k_cache.dtype != v_cache.dtype or \
+            k_cache.dim() != 4 or k_cache.shape[1:] != v_cache.shape[1:]:
+        raise ValueError("k_cache and v_cache must be alike, bfloat16 or float16, of 4 dims")
+    num_pages, a.page_size, a.num_kv_heads, a.head_dim = _cache_dims(k_cache, kv_layout)
+    a.num_pages = min(num_pages, v_cache.shape[0])
+    a.k_cache, a.v_cache = _ptr(k_cache), _ptr(v_cache)
+    a.batch, a.kv_layout = batch, _LAYOUT[kv_layout]
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or \
+                page_table.shape[0] != batch:
+            raise ValueError("page_table must be int32 [batch, max_pages]")
+        a.page_table, a.max_pages = _ptr(page_table), page_table.shape[1]
+
+
+def _slot_arrays(a, batch: int, **arrays):
+    """Weights (float32) and positions (int32), [batch, slot_heads, slots]."""
+    shape = None
+    for name, (t, dtype) in arrays.items():
+        if t is None:
+            continue
+        if t.dtype != dtype or t.dim() != 3 or t.shape[0] != batch or \
+                (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} must be {dtype} [batch, slot_heads, slots], "
+                             "as the other arrays of slots")
+        shape = t.shape
+        setattr(a, name, _ptr(t))
+    if shape is not None:
+        a.slot_heads, a.slot_stride = shape[1], shape[2]
+
+
+def rope_append_args(q, k, v, positions, *, q_out=None, k_out=None,
+                     layout: str = "half", rotary_dim: int = 0,
+                     rope_base: float = 0.0, inv_freq=None, magnitude: float = 1.0,
+                     inverse: bool = False, k_cache=None, v_cache=None,
+                     page_table=None, from_lens=None, row_offsets=None,
+                     slot_positions=None, slot_weights=None, new_lens=None,
+                     kv_layout: str = "NHD", workspace=None) -> RopeArgs:
+    """Arguments of ds_rope_append.  q [rows, H_q, D], k and v [rows, H_kv, D]
+    (bfloat16 or float16) may be slices of wider rows; q may be None.  Without
+    k_cache the rotation alone: q into q_out, k (or None) into k_out.  With a
+    cache (paged with page_table, else compact) the rows go to the slots from
+    from_lens on; slot_positions and slot_weights are [batch, 1 or H_kv, slots]."""
+    a = RopeArgs()
+    load().ds_rope_args_default(C.byref(a))
+    ref = q if q is not None else k
+    if ref is None or ref.dtype not in _KV_DTYPE:
+        raise ValueError("q or k must be given, bfloat16 or float16")
+    a.dtype = _KV_DTYPE[ref.dtype]
+    a.q, a.q_row_stride, qs = _typed_rows(q, ref.dtype, "q")
+    a.k, a.k_row_stride, ks = _typed_rows(k, ref.dtype, "k")
+    a.v, a.v_row_stride, vs = _typed_rows(v, ref.dtype, "v")
+    a.q_out, a.q_out_row_stride, qo = _typed_rows(q_out, ref.dtype, "q_out")
+    a.k_out, a.k_out_row_stride, ko = _typed_rows(k_out, ref.dtype, "k_out")
+    if qs != qo or (ks != ko and (k_cache is None or k_out is not None)) or \
+            (q is not None and k is not None and (qs[0], qs[2]) != (ks[0], ks[2])):
+        raise ValueError("q, k and their outputs must agree in rows, heads and head_dim")
+    a.n_rows, a.num_q_heads, a.num_kv_heads = ref.shape[0], qs[1], ks[1]
+    a.head_dim = ref.shape[2]
+    a.positions = _int32(positions, a.n_rows, "positions")
+    a.layout, a.rotary_dim = _ROPE_LAYOUT[layout], rotary_dim
+    a.rope_base, a.magnitude, a.inverse = rope_base, magnitude, 1 if inverse else 0
+    if inv_freq is not None:
+        if len(inv_freq) != (rotary_dim or a.head_dim) // 2:
+            raise ValueError("inv_freq must hold rotary_dim / 2 values")
+        a._keep = (C.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
+        a.inv_freq = C.cast(a._keep, C.POINTER(C.c_double))
+    if k_cache is not None:
+        if ks != vs or k_cache.dtype != ref.dtype:
+            raise ValueError("k and v must agree in shape, and with the cache in type")
+        batch = row_offsets.shape[0] - 1
+        _draft_cache(a, k_cache, v_cache, page_table, kv_layout, batch)
+        if (a.num_kv_heads, a.head_dim) != ks[1:]:
+            raise ValueError("rows and cache must agree in heads and head_dim")
+        a.from_lens = _int32(from_lens, batch, "from_lens")
+        a.row_offsets = _int32(row_offsets, None, "row_offsets")
+        a.new_lens = _int32(new_lens, batch, "new_lens")
+        _slot_arrays(a, batch, slot_positions=(slot_positions, torch.int32),
+                     slot_weights=(slot_weights, torch.float32))
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_rope_append(args: RopeArgs, stream=None):
+    _check(load().ds_rope_append(C.byref(args), _stream(stream)))
+
+
+def decode_attn_args(q, k_cache, v_cache, page_table, lens, *, out, lse=None,
+                     weights_in=None, weights_out=None, decay: float = 1.0,
+                     window: int = 0, sinks: int = 0, scale: float = 0.0,
+                     kv_layout: str = "NHD", num_sms: int = 0,
+                     workspace=None) -> DecodeArgs:
+    """Arguments of ds_decode_attn: q [batch, H_q, D] (rows may be slices of
+    wider ones), a paged cache (page_table) or a compact one (None), out
+    [batch, H_q, D] of q's type or float32, lse [batch, H_q], weights [batch, 1
+    or H_kv, slots]."""
+    a = DecodeArgs()
+    load().ds_decode_args_default(C.byref(a))
+    if q.dtype not in _KV_DTYPE or q.dtype != k_cache.dtype:
+        raise ValueError("q and the cache must be of one type, bfloat16 or float16")
+    a.q, a.q_row_stride, (batch, a.num_q_heads, d) = _typed_rows(q, q.dtype, "q")
+    a.dtype = _KV_DTYPE[q.dtype]
+    _draft_cache(a, k_cache, v_cache, page_table, kv_layout, batch)
+    if a.head_dim != d or out.shape != q.shape or out.dtype not in (q.dtype, torch.float32):
+        raise ValueError("q, out and the cache must agree in heads and head_dim, out in q's "
+                         "type or float32")
+    a.lens, a.out, a.out_f32 = _int32(lens, batch, "lens"), _ptr(out), \
+        1 if out.dtype == torch.float32 else 0
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2]):
+        raise ValueError("lse must be float32 [batch, H_q]")
+    a.lse = _ptr(lse)
+    _slot_arrays(a, batch, weights_in=(weights_in, torch.float32),
+                 weights_out=(weights_out, torch.float32))
+    a.decay, a.window, a.sinks, a.scale, a.num_sms = decay, window, sinks, scale, num_sms
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_decode_attn_workspace_size(args: DecodeArgs) -> int:
+    n = C.c_size_t(0)
+    _check(load().ds_decode_attn_workspace_size(C.byref(args), C.byref(n)))
+    return n.value
+
+
+def ds_decode_attn(args: DecodeArgs, stream=None):
+    _check(load().ds_decode_attn(C.byref(args), _stream(stream)))
+
+
+def evict_args(k_cache, v_cache, page_table, lens, *, weights, positions,
+               next_positions, new_lens, budget: int, trigger: int = 0,
+               recent: int = 0, sinks: int = 0, weights_out=None,
+               positions_out=None, kv_layout: str = "NHD",
+               workspace=None) -> EvictArgs:
+    """Arguments of ds_cache_evict; weights and positions (and their outputs,
+    None: in place) are [batch, 1 or H_kv, slots]."""
+    a = EvictArgs()
+    load().ds_evict_args_default(C.byref(a))
+    batch = lens.shape[0]
+    _draft_cache(a, k_cache, v_cache, page_table, kv_layout, batch)
+    a.lens = _int32(lens, batch, "lens")
+    _slot_arrays(a, batch, weights=(weights, torch.float32), positions=(positions, torch.int32),
+                 weights_out=(weights_out, torch.float32),
+                 positions_out=(positions_out, torch.int32))
+    a.next_positions = _int32(next_positions, batch, "next_positions")
+    a.new_lens = _int32(new_lens, batch, "new_lens")
+    a.budget, a.trigger, a.recent, a.sinks = budget, trigger, recent, sinks
+    _set_workspace(a, workspace)
+    return a
+
+
+def ds_cache_evict_workspace_size(args: EvictArgs) -> int:
+    n = C.c_size_t(0)
+    _check(load().ds_cache_evict_workspace_size(C.byref(args), C.byref(n)))
+    return n.value
+
+
+def ds_cache_evict(args: EvictArgs, stream=None):
+    _check(load().ds_cache_evict(C.byref(args), _stream(stream)))
 
 
 def ds_workspace_init(workspace: torch.Tensor, stream=None):

@@ -21,7 +21,7 @@ LIB_NAME = "libds_verify.so"
 SOURCES = ["abi.cpp", "verify_attn.cu", "verify_tc.cu", "topk_gather.cu",
            "accept.cu", "accept_static.cu", "kv_commit.cu",
            "norm_rope.cu", "kv4_rows.cu", "kv4_attn.cu", "kv4_tc.cu",
-           "kv4_few.cu"]
+           "kv4_few.cu", "rope_append.cu", "decode_attn.cu", "cache_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "-I" + INCLUDE, "-I" + CSRC]

@@ -136,6 +136,44 @@ AcceptLayout accept_layout(const ds_accept_args& a) {
   return L;
 }
 
+DecodeLayout decode_layout(const ds_decode_args& a, int num_sms) {
+  DecodeLayout L;
+  L.ctas = num_sms;
+  L.slots = a.page_table ? (int64_t)a.max_pages * a.page_size : a.page_size;
+  const size_t group = (size_t)(a.num_q_heads / a.num_kv_heads);
+  const size_t segs = (size_t)a.batch * a.num_kv_heads;
+  size_t off = kStatusBytes;
+  L.desc = off;
+  off = align_up(off + segs * sizeof(int32_t) * 2);
+  L.part_ml = off;
+  off = align_up(off + (segs + L.ctas) * group * sizeof(float) * 2);
+  L.part_o = off;
+  off = align_up(off + (segs + L.ctas) * group * a.head_dim * sizeof(float));
+  L.logits = off;
+  if (a.weights_out)
+    off = align_up(off + segs * (size_t)L.slots * group * sizeof(float));
+  L.total = off;
+  return L;
+}
+
+EvictLayout evict_layout(const ds_evict_args& a) {
+  EvictLayout L;
+  const size_t segs = (size_t)a.batch * a.slot_heads;
+  const int64_t slots = a.page_table ? (int64_t)a.max_pages * a.page_size : a.page_size;
+  // as many moves as there are slots below the budget, or behind it
+  const int64_t behind = slots - a.budget;
+  L.moves = behind <= 0 ? 0 : (behind < a.budget ? behind : a.budget);
+  size_t off = kStatusBytes;
+  L.count = off;
+  off = align_up(off + segs * sizeof(int32_t));
+  L.src = off;
+  off = align_up(off + segs * (size_t)L.moves * sizeof(int32_t));
+  L.dst = off;
+  off = align_up(off + segs * (size_t)L.moves * sizeof(int32_t));
+  L.total = off;
+  return L;
+}
+
 ds_verify_args kv4_as_verify(const ds_kv4_attn_args& a) {
   ds_verify_args v;
   ds_verify_args_default(&v);
@@ -187,6 +225,10 @@ int64_t ds_struct_size(int32_t which) {
     case 5: return (int64_t)sizeof(ds_norm_rope_args);
     case 6: return (int64_t)sizeof(ds_kv4_rows_args);
     case 8: return (int64_t)sizeof(ds_kv4_attn_args);
+    case 9: return (int64_t)sizeof(ds_rope_scaling);
+    case 10: return (int64_t)sizeof(ds_rope_args);
+    case 11: return (int64_t)sizeof(ds_decode_args);
+    case 12: return (int64_t)sizeof(ds_evict_args);
     default: return -1;
   }
 }
@@ -645,6 +687,329 @@ ds_status ds_kv4_verify_attn(const ds_kv4_attn_args* a, void* stream) {
   if (a->n_nodes == 0) return ok();
   cudaError_t e = ds::launch_kv4_attn(*a, L, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "ds_kv4_verify_attn launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_rope_scaling_default(ds_rope_scaling* s) {
+  if (!s) return;
+  std::memset(s, 0, sizeof(*s));
+  s->factor = 1.0;
+}
+
+ds_status ds_rope_frequencies(const ds_rope_scaling* s, double* inv_freq, float* magnitude) {
+  REQUIRE(s, DS_ERR_INVALID_ARG, "scaling is NULL");
+  REQUIRE(inv_freq && magnitude, DS_ERR_INVALID_ARG, "inv_freq or magnitude is NULL");
+  REQUIRE(s->kind >= DS_ROPE_SCALE_NONE && s->kind <= DS_ROPE_SCALE_RAMP, DS_ERR_INVALID_ARG,
+          "kind %d is not a ds_rope_scale", s->kind);
+  REQUIRE(s->rotary_dim >= 2 && s->rotary_dim <= 128 && s->rotary_dim % 2 == 0,
+          DS_ERR_UNSUPPORTED, "rotary_dim %d: even, 2 to 128", s->rotary_dim);
+  REQUIRE(std::isfinite(s->base) && s->base > 1.0, DS_ERR_INVALID_ARG,
+          "base must be finite and above 1");
+  REQUIRE(s->kind == DS_ROPE_SCALE_NONE || (std::isfinite(s->factor) && s->factor >= 1.0),
+          DS_ERR_INVALID_ARG, "factor must be finite and at least 1");
+  if (s->kind >= DS_ROPE_SCALE_BANDS) {
+    REQUIRE(std::isfinite(s->original_len) && s->original_len > 0.0, DS_ERR_INVALID_ARG,
+            "original_len must be finite and above 0");
+    REQUIRE(std::isfinite(s->high) && s->low > 0.0 && s->low < s->high, DS_ERR_INVALID_ARG,
+            "low (%g) and high (%g): 0 < low < high", s->low, s->high);
+  }
+  const double kTau = 6.283185307179586476925;
+  const int r = s->rotary_dim;
+  double lo = 0.0, hi = 0.0;
+  if (s->kind == DS_ROPE_SCALE_RAMP) {
+    auto at = [&](double n) {
+      return r * std::log(s->original_len / (kTau * n)) / (2.0 * std::log(s->base));
+    };
+    lo = std::fmax(0.0, std::floor(at(s->high)));
+    hi = std::fmin(r - 1.0, std::ceil(at(s->low)));
+  }
+  for (int j = 0; j < r / 2; ++j) {
+    const double th = std::pow(s->base, -2.0 * j / r);
+    double keep = 1.0;                            // share of th as it is
+    if (s->kind == DS_ROPE_SCALE_LINEAR) keep = 0.0;
+    if (s->kind == DS_ROPE_SCALE_BANDS)
+      keep = (s->original_len * th / kTau - s->low) / (s->high - s->low);
+    if (s->kind == DS_ROPE_SCALE_RAMP) keep = 1.0 - (j - lo) / std::fmax(hi - lo, 1e-3);
+    keep = std::fmin(1.0, std::fmax(0.0, keep));
+    inv_freq[j] = keep == 1.0 ? th : th * (keep + (1.0 - keep) / s->factor);
+  }
+  *magnitude = s->kind == DS_ROPE_SCALE_RAMP ? (float)(0.1 * std::log(s->factor) + 1.0) : 1.f;
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// The sizes of a draft's cache (rope, decode and evict arguments alike).
+static ds_status check_draft_cache(const int32_t* page_table, int batch, int hkv, int d,
+                                   int page_size, int num_pages, int max_pages, int kv_layout) {
+  REQUIRE(batch >= 1 && batch <= 65536, DS_ERR_INVALID_ARG,
+          "batch must lie in 1 .. 65536 (got %d)", batch);
+  REQUIRE(hkv >= 1 && hkv <= 1024, DS_ERR_INVALID_ARG, "num_kv_heads %d (1 to 1024)", hkv);
+  REQUIRE(d == 64 || d == 128, DS_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", d);
+  REQUIRE(kv_layout == DS_KV_NHD || kv_layout == DS_KV_HND, DS_ERR_INVALID_ARG,
+          "kv_layout %d is not a ds_kv_layout", kv_layout);
+  REQUIRE(num_pages >= 1, DS_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if (page_table) {
+    REQUIRE(page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128,
+            DS_ERR_UNSUPPORTED, "page_size %d (16, 32, 64 or 128 with a page_table)", page_size);
+    REQUIRE(max_pages >= 1, DS_ERR_INVALID_ARG, "max_pages must be >= 1");
+    REQUIRE((int64_t)max_pages * page_size <= ds::kDraftMaxSlots, DS_ERR_UNSUPPORTED,
+            "max_pages * page_size must not exceed 2^30");
+  } else {
+    REQUIRE(page_size >= 1 && page_size <= ds::kDraftMaxSlots, DS_ERR_INVALID_ARG,
+            "page_size (the capacity of a compact cache) %d must lie in 1 .. 2^30", page_size);
+    REQUIRE(num_pages >= batch, DS_ERR_INVALID_ARG,
+            "num_pages %d < batch %d of a compact cache", num_pages, batch);
+  }
+  REQUIRE((int64_t)(num_pages + (int64_t)1) * hkv < (int64_t)1 << 31, DS_ERR_UNSUPPORTED,
+          "num_pages * num_kv_heads must stay below 2^31");
+  // (factor by factor: the product of all four can leave 64 bits)
+  REQUIRE((int64_t)num_pages * hkv * d <= ((int64_t)1 << 40) / page_size, DS_ERR_UNSUPPORTED,
+          "cache too large");
+  return DS_OK;
+}
+
+static ds_status check_pools(const void* k_cache, const void* v_cache) {
+  REQUIRE(k_cache && v_cache, DS_ERR_INVALID_ARG, "k_cache/v_cache is NULL");
+  REQUIRE(aligned16(k_cache) && aligned16(v_cache), DS_ERR_INVALID_ARG,
+          "k_cache and v_cache must be 16-byte aligned");
+  return DS_OK;
+}
+
+static ds_status check_slots(int slot_heads, int64_t slot_stride, int hkv,
+                             const int32_t* page_table, int page_size, int max_pages) {
+  REQUIRE(slot_heads == 1 || slot_heads == hkv, DS_ERR_INVALID_ARG,
+          "slot_heads %d: 1 or num_kv_heads (%d)", slot_heads, hkv);
+  const int64_t slots = page_table ? (int64_t)max_pages * page_size : page_size;
+  REQUIRE(slot_stride >= slots && slot_stride <= (int64_t)1 << 31, DS_ERR_INVALID_ARG,
+          "slot_stride %lld < slots of a sequence %lld (or above 2^31)", (long long)slot_stride,
+          (long long)slots);
+  return DS_OK;
+}
+
+static ds_status check_status(const void* workspace, size_t bytes) {
+  REQUIRE(workspace, DS_ERR_WORKSPACE, "workspace is NULL");
+  REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 3) == 0, DS_ERR_WORKSPACE,
+          "workspace must be 4-byte aligned");
+  REQUIRE(bytes >= ds::kStatusBytes, DS_ERR_WORKSPACE, "workspace_bytes %zu < %zu", bytes,
+          ds::kStatusBytes);
+  return DS_OK;
+}
+
+void ds_rope_args_default(ds_rope_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+  a->kv_layout = DS_KV_NHD;
+  a->slot_heads = 1;
+  a->magnitude = 1.f;
+}
+
+static ds_status check_rows(const char* name, const void* p, int64_t stride, int heads, int d) {
+  REQUIRE(p, DS_ERR_INVALID_ARG, "%s is NULL", name);
+  REQUIRE(aligned16(p), DS_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  REQUIRE(stride % 8 == 0 && stride >= (int64_t)heads * d, DS_ERR_INVALID_ARG,
+          "%s_row_stride %lld must be a multiple of 8 of at least heads * head_dim", name,
+          (long long)stride);
+  return DS_OK;
+}
+
+ds_status ds_rope_append(const ds_rope_args* a, void* stream) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  const bool cache = a->k_cache != nullptr;
+  REQUIRE(a->n_rows >= 0, DS_ERR_INVALID_ARG, "n_rows must be >= 0 (got %d)", a->n_rows);
+  REQUIRE(a->num_q_heads >= 0 && a->num_kv_heads >= 0 && a->num_q_heads <= 65536 &&
+              a->num_kv_heads <= 1024 && a->num_q_heads + a->num_kv_heads >= 1,
+          DS_ERR_INVALID_ARG, "num_q_heads (%d, at most 65536) and num_kv_heads (%d, at most "
+          "1024): at least one head", a->num_q_heads, a->num_kv_heads);
+  REQUIRE(a->head_dim == 64 || a->head_dim == 128, DS_ERR_UNSUPPORTED,
+          "head_dim %d: only 64 and 128 are supported", a->head_dim);
+  REQUIRE(a->dtype == DS_KV_BF16 || a->dtype == DS_KV_F16, DS_ERR_INVALID_ARG,
+          "dtype %d is not a ds_kv_dtype", a->dtype);
+  REQUIRE(a->layout == DS_ROPE_HALF || a->layout == DS_ROPE_INTERLEAVED, DS_ERR_INVALID_ARG,
+          "layout %d is not a ds_rope_layout", a->layout);
+  REQUIRE(a->rotary_dim >= 0 && a->rotary_dim <= a->head_dim && a->rotary_dim % 16 == 0,
+          DS_ERR_UNSUPPORTED, "rotary_dim %d: a multiple of 16 up to head_dim", a->rotary_dim);
+  REQUIRE(a->inverse == 0 || a->inverse == 1, DS_ERR_INVALID_ARG, "inverse must be 0 or 1");
+  REQUIRE(a->rope_base >= 0.f && a->rope_base < 3.0e38f, DS_ERR_INVALID_ARG,
+          "rope_base must be 0 (with inv_freq) or a finite positive base");
+  REQUIRE((a->rope_base > 0.f) != (a->inv_freq != nullptr), DS_ERR_INVALID_ARG,
+          "either rope_base or inv_freq must be given");
+  REQUIRE(std::isfinite(a->magnitude), DS_ERR_INVALID_ARG, "magnitude is not finite");
+  const int r = a->rotary_dim ? a->rotary_dim : a->head_dim;
+  if (a->inv_freq)
+    for (int j = 0; j < r / 2; ++j)
+      REQUIRE(std::isfinite(a->inv_freq[j]), DS_ERR_INVALID_ARG, "inv_freq[%d] is not finite", j);
+  ds_status st = check_status(a->workspace, a->workspace_bytes);
+  if (st != DS_OK) return st;
+  if (cache) {
+    st = check_draft_cache(a->page_table, a->batch, a->num_kv_heads, a->head_dim, a->page_size,
+                           a->num_pages, a->max_pages, a->kv_layout);
+    if (st == DS_OK) st = check_pools(a->k_cache, a->v_cache);
+    if (st != DS_OK) return st;
+    REQUIRE(a->from_lens && a->row_offsets, DS_ERR_INVALID_ARG, "from_lens/row_offsets is NULL");
+    REQUIRE(!a->new_lens || (const void*)a->new_lens != (const void*)a->from_lens,
+            DS_ERR_INVALID_ARG, "new_lens must not alias from_lens");
+    if (a->slot_positions || a->slot_weights) {
+      st = check_slots(a->slot_heads, a->slot_stride, a->num_kv_heads, a->page_table,
+                       a->page_size, a->max_pages);
+      if (st != DS_OK) return st;
+    }
+  }
+  if (a->n_rows == 0 && !(cache && a->new_lens)) return ok();
+  if (a->n_rows > 0) {
+    REQUIRE(a->positions, DS_ERR_INVALID_ARG, "positions is NULL");
+    if (a->num_q_heads > 0) {
+      st = check_rows("q", a->q, a->q_row_stride, a->num_q_heads, a->head_dim);
+      if (st == DS_OK)
+        st = check_rows("q_out", a->q_out, a->q_out_row_stride, a->num_q_heads, a->head_dim);
+      if (st != DS_OK) return st;
+      REQUIRE(a->q != a->q_out || a->q_row_stride == a->q_out_row_stride || a->n_rows == 1,
+              DS_ERR_INVALID_ARG, "q_out is q: their row strides must agree");
+    }
+    if (a->num_kv_heads > 0) {
+      st = check_rows("k", a->k, a->k_row_stride, a->num_kv_heads, a->head_dim);
+      if (st == DS_OK && (a->k_out || !cache))
+        st = check_rows("k_out", a->k_out, a->k_out_row_stride, a->num_kv_heads, a->head_dim);
+      if (st == DS_OK && cache)
+        st = check_rows("v", a->v, a->v_row_stride, a->num_kv_heads, a->head_dim);
+      if (st != DS_OK) return st;
+      REQUIRE(a->k != a->k_out || a->k_row_stride == a->k_out_row_stride || a->n_rows == 1,
+              DS_ERR_INVALID_ARG, "k_out is k: their row strides must agree");
+    }
+  }
+  cudaError_t e = ds::launch_rope_append(*a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_rope_append launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_decode_args_default(ds_decode_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+  a->kv_layout = DS_KV_NHD;
+  a->slot_heads = 1;
+  a->decay = 1.f;
+}
+
+static ds_status check_decode(const ds_decode_args* a, int* sms) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  ds_status st = check_draft_cache(a->page_table, a->batch, a->num_kv_heads, a->head_dim,
+                                   a->page_size, a->num_pages, a->max_pages, a->kv_layout);
+  if (st != DS_OK) return st;
+  REQUIRE(a->num_q_heads >= a->num_kv_heads && a->num_q_heads % a->num_kv_heads == 0,
+          DS_ERR_UNSUPPORTED, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
+          a->num_q_heads, a->num_kv_heads);
+  REQUIRE(a->num_q_heads / a->num_kv_heads <= 16, DS_ERR_UNSUPPORTED,
+          "num_q_heads / num_kv_heads = %d: at most 16", a->num_q_heads / a->num_kv_heads);
+  REQUIRE(a->dtype == DS_KV_BF16 || a->dtype == DS_KV_F16, DS_ERR_INVALID_ARG,
+          "dtype %d is not a ds_kv_dtype", a->dtype);
+  REQUIRE(a->out_f32 == 0 || a->out_f32 == 1, DS_ERR_INVALID_ARG, "out_f32 must be 0 or 1");
+  REQUIRE(std::isfinite(a->scale) && a->scale >= 0.f && a->scale < 1e38f, DS_ERR_INVALID_ARG,
+          "scale must be finite, >= 0 and below 1e38 (0 selects 1/sqrt(head_dim))");
+  REQUIRE(a->window >= 0 && a->sinks >= 0, DS_ERR_INVALID_ARG,
+          "window (%d) and sinks (%d) must be >= 0", a->window, a->sinks);
+  REQUIRE(std::isfinite(a->decay) && a->decay >= 0.f, DS_ERR_INVALID_ARG,
+          "decay must be finite and >= 0");
+  REQUIRE(a->weights_out || !a->weights_in, DS_ERR_INVALID_ARG,
+          "weights_in is given, weights_out is NULL");
+  if (a->weights_out) {
+    st = check_slots(a->slot_heads, a->slot_stride, a->num_kv_heads, a->page_table, a->page_size,
+                     a->max_pages);
+    if (st != DS_OK) return st;
+  }
+  REQUIRE(a->num_sms >= 0 && a->num_sms <= 4096, DS_ERR_INVALID_ARG,
+          "num_sms must lie in 0 .. 4096");
+  *sms = a->num_sms;
+  if (*sms == 0 && device_sms(sms) != 0)
+    return fail(DS_ERR_CUDA, "num_sms is 0 and the device SM count is unavailable");
+  return DS_OK;
+}
+
+ds_status ds_decode_attn_workspace_size(const ds_decode_args* a, size_t* bytes) {
+  int sms = 0;
+  ds_status st = check_decode(a, &sms);
+  if (st != DS_OK) return st;
+  REQUIRE(bytes, DS_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ds::decode_layout(*a, sms).total;
+  return ok();
+}
+
+ds_status ds_decode_attn(const ds_decode_args* a, void* stream) {
+  int sms = 0;
+  ds_status st = check_decode(a, &sms);
+  if (st != DS_OK) return st;
+  st = check_pools(a->k_cache, a->v_cache);
+  if (st != DS_OK) return st;
+  REQUIRE(a->q && a->lens && a->out, DS_ERR_INVALID_ARG, "q/lens/out is NULL");
+  REQUIRE(aligned16(a->q) && aligned16(a->out), DS_ERR_INVALID_ARG,
+          "q and out must be 16-byte aligned");
+  REQUIRE(a->q_row_stride % 8 == 0 &&
+              a->q_row_stride >= (int64_t)a->num_q_heads * a->head_dim,
+          DS_ERR_INVALID_ARG, "q_row_stride %lld must be a multiple of 8 of at least "
+          "num_q_heads * head_dim", (long long)a->q_row_stride);
+  REQUIRE(a->workspace, DS_ERR_WORKSPACE, "workspace is NULL");
+  REQUIRE((reinterpret_cast<uintptr_t>(a->workspace) & (ds::kAlign - 1)) == 0,
+          DS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const ds::DecodeLayout L = ds::decode_layout(*a, sms);
+  REQUIRE(a->workspace_bytes >= L.total, DS_ERR_WORKSPACE,
+          "workspace_bytes %zu < required %zu", a->workspace_bytes, L.total);
+  cudaError_t e = ds::launch_decode_attn(*a, L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_decode_attn launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+void ds_evict_args_default(ds_evict_args* a) {
+  if (!a) return;
+  std::memset(a, 0, sizeof(*a));
+  a->kv_layout = DS_KV_NHD;
+  a->slot_heads = 1;
+}
+
+static ds_status check_evict(const ds_evict_args* a) {
+  REQUIRE(a, DS_ERR_INVALID_ARG, "args is NULL");
+  ds_status st = check_draft_cache(a->page_table, a->batch, a->num_kv_heads, a->head_dim,
+                                   a->page_size, a->num_pages, a->max_pages, a->kv_layout);
+  if (st != DS_OK) return st;
+  st = check_slots(a->slot_heads, a->slot_stride, a->num_kv_heads, a->page_table, a->page_size,
+                   a->max_pages);
+  if (st != DS_OK) return st;
+  REQUIRE((int64_t)a->batch * a->slot_heads <= 65536, DS_ERR_UNSUPPORTED,
+          "batch * slot_heads must not exceed 65536");
+  REQUIRE(a->budget >= 1, DS_ERR_INVALID_ARG, "budget must be >= 1 (got %d)", a->budget);
+  REQUIRE(a->trigger >= 0, DS_ERR_INVALID_ARG, "trigger must be >= 0");
+  REQUIRE(a->recent >= 0 && a->sinks >= 0, DS_ERR_INVALID_ARG,
+          "recent (%d) and sinks (%d) must be >= 0", a->recent, a->sinks);
+  REQUIRE((int64_t)a->recent + a->sinks <= a->budget, DS_ERR_INVALID_ARG,
+          "recent (%d) + sinks (%d) above budget (%d)", a->recent, a->sinks, a->budget);
+  return DS_OK;
+}
+
+ds_status ds_cache_evict_workspace_size(const ds_evict_args* a, size_t* bytes) {
+  ds_status st = check_evict(a);
+  if (st != DS_OK) return st;
+  REQUIRE(bytes, DS_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = ds::evict_layout(*a).total;
+  return ok();
+}
+
+ds_status ds_cache_evict(const ds_evict_args* a, void* stream) {
+  ds_status st = check_evict(a);
+  if (st != DS_OK) return st;
+  st = check_pools(a->k_cache, a->v_cache);
+  if (st != DS_OK) return st;
+  REQUIRE(a->lens && a->weights && a->positions && a->next_positions && a->new_lens,
+          DS_ERR_INVALID_ARG, "lens/weights/positions/next_positions/new_lens is NULL");
+  REQUIRE((const void*)a->new_lens != (const void*)a->lens, DS_ERR_INVALID_ARG,
+          "new_lens must not alias lens");
+  REQUIRE(a->workspace, DS_ERR_WORKSPACE, "workspace is NULL");
+  REQUIRE((reinterpret_cast<uintptr_t>(a->workspace) & (ds::kAlign - 1)) == 0,
+          DS_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const ds::EvictLayout L = ds::evict_layout(*a);
+  REQUIRE(a->workspace_bytes >= L.total, DS_ERR_WORKSPACE,
+          "workspace_bytes %zu < required %zu", a->workspace_bytes, L.total);
+  cudaError_t e = ds::launch_cache_evict(*a, L, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "ds_cache_evict launch");
   return ok();
 }
 

@@ -107,6 +107,37 @@ constexpr int kKv4MaxSlots = 1 << 30;
 int kv4_few_rows(const ds_kv4_attn_args& a);
 size_t kv4_counters(const ds_kv4_attn_args& a);
 
+// The draft's cache.
+constexpr int kDraftMaxSlots = 1 << 30;
+
+// Workspace of ds_decode_attn.  A segment is a sequence's kv head, number
+// b * num_kv_heads + head; a piece is what one block has of it.
+struct DecodeLayout {
+  int32_t ctas;         // blocks of the split pass, at most
+  int64_t slots;        // of a sequence
+  size_t desc;          // [segments] int2: first piece's place, pieces
+  size_t part_ml;       // [segments + ctas][group] float2: maximum (log2), sum
+  size_t part_o;        // [segments + ctas][group][head_dim] f32, not normalised
+  size_t logits;        // [segments][slots][group] f32 (log2), with weights only
+  size_t total;
+};
+
+// Workspace of ds_cache_evict; a segment is a sequence's slot head.
+struct EvictLayout {
+  int64_t moves;        // room for moves of a segment
+  size_t count;         // [segments] i32
+  size_t src, dst;      // [segments][moves] i32 slots
+  size_t total;
+};
+
+DecodeLayout decode_layout(const ds_decode_args& a, int num_sms);
+EvictLayout evict_layout(const ds_evict_args& a);
+cudaError_t launch_rope_append(const ds_rope_args& a, cudaStream_t stream);
+cudaError_t launch_decode_attn(const ds_decode_args& a, const DecodeLayout& L,
+                               cudaStream_t stream);
+cudaError_t launch_cache_evict(const ds_evict_args& a, const EvictLayout& L,
+                               cudaStream_t stream);
+
 // Sets the message ds_last_error returns on this thread; returns st.
 ds_status set_last_error(ds_status st, const char* msg);
 

@@ -1,0 +1,251 @@
+// Rotation by position of queries and keys, and the new tokens' keys and
+// values into the draft's cache (include/ds.h, ds_rope_append).
+//
+// (x, y) -> m (x cos a - y sin a, x sin a + y cos a) for every pair, a =
+// position * frequency; float32 with one rounding.
+//
+// Bound by memory when there are many rows, by latency when there are few.
+// D / 16 lanes hold one head, each two vectors of eight values that make up
+// whole pairs: the eight from 8l and their partners r/2 on (half), or the
+// sixteen from 16l (interleaved); heads' values past r the same way, unturned.
+// A warp takes a row and works on several heads at a time.
+#include <cuda_runtime.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "dev_common.cuh"
+#include "draft_cache.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+
+namespace ds {
+
+struct RopeKArgs {
+  const uint16_t* x[3];           // q, k, v
+  int64_t stride[3];
+  uint16_t* out[2];               // q, k (NULL: none)
+  int64_t out_stride[2];
+  const int32_t* positions;
+  const int32_t* from_lens;
+  const int32_t* row_offsets;
+  int32_t* slot_positions;
+  float* slot_weights;
+  int32_t* new_lens;
+  uint32_t* status;
+  DraftCache cache;
+  int64_t slot_stride;
+  int32_t n_rows, batch, hq, hkv, heads;   // heads = query + key (+ value) heads
+  int32_t slot_heads, rotary, write;       // write: there is a cache
+  int32_t per;                    // head groups of a warp
+  int32_t row_blocks;             // the blocks behind these look at the sequences
+  float magnitude, sin_sign;
+  unsigned long long turn[64];    // frequency j as a 64-bit fraction of a turn
+};
+
+constexpr int kRopeWarps = 8;             // warps of a block
+
+// The last sequence b with row_offsets[b] <= row (offsets that are not
+// monotone give some sequence; its own offsets are checked after).
+DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(offs + mid) <= row) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Rows [n0, n0 + n) and first slot of sequence b; false when they cannot be used.
+DS_DEV bool rope_rows_of(const RopeKArgs& a, int b, int& n0, int& n, int& from) {
+  n0 = __ldg(a.row_offsets + b);
+  const int n1 = __ldg(a.row_offsets + b + 1);
+  from = __ldg(a.from_lens + b);
+  n = n1 - n0;
+  return n0 >= 0 && n1 >= n0 && n1 <= a.n_rows && from >= 0 && (int64_t)from + n <= a.cache.slots;
+}
+
+template <bool BF>
+DS_DEV float2 unpack2(uint32_t w) {
+  if constexpr (BF)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF>
+DS_DEV uint32_t pack2(float lo, float hi) {
+  return BF ? ptx::pack_bf16x2(lo, hi) : ptx::pack_f16x2(lo, hi);
+}
+
+template <int D, bool BF, bool HALVES>
+__global__ void __launch_bounds__(32 * kRopeWarps) rope_append(const RopeKArgs a) {
+  constexpr int LPH = D / 16;             // lanes of a head
+  constexpr int HPW = 32 / LPH;           // heads of a warp at a time
+  __shared__ __align__(16) float2 s_cs[kRopeWarps][D / 2];
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The last blocks have a thread per sequence, which checks its offsets and
+  // length even when no row is mapped to it, and writes the new length.
+  if ((int)blockIdx.x >= a.row_blocks) {
+    const int b = (blockIdx.x - a.row_blocks) * 32 * kRopeWarps + threadIdx.x;
+    if (b >= a.batch || blockIdx.y > 0) return;
+    int n0, n, from;
+    const bool usable = rope_rows_of(a, b, n0, n, from);
+    if (!usable) flag(a.status, DS_DEV_BAD_LENGTH);
+    if (a.new_lens) a.new_lens[b] = usable ? from + n : from;
+    return;
+  }
+  const int64_t row64 = (int64_t)blockIdx.x * kRopeWarps + warp;
+  if (row64 >= a.n_rows) return;
+  const int row = (int)row64;
+  const int groups = (a.heads + HPW - 1) / HPW;
+  const int g0 = blockIdx.y * a.per, g1 = min(groups, g0 + a.per);
+  if (g0 >= g1) return;
+  const int pos = __ldg(a.positions + row);
+  if (pos < 0) {
+    if (lane == 0) flag(a.status, DS_DEV_BAD_LENGTH);
+    return;
+  }
+  int64_t at = -1;                        // the slot's place in the pools
+  if (a.write) {
+    const int b = row_owner(a.row_offsets, a.batch, row);
+    int n0, n, from;
+    if (!rope_rows_of(a, b, n0, n, from) || row < n0 || row >= n0 + n) return;
+    const int slot = from + (row - n0);
+    const int pg = slot_page(a.cache, b, slot);
+    if (pg >= 0) at = slot_at(a.cache, pg, slot);
+    else if (lane == 0) flag(a.status, DS_DEV_BAD_PAGE);
+    if (blockIdx.y == 0)
+      for (int h = lane; h < a.slot_heads; h += 32) {
+        const int64_t i = ((int64_t)b * a.slot_heads + h) * a.slot_stride + slot;
+        if (a.slot_positions) a.slot_positions[i] = pos;
+        if (a.slot_weights) a.slot_weights[i] = 0.f;
+      }
+  }
+  // position * frequency wraps modulo one turn in 64 bits; its upper half,
+  // read as a signed number, is the angle in units of pi / 2^31
+  float2* const cs = s_cs[warp];
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {
+    const int j = lane + 32 * k;
+    const unsigned long long t = (unsigned long long)pos * a.turn[j];
+    float sn, c;
+    sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &sn, &c);
+    cs[j] = make_float2(c * a.magnitude, sn * a.magnitude * a.sin_sign);
+  }
+  __syncwarp();
+  const int l = lane % LPH, sub = lane / LPH;
+  const bool turned = 16 * l < a.rotary;
+  // the lane's two vectors of a head
+  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
+  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
+  for (int gi = g0; gi < g1; ++gi) {
+    const int hh = gi * HPW + sub;
+    if (hh >= a.heads) continue;
+    const int ty = hh < a.hq ? 0 : hh < a.hq + a.hkv ? 1 : 2;
+    const int h = hh - (ty > 0 ? a.hq : 0) - (ty > 1 ? a.hkv : 0);
+    // plain loads: with q_out = q the same bytes are written below
+    const uint16_t* p = a.x[ty] + (int64_t)row * a.stride[ty] + (int64_t)h * D;
+    uint4 u = *reinterpret_cast<const uint4*>(p + e0);
+    uint4 v = *reinterpret_cast<const uint4*>(p + e1);
+    if (turned && ty < 2) {
+      uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (HALVES) {
+          const float2 x = unpack2<BF>(uw[i]), y = unpack2<BF>(vw[i]);
+          const float4 c = *reinterpret_cast<const float4*>(&cs[8 * l + 2 * i]);
+          uw[i] = pack2<BF>(x.x * c.x - y.x * c.y, x.y * c.z - y.y * c.w);
+          vw[i] = pack2<BF>(x.x * c.y + y.x * c.x, x.y * c.w + y.y * c.z);
+        } else {
+          const float2 x = unpack2<BF>(uw[i]), y = unpack2<BF>(vw[i]);
+          const float2 c = cs[8 * l + i], d = cs[8 * l + 4 + i];
+          uw[i] = pack2<BF>(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+          vw[i] = pack2<BF>(y.x * d.x - y.y * d.y, y.x * d.y + y.y * d.x);
+        }
+      }
+      u = make_uint4(uw[0], uw[1], uw[2], uw[3]);
+      v = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+    }
+    if (ty < 2 && a.out[ty]) {
+      uint16_t* o = a.out[ty] + (int64_t)row * a.out_stride[ty] + (int64_t)h * D;
+      *reinterpret_cast<uint4*>(o + e0) = u;
+      *reinterpret_cast<uint4*>(o + e1) = v;
+    }
+    if (ty > 0 && at >= 0) {
+      uint16_t* o = a.cache.pool[ty - 1] + at + (int64_t)h * a.cache.head_stride;
+      *reinterpret_cast<uint4*>(o + e0) = u;
+      *reinterpret_cast<uint4*>(o + e1) = v;
+    }
+  }
+}
+
+cudaError_t launch_rope_append(const ds_rope_args& g, cudaStream_t stream) {
+  RopeKArgs a = {};
+  const bool cache = g.k_cache != nullptr;
+  a.x[0] = static_cast<const uint16_t*>(g.q);
+  a.x[1] = static_cast<const uint16_t*>(g.k);
+  a.x[2] = static_cast<const uint16_t*>(g.v);
+  a.stride[0] = g.q_row_stride;
+  a.stride[1] = g.k_row_stride;
+  a.stride[2] = g.v_row_stride;
+  a.out[0] = static_cast<uint16_t*>(g.q_out);
+  a.out[1] = static_cast<uint16_t*>(g.k_out);
+  a.out_stride[0] = g.q_out_row_stride;
+  a.out_stride[1] = g.k_out_row_stride;
+  a.positions = g.positions;
+  a.n_rows = g.n_rows;
+  a.hq = g.num_q_heads;
+  a.hkv = g.num_kv_heads;
+  a.heads = a.hq + a.hkv * (cache ? 2 : 1);
+  a.rotary = g.rotary_dim ? g.rotary_dim : g.head_dim;
+  a.write = cache;
+  if (cache) {
+    a.cache = draft_cache(g);
+    a.from_lens = g.from_lens;
+    a.row_offsets = g.row_offsets;
+    a.batch = g.batch;
+    a.slot_positions = g.slot_positions;
+    a.slot_weights = g.slot_weights;
+    a.slot_heads = g.slot_positions || g.slot_weights ? g.slot_heads : 0;
+    a.slot_stride = g.slot_stride;
+    a.new_lens = g.new_lens;
+  }
+  a.status = static_cast<uint32_t*>(g.workspace);
+  a.magnitude = g.magnitude;
+  a.sin_sign = g.inverse ? -1.f : 1.f;
+  // a double's 53 bits leave each frequency (at most a radian in use) off by
+  // less than 2^-53 of a turn, and the angle, at positions below 2^31, by
+  // less than 2^-22 of one; at 2^17 by less than 2^-36
+  for (int j = 0; j < a.rotary / 2; ++j) {
+    const double turns = (g.inv_freq ? g.inv_freq[j]
+                                     : std::pow((double)g.rope_base, -2.0 * j / a.rotary)) /
+                         6.283185307179586;
+    const double frac = turns - std::floor(turns);   // whole turns drop out
+    a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
+  }
+  const int hpw = 32 / (g.head_dim / 16), groups = (a.heads + hpw - 1) / hpw;
+  const int slices = (int)std::max<int64_t>(
+      1, std::min<int64_t>(groups, 152 * 24 / std::max(1, g.n_rows)));
+  a.per = (groups + slices - 1) / slices;
+  a.row_blocks = (int)(((int64_t)g.n_rows + kRopeWarps - 1) / kRopeWarps);
+  const dim3 grid((unsigned)(a.row_blocks + (a.batch + 32 * kRopeWarps - 1) / (32 * kRopeWarps)),
+                  (unsigned)((groups + a.per - 1) / a.per));
+  const dim3 block(32 * kRopeWarps);
+  const bool bf = g.dtype == DS_KV_BF16, halves = g.layout == DS_ROPE_HALF;
+  auto go = [&](void (*k)(const RopeKArgs)) {
+    return launch_dependent(k, grid, block, 0, stream, a);
+  };
+  if (g.head_dim == 128) {
+    if (bf) return halves ? go(rope_append<128, true, true>) : go(rope_append<128, true, false>);
+    return halves ? go(rope_append<128, false, true>) : go(rope_append<128, false, false>);
+  }
+  if (bf) return halves ? go(rope_append<64, true, true>) : go(rope_append<64, true, false>);
+  return halves ? go(rope_append<64, false, true>) : go(rope_append<64, false, false>);
+}
+
+}  // namespace ds
