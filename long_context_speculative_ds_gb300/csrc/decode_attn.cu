@@ -8,6 +8,7 @@
 //   M = max m_i,  l = sum 2^(m_i - M) l_i,  out = sum 2^(m_i - M) o_i / l,
 // and turns logits s into weights 2^(s - M - log2 l), summed over heads.
 // Logits carry the factor log2 e, so that exponentials are powers of two.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -32,7 +33,7 @@ struct KArgs {
   int64_t q_stride;
   DraftCache cache;
   const int32_t* lens;
-  int32_t batch, hq, hkv, group, splits;
+  int32_t batch, hq, hkv, group;
   int32_t window, sinks;
   float scale;                  // softmax scale times log2 e
   void* out;
@@ -72,80 +73,497 @@ DS_DEV bool visible(const Range& r, int t) {
   return t < r.n && (t < r.sinks || t >= r.start);
 }
 
-template <bool BF>
-DS_DEV float up(uint16_t x) {
-  if constexpr (BF) return __uint_as_float((uint32_t)x << 16);
-  return __half2float(__ushort_as_half(x));
+// A block's range of the axis on which the segments' tiles lie one behind the
+// other, each segment behind a lead-in that stands for what its start and end
+// cost, so that many short segments weigh what they take.
+constexpr int kLead = 1;
+constexpr int kWarps = 8;                     // warps that compute
+constexpr int kThreads = 32 * (kWarps + 1);   // and one that loads
+
+struct Walk {
+  int64_t pos, left;            // start of the segment on the axis; units of the range to go
+  int b, h;                     // the segment
+  int64_t off;                  // units of it before the range
+};
+
+struct Plan {
+  Walk first;
+  int64_t quot, rem;            // blocks below rem have quot + 1 units, the others quot
+};
+
+struct Piece {
+  Range r;
+  int b, h;
+  int t0, t1;                   // tiles
+  int64_t pos;                  // of the segment
+};
+
+DS_DEV int64_t block_of(const Plan& p, int64_t u) {
+  const int64_t cut = p.rem * (p.quot + 1);
+  return u < cut ? u / (p.quot + 1) : p.rem + (u - cut) / p.quot;
 }
 
-// A piece of a segment, key by key on the ordinary units.
-template <int D, bool BF>
-__global__ void __launch_bounds__(128) split(const KArgs a) {
-  __shared__ float s_p[16][kTile];
-  __shared__ float s_q[16][D];
-  __shared__ int64_t s_at[kTile];
+DS_DEV Range seq_range(const KArgs& a, int b, bool report) {
+  return range_of(checked_len(__ldg(a.lens + b), a.cache.slots, a.status, report), a.window,
+                  a.sinks);
+}
+
+// The block's range, formed by all of its threads; false when it has none.
+DS_DEV bool make_plan(const KArgs& a, Plan& plan, int64_t (*s_sum)[2]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.batch + kThreads - 1) / kThreads;
+  const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
+  int64_t units = 0, tiles = 0;               // of this thread's sequences
+  for (int b = b0; b < b1; ++b) {
+    const int t = seq_range(a, b, blockIdx.x == 0).tiles;
+    tiles += t;
+    units += t > 0 ? t + kLead : 0;
+  }
+  units *= a.hkv;
+  tiles *= a.hkv;
+  int64_t incl = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (lane == 31) { s_sum[warp][0] = incl; s_sum[warp][1] = tiles; }
+  __syncthreads();
+  int64_t before = incl - units, all = 0, all_tiles = 0;
+  for (int w = 0; w <= kWarps; ++w) {
+    if (w < warp) before += s_sum[w][0];
+    all += s_sum[w][0];
+    all_tiles += s_sum[w][1];
+  }
+  const int64_t blocks = min((int64_t)gridDim.x, all_tiles);
+  if ((int64_t)blockIdx.x >= blocks) return false;
+  const int64_t quot = all / blocks, rem = all - quot * blocks;
+  const int64_t lo = blockIdx.x * quot + min((int64_t)blockIdx.x, rem);
+  if (before <= lo && lo < before + units) {  // one thread
+    int b = b0;
+    int64_t len = 0, off = lo - before;
+    for (;; ++b) {
+      const int t = seq_range(a, b, false).tiles;
+      len = t > 0 ? t + kLead : 0;
+      if (off < len * a.hkv) break;
+      off -= len * a.hkv;
+    }
+    plan.first.b = b;
+    plan.first.h = (int)(off / len);
+    plan.first.off = off - plan.first.h * len;
+    plan.first.pos = lo - plan.first.off;
+    plan.first.left = quot + ((int64_t)blockIdx.x < rem ? 1 : 0);
+    plan.quot = quot;
+    plan.rem = rem;
+  }
+  __syncthreads();
+  return true;
+}
+
+// The next piece of the walk; false at its end.
+DS_DEV bool next_piece(const KArgs& a, Walk& w, Piece& p) {
+  while (w.left > 0 && w.b < a.batch) {
+    const Range r = seq_range(a, w.b, false);
+    if (r.tiles == 0) {
+      ++w.b;
+      w.h = 0;
+      continue;
+    }
+    const int64_t len = r.tiles + kLead;
+    const int64_t take = min(w.left, len - w.off);
+    p.r = r;
+    p.b = w.b;
+    p.h = w.h;
+    p.pos = w.pos;
+    p.t0 = (int)max(w.off - kLead, (int64_t)0);
+    p.t1 = (int)(w.off + take - kLead);
+    w.left -= take;
+    w.pos += len;
+    w.off = 0;
+    if (++w.h == a.hkv) {
+      w.h = 0;
+      ++w.b;
+    }
+    if (p.t1 > p.t0) return true;             // else only part of the lead-in
+  }
+  return false;
+}
+
+DS_DEV void tma_load_4d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                             int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+DS_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+DS_DEV void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+DS_DEV uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <bool BF>
+DS_DEV void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF>
+DS_DEV uint32_t pack2(float lo, float hi) {
+  return BF ? ptx::pack_bf16x2(lo, hi) : ptx::pack_f16x2(lo, hi);
+}
+// (lo, hi) as a pair of the cache's type, and what that rounding left.
+template <bool BF>
+DS_DEV void split2(float lo, float hi, uint32_t& big, uint32_t& rest) {
+  big = pack2<BF>(lo, hi);
+  float2 b;
+  if constexpr (BF)
+    b = make_float2(__uint_as_float(big << 16), __uint_as_float(big & 0xffff0000u));
+  else
+    b = __half22float2(*reinterpret_cast<const __half2*>(&big));
+  rest = pack2<BF>(lo - b.x, hi - b.y);
+}
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int R = 8 * NT;                      // query rows
+  static constexpr int kSubBytes = 16 * D * 2;          // 16 keys of K or V
+  static constexpr int kStage = 2 * 4 * kSubBytes;      // a tile's K and V
+  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 5) : 11;
+  static constexpr size_t smem = 1024 + (size_t)kStages * kStage + kWarps * R * D * 4;
+  static_assert(smem + 1900 <= 232448, "ring and outputs within a block's shared memory");
+  // where value d of a row lies among the D of a warp's output row (rows turned
+  // so that the four rows that a warp writes at once fall into different banks)
+  static DS_DEV int turned(int row, int d) { return (d + 8 * (row >> 1)) & (D - 1); }
+};
+
+// (the header's fields come out of the block's static shared memory)
+struct Shared {
+  alignas(8) uint64_t full[16], empty[16];
+  Plan plan;
+  int64_t sum[kWarps + 1][2];
+  float m[kWarps][16], l[kWarps][16];
+  int abort;
+};
+static_assert(sizeof(Shared) <= 1900, "");
+
+template <int D, bool BF, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    split(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+          const KArgs a, const int hnd) {
+  using namespace ptx;
+  using C = Cfg<D, NT>;
+  constexpr int S = C::kStages;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+  float* const merge = reinterpret_cast<float*>(raw + (ring - smem_addr(raw)) + S * C::kStage);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_addr(&sh.full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 4);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid == kThreads - 1) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int seg = blockIdx.x, b = seg / a.hkv, h = seg % a.hkv, G = a.group;
-  const int n = checked_len(__ldg(a.lens + b), a.cache.slots, a.status,
-                            threadIdx.x == 0 && h == 0 && blockIdx.y == 0);
-  const Range r = range_of(n, a.window, a.sinks);
-  const int pieces = max(1, min(a.splits, r.tiles));
-  if (blockIdx.y == 0 && threadIdx.x == 0) a.desc[seg] = make_int2(seg * a.splits, pieces);
-  if ((int)blockIdx.y >= pieces) return;
-  const int t0 = (int)((int64_t)r.tiles * blockIdx.y / pieces);
-  const int t1 = (int)((int64_t)r.tiles * (blockIdx.y + 1) / pieces);
-  const int piece = seg * a.splits + blockIdx.y;
-  for (int i = threadIdx.x; i < G * D; i += 128)
-    s_q[i / D][i % D] = up<BF>(a.q[(int64_t)b * a.q_stride + (int64_t)(h * G) * D + i]);
-  float m[16], l[16], o[16];
-  for (int g = 0; g < G; ++g) { m[g] = -CUDART_INF_F; l[g] = 0.f; o[g] = 0.f; }
-  for (int t = t0; t < t1; ++t) {
-    const int slot0 = tile_slot(r, t);
-    __syncthreads();
-    if (threadIdx.x < kTile) {
-      const int slot = slot0 + threadIdx.x;
-      int64_t at = -1;                    // -1: not attended to, -2: no page
-      if (visible(r, slot)) {
-        const int pg = slot_page(a.cache, b, slot);
-        if (pg < 0) flag(a.status, DS_DEV_BAD_PAGE);
-        at = pg < 0 ? -2 : slot_at(a.cache, pg, slot) + (int64_t)h * a.cache.head_stride;
+  if (!make_plan(a, sh.plan, sh.sum)) return;
+  volatile int* const abort = &sh.abort;
+  Walk walk = sh.plan.first;
+  Piece pc;
+  int stage = 0, phase = 0;                   // of the next tile
+
+  if (warp == kWarps) {
+    // ---- the loader: lanes 0 to 3 bring the tile's K, 4 to 7 its V, a box of
+    // 16 slots each; page ids are read eight tiles ahead
+    const uint64_t policy = l2_evict_first();
+    const int sub = lane & 3, kind = (lane >> 2) & 1;
+    int64_t issued = 0;
+    bool ok = true;
+    while (ok && next_piece(a, walk, pc)) {
+      const Range r = pc.r;
+      auto sub_visible = [&](int t, int s) {
+        const int k0 = tile_slot(r, t) + 16 * s;
+        return t < pc.t1 && k0 < r.n && (k0 < r.sinks || k0 + 16 > r.start);
+      };
+      auto page_of = [&](int t, int s) {
+        return a.cache.page_table && sub_visible(t, s)
+                   ? __ldg(a.cache.page_table + (int64_t)pc.b * a.cache.max_pages +
+                           ((tile_slot(r, t) + 16 * s) >> a.cache.page_shift))
+                   : pc.b;
+      };
+      int ids = 0, next = page_of(pc.t0 + (lane >> 2), sub);
+      for (int t = pc.t0; t < pc.t1; ++t) {
+        const int k = (t - pc.t0) & 7;
+        if (k == 0) {
+          ids = next;
+          next = page_of(t + 8 + (lane >> 2), sub);
+        }
+        int pg = __shfl_sync(0xffffffffu, ids, k * 4 + sub);
+        if ((uint32_t)pg >= (uint32_t)a.cache.num_pages) {
+          // (a page past the pool reads as zeros)
+          if (lane < 4 && sub_visible(t, sub)) flag(a.status, DS_DEV_BAD_PAGE);
+          pg = a.cache.num_pages;
+        }
+        const bool vis = sub_visible(t, sub);
+        const int boxes = __popc(__ballot_sync(0xffffffffu, vis && lane < 8));
+        ok = mbar_wait(smem_addr(&sh.empty[stage]), phase ^ 1, abort);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_addr(&sh.full[stage]);
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * C::kSubBytes);
+        __syncwarp();
+        if (lane < 8 && vis) {
+          const int slot = tile_slot(r, t) + 16 * sub;
+          const int row = a.cache.page_table ? slot & (a.cache.page_size - 1) : slot;
+          const uint32_t dst = ring + stage * C::kStage + (kind * 4 + sub) * C::kSubBytes;
+          tma_load_4d_hint(dst, kind ? &tv : &tk, bar, 0, row, hnd ? 0 : pc.h * (D / 64),
+                           hnd ? pg * a.hkv + pc.h : pg, policy);
+        }
+        ++issued;
+        if (++stage == S) { stage = 0; phase ^= 1; }
       }
-      s_at[threadIdx.x] = at;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * kTile; i += 128) {
-      const int g = i / kTile, k = i % kTile;
-      const int64_t at = s_at[k];
-      float s = 0.f;
-      if (at >= 0)
-        for (int d = 0; d < D; ++d) s = fmaf(s_q[g][d], up<BF>(a.cache.pool[0][at + d]), s);
-      s = at == -1 ? -CUDART_INF_F : s * a.scale;
-      s_p[g][k] = s;
-      if (a.logits && at != -1)
-        a.logits[((int64_t)seg * a.cache.slots + slot0 + k) * G + g] = s;
-    }
-    __syncthreads();
-    for (int g = 0; g < G; ++g) {
-      float mx = m[g];
-      for (int k = 0; k < kTile; ++k) mx = fmaxf(mx, s_p[g][k]);
-      const float ref = mx == -CUDART_INF_F ? 0.f : mx;
-      const float f = exp2f(m[g] - ref);
-      m[g] = mx;
-      l[g] *= f;
-      o[g] *= f;
-      for (int k = 0; k < kTile; ++k) {
-        if (s_at[k] == -1) continue;
-        const float p = exp2f(s_p[g][k] - ref);
-        l[g] += p;
-        if (threadIdx.x < D && s_at[k] >= 0)
-          o[g] = fmaf(p, up<BF>(a.cache.pool[1][s_at[k] + threadIdx.x]), o[g]);
+    if (!ok) {                                // no copy may land behind the block's end
+      for (int i = 0; i < S && i < issued; ++i) {
+        if (--stage < 0) { stage = S - 1; phase ^= 1; }
+        drain_wait(smem_addr(&sh.full[stage]), phase);
       }
+      if (lane == 0) flag(a.status, DS_DEV_TIMEOUT);
     }
+    return;
   }
-  for (int g = 0; g < G; ++g) {
-    if (threadIdx.x < D) a.part_o[((int64_t)piece * G + g) * D + threadIdx.x] = o[g];
-    if (threadIdx.x == 0) a.part_ml[(int64_t)piece * G + g] = make_float2(m[g], l[g]);
+
+  // ---- the others: warps 0 to 3 and 4 to 7 take tiles in turn, a warp 16 keys
+  const int g = lane >> 2, t4 = lane & 3, G = a.group;
+  const int sub = warp & 3, team = warp >> 2;
+  int turn = 0;
+  // ldmatrix: this lane's row of K (keys 0-15, 8 channels a chunk) and of V
+  const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
+  const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
+  // a box is [64-channel half][16 slots][128 bytes], chunks swizzled by row
+  auto chunk_at = [&](uint32_t base, int row, int chunk) {
+    return base + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+  };
+  while (next_piece(a, walk, pc)) {
+    const Range r = pc.r;
+    const int64_t seg = (int64_t)pc.b * a.hkv + pc.h;
+    uint32_t q[NT][D / 16][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        q[i][ks][0] = q[i][ks][1] = 0u;
+        if (8 * i + g < G) {
+          const uint16_t* p = a.q + (int64_t)pc.b * a.q_stride +
+                              (int64_t)(pc.h * G + 8 * i + g) * D + ks * 16 + 2 * t4;
+          q[i][ks][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          q[i][ks][1] = __ldg(reinterpret_cast<const uint32_t*>(p + 8));
+        }
+      }
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      m[i][0] = m[i][1] = -CUDART_INF_F;
+      l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][d][j] = 0.f;
+    }
+    for (int t = pc.t0; t < pc.t1; ++t, turn ^= 1) {
+      const int st = stage, ph = phase;
+      if (++stage == S) { stage = 0; phase ^= 1; }
+      if (turn != team) continue;
+      const bool ok = mbar_wait(smem_addr(&sh.full[st]), ph, abort);
+      const int k0 = tile_slot(r, t) + 16 * sub;
+      if (__all_sync(0xffffffffu, ok) && k0 < r.n && (k0 < r.sinks || k0 + 16 > r.start)) {
+        const uint32_t kb = ring + st * C::kStage + sub * C::kSubBytes;
+        const uint32_t vb = kb + 4 * C::kSubBytes;
+        float s[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t x[4];
+          ldmatrix4(x, chunk_at(kb, krow, 2 * ks + kchunk));
+#pragma unroll
+          for (int i = 0; i < NT; ++i) mma<BF>(s[i], x, q[i][ks][0], q[i][ks][1]);
+        }
+        const bool whole = k0 + 16 <= r.n && (k0 >= r.start || k0 + 16 <= r.sinks);
+        const bool va = whole || visible(r, k0 + g), vc = whole || visible(r, k0 + g + 8);
+        float mx[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            s[i][j] = va ? s[i][j] * a.scale : -CUDART_INF_F;
+            s[i][2 + j] = vc ? s[i][2 + j] * a.scale : -CUDART_INF_F;
+            const int row = 8 * i + 2 * t4 + j;
+            if (a.logits && row < G) {
+              float* x = a.logits + (seg * a.cache.slots + k0 + g) * G + row;
+              if (va) x[0] = s[i][j];
+              if (vc) x[8 * G] = s[i][2 + j];
+            }
+            mx[i][j] = fmaxf(s[i][j], s[i][2 + j]);
+          }
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              mx[i][j] = fmaxf(mx[i][j], __shfl_xor_sync(0xffffffffu, mx[i][j], x));
+        // the reference point follows the maximum only when that has grown by
+        // more than 2^8: weights reach at most 2^8, and outputs are rarely scaled
+        bool grow = false;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) grow |= mx[i][j] > m[i][j] + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float now = fmaxf(m[i][j], mx[i][j]);
+              const float f = m[i][j] == now ? 1.f : ex2(m[i][j] - now);
+              m[i][j] = now;
+              l[i][j] *= f;
+#pragma unroll
+              for (int d = 0; d < D / 16; ++d) {
+                o[i][d][j] *= f;
+                o[i][d][2 + j] *= f;
+              }
+            }
+          }
+        }
+        uint32_t big[NT][2], rest[NT][2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          float p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float ref = m[i][j & 1] == -CUDART_INF_F ? 0.f : m[i][j & 1];
+            p[j] = ex2(s[i][j] - ref);
+            l[i][j & 1] += p[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            split2<BF>(p[2 * j], p[2 * j + 1], big[i][j], rest[i][j]);
+            big[i][j] = transpose8x8(big[i][j]);
+            rest[i][j] = transpose8x8(rest[i][j]);
+          }
+        }
+        // slots that are not attended to may hold anything: their V is zeroed
+        uint32_t keep[2] = {~0u, ~0u};
+        if (!whole)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            keep[j] = (visible(r, k0 + 8 * j + 2 * t4) ? 0xffffu : 0u) |
+                      (visible(r, k0 + 8 * j + 2 * t4 + 1) ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t x[4];
+          ldmatrix4_trans(x, chunk_at(vb, vrow, 2 * d + vchunk));
+          x[0] &= keep[0];
+          x[1] &= keep[0];
+          x[2] &= keep[1];
+          x[3] &= keep[1];
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            mma<BF>(o[i][d], x, big[i][0], big[i][1]);
+            mma<BF>(o[i][d], x, rest[i][0], rest[i][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
+    }
+    // ---- the warps' outputs joined, into the piece's place
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], x);
+    float* const mine = merge + warp * C::R * D;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = 8 * i + 2 * t4 + j;
+        if (g == 0) {
+          sh.m[warp][row] = m[i][j];
+          sh.l[warp][row] = l[i][j];
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          mine[row * D + C::turned(row, d * 16 + g)] = o[i][d][j];
+          mine[row * D + C::turned(row, d * 16 + g + 8)] = o[i][d][2 + j];
+        }
+      }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    const int64_t u = pc.pos + kLead;         // the segment's first tile on the axis
+    const int64_t piece = blockIdx.x + seg;
+    for (int i = tid; i < G * D / 4; i += 32 * kWarps) {
+      const int row = i / (D / 4), c = i % (D / 4);
+      float M = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][row]);
+      const float ref = M == -CUDART_INF_F ? 0.f : M;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float total = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(sh.m[w][row] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(
+            merge + (w * C::R + row) * D + C::turned(row, c * 4));
+        sum.x = fmaf(f, x.x, sum.x);
+        sum.y = fmaf(f, x.y, sum.y);
+        sum.z = fmaf(f, x.z, sum.z);
+        sum.w = fmaf(f, x.w, sum.w);
+        total = fmaf(f, sh.l[w][row], total);
+      }
+      *reinterpret_cast<float4*>(a.part_o + ((piece * G + row) * D + c * 4)) = sum;
+      if (c == 0) a.part_ml[piece * G + row] = make_float2(M, total);
+    }
+    if (tid == 0 && pc.t0 == 0) {             // numbered by block and segment, which never
+      const int64_t f = block_of(sh.plan, u); // both stand still, pieces have places of their own
+      a.desc[seg] = make_int2((int)(f + seg),
+                              (int)(block_of(sh.plan, u + r.tiles - 1) - f + 1));
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
   }
 }
 
@@ -255,6 +673,51 @@ __global__ void __launch_bounds__(32 * kFinishWarps) finish(const KArgs a, int r
   }
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  void* ptr = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                       &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<EncodeFn>(ptr);
+}
+
+// K or V as [64 channels][slots of a page][halves of heads][pages] (heads
+// before slots: the head is part of the page's coordinate): a box is 16 slots
+// of one head, [half][16][128 bytes], its chunks swizzled.
+bool cache_map(CUtensorMap* map, const void* base, const ds_decode_args& g) {
+  const cuuint64_t D = g.head_dim, P = g.page_size, H = g.num_kv_heads, N = g.num_pages;
+  const bool hnd = g.kv_layout == DS_KV_HND;
+  const cuuint64_t dims[4] = {64, P, (D / 64) * (hnd ? 1 : H), N * (hnd ? H : 1)};
+  const cuuint64_t strides[3] = {(hnd ? 1 : H) * D * 2, 128, P * (hnd ? 1 : H) * D * 2};
+  const cuuint32_t box[4] = {64, 16, (cuuint32_t)(D / 64), 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  static const EncodeFn fn = encode_fn();     // (the driver's, the same on every device)
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                  strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF, int NT>
+cudaError_t launch_split(const KArgs& a, const ds_decode_args& g, int ctas,
+                         cudaStream_t stream) {
+  CUtensorMap tk, tv;
+  if (!cache_map(&tk, g.k_cache, g) || !cache_map(&tv, g.v_cache, g))
+    return cudaErrorInvalidValue;
+  const size_t smem = Cfg<D, NT>::smem;
+  const cudaError_t e = allow_smem(split<D, BF, NT>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(split<D, BF, NT>, dim3(ctas), dim3(kThreads), smem, stream, tk, tv, a,
+                          g.kv_layout == DS_KV_HND ? 1 : 0);
+}
+
 }  // namespace decode
 
 cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
@@ -286,12 +749,18 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
   a.logits = g.weights_out ? reinterpret_cast<float*>(ws + L.logits) : nullptr;
   a.status = reinterpret_cast<uint32_t*>(ws);
-  const int segs = g.batch * g.num_kv_heads;
-  a.splits = std::max(1, L.ctas / segs);
   const bool bf = g.dtype == DS_KV_BF16;
-  auto k = g.head_dim == 128 ? (bf ? split<128, true> : split<128, false>)
-                             : (bf ? split<64, true> : split<64, false>);
-  cudaError_t e = launch_dependent(k, dim3(segs, a.splits), dim3(128), 0, stream, a);
+  cudaError_t e;
+  if (a.group <= 8)
+    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 1>(a, g, L.ctas, stream)
+                                : launch_split<128, false, 1>(a, g, L.ctas, stream))
+                          : (bf ? launch_split<64, true, 1>(a, g, L.ctas, stream)
+                                : launch_split<64, false, 1>(a, g, L.ctas, stream));
+  else
+    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 2>(a, g, L.ctas, stream)
+                                : launch_split<128, false, 2>(a, g, L.ctas, stream))
+                          : (bf ? launch_split<64, true, 2>(a, g, L.ctas, stream)
+                                : launch_split<64, false, 2>(a, g, L.ctas, stream));
   if (e != cudaSuccess) return e;
   const int row_blocks = (int)(((int64_t)g.batch * a.hq + kFinishWarps - 1) / kFinishWarps);
   const int spans = (int)((a.cache.slots + kSpan - 1) / kSpan);
