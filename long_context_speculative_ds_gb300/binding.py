@@ -616,6 +616,8 @@ def ds_kv4_verify_attn(args: Kv4AttnArgs, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# The draft's cache.  These argument structs keep their tensors alive
+# (`_tensors`): a call may be made long after they were built.
 _SCALES = {"none": DS_ROPE_SCALE_NONE, "linear": DS_ROPE_SCALE_LINEAR,
            "bands": DS_ROPE_SCALE_BANDS, "ramp": DS_ROPE_SCALE_RAMP}
 _ROPE_LAYOUT = {"half": DS_ROPE_HALF, "interleaved": DS_ROPE_INTERLEAVED}
@@ -738,6 +740,8 @@ def rope_append_args(q, k, v, positions, *, q_out=None, k_out=None,
         a.new_lens = _int32(new_lens, batch, "new_lens")
         _slot_arrays(a, batch, slot_positions=(slot_positions, torch.int32),
                      slot_weights=(slot_weights, torch.float32))
+    a._tensors = (q, k, v, positions, q_out, k_out, k_cache, v_cache, page_table, from_lens,
+                  row_offsets, slot_positions, slot_weights, new_lens, workspace)
     _set_workspace(a, workspace)
     return a
 
@@ -773,6 +777,8 @@ def decode_attn_args(q, k_cache, v_cache, page_table, lens, *, out, lse=None,
     _slot_arrays(a, batch, weights_in=(weights_in, torch.float32),
                  weights_out=(weights_out, torch.float32))
     a.decay, a.window, a.sinks, a.scale, a.num_sms = decay, window, sinks, scale, num_sms
+    a._tensors = (q, k_cache, v_cache, page_table, lens, out, lse, weights_in, weights_out,
+                  workspace)
     _set_workspace(a, workspace)
     return a
 
@@ -805,6 +811,8 @@ def evict_args(k_cache, v_cache, page_table, lens, *, weights, positions,
     a.next_positions = _int32(next_positions, batch, "next_positions")
     a.new_lens = _int32(new_lens, batch, "new_lens")
     a.budget, a.trigger, a.recent, a.sinks = budget, trigger, recent, sinks
+    a._tensors = (k_cache, v_cache, page_table, lens, weights, positions, weights_out,
+                  positions_out, next_positions, new_lens, workspace)
     _set_workspace(a, workspace)
     return a
 

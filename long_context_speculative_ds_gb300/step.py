@@ -45,7 +45,9 @@ class VerifyStep:
                  window: int, accept_mode: str, kv_layout: str = "NHD",
                  out_dtype: torch.dtype = torch.bfloat16, num_sms: int = 0,
                  device: str = "cuda", with_commit: bool = False,
-                 rope_base: float = 0.0):
+                 rope_base: float = 0.0, reserve: int = 0):
+        """reserve: slots of the compact cache behind the retrieved ones, for
+        a draft that decodes over it (draft.DraftCache)."""
         self.inp = inp
         self.chunk_size, self.top_k, self.window = chunk_size, top_k, window
         self.accept_mode = accept_mode
@@ -78,7 +80,7 @@ class VerifyStep:
                 chunk_size=chunk_size, out=self.out[l],
                 chunk_scores=self.scores, workspace=self.ws_verify,
                 kv_layout=kv_layout, accumulate=l > 0, num_sms=num_sms))
-        cap = top_k * chunk_size + window
+        cap = top_k * chunk_size + window + reserve
         self.capacity = cap
         self.out_k = torch.empty(bsz, cap, kv_heads, head_dim,
                                  dtype=torch.bfloat16, device=dev)
