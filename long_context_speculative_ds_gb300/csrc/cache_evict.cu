@@ -41,15 +41,14 @@ struct KArgs {
 
 constexpr int kThreads = 1024;
 
+// (without branches, so that the loads of many slots go out together)
 DS_DEV uint32_t rank_key(float w, int pos, int sinks, int64_t recent_from, bool& nan) {
-  if (pos < sinks || pos >= recent_from) return ~0u;
-  if (w != w) {
-    nan = true;
-    return 0u;
-  }
+  const bool must = pos < sinks || pos >= recent_from, none = w != w;
   const uint32_t u = __float_as_uint(w + 0.f);   // -0 becomes 0
   // (the largest key of a weight, +inf, is 0xff800000)
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  nan |= none && !must;
+  return must ? ~0u : none ? 0u : k;
 }
 
 // A cluster of blocks per segment, a contiguous part of its slots to each, and
@@ -61,27 +60,32 @@ constexpr int kBins = 2048;               // of a digit: 11, 11 and 10 bits
 
 struct Shared {
   uint32_t hist[3][kBins];
-  uint32_t forced;                        // slots that must stay
-  int warp_sum[2][32];
-  int block_sum[2][2];                    // [ties | come and free][...]: of this block
+  int2 warp_sum[2][32];
+  int2 block_sum[2];                      // of this block: ties; slots that come, that are freed
   uint32_t prefix, left, count;
 };
 
-// Exclusive prefix of one value per warp (the same on all its lanes) over the
-// block's warps, and the total.
-DS_DEV int warps_prefix(int v, int* s_warp, int& total) {
+// Exclusive prefix of two values per warp (the same on all its lanes) over the
+// block's warps, and the totals.
+DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) s_warp[warp] = v;
   __syncthreads();
-  const int w = s_warp[lane];
-  int incl = w;
+  const int2 w = s_warp[lane];
+  int2 incl = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
   }
-  total = __shfl_sync(0xffffffffu, incl, 31);
-  return __shfl_sync(0xffffffffu, incl - w, warp);
+  total.x = __shfl_sync(0xffffffffu, incl.x, 31);
+  total.y = __shfl_sync(0xffffffffu, incl.y, 31);
+  return make_int2(__shfl_sync(0xffffffffu, incl.x - w.x, warp),
+                   __shfl_sync(0xffffffffu, incl.y - w.y, warp));
 }
 
 __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
@@ -90,7 +94,9 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
   const int C = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid == 0) sh.forced = 0;
+  auto meet = [&] {                       // a barrier of the cluster
+    if (C == 1) __syncthreads(); else cl.sync();
+  };
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int seg = blockIdx.x / C, b = seg / a.slot_heads, w = seg % a.slot_heads;
@@ -117,13 +123,25 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
   const int rows = (n + 31) / 32, per = (rows + C * 32 - 1) / (C * 32);
   const int i0 = ((rank * 32 + warp) * per) * 32 + lane;
   bool nan = false;
-  auto read = [&](int j) {                // 0: no slot (no key of a slot is ranked by it
-    const int i = i0 + 32 * j;            // before the slot's own bounds are looked at)
-    return i < n ? rank_key(wt[i], ps[i], a.sinks, from, nan) : 0u;
+  auto read = [&](int j) {                // (slots past the end: some key, never looked at)
+    const int i = min(i0 + 32 * j, n - 1);
+    return rank_key(__ldg(wt + i), __ldg(ps + i), a.sinks, from, nan);
   };
   uint32_t kept[kKeep];
 #pragma unroll
-  for (int j = 0; j < kKeep; ++j) kept[j] = j < per ? read(j) : 0u;
+  for (int j0 = 0; j0 < kKeep; j0 += 8)
+    if (j0 < per) {
+      float w[8];
+      int p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = min(i0 + 32 * (j0 + j), n - 1);
+        w[j] = __ldg(wt + i);
+        p[j] = __ldg(ps + i);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) kept[j0 + j] = rank_key(w[j], p[j], a.sinks, from, nan);
+    }
   // f(key, slot) for each of the warp's rows of slots in order
   auto each = [&](auto f) {
 #pragma unroll
@@ -147,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
     });
     must = __reduce_add_sync(0xffffffffu, must);
     if (lane == 0 && must) atomicAdd(&hist[(1u << bits) - 1], must);
-    cl.sync();
+    meet();
     // thread t holds bins kBins - 1 - 2 t and the one below, of all blocks
     uint32_t x0 = 0, x1 = 0;
     for (int c = 0; c < C; ++c) {
@@ -162,10 +180,10 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
       const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    int unused;
+    int2 unused;
+    const int2 whole = make_int2(__shfl_sync(0xffffffffu, incl, 31), 0);
     const uint32_t above =
-        warps_prefix(__shfl_sync(0xffffffffu, incl, 31), sh.warp_sum[round & 1], unused) + incl -
-        x0 - x1;
+        warps_prefix(whole, sh.warp_sum[round & 1], unused).x + incl - x0 - x1;
     if (above < left && left <= above + x0 + x1) {   // one thread
       const bool first = left <= above + x0;
       sh.prefix = prefix << bits | (kBins - 1 - 2 * tid - (first ? 0 : 1));
@@ -176,50 +194,57 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
     prefix = sh.prefix;
     left = sh.left;
     same = sh.count;
+    if (left == same && round < 2) {      // all of the bin stay: what lies above it and these
+      prefix = (prefix << shift) - 1;     // (bin 0 cannot: more slots than stay)
+      left = same = 0;
+      break;
+    }
   }
   if (nan) flag(a.status, DS_DEV_BAD_VALUE);
-  // `left` of the `same` slots with key `prefix` stay, the lower ones
-  int ties0 = 0;                          // ties before this warp's slots
-  if (left < same) {
-    int ties = 0, total;
+  // above `prefix` all stay, and `left` of the `same` slots at it, the lower ones
+  const bool ties = left < same;
+  int ties0 = 0;                 // ties before this warp's slots
+  if (ties) {
+    int2 v = make_int2(0, 0), total;
     each([&](uint32_t k, int i) {
-      ties += __popc(__ballot_sync(0xffffffffu, i < n && k == prefix));
+      v.x += __popc(__ballot_sync(0xffffffffu, i < n && k == prefix));
     });
-    ties0 = warps_prefix(ties, sh.warp_sum[1], total);
-    if (tid == 0) sh.block_sum[0][0] = total;
-    cl.sync();
-    for (int c = 0; c < rank; ++c) ties0 += *cl.map_shared_rank(&sh.block_sum[0][0], c);
+    ties0 = warps_prefix(v, sh.warp_sum[1], total).x;
+    if (tid == 0) sh.block_sum[0] = total;
+    meet();
+    for (int c = 0; c < rank; ++c) ties0 += cl.map_shared_rank(&sh.block_sum[0], c)->x;
+  } else if (left > 0) {
+    --prefix;                             // (all at it stay; 0 cannot be)
   }
   const uint32_t below = (1u << lane) - 1;
-  // the row's slots that stay (ballot), with the ties counted on
   auto stays = [&](uint32_t k, int i, int& seen) {
-    const uint32_t tie = __ballot_sync(0xffffffffu, i < n && k == prefix);
-    const bool stay = i < n && (k > prefix || ((tie >> lane & 1) &&
-                                               seen + __popc(tie & below) < (int)left));
-    seen += __popc(tie);
+    bool stay = i < n && k > prefix;
+    if (ties) {
+      const bool tie = i < n && k == prefix;
+      const uint32_t all = __ballot_sync(0xffffffffu, tie);
+      stay |= tie && seen + __popc(all & below) < (int)left;
+      seen += __popc(all);
+    }
     return stay;
   };
-  int come = 0, freed = 0, seen = ties0;
+  int2 sum = make_int2(0, 0), total;
+  int seen = ties0;
   each([&](uint32_t k, int i) {
     const bool stay = stays(k, i, seen);
-    come += __popc(__ballot_sync(0xffffffffu, stay && i >= keep));
-    freed += __popc(__ballot_sync(0xffffffffu, !stay && i < keep));
+    sum.x += __popc(__ballot_sync(0xffffffffu, stay && i >= keep));
+    sum.y += __popc(__ballot_sync(0xffffffffu, !stay && i < keep));
   });
-  int total;
-  int come0 = warps_prefix(come, sh.warp_sum[0], total);
-  if (tid == 0) sh.block_sum[1][0] = total;
-  __syncthreads();
-  int freed0 = warps_prefix(freed, sh.warp_sum[1], total);
-  if (tid == 0) sh.block_sum[1][1] = total;
-  cl.sync();
+  int2 before = warps_prefix(sum, sh.warp_sum[0], total);
+  if (tid == 0) sh.block_sum[1] = total;
+  meet();
   int all = 0;
   for (int c = 0; c < C; ++c) {
-    const int* x = cl.map_shared_rank(&sh.block_sum[1][0], c);
+    const int2 x = *cl.map_shared_rank(&sh.block_sum[1], c);
     if (c < rank) {
-      come0 += x[0];
-      freed0 += x[1];
+      before.x += x.x;
+      before.y += x.y;
     }
-    all += x[0];
+    all += x.x;
   }
   int32_t* src = a.src + (int64_t)seg * a.moves;
   int32_t* dst = a.dst + (int64_t)seg * a.moves;
@@ -228,72 +253,76 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
     const bool stay = stays(k, i, seen);
     const uint32_t c = __ballot_sync(0xffffffffu, stay && i >= keep);
     const uint32_t f = __ballot_sync(0xffffffffu, !stay && i < keep);
-    if (c >> lane & 1) src[come0 + __popc(c & below)] = i;
-    if (f >> lane & 1) dst[freed0 + __popc(f & below)] = i;
-    come0 += __popc(c);
-    freed0 += __popc(f);
+    if (c >> lane & 1) src[before.x + __popc(c & below)] = i;
+    if (f >> lane & 1) dst[before.y + __popc(f & below)] = i;
+    before.x += __popc(c);
+    before.y += __popc(f);
     if (stay && i < keep) {
       if (wo) wo[i] = wt[i];
       if (po) po[i] = ps[i];
     }
   });
   if (tid == 0 && rank == 0) a.count[seg] = all;
-  cl.sync();                              // others may still read this block's sums
+  if (C > 1) cl.sync();                   // others may still read this block's sums
 }
 
-// A warp takes 32 moves of a segment and one kv head: a lane looks up one
-// move's places, then the rows go four at a time, a lane 16 bytes of K or V.
+// A warp takes the moves of a segment 32 kv heads' rows at a time (32 moves of
+// one head, or 4 of eight that move together): a lane looks up one move's
+// places, then the rows go eight (sixteen) at once, a lane 16 bytes of K or V,
+// a move's heads one behind the other.
 template <int D>
-__global__ void __launch_bounds__(256) move(const KArgs a) {
+__global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
   constexpr int VECS = D / 8;             // 16-byte vectors of a head's row
-  constexpr int AT = 32 / (2 * VECS);     // moves (their K and V) of a warp at once
+  constexpr int AT = 32 / (2 * VECS);     // rows (their K and V) of a warp at once
   constexpr int BATCH = 8;                // loads on their way
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int seg = blockIdx.x, b = seg / a.slot_heads, w = seg % a.slot_heads;
   const int lane = threadIdx.x & 31;
-  const int heads = a.slot_heads == 1 ? a.cache.num_kv_heads : 1;
+  const bool shared = a.slot_heads == 1;
+  const int heads = shared ? a.cache.num_kv_heads : 1, h0 = shared ? 0 : w;
   const int count = a.count[seg];
-  const int64_t items = (int64_t)((count + 31) / 32) * heads;
   const int32_t* src = a.src + (int64_t)seg * a.moves;
   const int32_t* dst = a.dst + (int64_t)seg * a.moves;
   uint16_t* const pool = lane % (2 * VECS) < VECS ? a.cache.pool[0] : a.cache.pool[1];
   const int col = lane % VECS * 8, mine = lane / (2 * VECS);
-  for (int64_t it = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); it < items;
-       it += (int64_t)gridDim.y * 8) {
-    const int i0 = (int)(it / heads) * 32, i = i0 + lane;
-    const int h = a.slot_heads == 1 ? (int)(it % heads) : w;
+  for (int64_t m0 = ((int64_t)blockIdx.y * 8 + (threadIdx.x >> 5)) * per; m0 < count;
+       m0 += (int64_t)gridDim.y * 8 * per) {
+    const int moves = (int)min((int64_t)per, count - m0);
     int64_t from = -1, to = -1;           // -1: nothing to move
-    if (i < count) {
-      const int s = src[i], d = dst[i];
-      if (it % heads == 0) {
-        const int64_t base = (int64_t)seg * a.slot_stride;
-        (a.weights_out ? a.weights_out : a.weights)[base + d] = a.weights[base + s];
-        (a.positions_out ? a.positions_out : a.positions)[base + d] = a.positions[base + s];
-      }
+    if (lane < moves) {
+      const int s = src[m0 + lane], d = dst[m0 + lane];
+      const int64_t base = (int64_t)seg * a.slot_stride;
+      (a.weights_out ? a.weights_out : a.weights)[base + d] = a.weights[base + s];
+      (a.positions_out ? a.positions_out : a.positions)[base + d] = a.positions[base + s];
       const int pf = slot_page(a.cache, b, s), pt = slot_page(a.cache, b, d);
       if (pf >= 0 && pt >= 0) {
-        from = slot_at(a.cache, pf, s) + (int64_t)h * a.cache.head_stride;
-        to = slot_at(a.cache, pt, d) + (int64_t)h * a.cache.head_stride;
+        from = slot_at(a.cache, pf, s) + (int64_t)h0 * a.cache.head_stride;
+        to = slot_at(a.cache, pt, d) + (int64_t)h0 * a.cache.head_stride;
       } else {
         flag(a.status, DS_DEV_BAD_PAGE);
       }
     }
-    const int rows = min(32, count - i0);
+    const int rows = moves * heads;
+    int m = mine / heads, h = mine % heads;       // of this lane's next row
     for (int r0 = 0; r0 < rows; r0 += AT * BATCH) {
       uint4 x[BATCH];
       int64_t at[BATCH];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
-        const int r = (r0 + k * AT + mine) & 31;
-        const int64_t f = __shfl_sync(0xffffffffu, from, r);
-        at[k] = __shfl_sync(0xffffffffu, to, r);
-        if (r0 + k * AT + mine >= rows) at[k] = -1;
-        if (at[k] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(pool + f + col));
+        const int64_t f = __shfl_sync(0xffffffffu, from, m & 31);
+        at[k] = __shfl_sync(0xffffffffu, to, m & 31);
+        const int64_t off = (int64_t)h * a.cache.head_stride + col;
+        if (r0 + k * AT + mine >= rows || at[k] < 0)
+          at[k] = -1;
+        else
+          at[k] += off;
+        if (at[k] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(pool + f + off));
+        for (h += AT; h >= heads; h -= heads) ++m;
       }
 #pragma unroll
       for (int k = 0; k < BATCH; ++k)
-        if (at[k] >= 0) *reinterpret_cast<uint4*>(pool + at[k] + col) = x[k];
+        if (at[k] >= 0) *reinterpret_cast<uint4*>(pool + at[k]) = x[k];
     }
   }
 }
@@ -353,12 +382,13 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   cfg.numAttrs = 2;
   cudaError_t e = cudaLaunchKernelEx(&cfg, select, a);
   if (e != cudaSuccess || L.moves == 0) return e;
-  // eight blocks an SM, as far as there can be moves
-  const int64_t warps = (L.moves + 31) / 32 * (g.slot_heads == 1 ? g.num_kv_heads : 1);
+  // moves of a warp at a time, and eight blocks an SM as far as there can be moves
+  const int per = std::max(1, 32 / (g.slot_heads == 1 ? g.num_kv_heads : 1));
+  const int64_t warps = (L.moves + per - 1) / per;
   const int rows = (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8,
                                                                152 * 8 / segs + 1));
   return launch_dependent(g.head_dim == 128 ? move<128> : move<64>, dim3(segs, rows), dim3(256),
-                          0, stream, a);
+                          0, stream, a, per);
 }
 
 }  // namespace ds
