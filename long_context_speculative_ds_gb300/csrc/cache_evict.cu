@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "dev_common.cuh"
 #include "draft_cache.cuh"
@@ -39,39 +40,40 @@ struct KArgs {
   uint32_t* status;
 };
 
-constexpr int kThreads = 1024;
-
 // (without branches, so that the loads of many slots go out together)
-DS_DEV uint32_t rank_key(float w, int pos, int sinks, int64_t recent_from, bool& nan) {
+DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan) {
   const bool must = pos < sinks || pos >= recent_from, none = w != w;
   const uint32_t u = __float_as_uint(w + 0.f);   // -0 becomes 0
   // (the largest key of a weight, +inf, is 0xff800000)
   const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
   nan |= none && !must;
-  return must ? ~0u : none ? 0u : k;
+  return must ? ~0u : none ? 1u : k;      // (-inf is 0x007fffff; 0: no slot)
 }
 
-// A cluster of blocks per segment, a contiguous part of its slots to each, and
-// of that a contiguous part to each warp: its slots i0 + 32 j + lane, j < per.
-// Keys of the first kKeep of these stay in registers; beyond (segments of more
-// than kKeep 1024 slots a block) they are formed anew from memory.
+// A cluster of blocks per segment; its rows of 32 slots in equal runs to the
+// warps, one behind the other.  Keys of a warp's first kKeep rows stay in
+// registers; beyond (segments of more than 16 slots a thread of the cluster)
+// they are formed anew from memory.
 constexpr int kKeep = 16;
 constexpr int kBins = 2048;               // of a digit: 11, 11 and 10 bits
+constexpr int kCluster = 16;              // blocks, at most
 
 struct Shared {
   uint32_t hist[3][kBins];
+  uint32_t part[3][32];                   // sums of 64 bins
   int2 warp_sum[2][32];
   int2 block_sum[2];                      // of this block: ties; slots that come, that are freed
   uint32_t prefix, left, count;
 };
 
 // Exclusive prefix of two values per warp (the same on all its lanes) over the
-// block's warps, and the totals.
+// block's NW warps, and the totals.
+template <int NW>
 DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) s_warp[warp] = v;
   __syncthreads();
-  const int2 w = s_warp[lane];
+  const int2 w = lane < NW ? s_warp[lane] : make_int2(0, 0);
   int2 incl = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -88,19 +90,25 @@ DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
                    __shfl_sync(0xffffffffu, incl.y - w.y, warp));
 }
 
-__global__ void __launch_bounds__(kThreads) select(const KArgs a) {
+// Mask of the first k of 32.
+DS_DEV uint32_t first_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; }
+
+template <int T>
+__global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
+  constexpr int NW = T / 32;
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 3 * kBins / 4; i += T)
+    reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   auto meet = [&] {                       // a barrier of the cluster
     if (C == 1) __syncthreads(); else cl.sync();
   };
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int seg = blockIdx.x / C, b = seg / a.slot_heads, w = seg % a.slot_heads;
-  const int len = __ldg(a.lens + b);
+  const int len = __ldg(a.lens + b), next = __ldg(a.next_positions + b);
   const int n = checked_len(len, a.cache.slots, a.status, tid == 0 && rank == 0 && w == 0);
   const bool cut = n > a.limit;
   const int keep = cut ? a.budget : n;
@@ -112,42 +120,52 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
   int32_t* po = a.positions_out ? a.positions_out + base : nullptr;
   if (!cut) {                             // (the whole cluster)
     if (tid == 0 && rank == 0) a.count[seg] = 0;
-    for (int i = rank * kThreads + tid; i < n; i += C * kThreads) {
+    for (int i = rank * T + tid; i < n; i += C * T) {
       if (wo) wo[i] = wt[i];
       if (po) po[i] = ps[i];
     }
     return;
   }
-  const int64_t from = (int64_t)__ldg(a.next_positions + b) - a.recent;
-  // rows of 32 slots: of the segment, of a warp
-  const int rows = (n + 31) / 32, per = (rows + C * 32 - 1) / (C * 32);
-  const int i0 = ((rank * 32 + warp) * per) * 32 + lane;
+  const int from = (int)max((int64_t)next - a.recent, (int64_t)INT_MIN);
+  const int rows = (n + 31) / 32, per = (rows + C * NW - 1) / (C * NW);
+  const int row0 = (rank * NW + warp) * per * 32;       // slot of the warp's first row
   bool nan = false;
-  auto read = [&](int j) {                // (slots past the end: some key, never looked at)
-    const int i = min(i0 + 32 * j, n - 1);
-    return rank_key(__ldg(wt + i), __ldg(ps + i), a.sinks, from, nan);
+  auto read = [&](int j) {
+    const int i = row0 + 32 * j + lane, at = min(i, n - 1);
+    const uint32_t k = rank_key(__ldg(wt + at), __ldg(ps + at), a.sinks, from, nan);
+    return i < n ? k : 0u;
   };
   uint32_t kept[kKeep];
 #pragma unroll
   for (int j0 = 0; j0 < kKeep; j0 += 8)
     if (j0 < per) {
-      float w[8];
+      float x[8];
       int p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = min(i0 + 32 * (j0 + j), n - 1);
-        w[j] = __ldg(wt + i);
+        const int i = min(row0 + 32 * (j0 + j) + lane, n - 1);
+        x[j] = __ldg(wt + i);
         p[j] = __ldg(ps + i);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) kept[j0 + j] = rank_key(w[j], p[j], a.sinks, from, nan);
+      for (int j = 0; j < 8; ++j) {
+        const int i = row0 + 32 * (j0 + j) + lane;
+        const uint32_t k = rank_key(x[j], p[j], a.sinks, from, nan);
+        kept[j0 + j] = i < n ? k : 0u;
+        // what is below the budget, into arrays of its own (`move` overwrites
+        // the slots that are given up)
+        if (j0 + j < per && i < keep) {
+          if (wo) wo[i] = x[j];
+          if (po) po[i] = p[j];
+        }
+      }
     }
-  // f(key, slot) for each of the warp's rows of slots in order
+  // f(key, row) for each of the warp's rows in order
   auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < kKeep; ++j)
-      if (j < per) f(kept[j], i0 + 32 * j);
-    for (int j = kKeep; j < per; ++j) f(read(j), i0 + 32 * j);
+      if (j < per) f(kept[j], j);
+    for (int j = kKeep; j < per; ++j) f(read(j), j);
   };
   __syncthreads();                        // the histograms are empty
   // ---- the keep-th largest key, digit by digit
@@ -156,39 +174,72 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
   for (int round = 0; round < 3; ++round) {
     const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
     uint32_t* const hist = sh.hist[round];
+    const uint32_t mask = (1u << bits) - 1;
     uint32_t must = 0;
-    each([&](uint32_t k, int i) {
-      const bool in = i < n && (round == 0 || (k >> (shift + bits)) == prefix);
+    each([&](uint32_t k, int) {
       // (slots that must stay are many of one key: counted apart)
-      if (in && k != ~0u) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-      if (in && k == ~0u) ++must;
+      const bool in = k != 0u && (round == 0 || (k >> (shift + bits)) == prefix);
+      if (in && k != ~0u) atomicAdd(&hist[(k >> shift) & mask], 1u);
+      must += in && k == ~0u;
     });
     must = __reduce_add_sync(0xffffffffu, must);
-    if (lane == 0 && must) atomicAdd(&hist[(1u << bits) - 1], must);
+    if (lane == 0 && must) atomicAdd(&hist[mask], must);
+    __syncthreads();
+    // sums of 64 bins first: blocks read one another's 32 of these and 64 bins
+    // (2,048 bins of 16 blocks took 5 us a digit)
+    for (int c = warp; c < 32; c += NW) {
+      const uint2 v = *reinterpret_cast<const uint2*>(hist + 64 * c + 2 * lane);
+      const uint32_t x = __reduce_add_sync(0xffffffffu, v.x + v.y);
+      if (lane == 0) sh.part[round][c] = x;
+    }
     meet();
-    // thread t holds bins kBins - 1 - 2 t and the one below, of all blocks
-    uint32_t x0 = 0, x1 = 0;
-    for (int c = 0; c < C; ++c) {
-      const uint2 v = *reinterpret_cast<const uint2*>(
-          cl.map_shared_rank(hist, c) + kBins - 2 - 2 * tid);
-      x0 += v.y;
-      x1 += v.x;
-    }
-    uint32_t incl = x0 + x1;
+    if (warp == 0) {
+      uint32_t x = 0;                     // lane l: part 31 - l, of all blocks
+      for (int c0 = 0; c0 < C; c0 += 4) { // (four blocks' on their way at once)
+        uint32_t v[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    int2 unused;
-    const int2 whole = make_int2(__shfl_sync(0xffffffffu, incl, 31), 0);
-    const uint32_t above =
-        warps_prefix(whole, sh.warp_sum[round & 1], unused).x + incl - x0 - x1;
-    if (above < left && left <= above + x0 + x1) {   // one thread
-      const bool first = left <= above + x0;
-      sh.prefix = prefix << bits | (kBins - 1 - 2 * tid - (first ? 0 : 1));
-      sh.left = left - above - (first ? 0 : x0);
-      sh.count = first ? x0 : x1;
+        for (int c = 0; c < 4; ++c)
+          v[c] = cl.map_shared_rank(&sh.part[round][0], (c0 + c) & (C - 1))[31 - lane];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x += c0 + c < C ? v[c] : 0;
+      }
+      uint32_t incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      int at = __ffs(__ballot_sync(0xffffffffu, left <= incl)) - 1;   // the first that reaches it
+      const uint32_t above = __shfl_sync(0xffffffffu, incl - x, at);
+      const int bin0 = 64 * (31 - at) + 62 - 2 * lane;  // lane's two bins, from the top down
+      uint32_t x0 = 0, x1 = 0;
+      for (int c0 = 0; c0 < C; c0 += 4) {
+        uint2 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[c] = *reinterpret_cast<const uint2*>(
+              cl.map_shared_rank(hist, (c0 + c) & (C - 1)) + bin0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x0 += c0 + c < C ? v[c].y : 0;
+          x1 += c0 + c < C ? v[c].x : 0;
+        }
+      }
+      incl = x0 + x1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      incl += above;
+      at = __ffs(__ballot_sync(0xffffffffu, left <= incl)) - 1;
+      if (lane == at) {
+        const uint32_t over = incl - x0 - x1;
+        const bool first = left <= over + x0;
+        sh.prefix = prefix << bits | (bin0 + (first ? 1 : 0));
+        sh.left = left - over - (first ? 0 : x0);
+        sh.count = first ? x0 : x1;
+      }
     }
     __syncthreads();
     prefix = sh.prefix;
@@ -203,65 +254,66 @@ __global__ void __launch_bounds__(kThreads) select(const KArgs a) {
   if (nan) flag(a.status, DS_DEV_BAD_VALUE);
   // above `prefix` all stay, and `left` of the `same` slots at it, the lower ones
   const bool ties = left < same;
-  int ties0 = 0;                 // ties before this warp's slots
+  int ties0 = 0;                          // ties before this warp's slots
   if (ties) {
     int2 v = make_int2(0, 0), total;
-    each([&](uint32_t k, int i) {
-      v.x += __popc(__ballot_sync(0xffffffffu, i < n && k == prefix));
-    });
-    ties0 = warps_prefix(v, sh.warp_sum[1], total).x;
+    each([&](uint32_t k, int) { v.x += __popc(__ballot_sync(0xffffffffu, k == prefix)); });
+    ties0 = warps_prefix<NW>(v, sh.warp_sum[1], total).x;
     if (tid == 0) sh.block_sum[0] = total;
     meet();
-    for (int c = 0; c < rank; ++c) ties0 += cl.map_shared_rank(&sh.block_sum[0], c)->x;
+    ties0 += __reduce_add_sync(
+        0xffffffffu, lane < rank ? cl.map_shared_rank(&sh.block_sum[0], lane)->x : 0);
   } else if (left > 0) {
     --prefix;                             // (all at it stay; 0 cannot be)
   }
   const uint32_t below = (1u << lane) - 1;
-  auto stays = [&](uint32_t k, int i, int& seen) {
-    bool stay = i < n && k > prefix;
+  // the row's slots that stay, as a mask
+  auto stays = [&](uint32_t k, int& seen) {
+    uint32_t m = __ballot_sync(0xffffffffu, k > prefix);
     if (ties) {
-      const bool tie = i < n && k == prefix;
-      const uint32_t all = __ballot_sync(0xffffffffu, tie);
-      stay |= tie && seen + __popc(all & below) < (int)left;
-      seen += __popc(all);
+      const uint32_t at = __ballot_sync(0xffffffffu, k == prefix);
+      m |= __ballot_sync(0xffffffffu, k == prefix && seen + __popc(at & below) < (int)left);
+      seen += __popc(at);
     }
-    return stay;
+    return m;
   };
   int2 sum = make_int2(0, 0), total;
-  int seen = ties0;
-  each([&](uint32_t k, int i) {
-    const bool stay = stays(k, i, seen);
-    sum.x += __popc(__ballot_sync(0xffffffffu, stay && i >= keep));
-    sum.y += __popc(__ballot_sync(0xffffffffu, !stay && i < keep));
+  int seen = ties0, seen_kept = 0;
+  uint32_t saved = 0;                     // lane j: row j's mask
+  each([&](uint32_t k, int j) {
+    const uint32_t m = stays(k, seen), low = first_bits(keep - row0 - 32 * j);
+    sum.x += __popc(m & ~low);
+    sum.y += __popc(~m & low);
+    if (j < kKeep) {
+      if (lane == j) saved = m;
+      seen_kept = seen;
+    }
   });
-  int2 before = warps_prefix(sum, sh.warp_sum[0], total);
+  int2 before = warps_prefix<NW>(sum, sh.warp_sum[0], total);
   if (tid == 0) sh.block_sum[1] = total;
   meet();
-  int all = 0;
-  for (int c = 0; c < C; ++c) {
-    const int2 x = *cl.map_shared_rank(&sh.block_sum[1], c);
-    if (c < rank) {
-      before.x += x.x;
-      before.y += x.y;
-    }
-    all += x.x;
-  }
+  const int2 other =
+      lane < C ? *cl.map_shared_rank(&sh.block_sum[1], lane) : make_int2(0, 0);
+  const int all = __reduce_add_sync(0xffffffffu, other.x);
+  before.x += __reduce_add_sync(0xffffffffu, lane < rank ? other.x : 0);
+  before.y += __reduce_add_sync(0xffffffffu, lane < rank ? other.y : 0);
   int32_t* src = a.src + (int64_t)seg * a.moves;
   int32_t* dst = a.dst + (int64_t)seg * a.moves;
-  seen = ties0;
-  each([&](uint32_t k, int i) {
-    const bool stay = stays(k, i, seen);
-    const uint32_t c = __ballot_sync(0xffffffffu, stay && i >= keep);
-    const uint32_t f = __ballot_sync(0xffffffffu, !stay && i < keep);
-    if (c >> lane & 1) src[before.x + __popc(c & below)] = i;
-    if (f >> lane & 1) dst[before.y + __popc(f & below)] = i;
-    before.x += __popc(c);
-    before.y += __popc(f);
-    if (stay && i < keep) {
-      if (wo) wo[i] = wt[i];
-      if (po) po[i] = ps[i];
+  seen = seen_kept;
+  for (int j = 0; j < per; ++j) {
+    const uint32_t m = j < kKeep ? __shfl_sync(0xffffffffu, saved, j) : stays(read(j), seen);
+    const int i = row0 + 32 * j + lane;
+    const uint32_t low = first_bits(keep - row0 - 32 * j);
+    const uint32_t come = m & ~low, free = ~m & low;
+    if (come >> lane & 1) src[before.x + __popc(come & below)] = i;
+    if (free >> lane & 1) dst[before.y + __popc(free & below)] = i;
+    before.x += __popc(come);
+    before.y += __popc(free);
+    if (j >= kKeep && i < keep) {
+      if (wo) wo[i] = __ldg(wt + i);
+      if (po) po[i] = __ldg(ps + i);
     }
-  });
+  }
   if (tid == 0 && rank == 0) a.count[seg] = all;
   if (C > 1) cl.sync();                   // others may still read this block's sums
 }
@@ -327,14 +379,15 @@ __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
   }
 }
 
-// Blocks of a segment's cluster: as many as fill the machine (two blocks of
-// 1024 threads on each of 152 SMs), but 2048 slots or more to each, where
-// another block costs more than it saves.
+// Blocks of a segment's cluster: segments of up to 4,096 slots take one block
+// of 256 threads, whose barriers cost less.  Longer ones take blocks of 512, as
+// many as fill the machine (two on each of 152 SMs), but with 1,024 slots or
+// more to each; more while a block's slots do not fit in its registers.
 int cluster_size(int segs, int64_t slots) {
+  if (slots <= 256 * kKeep) return 1;
   int c = 1;
-  while (c < 8 && (int64_t)segs * 2 * c <= 304 && slots / (2 * c) >= 2048) c *= 2;
-  // more while a block's slots do not fit in its registers
-  while (c < 8 && slots > (int64_t)c * kKeep * kThreads) c *= 2;
+  while (c < kCluster && (int64_t)segs * 2 * c <= 304 && slots / (2 * c) >= 1024) c *= 2;
+  while (c < kCluster && slots > (int64_t)c * kKeep * 512) c *= 2;
   return c;
 }
 
@@ -367,10 +420,17 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   a.dst = reinterpret_cast<int32_t*>(ws + L.dst);
   a.status = reinterpret_cast<uint32_t*>(ws);
   const int segs = g.batch * g.slot_heads;
+  const bool small = a.cache.slots <= 256 * kKeep;
   const int cluster = cluster_size(segs, a.cache.slots);
+  void (*const kernel)(KArgs) = small ? select<256> : select<512>;
+  cudaError_t e;
+  if (cluster > 8) {                      // larger than every device has to take
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(small ? 256 : 512);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -379,8 +439,8 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, select, a);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess || L.moves == 0) return e;
   // moves of a warp at a time, and eight blocks an SM as far as there can be moves
   const int per = std::max(1, 32 / (g.slot_heads == 1 ? g.num_kv_heads : 1));
