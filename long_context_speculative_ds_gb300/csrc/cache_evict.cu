@@ -51,12 +51,12 @@ DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan
 }
 
 // A cluster of blocks per segment; its rows of 32 slots in equal runs to the
-// warps, one behind the other.  Keys of a warp's first kKeep rows stay in
-// registers; beyond (segments of more than 16 slots a thread of the cluster)
-// they are formed anew from memory.
-constexpr int kKeep = 16;
+// warps, one behind the other.  Keys of a warp's first rows stay in shared
+// memory, as many as the launch has room for; beyond (segments of more than
+// 400,000 slots) they are formed anew from memory.
+constexpr int kMaxKeyBytes = 200 * 1024;
 constexpr int kBins = 2048;               // of a digit: 11, 11 and 10 bits
-constexpr int kCluster = 16;              // blocks, at most
+constexpr int kCluster = 8;               // blocks, at most
 
 struct Shared {
   uint32_t hist[3][kBins];
@@ -94,8 +94,9 @@ DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
 DS_DEV uint32_t first_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; }
 
 template <int T>
-__global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
+__global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int room) {
   constexpr int NW = T / 32;
+  extern __shared__ uint32_t s_keys[];    // [warp][room rows][32]
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = cl.num_blocks(), rank = cl.block_rank();
@@ -135,37 +136,35 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
     const uint32_t k = rank_key(__ldg(wt + at), __ldg(ps + at), a.sinks, from, nan);
     return i < n ? k : 0u;
   };
-  uint32_t kept[kKeep];
+  uint32_t* const mine = s_keys + warp * room * 32 + lane;
+  const int kept = min(per, room);
+  for (int j0 = 0; j0 < per; j0 += 8) {   // eight rows' loads on their way together
+    float x[8];
+    int p[8];
 #pragma unroll
-  for (int j0 = 0; j0 < kKeep; j0 += 8)
-    if (j0 < per) {
-      float x[8];
-      int p[8];
+    for (int j = 0; j < 8; ++j) {
+      const int i = min(row0 + 32 * (j0 + j) + lane, n - 1);
+      x[j] = __ldg(wt + i);
+      p[j] = __ldg(ps + i);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = min(row0 + 32 * (j0 + j) + lane, n - 1);
-        x[j] = __ldg(wt + i);
-        p[j] = __ldg(ps + i);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = row0 + 32 * (j0 + j) + lane;
-        const uint32_t k = rank_key(x[j], p[j], a.sinks, from, nan);
-        kept[j0 + j] = i < n ? k : 0u;
-        // what is below the budget, into arrays of its own (`move` overwrites
-        // the slots that are given up)
-        if (j0 + j < per && i < keep) {
-          if (wo) wo[i] = x[j];
-          if (po) po[i] = p[j];
-        }
+    for (int j = 0; j < 8; ++j) {
+      const int i = row0 + 32 * (j0 + j) + lane;
+      const uint32_t k = rank_key(x[j], p[j], a.sinks, from, nan);
+      if (j0 + j < kept) mine[32 * (j0 + j)] = i < n ? k : 0u;
+      // what is below the budget, into arrays of its own (`move` overwrites
+      // the slots that are given up)
+      if (j0 + j < per && i < keep) {
+        if (wo) wo[i] = x[j];
+        if (po) po[i] = p[j];
       }
     }
+  }
   // f(key, row) for each of the warp's rows in order
   auto each = [&](auto f) {
-#pragma unroll
-    for (int j = 0; j < kKeep; ++j)
-      if (j < per) f(kept[j], j);
-    for (int j = kKeep; j < per; ++j) f(read(j), j);
+#pragma unroll 4
+    for (int j = 0; j < kept; ++j) f(mine[32 * j], j);
+    for (int j = kept; j < per; ++j) f(read(j), j);
   };
   __syncthreads();                        // the histograms are empty
   // ---- the keep-th largest key, digit by digit
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
     if (lane == 0 && must) atomicAdd(&hist[mask], must);
     __syncthreads();
     // sums of 64 bins first: blocks read one another's 32 of these and 64 bins
-    // (2,048 bins of 16 blocks took 5 us a digit)
+    // (all bins of 16 blocks took 5 us a digit)
     for (int c = warp; c < 32; c += NW) {
       const uint2 v = *reinterpret_cast<const uint2*>(hist + 64 * c + 2 * lane);
       const uint32_t x = __reduce_add_sync(0xffffffffu, v.x + v.y);
@@ -194,14 +193,14 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
     }
     meet();
     if (warp == 0) {
-      uint32_t x = 0;                     // lane l: part 31 - l, of all blocks
-      for (int c0 = 0; c0 < C; c0 += 4) { // (four blocks' on their way at once)
-        uint32_t v[4];
+      uint32_t x = sh.part[round][31 - lane];   // lane l: part 31 - l, of all blocks
+      if (C > 1) {                        // (their loads on their way together)
+        uint32_t v[kCluster];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          v[c] = cl.map_shared_rank(&sh.part[round][0], (c0 + c) & (C - 1))[31 - lane];
+        for (int c = 1; c < kCluster; ++c)
+          v[c] = cl.map_shared_rank(&sh.part[round][0], (rank + c) & (C - 1))[31 - lane];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x += c0 + c < C ? v[c] : 0;
+        for (int c = 1; c < kCluster; ++c) x += c < C ? v[c] : 0;
       }
       uint32_t incl = x;
 #pragma unroll
@@ -212,17 +211,18 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
       int at = __ffs(__ballot_sync(0xffffffffu, left <= incl)) - 1;   // the first that reaches it
       const uint32_t above = __shfl_sync(0xffffffffu, incl - x, at);
       const int bin0 = 64 * (31 - at) + 62 - 2 * lane;  // lane's two bins, from the top down
-      uint32_t x0 = 0, x1 = 0;
-      for (int c0 = 0; c0 < C; c0 += 4) {
-        uint2 v[4];
+      const uint2 own = *reinterpret_cast<const uint2*>(hist + bin0);
+      uint32_t x0 = own.y, x1 = own.x;
+      if (C > 1) {
+        uint2 v[kCluster];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 1; c < kCluster; ++c)
           v[c] = *reinterpret_cast<const uint2*>(
-              cl.map_shared_rank(hist, (c0 + c) & (C - 1)) + bin0);
+              cl.map_shared_rank(hist, (rank + c) & (C - 1)) + bin0);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x0 += c0 + c < C ? v[c].y : 0;
-          x1 += c0 + c < C ? v[c].x : 0;
+        for (int c = 1; c < kCluster; ++c) {
+          x0 += c < C ? v[c].y : 0;
+          x1 += c < C ? v[c].x : 0;
         }
       }
       incl = x0 + x1;
@@ -277,18 +277,19 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
     }
     return m;
   };
+  // (a row's mask takes the place of its first key)
   int2 sum = make_int2(0, 0), total;
-  int seen = ties0, seen_kept = 0;
-  uint32_t saved = 0;                     // lane j: row j's mask
+  int seen = ties0, seen_kept = ties0;
   each([&](uint32_t k, int j) {
     const uint32_t m = stays(k, seen), low = first_bits(keep - row0 - 32 * j);
     sum.x += __popc(m & ~low);
     sum.y += __popc(~m & low);
-    if (j < kKeep) {
-      if (lane == j) saved = m;
+    if (j < kept) {
+      if (lane == 0) mine[32 * j] = m;
       seen_kept = seen;
     }
   });
+  __syncwarp();
   int2 before = warps_prefix<NW>(sum, sh.warp_sum[0], total);
   if (tid == 0) sh.block_sum[1] = total;
   meet();
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
   int32_t* dst = a.dst + (int64_t)seg * a.moves;
   seen = seen_kept;
   for (int j = 0; j < per; ++j) {
-    const uint32_t m = j < kKeep ? __shfl_sync(0xffffffffu, saved, j) : stays(read(j), seen);
+    const uint32_t m = j < kept ? mine[32 * j - lane] : stays(read(j), seen);
     const int i = row0 + 32 * j + lane;
     const uint32_t low = first_bits(keep - row0 - 32 * j);
     const uint32_t come = m & ~low, free = ~m & low;
@@ -309,10 +310,6 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a) {
     if (free >> lane & 1) dst[before.y + __popc(free & below)] = i;
     before.x += __popc(come);
     before.y += __popc(free);
-    if (j >= kKeep && i < keep) {
-      if (wo) wo[i] = __ldg(wt + i);
-      if (po) po[i] = __ldg(ps + i);
-    }
   }
   if (tid == 0 && rank == 0) a.count[seg] = all;
   if (C > 1) cl.sync();                   // others may still read this block's sums
@@ -379,15 +376,17 @@ __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
   }
 }
 
-// Blocks of a segment's cluster: segments of up to 4,096 slots take one block
+// Blocks of a segment's cluster.  Segments of up to 4,096 slots take one block
 // of 256 threads, whose barriers cost less.  Longer ones take blocks of 512, as
-// many as fill the machine (two on each of 152 SMs), but with 1,024 slots or
-// more to each; more while a block's slots do not fit in its registers.
+// many as fill the machine, but with 2,048 slots or more to each; more while a
+// block's keys do not fit beside another block's.  (Blocks of which only one
+// fits an SM leave no place for 16 clusters of eight at once: 16 segments of
+// 128K took two waves, 44 us.)
 int cluster_size(int segs, int64_t slots) {
-  if (slots <= 256 * kKeep) return 1;
+  if (slots <= 4096) return 1;
   int c = 1;
-  while (c < kCluster && (int64_t)segs * 2 * c <= 304 && slots / (2 * c) >= 1024) c *= 2;
-  while (c < kCluster && slots > (int64_t)c * kKeep * 512) c *= 2;
+  while (c < kCluster && (int64_t)segs * 2 * c <= 152 && slots / (2 * c) >= 2048) c *= 2;
+  while (c < kCluster && slots * 4 > (int64_t)c * kMaxKeyBytes / 3) c *= 2;
   return c;
 }
 
@@ -420,17 +419,19 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   a.dst = reinterpret_cast<int32_t*>(ws + L.dst);
   a.status = reinterpret_cast<uint32_t*>(ws);
   const int segs = g.batch * g.slot_heads;
-  const bool small = a.cache.slots <= 256 * kKeep;
-  const int cluster = cluster_size(segs, a.cache.slots);
-  void (*const kernel)(KArgs) = small ? select<256> : select<512>;
-  cudaError_t e;
-  if (cluster > 8) {                      // larger than every device has to take
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+  const bool small = a.cache.slots <= 4096;
+  const int cluster = cluster_size(segs, a.cache.slots), warps_of = small ? 8 : 16;
+  void (*const kernel)(KArgs, int) = small ? select<256> : select<512>;
+  // rows of 32 keys that a warp has room for
+  const int64_t need = (a.cache.slots + 32 * cluster * warps_of - 1) / (32 * cluster * warps_of);
+  const int room = (int)std::min<int64_t>(need, kMaxKeyBytes / (128 * warps_of));
+  const size_t smem = (size_t)room * 128 * warps_of;
+  cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * cluster));
-  cfg.blockDim = dim3(small ? 256 : 512);
+  cfg.blockDim = dim3(warps_of * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -440,7 +441,7 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, a, room);
   if (e != cudaSuccess || L.moves == 0) return e;
   // moves of a warp at a time, and eight blocks an SM as far as there can be moves
   const int per = std::max(1, 32 / (g.slot_heads == 1 ? g.num_kv_heads : 1));
