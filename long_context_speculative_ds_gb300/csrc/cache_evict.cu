@@ -138,31 +138,58 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   };
   uint32_t* const mine = s_keys + warp * room * 32 + lane;
   const int kept = min(per, room);
-  for (int j0 = 0; j0 < per; j0 += 8) {   // eight rows' loads on their way together
-    float x[8];
-    int p[8];
+  // Eight rows' loads on their way together, the next eight's behind them; what
+  // is below the budget goes into arrays of its own at once (`move` overwrites
+  // the slots that are given up).
+  float x[8];
+  int p[8];
+  auto fetch = [&](int j0) {
+    const int i0 = row0 + 32 * j0 + lane;
+    const float* const xs = wt + i0;
+    const int32_t* const qs = ps + i0;
+    if (row0 + 32 * (j0 + 8) <= n) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = min(row0 + 32 * (j0 + j) + lane, n - 1);
-      x[j] = __ldg(wt + i);
-      p[j] = __ldg(ps + i);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = row0 + 32 * (j0 + j) + lane;
-      const uint32_t k = rank_key(x[j], p[j], a.sinks, from, nan);
-      if (j0 + j < kept) mine[32 * (j0 + j)] = i < n ? k : 0u;
-      // what is below the budget, into arrays of its own (`move` overwrites
-      // the slots that are given up)
-      if (j0 + j < per && i < keep) {
-        if (wo) wo[i] = x[j];
-        if (po) po[i] = p[j];
+      for (int j = 0; j < 8; ++j) {
+        x[j] = __ldg(xs + 32 * j);
+        p[j] = __ldg(qs + 32 * j);
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < n) {
+          x[j] = __ldg(xs + 32 * j);
+          p[j] = __ldg(qs + 32 * j);
+        }
     }
+  };
+  fetch(0);
+  for (int j0 = 0; j0 < per; j0 += 8) {
+    const int i0 = row0 + 32 * j0 + lane;
+    uint32_t k[8];
+    if ((wo || po) && row0 + 32 * j0 < keep) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < per && i0 + 32 * j < keep) {
+          if (wo) wo[i0 + 32 * j] = x[j];
+          if (po) po[i0 + 32 * j] = p[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = j0 + j < per && i0 + 32 * j < n;
+      bool none = false;
+      k[j] = rank_key(x[j], p[j], a.sinks, from, none);
+      nan |= none && in;
+      if (!in) k[j] = 0u;
+    }
+    if (j0 + 8 < per) fetch(j0 + 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < kept) mine[32 * (j0 + j)] = k[j];
   }
   // f(key, row) for each of the warp's rows in order
   auto each = [&](auto f) {
-#pragma unroll 4
+#pragma unroll 8
     for (int j = 0; j < kept; ++j) f(mine[32 * j], j);
     for (int j = kept; j < per; ++j) f(read(j), j);
   };
@@ -300,17 +327,20 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   before.y += __reduce_add_sync(0xffffffffu, lane < rank ? other.y : 0);
   int32_t* src = a.src + (int64_t)seg * a.moves;
   int32_t* dst = a.dst + (int64_t)seg * a.moves;
+  src += before.x;
+  dst += before.y;
+  auto list = [&](uint32_t m, int j) {
+    const int i = row0 + 32 * j;
+    const uint32_t low = first_bits(keep - i), come = m & ~low, free = ~m & low;
+    if (come >> lane & 1) src[__popc(come & below)] = i + lane;
+    if (free >> lane & 1) dst[__popc(free & below)] = i + lane;
+    src += __popc(come);
+    dst += __popc(free);
+  };
+#pragma unroll 8
+  for (int j = 0; j < kept; ++j) list(mine[32 * j - lane], j);
   seen = seen_kept;
-  for (int j = 0; j < per; ++j) {
-    const uint32_t m = j < kept ? mine[32 * j - lane] : stays(read(j), seen);
-    const int i = row0 + 32 * j + lane;
-    const uint32_t low = first_bits(keep - row0 - 32 * j);
-    const uint32_t come = m & ~low, free = ~m & low;
-    if (come >> lane & 1) src[before.x + __popc(come & below)] = i;
-    if (free >> lane & 1) dst[before.y + __popc(free & below)] = i;
-    before.x += __popc(come);
-    before.y += __popc(free);
-  }
+  for (int j = kept; j < per; ++j) list(stays(read(j), seen), j);
   if (tid == 0 && rank == 0) a.count[seg] = all;
   if (C > 1) cl.sync();                   // others may still read this block's sums
 }
