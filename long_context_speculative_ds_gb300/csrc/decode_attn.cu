@@ -567,110 +567,192 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins (max, sum) pairs over the warp.
-DS_DEV float2 join_ml(float2 x) {
-  const float M = warp_max(x.x);
-  const float ref = M == -CUDART_INF_F ? 0.f : M;
-  return make_float2(M, warp_sum(x.y * exp2f(x.x - ref)));
+// (max, sum) of two parts of a row.
+DS_DEV float2 join_ml(float2 x, float2 y) {
+  const float M = fmaxf(x.x, y.x), ref = M == -CUDART_INF_F ? 0.f : M;
+  return make_float2(M, x.y * ptx::ex2(x.x - ref) + y.y * ptx::ex2(y.x - ref));
 }
-// (max, sum) of a row over its pieces; all lanes of a warp.
-DS_DEV float2 row_ml(const KArgs& a, int2 d, int row) {
-  float2 ml = make_float2(-CUDART_INF_F, 0.f);
-  for (int i = threadIdx.x & 31; i < d.y; i += 32) {
-    const float2 x = a.part_ml[(int64_t)(d.x + i) * a.group + row];
-    const float M = fmaxf(ml.x, x.x), ref = M == -CUDART_INF_F ? 0.f : M;
-    ml = make_float2(M, ml.y * exp2f(ml.x - ref) + x.y * exp2f(x.x - ref));
-  }
-  return join_ml(ml);
+// Joined over N neighbouring lanes.
+template <int N>
+DS_DEV float2 join_lanes(float2 x) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1)
+    x = join_ml(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o),
+                               __shfl_xor_sync(0xffffffffu, x.y, o)));
+  return x;
 }
 
 constexpr int kFinishWarps = 8;
-constexpr int kSpan = 1024;     // slots of a weights item
+constexpr int kFinishThreads = 32 * kFinishWarps;
 
+// An output row, by a warp: lane l has values 4 l .. 4 l + 3 (2 l at D = 64) of
+// eight pieces on their way at once.
 template <int D>
-__global__ void __launch_bounds__(32 * kFinishWarps) finish(const KArgs a, int row_blocks,
-                                                            int spans) {
-  __shared__ float s_ref[16];
+DS_DEV void finish_row(const KArgs& a, int64_t row) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31, G = a.group;
+  const int b = (int)(row / a.hq), hq = (int)(row % a.hq), h = hq / G, g = hq % G;
+  const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
+  float o[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) o[k] = 0.f;
+  float lse = -CUDART_INF_F;
+  if (n > 0) {
+    const int2 d = a.desc[b * a.hkv + h];
+    const float2* ml = a.part_ml + (int64_t)d.x * G + g;
+    const float* po = a.part_o + ((int64_t)d.x * G + g) * D + lane * V;
+    float2 all = make_float2(-CUDART_INF_F, 0.f);
+    for (int i0 = 0; i0 < d.y; i0 += 32) {        // 32 pieces, a lane each
+      const int m = min(32, d.y - i0);
+      float2 x = make_float2(-CUDART_INF_F, 0.f);
+      if (lane < m) x = ml[(int64_t)(i0 + lane) * G];
+      const float2 now = join_ml(all, join_lanes<32>(x));
+      const float ref = now.x == -CUDART_INF_F ? 0.f : now.x;
+      const float f = ptx::ex2(x.x - ref), old = ptx::ex2(all.x - ref);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] *= old;
+      for (int i = 0; i < m; i += 8) {
+        float v[8][V];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float* p = po + (int64_t)(i0 + min(i + j, m - 1)) * G * D;
+          if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            v[j][0] = y.x; v[j][1] = y.y; v[j][2] = y.z; v[j][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            v[j][0] = y.x; v[j][1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float w = i + j < m ? __shfl_sync(0xffffffffu, f, i + j) : 0.f;
+#pragma unroll
+          for (int k = 0; k < V; ++k)
+            if (i + j < m) o[k] = fmaf(w, v[j][k], o[k]);
+        }
+      }
+      all = now;
+    }
+    const float inv = 1.f / all.y;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[k] *= inv;
+    lse = (all.x + log2f(all.y)) * 0.6931471805599453f;
+  }
+  if (a.lse && lane == 0) a.lse[row] = lse;
+  const int64_t at = row * D + lane * V;
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    if (a.out_type == 2)
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + k) = make_float2(o[k], o[k + 1]);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + k) =
+          a.out_type == 0 ? ptx::pack_bf16x2(o[k], o[k + 1]) : ptx::pack_f16x2(o[k], o[k + 1]);
+  }
+}
+
+// Logits of rows g0 .. g0 + 3 of a slot's G, in a piece as wide as G allows;
+// rows past the last repeat it.
+DS_DEV void load_logits(float (&s)[4], const float* p, int g0, int G) {
+  if ((G & 3) == 0) {
+    const float4 v = *reinterpret_cast<const float4*>(p + g0);
+    s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = p[min(g0 + j, G - 1)];
+  }
+}
+
+// Output rows (the first blocks), and the weights of SLOTS x 256 slots of a
+// (sequence, slot head) a time: the rows whose weights a slot sums go in chunks
+// of up to four of one kv head, CHUNKS at once, so that a thread has 16 loads
+// on its way beside the rows' own sums, which eight lanes join a row.
+template <int D, int SLOTS, int CHUNKS>
+__global__ void __launch_bounds__(kFinishThreads, 2) finish(const KArgs a, int row_blocks) {
+  __shared__ float s_ref[32];
+  constexpr int SPAN = SLOTS * kFinishThreads;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.group;
+  const int tid = threadIdx.x, G = a.group;
   if ((int)blockIdx.x < row_blocks) {     // a warp per output row
-    const int64_t row = (int64_t)blockIdx.x * kFinishWarps + warp;
-    if (row >= (int64_t)a.batch * a.hq) return;
-    const int b = (int)(row / a.hq), hq = (int)(row % a.hq), h = hq / G, g = hq % G;
-    const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
-    float o[D / 32];
-    float2 ml = make_float2(-CUDART_INF_F, 0.f);
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
-    if (n > 0) {
-      const int2 d = a.desc[b * a.hkv + h];
-      ml = row_ml(a, d, g);
-      const float ref = ml.x == -CUDART_INF_F ? 0.f : ml.x;
-      for (int i = 0; i < d.y; ++i) {
-        const int64_t p = (int64_t)(d.x + i) * G + g;
-        const float f = exp2f(a.part_ml[p].x - ref);
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          o[k] = fmaf(f, a.part_o[p * D + lane * (D / 32) + k], o[k]);
-      }
-      const float inv = 1.f / ml.y;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) o[k] *= inv;
-    }
-    if (a.lse && lane == 0)
-      a.lse[row] = n > 0 ? (ml.x + log2f(ml.y)) * 0.6931471805599453f : -CUDART_INF_F;
-    const int64_t at = row * D + lane * (D / 32);
-#pragma unroll
-    for (int k = 0; k < D / 32; k += 2) {
-      if (a.out_type == 2)
-        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + k) =
-            make_float2(o[k], o[k + 1]);
-      else
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + k) =
-            a.out_type == 0 ? ptx::pack_bf16x2(o[k], o[k + 1]) : ptx::pack_f16x2(o[k], o[k + 1]);
-    }
+    const int64_t row = (int64_t)blockIdx.x * kFinishWarps + (tid >> 5);
+    if (row < (int64_t)a.batch * a.hq) finish_row<D>(a, row);
     return;
   }
-  // the others: weights of up to kSpan slots of a (sequence, slot head)
+  const int64_t spans = (a.cache.slots + SPAN - 1) / SPAN;
   const int64_t items = (int64_t)a.batch * a.slot_heads * spans;
+  const int per_head = (G + 3) / 4;       // chunks
+  const int chunks = per_head * (a.slot_heads == 1 ? a.hkv : 1);
   for (int64_t it = blockIdx.x - row_blocks; it < items; it += gridDim.x - row_blocks) {
     const int64_t bw = it / spans;
-    const int b = (int)(bw / a.slot_heads), w = (int)(bw % a.slot_heads);
+    const int b = (int)(bw / a.slot_heads);
     const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
-    const int64_t t0 = (it % spans) * kSpan;
-    if (t0 >= n) continue;
+    const int64_t start = (it % spans) * SPAN;
+    if (start >= n) continue;
+    const int t0 = (int)start + tid;
     const Range r = range_of(n, a.window, a.sinks);
-    float sum[kSpan / (32 * kFinishWarps)];
-    const int64_t at = bw * a.slot_stride + t0;
+    const int64_t seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
+    auto slot = [&](int k) { return min(t0 + k * kFinishThreads, n - 1); };   // (past the end: unused)
+    const int64_t at = bw * a.slot_stride;
+    float sum[SLOTS];
+    for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
+      float s[CHUNKS][SLOTS][4];
 #pragma unroll
-    for (int k = 0; k < kSpan / (32 * kFinishWarps); ++k) {
-      const int t = k * 32 * kFinishWarps + threadIdx.x;
-      sum[k] = a.w_in && t0 + t < n ? a.w_in[at + t] * a.decay : 0.f;
-    }
-    for (int h = a.slot_heads == 1 ? 0 : w; h < (a.slot_heads == 1 ? a.hkv : w + 1); ++h) {
-      const int seg = b * a.hkv + h;
-      __syncthreads();
-      const int2 d = a.desc[seg];
-      for (int g = warp; g < G; g += kFinishWarps) {
-        const float2 ml = row_ml(a, d, g);
-        if (lane == 0) s_ref[g] = ml.x + log2f(ml.y);
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int ch = min(c0 + c, chunks - 1);
+        const float* p = a.logits + (seg0 + ch / per_head) * a.cache.slots * G;
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k)
+          load_logits(s[c][k], p + (int64_t)slot(k) * G, ch % per_head * 4, G);
+      }
+      if (c0 == 0) {
+#pragma unroll
+        for (int k = 0; k < SLOTS; ++k) sum[k] = a.w_in ? a.w_in[at + slot(k)] * a.decay : 0.f;
+      }
+      __syncthreads();                    // the last ones' sums are used
+      {
+        const int i = tid / 8, ch = min(c0 + i / 4, chunks - 1), g = ch % per_head * 4 + i % 4;
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
+        if (row) {
+          const int2 d = a.desc[seg0 + ch / per_head];
+          const float2* p = a.part_ml + (int64_t)d.x * G + g;
+          for (int j = tid & 7; j < d.y; j += 8) ml = join_ml(ml, p[(int64_t)j * G]);
+        }
+        ml = join_lanes<8>(ml);
+        // (no row: a sum of infinity, weights of zero)
+        if (i < 32 && (tid & 7) == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kSpan / (32 * kFinishWarps); ++k) {
-        const int t = (int)t0 + k * 32 * kFinishWarps + threadIdx.x;
-        if (!visible(r, t)) continue;
-        const float* s = a.logits + ((int64_t)seg * a.cache.slots + t) * G;
-        for (int g = 0; g < G; ++g) sum[k] += exp2f(s[g] - s_ref[g]);
-      }
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float ref = s_ref[4 * c + j];
+          if (ref != CUDART_INF_F) {
+#pragma unroll
+            for (int k = 0; k < SLOTS; ++k) {
+              const float p = ptx::ex2(s[c][k][j] - ref);
+              sum[k] += visible(r, slot(k)) ? p : 0.f;
+            }
+          }
+        }
     }
 #pragma unroll
-    for (int k = 0; k < kSpan / (32 * kFinishWarps); ++k) {
-      const int t = k * 32 * kFinishWarps + threadIdx.x;
-      if (t0 + t < n) a.w_out[at + t] = sum[k];
-    }
+    for (int k = 0; k < SLOTS; ++k)
+      if (t0 + k * kFinishThreads < n) a.w_out[at + t0 + k * kFinishThreads] = sum[k];
   }
+}
+
+template <int D, int SLOTS, int CHUNKS>
+cudaError_t launch_finish(const KArgs& a, cudaStream_t stream) {
+  const int row_blocks = (int)(((int64_t)a.batch * a.hq + kFinishWarps - 1) / kFinishWarps);
+  const int span = SLOTS * kFinishThreads;
+  const int64_t items =
+      a.w_out ? (int64_t)a.batch * a.slot_heads * ((a.cache.slots + span - 1) / span) : 0;
+  const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 4);
+  return launch_dependent(finish<D, SLOTS, CHUNKS>, dim3(grid), dim3(kFinishThreads), 0, stream, a,
+                          row_blocks);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -762,12 +844,15 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
                           : (bf ? launch_split<64, true, 2>(a, g, L.ctas, stream)
                                 : launch_split<64, false, 2>(a, g, L.ctas, stream));
   if (e != cudaSuccess) return e;
-  const int row_blocks = (int)(((int64_t)g.batch * a.hq + kFinishWarps - 1) / kFinishWarps);
-  const int spans = (int)((a.cache.slots + kSpan - 1) / kSpan);
-  const int64_t items = g.weights_out ? (int64_t)g.batch * g.slot_heads * spans : 0;
-  const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 8);
-  return launch_dependent(g.head_dim == 128 ? finish<128> : finish<64>, dim3(grid),
-                          dim3(32 * kFinishWarps), 0, stream, a, row_blocks, spans);
+  // chunks of up to four rows whose weights a slot sums
+  const int chunks = (a.group + 3) / 4 * (a.slot_heads == 1 ? a.hkv : 1);
+  if (g.head_dim == 128)
+    return chunks == 1  ? launch_finish<128, 16, 1>(a, stream)
+           : chunks < 8 ? launch_finish<128, 4, 4>(a, stream)
+                        : launch_finish<128, 2, 8>(a, stream);
+  return chunks == 1  ? launch_finish<64, 16, 1>(a, stream)
+         : chunks < 8 ? launch_finish<64, 4, 4>(a, stream)
+                      : launch_finish<64, 2, 8>(a, stream);
 }
 
 }  // namespace ds
