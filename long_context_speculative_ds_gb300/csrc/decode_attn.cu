@@ -34,6 +34,7 @@ struct KArgs {
   DraftCache cache;
   const int32_t* lens;
   int32_t batch, hq, hkv, group;
+  int32_t resident;             // blocks that run at once
   int32_t window, sinks;
   float scale;                  // softmax scale times log2 e
   void* out;
@@ -73,12 +74,16 @@ DS_DEV bool visible(const Range& r, int t) {
   return t < r.n && (t < r.sinks || t >= r.start);
 }
 
-// A block's range of the axis on which the segments' tiles lie one behind the
-// other, each segment behind a lead-in that stands for what its start and end
-// cost, so that many short segments weigh what they take.
+// The axis on which the segments' tiles lie one behind the other, each segment
+// behind a lead-in that stands for what its start and end cost, is cut into
+// ranges, one a block.  Two blocks are resident on an SM.  SMs differ by some
+// 10 % in what they get of the memory's bandwidth, so the first blocks, as many
+// as are resident, take 8/10 of the axis, and twice as many small ones the rest,
+// which go to the SMs that are done first.
 constexpr int kLead = 1;
-constexpr int kWarps = 8;                     // warps that compute
+constexpr int kWarps = 4;                     // warps that compute
 constexpr int kThreads = 32 * (kWarps + 1);   // and one that loads
+constexpr int kFewUnits = 16;                 // of a large range, for small ones to pay
 
 struct Walk {
   int64_t pos, left;            // start of the segment on the axis; units of the range to go
@@ -88,8 +93,23 @@ struct Walk {
 
 struct Plan {
   Walk first;
-  int64_t quot, rem;            // blocks below rem have quot + 1 units, the others quot
+  int64_t units;
+  int large, small;             // ranges of each size
 };
+
+// First unit of range i: a large range weighs 8, a small one 1.
+DS_DEV int64_t range_start(const Plan& p, int i) {
+  const int64_t w = 8ll * min(i, p.large) + max(i - p.large, 0);
+  return p.units * w / (8ll * p.large + p.small);
+}
+// The range that unit u lies in.
+DS_DEV int range_with(const Plan& p, int64_t u) {
+  const int64_t w = u * (8ll * p.large + p.small) / p.units;
+  int i = (int)(w < 8ll * p.large ? w / 8 : p.large + (w - 8ll * p.large));
+  while (i > 0 && range_start(p, i) > u) --i;
+  while (i + 1 < p.large + p.small && range_start(p, i + 1) <= u) ++i;
+  return i;
+}
 
 struct Piece {
   Range r;
@@ -97,11 +117,6 @@ struct Piece {
   int t0, t1;                   // tiles
   int64_t pos;                  // of the segment
 };
-
-DS_DEV int64_t block_of(const Plan& p, int64_t u) {
-  const int64_t cut = p.rem * (p.quot + 1);
-  return u < cut ? u / (p.quot + 1) : p.rem + (u - cut) / p.quot;
-}
 
 DS_DEV Range seq_range(const KArgs& a, int b, bool report) {
   return range_of(checked_len(__ldg(a.lens + b), a.cache.slots, a.status, report), a.window,
@@ -136,10 +151,15 @@ DS_DEV bool make_plan(const KArgs& a, Plan& plan, int64_t (*s_sum)[2]) {
     all += s_sum[w][0];
     all_tiles += s_sum[w][1];
   }
-  const int64_t blocks = min((int64_t)gridDim.x, all_tiles);
-  if ((int64_t)blockIdx.x >= blocks) return false;
-  const int64_t quot = all / blocks, rem = all - quot * blocks;
-  const int64_t lo = blockIdx.x * quot + min((int64_t)blockIdx.x, rem);
+  Plan p;
+  p.units = all;
+  p.large = (int)min((int64_t)min(a.resident, (int)gridDim.x), all_tiles);
+  p.small = (int)gridDim.x - p.large;
+  // small ranges only when all blocks have some tiles
+  if (p.small > 2 * p.large) p.small = 2 * p.large;
+  if (all < (int64_t)kFewUnits * p.large) p.small = 0;
+  if ((int)blockIdx.x >= p.large + p.small) return false;
+  const int64_t lo = range_start(p, blockIdx.x);
   if (before <= lo && lo < before + units) {  // one thread
     int b = b0;
     int64_t len = 0, off = lo - before;
@@ -153,9 +173,10 @@ DS_DEV bool make_plan(const KArgs& a, Plan& plan, int64_t (*s_sum)[2]) {
     plan.first.h = (int)(off / len);
     plan.first.off = off - plan.first.h * len;
     plan.first.pos = lo - plan.first.off;
-    plan.first.left = quot + ((int64_t)blockIdx.x < rem ? 1 : 0);
-    plan.quot = quot;
-    plan.rem = rem;
+    plan.first.left = range_start(p, blockIdx.x + 1) - lo;
+    plan.units = p.units;
+    plan.large = p.large;
+    plan.small = p.small;
   }
   __syncthreads();
   return true;
@@ -245,40 +266,38 @@ DS_DEV void split2(float lo, float hi, uint32_t& big, uint32_t& rest) {
   rest = pack2<BF>(lo - b.x, hi - b.y);
 }
 
-template <int D, int NT>
+template <int D>
 struct Cfg {
-  static constexpr int R = 8 * NT;                      // query rows
   static constexpr int kSubBytes = 16 * D * 2;          // 16 keys of K or V
   static constexpr int kStage = 2 * 4 * kSubBytes;      // a tile's K and V
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 6 : 5) : 11;
-  static constexpr size_t smem = 1024 + (size_t)kStages * kStage + kWarps * R * D * 4;
-  static_assert(smem + 1900 <= 232448, "ring and outputs within a block's shared memory");
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  // ring, and the warps' outputs of eight rows
+  static constexpr size_t smem = (size_t)kStages * kStage + kWarps * 8 * D * 4;
   // where value d of a row lies among the D of a warp's output row (rows turned
   // so that the four rows that a warp writes at once fall into different banks)
   static DS_DEV int turned(int row, int d) { return (d + 8 * (row >> 1)) & (D - 1); }
 };
 
-// (the header's fields come out of the block's static shared memory)
 struct Shared {
-  alignas(8) uint64_t full[16], empty[16];
+  alignas(8) uint64_t full[6], empty[6];
   Plan plan;
   int64_t sum[kWarps + 1][2];
-  float m[kWarps][16], l[kWarps][16];
+  float m[kWarps][8], l[kWarps][8];
   int abort;
 };
-static_assert(sizeof(Shared) <= 1900, "");
+static_assert(2 * (Cfg<128>::smem + sizeof(Shared) + 1024 + 16) <= 233472, "two blocks an SM");
 
 template <int D, bool BF, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     split(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
           const KArgs a, const int hnd) {
   using namespace ptx;
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   constexpr int S = C::kStages;
-  extern __shared__ unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char raw[];
   __shared__ Shared sh;
-  const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
-  float* const merge = reinterpret_cast<float*>(raw + (ring - smem_addr(raw)) + S * C::kStage);
+  const uint32_t ring = smem_addr(raw);
+  float* const merge = reinterpret_cast<float*>(raw + S * C::kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -363,10 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // ---- the others: warps 0 to 3 and 4 to 7 take tiles in turn, a warp 16 keys
+  // ---- the others: a warp takes 16 keys of every tile
   const int g = lane >> 2, t4 = lane & 3, G = a.group;
-  const int sub = warp & 3, team = warp >> 2;
-  int turn = 0;
+  const int sub = warp;
   // ldmatrix: this lane's row of K (keys 0-15, 8 channels a chunk) and of V
   const int krow = (lane & 7) + ((lane >> 3) & 1) * 8, kchunk = lane >> 4;
   const int vrow = (lane & 7) + (lane >> 4) * 8, vchunk = (lane >> 3) & 1;
@@ -400,10 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][d][j] = 0.f;
     }
-    for (int t = pc.t0; t < pc.t1; ++t, turn ^= 1) {
+    for (int t = pc.t0; t < pc.t1; ++t) {
       const int st = stage, ph = phase;
       if (++stage == S) { stage = 0; phase ^= 1; }
-      if (turn != team) continue;
       const bool ok = mbar_wait(smem_addr(&sh.full[st]), ph, abort);
       const int k0 = tile_slot(r, t) + 16 * sub;
       if (__all_sync(0xffffffffu, ok) && k0 < r.n && (k0 < r.sinks || k0 + 16 > r.start)) {
@@ -510,19 +527,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
     }
-    // ---- the warps' outputs joined, into the piece's place
+    // ---- the warps' outputs joined, eight rows at a time, into the piece's place
+    const int64_t piece = blockIdx.x + seg;
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) l[i][j] += __shfl_xor_sync(0xffffffffu, l[i][j], x);
-    float* const mine = merge + warp * C::R * D;
+    float* const mine = merge + warp * 8 * D;
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int row = 8 * i + 2 * t4 + j;
+        const int row = 2 * t4 + j;
         if (g == 0) {
           sh.m[warp][row] = m[i][j];
           sh.l[warp][row] = l[i][j];
@@ -533,37 +551,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           mine[row * D + C::turned(row, d * 16 + g + 8)] = o[i][d][2 + j];
         }
       }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-    const int64_t u = pc.pos + kLead;         // the segment's first tile on the axis
-    const int64_t piece = blockIdx.x + seg;
-    for (int i = tid; i < G * D / 4; i += 32 * kWarps) {
-      const int row = i / (D / 4), c = i % (D / 4);
-      float M = -CUDART_INF_F;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+      for (int x = tid; x < min(8, G - 8 * i) * D / 4; x += 32 * kWarps) {
+        const int row = x / (D / 4), c = x % (D / 4);
+        float M = -CUDART_INF_F;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][row]);
-      const float ref = M == -CUDART_INF_F ? 0.f : M;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float total = 0.f;
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][row]);
+        const float ref = M == -CUDART_INF_F ? 0.f : M;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(sh.m[w][row] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(
-            merge + (w * C::R + row) * D + C::turned(row, c * 4));
-        sum.x = fmaf(f, x.x, sum.x);
-        sum.y = fmaf(f, x.y, sum.y);
-        sum.z = fmaf(f, x.z, sum.z);
-        sum.w = fmaf(f, x.w, sum.w);
-        total = fmaf(f, sh.l[w][row], total);
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(sh.m[w][row] - ref);
+          const float4 y = *reinterpret_cast<const float4*>(
+              merge + (w * 8 + row) * D + C::turned(row, c * 4));
+          sum.x = fmaf(f, y.x, sum.x);
+          sum.y = fmaf(f, y.y, sum.y);
+          sum.z = fmaf(f, y.z, sum.z);
+          sum.w = fmaf(f, y.w, sum.w);
+          total = fmaf(f, sh.l[w][row], total);
+        }
+        *reinterpret_cast<float4*>(a.part_o + ((piece * G + 8 * i + row) * D + c * 4)) = sum;
+        if (c == 0) a.part_ml[piece * G + 8 * i + row] = make_float2(M, total);
       }
-      *reinterpret_cast<float4*>(a.part_o + ((piece * G + row) * D + c * 4)) = sum;
-      if (c == 0) a.part_ml[piece * G + row] = make_float2(M, total);
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     }
-    if (tid == 0 && pc.t0 == 0) {             // numbered by block and segment, which never
-      const int64_t f = block_of(sh.plan, u); // both stand still, pieces have places of their own
-      a.desc[seg] = make_int2((int)(f + seg),
-                              (int)(block_of(sh.plan, u + r.tiles - 1) - f + 1));
+    if (tid == 0 && pc.t0 == 0) {             // numbered by range and segment, which never
+      const int64_t u = pc.pos + kLead;       // both stand still, pieces have places of their own
+      const int f = range_with(sh.plan, u);   // (u: the segment's first tile on the axis)
+      a.desc[seg] = make_int2((int)(f + seg), range_with(sh.plan, u + r.tiles - 1) - f + 1);
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
   }
 }
 
@@ -585,25 +602,28 @@ DS_DEV float2 join_lanes(float2 x) {
 constexpr int kFinishWarps = 8;
 constexpr int kFinishThreads = 32 * kFinishWarps;
 
-// An output row, by a warp: lane l has values 4 l .. 4 l + 3 (2 l at D = 64) of
-// eight pieces on their way at once.
+// An output row by WPR warps, which share its pieces: lane l has values 4 l ..
+// 4 l + 3 (2 l at D = 64) of eight pieces on their way at once.
 template <int D>
-DS_DEV void finish_row(const KArgs& a, int64_t row) {
+DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const int parts,
+                       float (*s_o)[D], float2* s_ml) {
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31, G = a.group;
-  const int b = (int)(row / a.hq), hq = (int)(row % a.hq), h = hq / G, g = hq % G;
-  const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
+  const bool real = row < (int64_t)a.batch * a.hq;
+  const int b = real ? (int)(row / a.hq) : 0, hq = real ? (int)(row % a.hq) : 0;
+  const int h = hq / G, g = hq % G;
+  const int n = real ? checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false) : 0;
   float o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.f;
-  float lse = -CUDART_INF_F;
+  float2 all = make_float2(-CUDART_INF_F, 0.f);
   if (n > 0) {
     const int2 d = a.desc[b * a.hkv + h];
+    const int p0 = (int)((int64_t)d.y * part / parts), p1 = (int)((int64_t)d.y * (part + 1) / parts);
     const float2* ml = a.part_ml + (int64_t)d.x * G + g;
     const float* po = a.part_o + ((int64_t)d.x * G + g) * D + lane * V;
-    float2 all = make_float2(-CUDART_INF_F, 0.f);
-    for (int i0 = 0; i0 < d.y; i0 += 32) {        // 32 pieces, a lane each
-      const int m = min(32, d.y - i0);
+    for (int i0 = p0; i0 < p1; i0 += 32) {        // 32 pieces, a lane each
+      const int m = min(32, p1 - i0);
       float2 x = make_float2(-CUDART_INF_F, 0.f);
       if (lane < m) x = ml[(int64_t)(i0 + lane) * G];
       const float2 now = join_ml(all, join_lanes<32>(x));
@@ -626,7 +646,7 @@ DS_DEV void finish_row(const KArgs& a, int64_t row) {
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float w = i + j < m ? __shfl_sync(0xffffffffu, f, i + j) : 0.f;
+          const float w = __shfl_sync(0xffffffffu, f, (i + j) & 31);
 #pragma unroll
           for (int k = 0; k < V; ++k)
             if (i + j < m) o[k] = fmaf(w, v[j][k], o[k]);
@@ -634,12 +654,31 @@ DS_DEV void finish_row(const KArgs& a, int64_t row) {
       }
       all = now;
     }
+  }
+  if (parts > 1) {                        // the whole block works on this row
+    const int warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_o[warp][lane * V + k] = o[k];
+    if (lane == 0) s_ml[warp] = all;
+    __syncthreads();
+    if (part > 0) return;
+    for (int w = 1; w < parts; ++w) {
+      const float2 x = s_ml[w], now = join_ml(all, x);
+      const float ref = now.x == -CUDART_INF_F ? 0.f : now.x;
+      const float f = ptx::ex2(x.x - ref), old = ptx::ex2(all.x - ref);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] = fmaf(f, s_o[w][lane * V + k], o[k] * old);
+      all = now;
+    }
+  }
+  if (!real) return;
+  if (n > 0) {
     const float inv = 1.f / all.y;
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] *= inv;
-    lse = (all.x + log2f(all.y)) * 0.6931471805599453f;
   }
-  if (a.lse && lane == 0) a.lse[row] = lse;
+  if (a.lse && lane == 0)
+    a.lse[row] = n > 0 ? (all.x + log2f(all.y)) * 0.6931471805599453f : -CUDART_INF_F;
   const int64_t at = row * D + lane * V;
 #pragma unroll
   for (int k = 0; k < V; k += 2) {
@@ -666,93 +705,104 @@ DS_DEV void load_logits(float (&s)[4], const float* p, int g0, int G) {
 // Output rows (the first blocks), and the weights of SLOTS x 256 slots of a
 // (sequence, slot head) a time: the rows whose weights a slot sums go in chunks
 // of up to four of one kv head, CHUNKS at once, so that a thread has 16 loads
-// on its way beside the rows' own sums, which eight lanes join a row.
+// on its way beside the rows' own sums, which 8 to 32 lanes join a row.  With
+// CHUNKS 0 there are output rows only.
 template <int D, int SLOTS, int CHUNKS>
-__global__ void __launch_bounds__(kFinishThreads, 2) finish(const KArgs a, int row_blocks) {
+__global__ void __launch_bounds__(kFinishThreads, CHUNKS ? 2 : 4)
+    finish(const KArgs a, const int row_blocks, const int parts) {
   __shared__ float s_ref[32];
-  constexpr int SPAN = SLOTS * kFinishThreads;
+  __shared__ float s_o[kFinishWarps][D];
+  __shared__ float2 s_ml[kFinishWarps];
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int tid = threadIdx.x, G = a.group;
-  if ((int)blockIdx.x < row_blocks) {     // a warp per output row
-    const int64_t row = (int64_t)blockIdx.x * kFinishWarps + (tid >> 5);
-    if (row < (int64_t)a.batch * a.hq) finish_row<D>(a, row);
+  if (CHUNKS == 0 || (int)blockIdx.x < row_blocks) {      // `parts` warps per output row
+    const int w = blockIdx.x * kFinishWarps + (tid >> 5);
+    finish_row<D>(a, w / parts, w % parts, parts, s_o, s_ml);
     return;
   }
-  const int64_t spans = (a.cache.slots + SPAN - 1) / SPAN;
-  const int64_t items = (int64_t)a.batch * a.slot_heads * spans;
-  const int per_head = (G + 3) / 4;       // chunks
-  const int chunks = per_head * (a.slot_heads == 1 ? a.hkv : 1);
-  for (int64_t it = blockIdx.x - row_blocks; it < items; it += gridDim.x - row_blocks) {
-    const int64_t bw = it / spans;
-    const int b = (int)(bw / a.slot_heads);
-    const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
-    const int64_t start = (it % spans) * SPAN;
-    if (start >= n) continue;
-    const int t0 = (int)start + tid;
-    const Range r = range_of(n, a.window, a.sinks);
-    const int64_t seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
-    auto slot = [&](int k) { return min(t0 + k * kFinishThreads, n - 1); };   // (past the end: unused)
-    const int64_t at = bw * a.slot_stride;
-    float sum[SLOTS];
-    for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
-      float s[CHUNKS][SLOTS][4];
+  if constexpr (CHUNKS > 0) {
+    constexpr int SPAN = SLOTS * kFinishThreads;
+    constexpr int LPR = kFinishThreads / (4 * CHUNKS) < 32 ? kFinishThreads / (4 * CHUNKS) : 32;
+    const int64_t spans = (a.cache.slots + SPAN - 1) / SPAN;
+    const int64_t items = (int64_t)a.batch * a.slot_heads * spans;
+    const int per_head = (G + 3) / 4;       // chunks
+    const int chunks = per_head * (a.slot_heads == 1 ? a.hkv : 1);
+    for (int64_t it = blockIdx.x - row_blocks; it < items; it += gridDim.x - row_blocks) {
+      const int64_t bw = it / spans;
+      const int b = (int)(bw / a.slot_heads);
+      const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
+      const int64_t start = (it % spans) * SPAN;
+      if (start >= n) continue;
+      const int t0 = (int)start + tid;
+      const Range r = range_of(n, a.window, a.sinks);
+      const int64_t seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
+      auto slot = [&](int k) { return min(t0 + k * kFinishThreads, n - 1); };   // (past the end: unused)
+      const int64_t at = bw * a.slot_stride;
+      float sum[SLOTS];
+      for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
+        float s[CHUNKS][SLOTS][4];
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int ch = min(c0 + c, chunks - 1);
-        const float* p = a.logits + (seg0 + ch / per_head) * a.cache.slots * G;
+        for (int c = 0; c < CHUNKS; ++c) {
+          const int ch = min(c0 + c, chunks - 1);
+          const float* p = a.logits + (seg0 + ch / per_head) * a.cache.slots * G;
 #pragma unroll
-        for (int k = 0; k < SLOTS; ++k)
-          load_logits(s[c][k], p + (int64_t)slot(k) * G, ch % per_head * 4, G);
-      }
-      if (c0 == 0) {
-#pragma unroll
-        for (int k = 0; k < SLOTS; ++k) sum[k] = a.w_in ? a.w_in[at + slot(k)] * a.decay : 0.f;
-      }
-      __syncthreads();                    // the last ones' sums are used
-      {
-        const int i = tid / 8, ch = min(c0 + i / 4, chunks - 1), g = ch % per_head * 4 + i % 4;
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
-        if (row) {
-          const int2 d = a.desc[seg0 + ch / per_head];
-          const float2* p = a.part_ml + (int64_t)d.x * G + g;
-          for (int j = tid & 7; j < d.y; j += 8) ml = join_ml(ml, p[(int64_t)j * G]);
+          for (int k = 0; k < SLOTS; ++k)
+            load_logits(s[c][k], p + (int64_t)slot(k) * G, ch % per_head * 4, G);
         }
-        ml = join_lanes<8>(ml);
-        // (no row: a sum of infinity, weights of zero)
-        if (i < 32 && (tid & 7) == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
-      }
-      __syncthreads();
+        if (c0 == 0) {
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c)
+          for (int k = 0; k < SLOTS; ++k) sum[k] = a.w_in ? a.w_in[at + slot(k)] * a.decay : 0.f;
+        }
+        __syncthreads();                    // the last ones' sums are used
+        {
+          const int i = tid / LPR, ch = min(c0 + i / 4, chunks - 1), g = ch % per_head * 4 + i % 4;
+          float2 ml = make_float2(-CUDART_INF_F, 0.f);
+          const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
+          if (row) {
+            const int2 d = a.desc[seg0 + ch / per_head];
+            const float2* p = a.part_ml + (int64_t)d.x * G + g;
+#pragma unroll 4
+            for (int j = tid % LPR; j < d.y; j += LPR) ml = join_ml(ml, p[(int64_t)j * G]);
+          }
+          ml = join_lanes<LPR>(ml);
+          // (no row: a sum of infinity, weights of zero)
+          if (i < 4 * CHUNKS && tid % LPR == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
+        }
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float ref = s_ref[4 * c + j];
-          if (ref != CUDART_INF_F) {
+        for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-            for (int k = 0; k < SLOTS; ++k) {
-              const float p = ptx::ex2(s[c][k][j] - ref);
-              sum[k] += visible(r, slot(k)) ? p : 0.f;
+          for (int j = 0; j < 4; ++j) {
+            const float ref = s_ref[4 * c + j];
+            if (ref != CUDART_INF_F) {
+#pragma unroll
+              for (int k = 0; k < SLOTS; ++k) {
+                const float p = ptx::ex2(s[c][k][j] - ref);
+                sum[k] += visible(r, slot(k)) ? p : 0.f;
+              }
             }
           }
-        }
-    }
+      }
 #pragma unroll
-    for (int k = 0; k < SLOTS; ++k)
-      if (t0 + k * kFinishThreads < n) a.w_out[at + t0 + k * kFinishThreads] = sum[k];
+      for (int k = 0; k < SLOTS; ++k)
+        if (t0 + k * kFinishThreads < n) a.w_out[at + t0 + k * kFinishThreads] = sum[k];
+    }
   }
 }
 
 template <int D, int SLOTS, int CHUNKS>
-cudaError_t launch_finish(const KArgs& a, cudaStream_t stream) {
-  const int row_blocks = (int)(((int64_t)a.batch * a.hq + kFinishWarps - 1) / kFinishWarps);
-  const int span = SLOTS * kFinishThreads;
+cudaError_t launch_finish(const KArgs& a, int pieces, cudaStream_t stream) {
+  // a block per row when a segment may have many pieces, else a warp
+  const int parts = pieces > 16 ? kFinishWarps : 1;
+  const int row_blocks =
+      (int)(((int64_t)a.batch * a.hq * parts + kFinishWarps - 1) / kFinishWarps);
+  const int span = std::max(1, SLOTS * kFinishThreads);
   const int64_t items =
       a.w_out ? (int64_t)a.batch * a.slot_heads * ((a.cache.slots + span - 1) / span) : 0;
   const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 4);
   return launch_dependent(finish<D, SLOTS, CHUNKS>, dim3(grid), dim3(kFinishThreads), 0, stream, a,
-                          row_blocks);
+                          row_blocks, parts);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -788,15 +838,15 @@ bool cache_map(CUtensorMap* map, const void* base, const ds_decode_args& g) {
 }
 
 template <int D, bool BF, int NT>
-cudaError_t launch_split(const KArgs& a, const ds_decode_args& g, int ctas,
+cudaError_t launch_split(const KArgs& a, const ds_decode_args& g, int blocks,
                          cudaStream_t stream) {
   CUtensorMap tk, tv;
   if (!cache_map(&tk, g.k_cache, g) || !cache_map(&tv, g.v_cache, g))
     return cudaErrorInvalidValue;
-  const size_t smem = Cfg<D, NT>::smem;
+  const size_t smem = Cfg<D>::smem;
   const cudaError_t e = allow_smem(split<D, BF, NT>, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(split<D, BF, NT>, dim3(ctas), dim3(kThreads), smem, stream, tk, tv, a,
+  return launch_dependent(split<D, BF, NT>, dim3(blocks), dim3(kThreads), smem, stream, tk, tv, a,
                           g.kv_layout == DS_KV_HND ? 1 : 0);
 }
 
@@ -814,6 +864,7 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   a.hq = g.num_q_heads;
   a.hkv = g.num_kv_heads;
   a.group = a.hq / a.hkv;
+  a.resident = 2 * L.sms;
   a.window = g.window;
   a.sinks = g.sinks;
   a.scale = (g.scale > 0.f ? g.scale : 1.f / std::sqrt((float)g.head_dim)) * kLog2e;
@@ -834,25 +885,28 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   const bool bf = g.dtype == DS_KV_BF16;
   cudaError_t e;
   if (a.group <= 8)
-    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 1>(a, g, L.ctas, stream)
-                                : launch_split<128, false, 1>(a, g, L.ctas, stream))
-                          : (bf ? launch_split<64, true, 1>(a, g, L.ctas, stream)
-                                : launch_split<64, false, 1>(a, g, L.ctas, stream));
+    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 1>(a, g, L.ranges, stream)
+                                : launch_split<128, false, 1>(a, g, L.ranges, stream))
+                          : (bf ? launch_split<64, true, 1>(a, g, L.ranges, stream)
+                                : launch_split<64, false, 1>(a, g, L.ranges, stream));
   else
-    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 2>(a, g, L.ctas, stream)
-                                : launch_split<128, false, 2>(a, g, L.ctas, stream))
-                          : (bf ? launch_split<64, true, 2>(a, g, L.ctas, stream)
-                                : launch_split<64, false, 2>(a, g, L.ctas, stream));
+    e = g.head_dim == 128 ? (bf ? launch_split<128, true, 2>(a, g, L.ranges, stream)
+                                : launch_split<128, false, 2>(a, g, L.ranges, stream))
+                          : (bf ? launch_split<64, true, 2>(a, g, L.ranges, stream)
+                                : launch_split<64, false, 2>(a, g, L.ranges, stream));
   if (e != cudaSuccess) return e;
-  // chunks of up to four rows whose weights a slot sums
-  const int chunks = (a.group + 3) / 4 * (a.slot_heads == 1 ? a.hkv : 1);
+  // chunks of up to four rows whose weights a slot sums; pieces of a segment
+  const int chunks = !a.w_out ? 0 : (a.group + 3) / 4 * (a.slot_heads == 1 ? a.hkv : 1);
+  const int pieces = L.ranges / (a.batch * a.hkv) + 1;
   if (g.head_dim == 128)
-    return chunks == 1  ? launch_finish<128, 16, 1>(a, stream)
-           : chunks < 8 ? launch_finish<128, 4, 4>(a, stream)
-                        : launch_finish<128, 2, 8>(a, stream);
-  return chunks == 1  ? launch_finish<64, 16, 1>(a, stream)
-         : chunks < 8 ? launch_finish<64, 4, 4>(a, stream)
-                      : launch_finish<64, 2, 8>(a, stream);
+    return chunks == 0   ? launch_finish<128, 0, 0>(a, pieces, stream)
+           : chunks == 1 ? launch_finish<128, 16, 1>(a, pieces, stream)
+           : chunks < 8  ? launch_finish<128, 4, 4>(a, pieces, stream)
+                         : launch_finish<128, 2, 8>(a, pieces, stream);
+  return chunks == 0   ? launch_finish<64, 0, 0>(a, pieces, stream)
+         : chunks == 1 ? launch_finish<64, 16, 1>(a, pieces, stream)
+         : chunks < 8  ? launch_finish<64, 4, 4>(a, pieces, stream)
+                       : launch_finish<64, 2, 8>(a, pieces, stream);
 }
 
 }  // namespace ds

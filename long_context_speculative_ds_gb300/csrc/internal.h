@@ -111,13 +111,15 @@ size_t kv4_counters(const ds_kv4_attn_args& a);
 constexpr int kDraftMaxSlots = 1 << 30;
 
 // Workspace of ds_decode_attn.  A segment is a sequence's kv head, number
-// b * num_kv_heads + head; a piece is what one block has of it.
+// b * num_kv_heads + head; the work is cut into ranges, and a piece is what one
+// of them has of a segment.
 struct DecodeLayout {
-  int32_t ctas;         // blocks of the split pass, at most
+  int32_t sms;
+  int32_t ranges;       // blocks of the split pass, at most
   int64_t slots;        // of a sequence
   size_t desc;          // [segments] int2: first piece's place, pieces
-  size_t part_ml;       // [segments + ctas][group] float2: maximum (log2), sum
-  size_t part_o;        // [segments + ctas][group][head_dim] f32, not normalised
+  size_t part_ml;       // [segments + ranges][group] float2: maximum (log2), sum
+  size_t part_o;        // [segments + ranges][group][head_dim] f32, not normalised
   size_t logits;        // [segments][slots][group] f32 (log2), with weights only
   size_t total;
 };
