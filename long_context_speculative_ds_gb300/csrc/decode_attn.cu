@@ -612,13 +612,13 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
   const bool real = row < (int64_t)a.batch * a.hq;
   const int b = real ? (int)(row / a.hq) : 0, hq = real ? (int)(row % a.hq) : 0;
   const int h = hq / G, g = hq % G;
+  const int2 d = a.desc[b * a.hkv + h];   // (beside the length; not looked at without one)
   const int n = real ? checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false) : 0;
   float o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.f;
   float2 all = make_float2(-CUDART_INF_F, 0.f);
   if (n > 0) {
-    const int2 d = a.desc[b * a.hkv + h];
     const int p0 = (int)((int64_t)d.y * part / parts), p1 = (int)((int64_t)d.y * (part + 1) / parts);
     const float2* ml = a.part_ml + (int64_t)d.x * G + g;
     const float* po = a.part_o + ((int64_t)d.x * G + g) * D + lane * V;
@@ -626,13 +626,8 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
       const int m = min(32, p1 - i0);
       float2 x = make_float2(-CUDART_INF_F, 0.f);
       if (lane < m) x = ml[(int64_t)(i0 + lane) * G];
-      const float2 now = join_ml(all, join_lanes<32>(x));
-      const float ref = now.x == -CUDART_INF_F ? 0.f : now.x;
-      const float f = ptx::ex2(x.x - ref), old = ptx::ex2(all.x - ref);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[k] *= old;
-      for (int i = 0; i < m; i += 8) {
-        float v[8][V];
+      float v[8][V];
+      auto load = [&](int i) {            // (past the last: the last one's, unused)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float* p = po + (int64_t)(i0 + min(i + j, m - 1)) * G * D;
@@ -644,6 +639,15 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
             v[j][0] = y.x; v[j][1] = y.y;
           }
         }
+      };
+      load(0);
+      const float2 now = join_ml(all, join_lanes<32>(x));
+      const float ref = now.x == -CUDART_INF_F ? 0.f : now.x;
+      const float f = ptx::ex2(x.x - ref), old = ptx::ex2(all.x - ref);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] *= old;
+      for (int i = 0; i < m; i += 8) {
+        if (i > 0) load(i);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float w = __shfl_sync(0xffffffffu, f, (i + j) & 31);
@@ -728,47 +732,54 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS ? 2 : 4)
     const int64_t items = (int64_t)a.batch * a.slot_heads * spans;
     const int per_head = (G + 3) / 4;       // chunks
     const int chunks = per_head * (a.slot_heads == 1 ? a.hkv : 1);
+    // this thread's part of a row's sum: row i % 4 of chunk i / 4, pieces from l on
+    const int i = tid / LPR, l = tid % LPR;
     for (int64_t it = blockIdx.x - row_blocks; it < items; it += gridDim.x - row_blocks) {
       const int64_t bw = it / spans;
       const int b = (int)(bw / a.slot_heads);
+      const int64_t seg0 =
+          (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
+      // (beside the length; not looked at without one)
+      int2 d = a.desc[seg0 + min(i / 4, chunks - 1) / per_head];
       const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
       const int64_t start = (it % spans) * SPAN;
       if (start >= n) continue;
       const int t0 = (int)start + tid;
       const Range r = range_of(n, a.window, a.sinks);
-      const int64_t seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
-      auto slot = [&](int k) { return min(t0 + k * kFinishThreads, n - 1); };   // (past the end: unused)
+      // slots past the end: the thread's first again (or the last one), unused
+      const int first = min(t0, n - 1);
+      auto slot = [&](int k) { return t0 + k * kFinishThreads < n ? k * kFinishThreads : 0; };
       const int64_t at = bw * a.slot_stride;
-      float sum[SLOTS];
+      float sum[SLOTS], old[SLOTS];
+#pragma unroll
+      for (int k = 0; k < SLOTS; ++k) {
+        sum[k] = 0.f;
+        old[k] = a.w_in ? a.w_in[at + first + slot(k)] : 0.f;
+      }
       for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
+        const int mine = min(c0 + i / 4, chunks - 1), g = mine % per_head * 4 + i % 4;
+        const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
+        if (c0 > 0) d = a.desc[seg0 + mine / per_head];
+        const float2* const p_ml = a.part_ml + (int64_t)d.x * G + g;
+        float2 ml = make_float2(-CUDART_INF_F, 0.f);
+        if (row && l < d.y) ml = p_ml[(int64_t)l * G];
         float s[CHUNKS][SLOTS][4];
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
           const int ch = min(c0 + c, chunks - 1);
-          const float* p = a.logits + (seg0 + ch / per_head) * a.cache.slots * G;
+          const float* p = a.logits + ((seg0 + ch / per_head) * a.cache.slots + first) * G;
 #pragma unroll
           for (int k = 0; k < SLOTS; ++k)
-            load_logits(s[c][k], p + (int64_t)slot(k) * G, ch % per_head * 4, G);
+            load_logits(s[c][k], p + slot(k) * G, ch % per_head * 4, G);
         }
-        if (c0 == 0) {
-#pragma unroll
-          for (int k = 0; k < SLOTS; ++k) sum[k] = a.w_in ? a.w_in[at + slot(k)] * a.decay : 0.f;
-        }
-        __syncthreads();                    // the last ones' sums are used
-        {
-          const int i = tid / LPR, ch = min(c0 + i / 4, chunks - 1), g = ch % per_head * 4 + i % 4;
-          float2 ml = make_float2(-CUDART_INF_F, 0.f);
-          const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
-          if (row) {
-            const int2 d = a.desc[seg0 + ch / per_head];
-            const float2* p = a.part_ml + (int64_t)d.x * G + g;
+        __syncthreads();                  // the last ones' sums are used
+        if (row) {
 #pragma unroll 4
-            for (int j = tid % LPR; j < d.y; j += LPR) ml = join_ml(ml, p[(int64_t)j * G]);
-          }
-          ml = join_lanes<LPR>(ml);
-          // (no row: a sum of infinity, weights of zero)
-          if (i < 4 * CHUNKS && tid % LPR == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
+          for (int j = l + LPR; j < d.y; j += LPR) ml = join_ml(ml, p_ml[(int64_t)j * G]);
         }
+        ml = join_lanes<LPR>(ml);
+        // (no row: a sum of infinity, weights of zero)
+        if (i < 4 * CHUNKS && l == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
         __syncthreads();
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c)
@@ -779,14 +790,15 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS ? 2 : 4)
 #pragma unroll
               for (int k = 0; k < SLOTS; ++k) {
                 const float p = ptx::ex2(s[c][k][j] - ref);
-                sum[k] += visible(r, slot(k)) ? p : 0.f;
+                sum[k] += visible(r, first + slot(k)) ? p : 0.f;
               }
             }
           }
       }
 #pragma unroll
       for (int k = 0; k < SLOTS; ++k)
-        if (t0 + k * kFinishThreads < n) a.w_out[at + t0 + k * kFinishThreads] = sum[k];
+        if (t0 + k * kFinishThreads < n)
+          a.w_out[at + t0 + k * kFinishThreads] = fmaf(old[k], a.decay, sum[k]);
     }
   }
 }
@@ -800,7 +812,7 @@ cudaError_t launch_finish(const KArgs& a, int pieces, cudaStream_t stream) {
   const int span = std::max(1, SLOTS * kFinishThreads);
   const int64_t items =
       a.w_out ? (int64_t)a.batch * a.slot_heads * ((a.cache.slots + span - 1) / span) : 0;
-  const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 4);
+  const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 4 * 2);
   return launch_dependent(finish<D, SLOTS, CHUNKS>, dim3(grid), dim3(kFinishThreads), 0, stream, a,
                           row_blocks, parts);
 }
