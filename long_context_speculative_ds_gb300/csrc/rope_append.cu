@@ -47,6 +47,7 @@ struct RopeKArgs {
 };
 
 constexpr int kRopeWarps = 8;             // warps of a block
+constexpr int kRopeBatch = 4;             // head groups of a warp, their loads together
 
 // The last sequence b with row_offsets[b] <= row (offsets that are not
 // monotone give some sequence; its own offsets are checked after).
@@ -80,8 +81,32 @@ DS_DEV uint32_t pack2(float lo, float hi) {
   return BF ? ptx::pack_bf16x2(lo, hi) : ptx::pack_f16x2(lo, hi);
 }
 
+// A lane's eight pairs of a head: (u, v) value by value (half), or neighbours
+// in u and in v; cs: their cosines and sines, two pairs an entry.
+template <bool BF, bool HALVES>
+DS_DEV void turn(uint4& u, uint4& v, const float4 (&cs)[4]) {
+  uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2<BF>(uw[i]), y = unpack2<BF>(vw[i]);
+    if constexpr (HALVES) {
+      const float4 c = cs[i];
+      uw[i] = pack2<BF>(x.x * c.x - y.x * c.y, x.y * c.z - y.y * c.w);
+      vw[i] = pack2<BF>(x.x * c.y + y.x * c.x, x.y * c.w + y.y * c.z);
+    } else {
+      const float cx = i & 1 ? cs[i / 2].z : cs[i / 2].x, sx = i & 1 ? cs[i / 2].w : cs[i / 2].y;
+      const float cy = i & 1 ? cs[2 + i / 2].z : cs[2 + i / 2].x;
+      const float sy = i & 1 ? cs[2 + i / 2].w : cs[2 + i / 2].y;
+      uw[i] = pack2<BF>(x.x * cx - x.y * sx, x.x * sx + x.y * cx);
+      vw[i] = pack2<BF>(y.x * cy - y.y * sy, y.x * sy + y.y * cy);
+    }
+  }
+  u = make_uint4(uw[0], uw[1], uw[2], uw[3]);
+  v = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+}
+
 template <int D, bool BF, bool HALVES>
-__global__ void __launch_bounds__(32 * kRopeWarps) rope_append(const RopeKArgs a) {
+__global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append(const RopeKArgs a) {
   constexpr int LPH = D / 16;             // lanes of a head
   constexpr int HPW = 32 / LPH;           // heads of a warp at a time
   __shared__ __align__(16) float2 s_cs[kRopeWarps][D / 2];
@@ -105,7 +130,35 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append(const RopeKArgs a
   const int groups = (a.heads + HPW - 1) / HPW;
   const int g0 = blockIdx.y * a.per, g1 = min(groups, g0 + a.per);
   if (g0 >= g1) return;
+  const int l = lane % LPH, sub = lane / LPH;
+  const bool turned = 16 * l < a.rotary;
+  // the lane's two vectors of a head
+  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
+  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
+  // the heads of a row: query, key, value
+  auto which = [&](int hh, int& h) {
+    const int ty = hh < a.hq ? 0 : hh < a.hq + a.hkv ? 1 : 2;
+    h = hh - (ty > 0 ? a.hq : 0) - (ty > 1 ? a.hkv : 0);
+    return ty;
+  };
+  uint4 u[kRopeBatch], v[kRopeBatch];
+  auto load = [&](int gb) {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int hh = (gb + k) * HPW + sub;
+      if (gb + k >= g1 || hh >= a.heads) continue;
+      int h;
+      const int ty = which(hh, h);
+      // plain loads: with q_out = q the same bytes are written below
+      const uint16_t* p = (ty == 0 ? a.x[0] : ty == 1 ? a.x[1] : a.x[2]) +
+                          row * (ty == 0 ? a.stride[0] : ty == 1 ? a.stride[1] : a.stride[2]) +
+                          (int64_t)h * D;
+      u[k] = *reinterpret_cast<const uint4*>(p + e0);
+      v[k] = *reinterpret_cast<const uint4*>(p + e1);
+    }
+  };
   const int pos = __ldg(a.positions + row);
+  load(g0);                               // beside what the position asks for
   if (pos < 0) {
     if (lane == 0) flag(a.status, DS_DEV_BAD_LENGTH);
     return;
@@ -129,57 +182,38 @@ __global__ void __launch_bounds__(32 * kRopeWarps) rope_append(const RopeKArgs a
   // position * frequency wraps modulo one turn in 64 bits; its upper half,
   // read as a signed number, is the angle in units of pi / 2^31
   float2* const cs = s_cs[warp];
-#pragma unroll
-  for (int k = 0; k < D / 64; ++k) {
-    const int j = lane + 32 * k;
+  for (int j = lane; j < a.rotary / 2; j += 32) {
     const unsigned long long t = (unsigned long long)pos * a.turn[j];
     float sn, c;
     sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &sn, &c);
     cs[j] = make_float2(c * a.magnitude, sn * a.magnitude * a.sin_sign);
   }
   __syncwarp();
-  const int l = lane % LPH, sub = lane / LPH;
-  const bool turned = 16 * l < a.rotary;
-  // the lane's two vectors of a head
-  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
-  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
-  for (int gi = g0; gi < g1; ++gi) {
-    const int hh = gi * HPW + sub;
-    if (hh >= a.heads) continue;
-    const int ty = hh < a.hq ? 0 : hh < a.hq + a.hkv ? 1 : 2;
-    const int h = hh - (ty > 0 ? a.hq : 0) - (ty > 1 ? a.hkv : 0);
-    // plain loads: with q_out = q the same bytes are written below
-    const uint16_t* p = a.x[ty] + (int64_t)row * a.stride[ty] + (int64_t)h * D;
-    uint4 u = *reinterpret_cast<const uint4*>(p + e0);
-    uint4 v = *reinterpret_cast<const uint4*>(p + e1);
-    if (turned && ty < 2) {
-      uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
+  float4 rot[4];                          // of this lane's pairs, for all heads
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (HALVES) {
-          const float2 x = unpack2<BF>(uw[i]), y = unpack2<BF>(vw[i]);
-          const float4 c = *reinterpret_cast<const float4*>(&cs[8 * l + 2 * i]);
-          uw[i] = pack2<BF>(x.x * c.x - y.x * c.y, x.y * c.z - y.y * c.w);
-          vw[i] = pack2<BF>(x.x * c.y + y.x * c.x, x.y * c.w + y.y * c.z);
-        } else {
-          const float2 x = unpack2<BF>(uw[i]), y = unpack2<BF>(vw[i]);
-          const float2 c = cs[8 * l + i], d = cs[8 * l + 4 + i];
-          uw[i] = pack2<BF>(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
-          vw[i] = pack2<BF>(y.x * d.x - y.y * d.y, y.x * d.y + y.y * d.x);
-        }
+  for (int i = 0; i < 4; ++i)
+    rot[i] = turned ? *reinterpret_cast<const float4*>(&cs[8 * l + 2 * i])
+                    : make_float4(1.f, 0.f, 1.f, 0.f);
+  for (int gb = g0; gb < g1; gb += kRopeBatch) {
+    if (gb > g0) load(gb);
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int hh = (gb + k) * HPW + sub;
+      if (gb + k >= g1 || hh >= a.heads) continue;
+      int h;
+      const int ty = which(hh, h);
+      if (turned && ty < 2) turn<BF, HALVES>(u[k], v[k], rot);
+      uint16_t* o = ty == 0 ? a.out[0] : ty == 1 ? a.out[1] : nullptr;
+      if (o) {
+        o += row * (ty == 0 ? a.out_stride[0] : a.out_stride[1]) + (int64_t)h * D;
+        *reinterpret_cast<uint4*>(o + e0) = u[k];
+        *reinterpret_cast<uint4*>(o + e1) = v[k];
       }
-      u = make_uint4(uw[0], uw[1], uw[2], uw[3]);
-      v = make_uint4(vw[0], vw[1], vw[2], vw[3]);
-    }
-    if (ty < 2 && a.out[ty]) {
-      uint16_t* o = a.out[ty] + (int64_t)row * a.out_stride[ty] + (int64_t)h * D;
-      *reinterpret_cast<uint4*>(o + e0) = u;
-      *reinterpret_cast<uint4*>(o + e1) = v;
-    }
-    if (ty > 0 && at >= 0) {
-      uint16_t* o = a.cache.pool[ty - 1] + at + (int64_t)h * a.cache.head_stride;
-      *reinterpret_cast<uint4*>(o + e0) = u;
-      *reinterpret_cast<uint4*>(o + e1) = v;
+      if (ty > 0 && at >= 0) {
+        o = (ty == 1 ? a.cache.pool[0] : a.cache.pool[1]) + at + (int64_t)h * a.cache.head_stride;
+        *reinterpret_cast<uint4*>(o + e0) = u[k];
+        *reinterpret_cast<uint4*>(o + e1) = v[k];
+      }
     }
   }
 }
