@@ -138,13 +138,12 @@ AcceptLayout accept_layout(const ds_accept_args& a) {
 
 DecodeLayout decode_layout(const ds_decode_args& a, int num_sms) {
   DecodeLayout L;
-  L.sms = num_sms;
   L.slots = a.page_table ? (int64_t)a.max_pages * a.page_size : a.page_size;
   const size_t group = (size_t)(a.num_q_heads / a.num_kv_heads);
   const size_t segs = (size_t)a.batch * a.num_kv_heads;
-  // two large ranges an SM and twice as many small ones, but none without a tile
+  // two an SM, but none without a tile
   const int64_t tiles = (int64_t)segs * ((L.slots + 63) / 64);
-  L.ranges = (int32_t)(tiles < 6 * num_sms ? tiles : 6 * num_sms);
+  L.ranges = (int32_t)(tiles < 2 * num_sms ? tiles : 2 * num_sms);
   size_t off = kStatusBytes;
   L.desc = off;
   off = align_up(off + segs * sizeof(int32_t) * 2);

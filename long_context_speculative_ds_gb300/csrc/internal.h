@@ -114,7 +114,6 @@ constexpr int kDraftMaxSlots = 1 << 30;
 // b * num_kv_heads + head; the work is cut into ranges, and a piece is what one
 // of them has of a segment.
 struct DecodeLayout {
-  int32_t sms;
   int32_t ranges;       // blocks of the split pass, at most
   int64_t slots;        // of a sequence
   size_t desc;          // [segments] int2: first piece's place, pieces

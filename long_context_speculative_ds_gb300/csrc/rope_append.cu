@@ -46,7 +46,7 @@ struct RopeKArgs {
   unsigned long long turn[64];    // frequency j as a 64-bit fraction of a turn
 };
 
-constexpr int kRopeWarps = 8;             // warps of a block
+constexpr int kRopeWarps = 4;             // warps of a block
 constexpr int kRopeBatch = 4;             // head groups of a warp, their loads together
 
 // The last sequence b with row_offsets[b] <= row (offsets that are not
@@ -106,7 +106,7 @@ DS_DEV void turn(uint4& u, uint4& v, const float4 (&cs)[4]) {
 }
 
 template <int D, bool BF, bool HALVES>
-__global__ void __launch_bounds__(32 * kRopeWarps, 3) rope_append(const RopeKArgs a) {
+__global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArgs a) {
   constexpr int LPH = D / 16;             // lanes of a head
   constexpr int HPW = 32 / LPH;           // heads of a warp at a time
   __shared__ __align__(16) float2 s_cs[kRopeWarps][D / 2];
