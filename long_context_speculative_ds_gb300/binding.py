@@ -234,6 +234,8 @@ def load(path: Optional[str] = None) -> C.CDLL:
                  "ds_decode_attn_workspace_size", "ds_decode_attn",
                  "ds_cache_evict_workspace_size", "ds_cache_evict"):
         getattr(lib, name).restype = C.c_int
+    for name in ("ds_rope_append", "ds_decode_attn", "ds_cache_evict"):
+        getattr(lib, name).argtypes = [_p, _p]
     for which, cls in ((0, VerifyArgs), (1, GatherArgs), (2, AcceptArgs),
                        (3, CommitArgs), (4, AppendArgs), (5, NormRopeArgs),
                        (6, Kv4RowsArgs), (8, Kv4AttnArgs), (9, RopeScaling),
@@ -616,8 +618,31 @@ def ds_kv4_verify_attn(args: Kv4AttnArgs, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# The draft's cache.  These argument structs keep their tensors alive
-# (`_tensors`): a call may be made long after they were built.
+# The draft's cache.  These argument structs keep their tensors alive: a call
+# may be made long after they were built.  A call refuses tensors that are not
+# all on the current CUDA device.
+def _keep(args, *tensors):
+    args._tensors = tensors
+    devices = {t.device for t in tensors if t is not None}
+    one = devices.pop() if len(devices) == 1 else None
+    args._device = one.index if one is not None and one.type == "cuda" else None
+    return args
+
+
+_current = _get_device or torch.cuda.current_device
+
+
+def _draft_call(fn, args, stream):
+    # (in few steps: a small call takes the GPU less time than it takes here)
+    dev = args._device
+    if dev is None or dev != _current():
+        raise ValueError(f"{fn.__name__}: its tensors must be on the current CUDA device")
+    status = fn(C.byref(args), _raw_stream(dev) if stream is None and _raw_stream is not None
+                else _stream(stream))
+    if status != DS_OK:
+        _check(status)
+
+
 _SCALES = {"none": DS_ROPE_SCALE_NONE, "linear": DS_ROPE_SCALE_LINEAR,
            "bands": DS_ROPE_SCALE_BANDS, "ramp": DS_ROPE_SCALE_RAMP}
 _ROPE_LAYOUT = {"half": DS_ROPE_HALF, "interleaved": DS_ROPE_INTERLEAVED}
@@ -726,8 +751,8 @@ def rope_append_args(q, k, v, positions, *, q_out=None, k_out=None,
     if inv_freq is not None:
         if len(inv_freq) != (rotary_dim or a.head_dim) // 2:
             raise ValueError("inv_freq must hold rotary_dim / 2 values")
-        a._keep = (C.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
-        a.inv_freq = C.cast(a._keep, C.POINTER(C.c_double))
+        a._table = (C.c_double * len(inv_freq))(*[float(x) for x in inv_freq])
+        a.inv_freq = C.cast(a._table, C.POINTER(C.c_double))
     if k_cache is not None:
         if ks != vs or k_cache.dtype != ref.dtype:
             raise ValueError("k and v must agree in shape, and with the cache in type")
@@ -740,14 +765,13 @@ def rope_append_args(q, k, v, positions, *, q_out=None, k_out=None,
         a.new_lens = _int32(new_lens, batch, "new_lens")
         _slot_arrays(a, batch, slot_positions=(slot_positions, torch.int32),
                      slot_weights=(slot_weights, torch.float32))
-    a._tensors = (q, k, v, positions, q_out, k_out, k_cache, v_cache, page_table, from_lens,
-                  row_offsets, slot_positions, slot_weights, new_lens, workspace)
     _set_workspace(a, workspace)
-    return a
+    return _keep(a, q, k, v, positions, q_out, k_out, k_cache, v_cache, page_table, from_lens,
+                 row_offsets, slot_positions, slot_weights, new_lens, workspace)
 
 
 def ds_rope_append(args: RopeArgs, stream=None):
-    _check(load().ds_rope_append(C.byref(args), _stream(stream)))
+    _draft_call((_LIB or load()).ds_rope_append, args, stream)
 
 
 def decode_attn_args(q, k_cache, v_cache, page_table, lens, *, out, lse=None,
@@ -777,10 +801,9 @@ def decode_attn_args(q, k_cache, v_cache, page_table, lens, *, out, lse=None,
     _slot_arrays(a, batch, weights_in=(weights_in, torch.float32),
                  weights_out=(weights_out, torch.float32))
     a.decay, a.window, a.sinks, a.scale, a.num_sms = decay, window, sinks, scale, num_sms
-    a._tensors = (q, k_cache, v_cache, page_table, lens, out, lse, weights_in, weights_out,
-                  workspace)
     _set_workspace(a, workspace)
-    return a
+    return _keep(a, q, k_cache, v_cache, page_table, lens, out, lse, weights_in, weights_out,
+                 workspace)
 
 
 def ds_decode_attn_workspace_size(args: DecodeArgs) -> int:
@@ -790,7 +813,7 @@ def ds_decode_attn_workspace_size(args: DecodeArgs) -> int:
 
 
 def ds_decode_attn(args: DecodeArgs, stream=None):
-    _check(load().ds_decode_attn(C.byref(args), _stream(stream)))
+    _draft_call((_LIB or load()).ds_decode_attn, args, stream)
 
 
 def evict_args(k_cache, v_cache, page_table, lens, *, weights, positions,
@@ -811,10 +834,9 @@ def evict_args(k_cache, v_cache, page_table, lens, *, weights, positions,
     a.next_positions = _int32(next_positions, batch, "next_positions")
     a.new_lens = _int32(new_lens, batch, "new_lens")
     a.budget, a.trigger, a.recent, a.sinks = budget, trigger, recent, sinks
-    a._tensors = (k_cache, v_cache, page_table, lens, weights, positions, weights_out,
-                  positions_out, next_positions, new_lens, workspace)
     _set_workspace(a, workspace)
-    return a
+    return _keep(a, k_cache, v_cache, page_table, lens, weights, positions, weights_out,
+                 positions_out, next_positions, new_lens, workspace)
 
 
 def ds_cache_evict_workspace_size(args: EvictArgs) -> int:
@@ -824,7 +846,7 @@ def ds_cache_evict_workspace_size(args: EvictArgs) -> int:
 
 
 def ds_cache_evict(args: EvictArgs, stream=None):
-    _check(load().ds_cache_evict(C.byref(args), _stream(stream)))
+    _draft_call((_LIB or load()).ds_cache_evict, args, stream)
 
 
 def ds_workspace_init(workspace: torch.Tensor, stream=None):

@@ -901,6 +901,9 @@ static ds_status check_decode(const ds_decode_args* a, int* sms) {
   REQUIRE(a->num_q_heads >= a->num_kv_heads && a->num_q_heads % a->num_kv_heads == 0,
           DS_ERR_UNSUPPORTED, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
           a->num_q_heads, a->num_kv_heads);
+  // (a stride of the copies' tensor maps)
+  REQUIRE((int64_t)a->page_size * a->num_kv_heads * a->head_dim < (int64_t)1 << 39,
+          DS_ERR_UNSUPPORTED, "cache too large: a page of 2^39 elements or more");
   REQUIRE(a->num_q_heads / a->num_kv_heads <= 16, DS_ERR_UNSUPPORTED,
           "num_q_heads / num_kv_heads = %d: at most 16", a->num_q_heads / a->num_kv_heads);
   REQUIRE(a->dtype == DS_KV_BF16 || a->dtype == DS_KV_F16, DS_ERR_INVALID_ARG,

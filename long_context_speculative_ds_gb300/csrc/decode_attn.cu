@@ -97,8 +97,8 @@ struct Plan {
 
 // First unit of range i, and the range that unit u lies in.
 DS_DEV int64_t range_start(const Plan& p, int i) { return p.units * i / p.ranges; }
-DS_DEV int range_with(const Plan& p, int64_t u) {
-  return (int)(((u + 1) * p.ranges - 1) / p.units);   // the last i with units i / ranges <= u
+DS_DEV int range_with(const Plan& p, int64_t u) {     // the last i with units i / ranges <= u
+  return (int)min(((u + 1) * p.ranges - 1) / p.units, (int64_t)p.ranges - 1);
 }
 
 struct Piece {
@@ -149,12 +149,13 @@ DS_DEV bool make_plan(const KArgs& a, Plan& plan, int64_t (*s_sum)[2]) {
   if (before <= lo && lo < before + units) {  // one thread
     int b = b0;
     int64_t len = 0, off = lo - before;
-    for (;; ++b) {
+    for (; b < b1; ++b) {
       const int t = seq_range(a, b, false).tiles;
       len = t > 0 ? t + kLead : 0;
       if (off < len * a.hkv) break;
       off -= len * a.hkv;
     }
+    len = max(len, (int64_t)1);
     plan.first.b = b;
     plan.first.h = (int)(off / len);
     plan.first.off = off - plan.first.h * len;
@@ -266,9 +267,10 @@ struct Cfg {
 struct Shared {
   alignas(8) uint64_t full[6], empty[6];
   Plan plan;
+  Piece piece;                                // of the warps that compute
   int64_t sum[kWarps + 1][2];
   float m[kWarps][8], l[kWarps][8];
-  int abort;
+  int abort, more;
 };
 static_assert(2 * (Cfg<128>::smem + sizeof(Shared) + 1024 + 16) <= 233472, "two blocks an SM");
 
@@ -377,7 +379,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto chunk_at = [&](uint32_t base, int row, int chunk) {
     return base + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
   };
-  while (next_piece(a, walk, pc)) {
+  // (one thread walks for all four warps, which meet at barriers a piece long)
+  if (tid == 0) sh.more = next_piece(a, walk, sh.piece);
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+  while (sh.more) {
+    pc = sh.piece;
     const Range r = pc.r;
     const int64_t seg = (int64_t)pc.b * a.hkv + pc.h;
     uint32_t q[NT][D / 16][2];
@@ -559,12 +565,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<float4*>(a.part_o + ((piece * G + 8 * i + row) * D + c * 4)) = sum;
         if (c == 0) a.part_ml[piece * G + 8 * i + row] = make_float2(M, total);
       }
+      if (i == NT - 1 && tid == 0) {
+        if (pc.t0 == 0) {                     // numbered by range and segment, which never
+          const int64_t u = pc.pos + kLead;   // both stand still, pieces have places of their own
+          const int f = range_with(sh.plan, u);   // (u: the segment's first tile on the axis)
+          a.desc[seg] = make_int2((int)(f + seg), range_with(sh.plan, u + r.tiles - 1) - f + 1);
+        }
+        sh.more = next_piece(a, walk, sh.piece);
+      }
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-    }
-    if (tid == 0 && pc.t0 == 0) {             // numbered by range and segment, which never
-      const int64_t u = pc.pos + kLead;       // both stand still, pieces have places of their own
-      const int f = range_with(sh.plan, u);   // (u: the segment's first tile on the axis)
-      a.desc[seg] = make_int2((int)(f + seg), range_with(sh.plan, u + r.tiles - 1) - f + 1);
     }
   }
 }

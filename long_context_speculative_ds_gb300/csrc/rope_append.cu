@@ -49,13 +49,18 @@ struct RopeKArgs {
 constexpr int kRopeWarps = 4;             // warps of a block
 constexpr int kRopeBatch = 4;             // head groups of a warp, their loads together
 
-// The last sequence b with row_offsets[b] <= row (offsets that are not
-// monotone give some sequence; its own offsets are checked after).
+// The sequence before the first row_offsets[b] above row, by all lanes of a
+// warp, 32 at a time (offsets that are not monotone give some sequence; its own
+// offsets are checked after).
 DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
-  int lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(offs + mid) <= row) lo = mid; else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 31) / 32, i = lane * step;
+    const uint32_t at = __ballot_sync(0xffffffffu, i < n && __ldg(offs + lo + min(i, n - 1)) <= row);
+    const int k = max(__ffs(~at) - 2, at == ~0u ? 31 : 0);   // last of the run from lane 0
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   return lo;
 }
@@ -255,10 +260,16 @@ cudaError_t launch_rope_append(const ds_rope_args& g, cudaStream_t stream) {
   // a double's 53 bits leave each frequency (at most a radian in use) off by
   // less than 2^-53 of a turn, and the angle, at positions below 2^31, by
   // less than 2^-22 of one; at 2^17 by less than 2^-36
+  // (base^(-2j/r) as a product of two powers: sixteen calls of pow, not 64)
+  constexpr double kTau = 6.283185307179586;
+  double lo[8], hi[8];
+  if (!g.inv_freq)
+    for (int k = 0; k < 8; ++k) {
+      lo[k] = std::pow((double)g.rope_base, -2.0 * k / a.rotary);
+      hi[k] = std::pow((double)g.rope_base, -16.0 * k / a.rotary) / kTau;
+    }
   for (int j = 0; j < a.rotary / 2; ++j) {
-    const double turns = (g.inv_freq ? g.inv_freq[j]
-                                     : std::pow((double)g.rope_base, -2.0 * j / a.rotary)) /
-                         6.283185307179586;
+    const double turns = g.inv_freq ? g.inv_freq[j] / kTau : lo[j & 7] * hi[j >> 3];
     const double frac = turns - std::floor(turns);   // whole turns drop out
     a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
   }

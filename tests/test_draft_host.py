@@ -2,7 +2,9 @@
 sizes, frequencies against the oracle, workspace sizes, and refusals by name
 before any device call."""
 import ctypes as C
-import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -222,6 +224,12 @@ def test_decode_refuses_by_name(lib, field, value, status, word):
     _refused(lib, "ds_decode_attn", _decode(**{field: value}), status, word)
 
 
+def test_decode_large_pages(lib):
+    a = _decode(page_table=None, page_size=1 << 30, num_pages=2, num_kv_heads=8,
+                slot_stride=1 << 30, batch=2, num_q_heads=8)
+    _refused(lib, "ds_decode_attn", a, B.DS_ERR_UNSUPPORTED, "cache too large")
+
+
 def test_decode_workspace(lib):
     size = lambda **kw: B.ds_decode_attn_workspace_size(_decode(**kw))
     with_weights, without = size(), size(weights_out=None, slot_stride=0)
@@ -288,3 +296,38 @@ def test_binding_refuses_mixed_tensors():
                      weights=torch.zeros(2, 1, 10),
                      positions=torch.zeros(2, 1, 10, dtype=torch.int32), next_positions=lens,
                      new_lens=lens, budget=4)
+
+
+def test_calls_refuse_tensors_of_another_device():
+    q, ws = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(256, dtype=torch.uint8)
+    pos = torch.zeros(2, dtype=torch.int32)
+    a = B.rope_append_args(q, None, None, pos, q_out=q, rope_base=1e4, workspace=ws)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        B.ds_rope_append(a)
+    cache = torch.zeros(2, 10, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        B.ds_decode_attn(B.decode_attn_args(q, cache, cache, None, pos, out=q, workspace=ws))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        B.ds_cache_evict(B.evict_args(
+            cache, cache, None, pos, weights=torch.zeros(2, 1, 10),
+            positions=torch.zeros(2, 1, 10, dtype=torch.int32), next_positions=pos,
+            new_lens=torch.zeros(2, dtype=torch.int32), budget=4, workspace=ws))
+
+
+def test_launches_of_any_batch(tmp_path):
+    """The library's own objects over a runtime that only keeps account."""
+    objs = [os.path.join(build.OUT_DIR, "_obj", s + ".o") for s in build.SOURCES]
+    build.build(force=not all(os.path.exists(o) for o in objs))
+    cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
+    libs = os.path.join(cuda, "lib64")
+    if not os.path.exists(os.path.join(libs, "libcudart.so")):
+        pytest.skip("no shared CUDA runtime to take the kernels' registration")
+    here = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native")
+    out = str(tmp_path / "draft_launches")
+    r = subprocess.run(["g++", "-std=c++17", "-O1", "-I" + build.INCLUDE,
+                        "-I" + os.path.join(cuda, "include"),
+                        os.path.join(here, "draft_launches.cpp"), *objs, "-o", out, "-L" + libs,
+                        "-lcudart", "-Wl,-rpath," + libs], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([out], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout + r.stderr
