@@ -64,6 +64,7 @@ struct Shared {
   int2 warp_sum[2][32];
   int2 block_sum[2];                      // of this block: ties; slots that come, that are freed
   uint32_t prefix, left, count;
+  unsigned long long least[32];           // of each warp
 };
 
 // Exclusive prefix of two values per warp (the same on all its lanes) over the
@@ -193,6 +194,38 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
     for (int j = 0; j < kept; ++j) f(mine[32 * j], j);
     for (int j = kept; j < per; ++j) f(read(j), j);
   };
+  // ---- one slot to give up, as a cache at its budget does every token: the
+  // lightest, of equal ones the last; the one behind the budget takes its place
+  // (a call on 2,049 slots 6.3 us instead of 11.4)
+  if (n - keep == 1) {
+    unsigned long long least = ~0ull;     // key, then slot from the end
+    each([&](uint32_t k, int j) {
+      const unsigned long long x =
+          (unsigned long long)k << 32 | (uint32_t)~(row0 + 32 * j + lane);
+      if (k != 0u) least = min(least, x);
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) sh.least[warp] = least;
+    meet();
+    if (warp == 0 && rank == 0) {
+      least = ~0ull;
+      for (int c = 0; c < C; ++c)
+        if (lane < NW) least = min(least, cl.map_shared_rank(&sh.least[0], c)[lane]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+      const int gone = (int)~(uint32_t)least;
+      if (lane == 0) {
+        a.count[seg] = gone < keep;
+        a.src[(int64_t)seg * a.moves] = keep;
+        a.dst[(int64_t)seg * a.moves] = gone;
+      }
+    }
+    if (nan) flag(a.status, DS_DEV_BAD_VALUE);
+    if (C > 1) cl.sync();                 // others may still be read
+    return;
+  }
   __syncthreads();                        // the histograms are empty
   // ---- the keep-th largest key, digit by digit
   uint32_t prefix = 0, left = keep, same = 0;

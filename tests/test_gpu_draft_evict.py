@@ -168,6 +168,34 @@ def test_weights_of_every_kind(kind):
         assert st == status
 
 
+@pytest.mark.parametrize("kind", ["equal", "nan", "all nan", "forced", "last", "inf"])
+@pytest.mark.parametrize("slots", [2, 65, 4096, 4097, 30001])
+def test_one_slot_given_up(kind, slots):
+    """The budget exceeded by one: what a cache at its budget does every token."""
+    lens, budget = [slots, slots - 1], slots - 1
+    pools, table, w, pos = make(lens, 2, 64, "NHD", 0, 2, slots, slots, ties=False)
+    recent = sinks = 0
+    if kind == "equal":
+        w.fill_(0.25)
+    elif kind == "nan":
+        w[:, :, slots // 2] = math.nan
+        w[:, :, slots // 3] = math.nan
+    elif kind == "all nan":
+        w.fill_(math.nan)
+    elif kind == "forced":
+        pos.fill_(0)
+        sinks = 1
+    elif kind == "last":                             # the slot behind the budget itself
+        w[:, :, slots - 1] = -1.0
+    else:
+        w.fill_(-math.inf)
+        w[:, 0, :slots - 1] = math.inf
+    status = B.DS_DEV_BAD_VALUE if kind.endswith("nan") else 0
+    for st in both(pools, table, lens, w, pos, [10 ** 6] * 2, budget=budget, recent=recent,
+                   sinks=sinks):
+        assert st == status
+
+
 def test_bad_lengths_and_pages():
     """A length that is none leaves its sequence alone; a token whose page is
     none stays where it is, its weight and position move."""
