@@ -52,11 +52,11 @@ DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan
 
 // A cluster of blocks per segment; its rows of 32 slots in equal runs to the
 // warps, one behind the other.  Keys of a warp's first rows stay in shared
-// memory, as many as the launch has room for; beyond (segments of more than
-// 400,000 slots) they are formed anew from memory.
+// memory, as many as the launch has room for; beyond (segments of more than some
+// 400,000 slots, 800,000 for few of them) they are formed anew from memory.
 constexpr int kMaxKeyBytes = 200 * 1024;
 constexpr int kBins = 2048;               // of a digit: 11, 11 and 10 bits
-constexpr int kCluster = 8;               // blocks, at most
+constexpr int kCluster = 16;              // blocks, at most
 
 struct Shared {
   uint32_t hist[3][kBins];
@@ -439,18 +439,24 @@ __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
   }
 }
 
-// Blocks of a segment's cluster.  Segments of up to 4,096 slots take one block
-// of 256 threads, whose barriers cost less.  Longer ones take blocks of 512, as
-// many as fill the machine, but with 2,048 slots or more to each; more while a
-// block's keys do not fit beside another block's.  (Blocks of which only one
-// fits an SM leave no place for 16 clusters of eight at once: 16 segments of
-// 128K took two waves, 44 us.)
-int cluster_size(int segs, int64_t slots) {
-  if (slots <= 4096) return 1;
+// Threads of a block and blocks of a segment's cluster.  Segments of up to 4,096
+// slots take one block of 256 threads, whose barriers cost less.  Longer ones
+// take up to eight blocks of 512, as many as fill the machine, but with 2,048
+// slots or more to each, and more while a block's keys do not fit beside two
+// others'.  Few segments beyond 65,536 slots take 16 blocks of 256 (16 segments
+// of 128K: 100 us instead of 105; but eight of 18K 69 instead of 66, and 64 of
+// 66K 168 instead of 148).  Blocks of which only one fits an SM leave no place
+// for 16 clusters at once (two waves, 44 us for the selection instead of 35).
+struct Shape {
+  int threads, cluster;
+};
+Shape shape_of(int segs, int64_t slots) {
+  if (slots <= 4096) return {256, 1};
+  if (slots > 65536 && segs <= 16) return {256, 16};
   int c = 1;
-  while (c < kCluster && (int64_t)segs * 2 * c <= 152 && slots / (2 * c) >= 2048) c *= 2;
-  while (c < kCluster && slots * 4 > (int64_t)c * kMaxKeyBytes / 3) c *= 2;
-  return c;
+  while (c < 8 && (int64_t)segs * 2 * c <= 152 && slots / (2 * c) >= 2048) c *= 2;
+  while (c < 8 && slots * 4 > (int64_t)c * kMaxKeyBytes / 3) c *= 2;
+  return {512, c};
 }
 
 }  // namespace evict
@@ -482,9 +488,14 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   a.dst = reinterpret_cast<int32_t*>(ws + L.dst);
   a.status = reinterpret_cast<uint32_t*>(ws);
   const int segs = g.batch * g.slot_heads;
-  const bool small = a.cache.slots <= 4096;
-  const int cluster = cluster_size(segs, a.cache.slots), warps_of = small ? 8 : 16;
-  void (*const kernel)(KArgs, int) = small ? select<256> : select<512>;
+  const Shape shape = shape_of(segs, a.cache.slots);
+  const int cluster = shape.cluster, warps_of = shape.threads / 32;
+  void (*const kernel)(KArgs, int) = shape.threads == 256 ? select<256> : select<512>;
+  if (cluster > 8) {                      // more than every device has to take
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   // rows of 32 keys that a warp has room for
   const int64_t need = (a.cache.slots + 32 * cluster * warps_of - 1) / (32 * cluster * warps_of);
   const int room = (int)std::min<int64_t>(need, kMaxKeyBytes / (128 * warps_of));

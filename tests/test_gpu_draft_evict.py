@@ -138,6 +138,36 @@ def test_long_segments(slots, hkv, budgets):
             assert st == 0
 
 
+@pytest.mark.parametrize("slots,batch,budget", [(900001, 1, 900000), (900001, 1, 300000),
+                                                (430000, 17, 200000)])
+def test_more_slots_than_a_cluster_keeps(slots, batch, budget):
+    """Keys that find no room in shared memory are formed anew in every pass."""
+    g = torch.Generator(device=DEV).manual_seed(slots + budget)
+    pool = torch.randint(-2 ** 15, 2 ** 15, (batch, slots, 1, 64), generator=g, device=DEV,
+                         dtype=torch.int16).view(torch.bfloat16)
+    w = torch.randint(0, 5000, (batch, 1, slots), generator=g, device=DEV).float()
+    pos = torch.arange(slots, dtype=torch.int32, device=DEV).repeat(batch, 1, 1)
+    before = pool.clone()
+    new, wo, po, ws, _ = run([pool, pool.clone()], None, [slots] * batch, w, pos,
+                             [slots] * batch, out=True, budget=budget, recent=1000, sinks=5)
+    assert new.tolist() == [budget] * batch and B.ds_device_status(ws) == 0
+    for b in range(batch):
+        rank = w[b, 0].double()
+        rank[:5], rank[slots - 1000:] = math.inf, math.inf
+        order = torch.sort(rank, descending=True, stable=True).indices
+        keep = torch.zeros(slots, dtype=torch.bool, device=DEV)
+        keep[order[:budget]] = True
+        src = keep[budget:].nonzero().flatten() + budget
+        dst = (~keep[:budget]).nonzero().flatten()
+        at = torch.arange(budget, device=DEV)
+        at[dst] = src
+        assert torch.equal(po[b, 0, :budget].long(), at)
+        assert torch.equal(wo[b, 0, :budget], w[b, 0, at])
+        assert torch.equal(pool[b, :budget].view(torch.int16), before[b, at].view(torch.int16))
+        assert torch.equal(pool[b, budget:].view(torch.int16),
+                           before[b, budget:].view(torch.int16))
+
+
 @pytest.mark.parametrize("kind", ["equal", "zeros", "inf", "negative", "nan", "tiny", "forced"])
 def test_weights_of_every_kind(kind):
     lens, budget = [3000, 700], 600
