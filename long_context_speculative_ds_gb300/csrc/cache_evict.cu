@@ -56,7 +56,6 @@ DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan
 // 400,000 slots, 800,000 for few of them) they are formed anew from memory.
 constexpr int kMaxKeyBytes = 200 * 1024;
 constexpr int kBins = 2048;               // of a digit: 11, 11 and 10 bits
-constexpr int kCluster = 16;              // blocks, at most
 
 struct Shared {
   uint32_t hist[3][kBins];
@@ -94,7 +93,8 @@ DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
 // Mask of the first k of 32.
 DS_DEV uint32_t first_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; }
 
-template <int T>
+// T threads; clusters of up to MAXC blocks (see shape_of)
+template <int T, int MAXC>
 __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int room) {
   constexpr int NW = T / 32;
   extern __shared__ uint32_t s_keys[];    // [warp][room rows][32]
@@ -255,12 +255,12 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
     if (warp == 0) {
       uint32_t x = sh.part[round][31 - lane];   // lane l: part 31 - l, of all blocks
       if (C > 1) {                        // (their loads on their way together)
-        uint32_t v[kCluster];
+        uint32_t v[MAXC];
 #pragma unroll
-        for (int c = 1; c < kCluster; ++c)
+        for (int c = 1; c < MAXC; ++c)
           v[c] = cl.map_shared_rank(&sh.part[round][0], (rank + c) & (C - 1))[31 - lane];
 #pragma unroll
-        for (int c = 1; c < kCluster; ++c) x += c < C ? v[c] : 0;
+        for (int c = 1; c < MAXC; ++c) x += c < C ? v[c] : 0;
       }
       uint32_t incl = x;
 #pragma unroll
@@ -274,13 +274,13 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
       const uint2 own = *reinterpret_cast<const uint2*>(hist + bin0);
       uint32_t x0 = own.y, x1 = own.x;
       if (C > 1) {
-        uint2 v[kCluster];
+        uint2 v[MAXC];
 #pragma unroll
-        for (int c = 1; c < kCluster; ++c)
+        for (int c = 1; c < MAXC; ++c)
           v[c] = *reinterpret_cast<const uint2*>(
               cl.map_shared_rank(hist, (rank + c) & (C - 1)) + bin0);
 #pragma unroll
-        for (int c = 1; c < kCluster; ++c) {
+        for (int c = 1; c < MAXC; ++c) {
           x0 += c < C ? v[c].y : 0;
           x1 += c < C ? v[c].x : 0;
         }
@@ -490,7 +490,7 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   const int segs = g.batch * g.slot_heads;
   const Shape shape = shape_of(segs, a.cache.slots);
   const int cluster = shape.cluster, warps_of = shape.threads / 32;
-  void (*const kernel)(KArgs, int) = shape.threads == 256 ? select<256> : select<512>;
+  void (*const kernel)(KArgs, int) = shape.threads == 256 ? select<256, 16> : select<512, 8>;
   if (cluster > 8) {                      // more than every device has to take
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
