@@ -40,6 +40,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "dev_common.cuh"
@@ -841,13 +842,16 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// (the driver's, the same on every device; looked for again when it was not found)
 EncodeFn encode_fn() {
-  void* ptr = nullptr;
+  static std::atomic<void*> found{nullptr};
+  void* ptr = found.load(std::memory_order_relaxed);
   cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                       &q) != cudaSuccess ||
-      q != cudaDriverEntryPointSuccess)
-    return nullptr;
+  if (!ptr && cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                               cudaEnableDefault, &q) == cudaSuccess) {
+    if (q != cudaDriverEntryPointSuccess) ptr = nullptr;
+    found.store(ptr, std::memory_order_relaxed);
+  }
   return reinterpret_cast<EncodeFn>(ptr);
 }
 
@@ -864,7 +868,7 @@ bool cache_map(CUtensorMap* map, const void* base, const ds_decode_args& g) {
   // (lines of 128 bytes are fetched as they are: asking the L2 for 256 brings the
   // neighbouring head's too, 61 us instead of 43 for eight contexts of 16K with
   // eight heads of 64, slots before heads)
-  static const EncodeFn fn = encode_fn();     // (the driver's, the same on every device)
+  const EncodeFn fn = encode_fn();
   return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
