@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int seg = blockIdx.x / C, b = seg / a.slot_heads, w = seg % a.slot_heads;
-  const int len = __ldg(a.lens + b), next = __ldg(a.next_positions + b);
+  const int len = a.lens[b], next = a.next_positions[b];
   const int n = checked_len(len, a.cache.slots, a.status, tid == 0 && rank == 0 && w == 0);
   const bool cut = n > a.limit;
   const int keep = cut ? a.budget : n;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   bool nan = false;
   auto read = [&](int j) {
     const int i = row0 + 32 * j + lane, at = min(i, n - 1);
-    const uint32_t k = rank_key(__ldg(wt + at), __ldg(ps + at), a.sinks, from, nan);
+    const uint32_t k = rank_key(wt[at], ps[at], a.sinks, from, nan);
     return i < n ? k : 0u;
   };
   uint32_t* const mine = s_keys + warp * room * 32 + lane;
@@ -159,15 +159,15 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
     if (row0 + 32 * (j0 + 8) <= n) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = __ldg(xs + 32 * j);
-        p[j] = __ldg(qs + 32 * j);
+        x[j] = xs[32 * j];
+        p[j] = qs[32 * j];
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (i0 + 32 * j < n) {
-          x[j] = __ldg(xs + 32 * j);
-          p[j] = __ldg(qs + 32 * j);
+          x[j] = xs[32 * j];
+          p[j] = qs[32 * j];
         }
     }
   };

@@ -135,7 +135,7 @@ struct Piece {
 };
 
 DS_DEV Range seq_range(const KArgs& a, int b, bool report) {
-  return range_of(checked_len(__ldg(a.lens + b), a.cache.slots, a.status, report), a.window,
+  return range_of(checked_len(a.lens[b], a.cache.slots, a.status, report), a.window,
                   a.sinks);
 }
 
@@ -152,6 +152,7 @@ DS_DEV bool make_plan(const KArgs& a, Plan& plan, int64_t (*s_sum)[2]) {
   }
   units *= a.hkv;
   tiles *= a.hkv;
+  if (tid == 0) plan.first.left = 0;
   int64_t incl = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -347,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       auto page_of = [&](int t, int s) {
         return a.cache.page_table && sub_visible(t, s)
-                   ? __ldg(a.cache.page_table + (int64_t)pc.b * a.cache.max_pages +
-                           ((tile_slot(r, t) + 16 * s) >> a.cache.page_shift))
+                   ? a.cache.page_table[(int64_t)pc.b * a.cache.max_pages +
+                                        ((tile_slot(r, t) + 16 * s) >> a.cache.page_shift)]
                    : pc.b;
       };
       int ids = 0, next = page_of(pc.t0 + (lane >> 2), sub);
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (8 * i + g < G) {
           const uint16_t* p = a.q + (int64_t)pc.b * a.q_stride +
                               (int64_t)(pc.h * G + 8 * i + g) * D + ks * 16 + 2 * t4;
-          q[i][ks][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          q[i][ks][1] = __ldg(reinterpret_cast<const uint32_t*>(p + 8));
+          q[i][ks][0] = *reinterpret_cast<const uint32_t*>(p);
+          q[i][ks][1] = *reinterpret_cast<const uint32_t*>(p + 8);
         }
       }
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     }
   }
+  if (tid == 0 && *abort) flag(a.status, DS_DEV_TIMEOUT);
 }
 
 // (max, sum) of two parts of a row.
@@ -633,7 +635,7 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
   const int b = real ? (int)(row / a.hq) : 0, hq = real ? (int)(row % a.hq) : 0;
   const int h = hq / G, g = hq % G;
   const int2 d = a.desc[b * a.hkv + h];   // (beside the length; not looked at without one)
-  const int n = real ? checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false) : 0;
+  const int n = real ? checked_len(a.lens[b], a.cache.slots, nullptr, false) : 0;
   float o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.f;
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS == 0 || SLOTS * CHUNKS 
           (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
       // (beside the length; not looked at without one)
       int2 d = a.desc[seg0 + min(i / 4, chunks - 1) / per_head];
-      const int n = checked_len(__ldg(a.lens + b), a.cache.slots, nullptr, false);
+      const int n = checked_len(a.lens[b], a.cache.slots, nullptr, false);
       const int64_t start = (it % spans) * SPAN;
       if (start >= n) continue;
       const int t0 = (int)start + tid;

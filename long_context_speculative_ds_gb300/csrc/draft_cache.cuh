@@ -1,5 +1,8 @@
 // Where a slot of the draft's cache lies (include/ds.h, "The draft's cache"),
-// shared by the kernels that write, read and move its rows.
+// shared by the kernels that write, read and move its rows.  These kernels start
+// before the one in front of them has ended (and wait for it), so what that one
+// may write (lengths, tables, sums) is read with ordinary loads, not as data that
+// stays the same while they run.
 #pragma once
 
 #include <stdint.h>
@@ -38,7 +41,7 @@ DraftCache draft_cache(const Args& g) {
 // Page of a slot of sequence b (0 <= slot < slots); -1 when its id is none.
 DS_DEV int slot_page(const DraftCache& c, int b, int slot) {
   if (!c.page_table) return b;
-  const int pg = __ldg(c.page_table + (int64_t)b * c.max_pages + (slot >> c.page_shift));
+  const int pg = c.page_table[(int64_t)b * c.max_pages + (slot >> c.page_shift)];
   return (uint32_t)pg < (uint32_t)c.num_pages ? pg : -1;
 }
 // Elements from the pool's start to head 0 of the slot, in page pg.

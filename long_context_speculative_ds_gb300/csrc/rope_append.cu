@@ -66,7 +66,7 @@ DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
   int lo = 0, n = batch;
   while (n > 1) {
     const int step = (n + 31) / 32, i = lane * step;
-    const uint32_t at = __ballot_sync(0xffffffffu, i < n && __ldg(offs + lo + min(i, n - 1)) <= row);
+    const uint32_t at = __ballot_sync(0xffffffffu, i < n && offs[lo + min(i, n - 1)] <= row);
     const int k = max(__ffs(~at) - 2, at == ~0u ? 31 : 0);   // last of the run from lane 0
     lo += k * step;
     n = min(step, n - k * step);
@@ -76,9 +76,9 @@ DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
 
 // Rows [n0, n0 + n) and first slot of sequence b; false when they cannot be used.
 DS_DEV bool rope_rows_of(const RopeKArgs& a, int b, int& n0, int& n, int& from) {
-  n0 = __ldg(a.row_offsets + b);
-  const int n1 = __ldg(a.row_offsets + b + 1);
-  from = __ldg(a.from_lens + b);
+  n0 = a.row_offsets[b];
+  const int n1 = a.row_offsets[b + 1];
+  from = a.from_lens[b];
   n = n1 - n0;
   return n0 >= 0 && n1 >= n0 && n1 <= a.n_rows && from >= 0 && (int64_t)from + n <= a.cache.slots;
 }
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
       v[k] = *reinterpret_cast<const uint4*>(p + e1);
     }
   };
-  const int pos = __ldg(a.positions + row);
+  const int pos = a.positions[row];
   load(g0);                               // beside what the position asks for
   if (pos < 0) {
     if (lane == 0) flag(a.status, DS_DEV_BAD_LENGTH);
