@@ -624,7 +624,7 @@ DS_DEV float2 join_lanes(float2 x) {
 constexpr int kFinishWarps = 8;
 constexpr int kFinishThreads = 32 * kFinishWarps;
 
-// An output row by WPR warps, which share its pieces: lane l has values 4 l ..
+// An output row by `parts` warps, which share its pieces: lane l has values 4 l ..
 // 4 l + 3 (2 l at D = 64) of eight pieces on their way at once.
 template <int D>
 DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const int parts,
@@ -634,8 +634,10 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
   const bool real = row < (int64_t)a.batch * a.hq;
   const int b = real ? (int)(row / a.hq) : 0, hq = real ? (int)(row % a.hq) : 0;
   const int h = hq / G, g = hq % G;
-  const int2 d = a.desc[b * a.hkv + h];   // (beside the length; not looked at without one)
   const int n = real ? checked_len(a.lens[b], a.cache.slots, nullptr, false) : 0;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int2 d = a.desc[b * a.hkv + h];   // (not looked at without slots)
   float o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.f;
@@ -739,9 +741,10 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS == 0 || SLOTS * CHUNKS 
   __shared__ float s_ref[32];
   __shared__ float s_o[kFinishWarps][D];
   __shared__ float2 s_ml[kFinishWarps];
-  grid_dep_wait();
-  grid_dep_launch_dependents();
   const int tid = threadIdx.x, G = a.group;
+  // Every block of the split pass has waited for what came before it when it lets
+  // this kernel's blocks start, so lengths and input weights are read, and places
+  // worked out, before this kernel's own wait.
   if (CHUNKS == 0 || (int)blockIdx.x < row_blocks) {      // `parts` warps per output row
     const int w = blockIdx.x * kFinishWarps + (tid >> 5);
     finish_row<D>(a, w / parts, w % parts, parts, s_o, s_ml);
@@ -756,71 +759,82 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS == 0 || SLOTS * CHUNKS 
     const int chunks = per_head * (a.slot_heads == 1 ? a.hkv : 1);
     // this thread's part of a row's sum: row i % 4 of chunk i / 4, pieces from l on
     const int i = tid / LPR, l = tid % LPR;
-    for (int64_t it = blockIdx.x - row_blocks; it < items; it += gridDim.x - row_blocks) {
+    int64_t seg0, at;                       // the item: first segment, place of its weights
+    int n, t0;                              // slots of its sequence, this thread's first
+    float old[SLOTS];
+    // slots past the end: the thread's first again (or the last one), unused
+    auto slot = [&](int k) { return t0 + k * kFinishThreads < n ? k * kFinishThreads : 0; };
+    auto item = [&](int64_t it) {
       const int64_t bw = it / spans;
       const int b = (int)(bw / a.slot_heads);
-      const int64_t seg0 =
-          (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
-      // (beside the length; not looked at without one)
-      int2 d = a.desc[seg0 + min(i / 4, chunks - 1) / per_head];
-      const int n = checked_len(a.lens[b], a.cache.slots, nullptr, false);
-      const int64_t start = (it % spans) * SPAN;
-      if (start >= n) continue;
-      const int t0 = (int)start + tid;
-      const Range r = range_of(n, a.window, a.sinks);
-      // slots past the end: the thread's first again (or the last one), unused
-      const int first = min(t0, n - 1);
-      auto slot = [&](int k) { return t0 + k * kFinishThreads < n ? k * kFinishThreads : 0; };
-      const int64_t at = bw * a.slot_stride;
-      float sum[SLOTS], old[SLOTS];
+      seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
+      at = bw * a.slot_stride;
+      n = checked_len(a.lens[b], a.cache.slots, nullptr, false);
+      const int64_t start = (it - bw * spans) * SPAN;
+      t0 = (int)start + tid;
+      if (start >= n) return false;
+      const float* p = a.w_in + at + min(t0, n - 1);
 #pragma unroll
-      for (int k = 0; k < SLOTS; ++k) {
-        sum[k] = 0.f;
-        old[k] = a.w_in ? a.w_in[at + first + slot(k)] : 0.f;
-      }
-      for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
-        const int mine = min(c0 + i / 4, chunks - 1), g = mine % per_head * 4 + i % 4;
-        const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
-        if (c0 > 0) d = a.desc[seg0 + mine / per_head];
-        const float2* const p_ml = a.part_ml + (int64_t)d.x * G + g;
-        float2 ml = make_float2(-CUDART_INF_F, 0.f);
-        if (row && l < d.y) ml = p_ml[(int64_t)l * G];
-        float s[CHUNKS][SLOTS][4];
+      for (int k = 0; k < SLOTS; ++k) old[k] = a.w_in ? p[slot(k)] : 0.f;
+      return true;
+    };
+    int64_t it = blockIdx.x - row_blocks;
+    bool work = it < items && item(it);
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    while (it < items) {
+      if (work) {
+        const Range r = range_of(n, a.window, a.sinks);
+        const int first = min(t0, n - 1);
+        float sum[SLOTS];
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          const int ch = min(c0 + c, chunks - 1);
-          const float* p = a.logits + ((seg0 + ch / per_head) * a.cache.slots + first) * G;
+        for (int k = 0; k < SLOTS; ++k) sum[k] = 0.f;
+        for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
+          const int mine = min(c0 + i / 4, chunks - 1), g = mine % per_head * 4 + i % 4;
+          const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
+          const int2 d = a.desc[seg0 + mine / per_head];
+          float s[CHUNKS][SLOTS][4];
 #pragma unroll
-          for (int k = 0; k < SLOTS; ++k)
-            load_logits(s[c][k], p + slot(k) * G, ch % per_head * 4, G);
-        }
-        __syncthreads();                  // the last ones' sums are used
-        if (row) {
-#pragma unroll 4
-          for (int j = l + LPR; j < d.y; j += LPR) ml = join_ml(ml, p_ml[(int64_t)j * G]);
-        }
-        ml = join_lanes<LPR>(ml);
-        // (no row: a sum of infinity, weights of zero)
-        if (i < 4 * CHUNKS && l == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
-        __syncthreads();
+          for (int c = 0; c < CHUNKS; ++c) {
+            const int ch = min(c0 + c, chunks - 1);
+            const float* p = a.logits + ((seg0 + ch / per_head) * a.cache.slots + first) * G;
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
+            for (int k = 0; k < SLOTS; ++k)
+              load_logits(s[c][k], p + slot(k) * G, ch % per_head * 4, G);
+          }
+          const float2* const p_ml = a.part_ml + (int64_t)d.x * G + g;
+          float2 ml = make_float2(-CUDART_INF_F, 0.f), ml2 = ml;
+          if (row && l < d.y) ml = p_ml[(int64_t)l * G];
+          if (row && l + LPR < d.y) ml2 = p_ml[(int64_t)(l + LPR) * G];
+          __syncthreads();                  // the last ones' sums are used
+          ml = join_ml(ml, ml2);
+          if (row)
+            for (int j = l + 2 * LPR; j < d.y; j += LPR) ml = join_ml(ml, p_ml[(int64_t)j * G]);
+          ml = join_lanes<LPR>(ml);
+          // (no row: a sum of infinity, weights of zero)
+          if (i < 4 * CHUNKS && l == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
+          __syncthreads();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ref = s_ref[4 * c + j];
-            if (ref != CUDART_INF_F) {
+          for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
-              for (int k = 0; k < SLOTS; ++k) {
-                const float p = ptx::ex2(s[c][k][j] - ref);
-                sum[k] += visible(r, first + slot(k)) ? p : 0.f;
+            for (int j = 0; j < 4; ++j) {
+              const float ref = s_ref[4 * c + j];
+              if (ref != CUDART_INF_F) {
+#pragma unroll
+                for (int k = 0; k < SLOTS; ++k) {
+                  const float p = ptx::ex2(s[c][k][j] - ref);
+                  sum[k] += visible(r, first + slot(k)) ? p : 0.f;
+                }
               }
             }
-          }
-      }
+        }
 #pragma unroll
-      for (int k = 0; k < SLOTS; ++k)
-        if (t0 + k * kFinishThreads < n)
-          a.w_out[at + t0 + k * kFinishThreads] = fmaf(old[k], a.decay, sum[k]);
+        for (int k = 0; k < SLOTS; ++k)
+          if (t0 + k * kFinishThreads < n)
+            a.w_out[at + t0 + k * kFinishThreads] = fmaf(old[k], a.decay, sum[k]);
+      }
+      it += gridDim.x - row_blocks;
+      work = it < items && item(it);
     }
   }
 }

@@ -267,18 +267,18 @@ cudaError_t launch_rope_append(const ds_rope_args& g, cudaStream_t stream) {
   a.magnitude = g.magnitude;
   a.sin_sign = g.inverse ? -1.f : 1.f;
   // a double's 53 bits leave each frequency (at most a radian in use) off by
-  // less than 2^-53 of a turn, and the angle, at positions below 2^31, by
-  // less than 2^-22 of one; at 2^17 by less than 2^-36
+  // less than 2^-52 of a turn, and the angle, at positions below 2^31, by
+  // less than 2^-21 of one; at 2^17 by less than 2^-35
   // (base^(-2j/r) as a product of two powers: sixteen calls of pow, not 64)
-  constexpr double kTau = 6.283185307179586;
+  constexpr double kTurns = 1.0 / 6.283185307179586;   // of a radian
   double lo[8], hi[8];
   if (!g.inv_freq)
     for (int k = 0; k < 8; ++k) {
       lo[k] = std::pow((double)g.rope_base, -2.0 * k / a.rotary);
-      hi[k] = std::pow((double)g.rope_base, -16.0 * k / a.rotary) / kTau;
+      hi[k] = std::pow((double)g.rope_base, -16.0 * k / a.rotary) * kTurns;
     }
   for (int j = 0; j < a.rotary / 2; ++j) {
-    const double turns = g.inv_freq ? g.inv_freq[j] / kTau : lo[j & 7] * hi[j >> 3];
+    const double turns = g.inv_freq ? g.inv_freq[j] * kTurns : lo[j & 7] * hi[j >> 3];
     const double frac = turns - std::floor(turns);   // whole turns drop out
     a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
   }

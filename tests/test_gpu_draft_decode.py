@@ -199,6 +199,46 @@ def test_weights_in_place_and_scale():
         assert B.ds_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("hw", [1, 4])
+def test_many_calls_in_a_row_in_place(hw, captured):
+    """Each call's sums are the next one's input, with no pause between them,
+    while lengths change and come back."""
+    lens, calls = [2500, 700, 64], 60
+    q, pools, table = make(lens, 8, 4, 128, torch.bfloat16, "NHD", 16, 3)
+    once = run(q, pools, table, lens, hw=hw)[2]
+    slots = once.shape[2]
+    w0 = torch.rand(3, hw, slots, device=DEV)
+    w, dev_lens, full = w0.clone(), i32(lens), i32(lens)
+    _, _, _, ws, a = run(q, pools, table, lens, hw=hw, w_in=w, in_place=True, decay=0.875,
+                         lens_dev=dev_lens)
+    w.copy_(w0)
+
+    def go():
+        for _ in range(calls // 3):
+            B.ds_decode_attn(a)
+            dev_lens.zero_()
+            B.ds_decode_attn(a)                      # no slots: nothing to add to
+            dev_lens.copy_(full)
+            B.ds_decode_attn(a)
+            B.ds_decode_attn(a)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+        graph.replay()
+    else:
+        go()
+    torch.cuda.synchronize()
+    f = 0.875 ** calls
+    for b, n in enumerate(lens):
+        want = f64(w0[b, :, :n]) * f + f64(once[b, :, :n]) * (1 - f) / 0.125
+        # a product and a sum a call, each off by half a step of the result
+        assert (np.abs(f64(w[b, :, :n]) - want) <= calls * 2.0 ** -23 * (want + 1)).all()
+        assert torch.equal(w[b, :, n:], w0[b, :, n:])
+    assert B.ds_device_status(ws) == 0
+
+
 def test_large_logits_and_infinities():
     """Logits up to thousands, a row dominated by one key, an infinite key."""
     lens = [300, 300, 300]
