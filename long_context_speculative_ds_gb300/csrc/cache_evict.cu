@@ -45,8 +45,13 @@ struct KArgs {
   int32_t recent, sinks;
   int32_t* new_lens;
   int32_t *count, *src, *dst;
+  int32_t alone;                 // no second kernel: `select` moves the rows itself
   uint32_t* status;
 };
+
+// Segments that can have no more moves than this are moved by `select`: a token
+// given up per call by a cache with a few slots above its budget saves a launch.
+constexpr int kFewMoves = 64;
 
 // (without branches, so that the loads of many slots go out together)
 DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan) {
@@ -56,6 +61,57 @@ DS_DEV uint32_t rank_key(float w, int pos, int sinks, int recent_from, bool& nan
   const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
   nan |= none && !must;
   return must ? ~0u : none ? 1u : k;      // (-inf is 0x007fffff; 0: no slot)
+}
+
+// Moves m0 .. m0 + moves - 1 (at most 32) of a segment, by a warp: a lane looks up
+// one move's places, then the rows go BATCH (twice as many at 64-wide heads) at
+// once, a lane 16 bytes of K or V, a move's heads one behind the other.
+template <int D, int BATCH>
+DS_DEV void move_rows(const KArgs& a, const int seg, const int64_t m0, const int moves) {
+  constexpr int VECS = D / 8;             // 16-byte vectors of a head's row
+  constexpr int AT = 32 / (2 * VECS);     // rows (their K and V) of a warp at once
+  const int b = seg / a.slot_heads, lane = threadIdx.x & 31;
+  const bool shared = a.slot_heads == 1;
+  const int heads = shared ? a.cache.num_kv_heads : 1, h0 = shared ? 0 : seg % a.slot_heads;
+  uint16_t* const pool = lane % (2 * VECS) < VECS ? a.cache.pool[0] : a.cache.pool[1];
+  const int col = lane % VECS * 8, mine = lane / (2 * VECS);
+  int64_t from = -1, to = -1;             // -1: nothing to move
+  if (lane < moves) {
+    const int s = a.src[(int64_t)seg * a.moves + m0 + lane];
+    const int d = a.dst[(int64_t)seg * a.moves + m0 + lane];
+    const int64_t base = (int64_t)seg * a.slot_stride;
+    (a.weights_out ? a.weights_out : a.weights)[base + d] = a.weights[base + s];
+    (a.positions_out ? a.positions_out : a.positions)[base + d] = a.positions[base + s];
+    const int pf = slot_page(a.cache, b, s), pt = slot_page(a.cache, b, d);
+    if (pf >= 0 && pt >= 0) {
+      from = slot_at(a.cache, pf, s) + (int64_t)h0 * a.cache.head_stride;
+      to = slot_at(a.cache, pt, d) + (int64_t)h0 * a.cache.head_stride;
+    } else {
+      flag(a.status, DS_DEV_BAD_PAGE);
+    }
+  }
+  __syncwarp();
+  const int rows = moves * heads;
+  int m = mine / heads, h = mine % heads; // of this lane's next row
+  for (int r0 = 0; r0 < rows; r0 += AT * BATCH) {
+    uint4 x[BATCH];
+    int64_t at[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t f = __shfl_sync(0xffffffffu, from, m & 31);
+      at[k] = __shfl_sync(0xffffffffu, to, m & 31);
+      const int64_t off = (int64_t)h * a.cache.head_stride + col;
+      if (r0 + k * AT + mine >= rows || at[k] < 0)
+        at[k] = -1;
+      else
+        at[k] += off;
+      if (at[k] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(pool + f + off));
+      for (h += AT; h >= heads; h -= heads) ++m;
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (at[k] >= 0) *reinterpret_cast<uint4*>(pool + at[k]) = x[k];
+  }
 }
 
 // A cluster of blocks per segment; its rows of 32 slots in equal runs to the
@@ -98,6 +154,11 @@ DS_DEV int2 warps_prefix(int2 v, int2* s_warp, int2& total) {
                    __shfl_sync(0xffffffffu, incl.y - w.y, warp));
 }
 
+DS_DEV void few_rows(const KArgs& a, const int seg, const int64_t m0, const int moves) {
+  if (a.head_dim == 128) move_rows<128, 4>(a, seg, m0, moves);
+  else move_rows<64, 4>(a, seg, m0, moves);
+}
+
 // Mask of the first k of 32.
 DS_DEV uint32_t first_bits(int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; }
 
@@ -118,14 +179,41 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int seg = blockIdx.x / C, b = seg / a.slot_heads, w = seg % a.slot_heads;
+  const int64_t base = (int64_t)seg * a.slot_stride;
+  const float* wt = a.weights + base;
+  const int32_t* ps = a.positions + base;
+  // Eight rows' loads on their way together, the next eight's behind them.  A
+  // segment of one block has its rows dealt by the slots there are, so that the
+  // first ones' loads go out beside the length's.
+  float x[8];
+  int p[8];
+  auto fetch = [&](const int slot0, const int end) {
+    const int i0 = slot0 + lane;
+    const float* const xs = wt + i0;
+    const int32_t* const qs = ps + i0;
+    if (slot0 + 32 * 8 <= end) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = xs[32 * j];
+        p[j] = qs[32 * j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + 32 * j < end) {
+          x[j] = xs[32 * j];
+          p[j] = qs[32 * j];
+        }
+    }
+  };
+  const bool single = T == 256 && C == 1;
   const int len = a.lens[b], next = a.next_positions[b];
+  int per = single ? ((int)a.cache.slots + 32 * NW - 1) / (32 * NW) : 0;   // rows of a warp
+  if (single) fetch(warp * per * 32, (int)a.cache.slots);
   const int n = checked_len(len, a.cache.slots, a.status, tid == 0 && rank == 0 && w == 0);
   const bool cut = n > a.limit;
   const int keep = cut ? a.budget : n;
   if (tid == 0 && rank == 0 && w == 0) a.new_lens[b] = cut ? keep : len;
-  const int64_t base = (int64_t)seg * a.slot_stride;
-  const float* wt = a.weights + base;
-  const int32_t* ps = a.positions + base;
   float* wo = a.weights_out ? a.weights_out + base : nullptr;
   int32_t* po = a.positions_out ? a.positions_out + base : nullptr;
   if (!cut) {                             // (the whole cluster)
@@ -137,7 +225,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
     return;
   }
   const int from = (int)max((int64_t)next - a.recent, (int64_t)INT_MIN);
-  const int rows = (n + 31) / 32, per = (rows + C * NW - 1) / (C * NW);
+  if (!single) per = ((n + 31) / 32 + C * NW - 1) / (C * NW);
   const int row0 = (rank * NW + warp) * per * 32;       // slot of the warp's first row
   bool nan = false;
   auto read = [&](int j) {
@@ -147,31 +235,9 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   };
   uint32_t* const mine = s_keys + warp * room * 32 + lane;
   const int kept = min(per, room);
-  // Eight rows' loads on their way together, the next eight's behind them; what
-  // is below the budget goes into arrays of its own at once (`move` overwrites
-  // the slots that are given up).
-  float x[8];
-  int p[8];
-  auto fetch = [&](int j0) {
-    const int i0 = row0 + 32 * j0 + lane;
-    const float* const xs = wt + i0;
-    const int32_t* const qs = ps + i0;
-    if (row0 + 32 * (j0 + 8) <= n) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = xs[32 * j];
-        p[j] = qs[32 * j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i0 + 32 * j < n) {
-          x[j] = xs[32 * j];
-          p[j] = qs[32 * j];
-        }
-    }
-  };
-  fetch(0);
+  // What is below the budget goes into arrays of its own at once (the moves
+  // overwrite the slots that are given up).
+  if (!single) fetch(row0, n);
   for (int j0 = 0; j0 < per; j0 += 8) {
     const int i0 = row0 + 32 * j0 + lane;
     uint32_t k[8];
@@ -191,7 +257,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
       nan |= none && in;
       if (!in) k[j] = 0u;
     }
-    if (j0 + 8 < per) fetch(j0 + 8);
+    if (j0 + 8 < per) fetch(row0 + 32 * (j0 + 8), n);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j0 + j < kept) mine[32 * (j0 + j)] = k[j];
@@ -204,7 +270,7 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   };
   // ---- one slot to give up, as a cache at its budget does every token: the
   // lightest, of equal ones the last; the one behind the budget takes its place
-  // (a call on 2,049 slots 6.3 us instead of 11.4)
+  // (a call on 2,049 slots 6.3 us instead of 11.4, and 4.1 without a second kernel)
   if (n - keep == 1) {
     unsigned long long least = ~0ull;     // key, then slot from the end
     each([&](uint32_t k, int j) {
@@ -229,6 +295,8 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
         a.src[(int64_t)seg * a.moves] = keep;
         a.dst[(int64_t)seg * a.moves] = gone;
       }
+      __syncwarp();
+      if (a.alone && gone < keep) few_rows(a, seg, 0, 1);
     }
     if (nan) flag(a.status, DS_DEV_BAD_VALUE);
     if (C > 1) cl.sync();                 // others may still be read
@@ -384,67 +452,23 @@ __global__ void __launch_bounds__(T, 1024 / T) select(const KArgs a, const int r
   for (int j = kept; j < per; ++j) list(stays(read(j), seen), j);
   if (tid == 0 && rank == 0) a.count[seg] = all;
   if (C > 1) cl.sync();                   // others may still read this block's sums
+  if (a.alone) {
+    if (C == 1) __syncthreads();          // the lists are whole
+    const int share = (all + C * NW - 1) / (C * NW), m0 = (rank * NW + warp) * share;
+    if (m0 < all) few_rows(a, seg, m0, min(share, all - m0));
+  }
 }
 
-// A warp takes the moves of a segment 32 kv heads' rows at a time (32 moves of
-// one head, or 4 of eight that move together): a lane looks up one move's
-// places, then the rows go eight (sixteen) at once, a lane 16 bytes of K or V,
-// a move's heads one behind the other.
+// The moves of a segment go 32 kv heads' rows to a warp at a time (32 moves of
+// one head, or 4 of eight that move together).
 template <int D>
 __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
-  constexpr int VECS = D / 8;             // 16-byte vectors of a head's row
-  constexpr int AT = 32 / (2 * VECS);     // rows (their K and V) of a warp at once
-  constexpr int BATCH = 8;                // loads on their way
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int seg = blockIdx.x, b = seg / a.slot_heads, w = seg % a.slot_heads;
-  const int lane = threadIdx.x & 31;
-  const bool shared = a.slot_heads == 1;
-  const int heads = shared ? a.cache.num_kv_heads : 1, h0 = shared ? 0 : w;
-  const int count = a.count[seg];
-  const int32_t* src = a.src + (int64_t)seg * a.moves;
-  const int32_t* dst = a.dst + (int64_t)seg * a.moves;
-  uint16_t* const pool = lane % (2 * VECS) < VECS ? a.cache.pool[0] : a.cache.pool[1];
-  const int col = lane % VECS * 8, mine = lane / (2 * VECS);
+  const int seg = blockIdx.x, count = a.count[seg];
   for (int64_t m0 = ((int64_t)blockIdx.y * 8 + (threadIdx.x >> 5)) * per; m0 < count;
-       m0 += (int64_t)gridDim.y * 8 * per) {
-    const int moves = (int)min((int64_t)per, count - m0);
-    int64_t from = -1, to = -1;           // -1: nothing to move
-    if (lane < moves) {
-      const int s = src[m0 + lane], d = dst[m0 + lane];
-      const int64_t base = (int64_t)seg * a.slot_stride;
-      (a.weights_out ? a.weights_out : a.weights)[base + d] = a.weights[base + s];
-      (a.positions_out ? a.positions_out : a.positions)[base + d] = a.positions[base + s];
-      const int pf = slot_page(a.cache, b, s), pt = slot_page(a.cache, b, d);
-      if (pf >= 0 && pt >= 0) {
-        from = slot_at(a.cache, pf, s) + (int64_t)h0 * a.cache.head_stride;
-        to = slot_at(a.cache, pt, d) + (int64_t)h0 * a.cache.head_stride;
-      } else {
-        flag(a.status, DS_DEV_BAD_PAGE);
-      }
-    }
-    const int rows = moves * heads;
-    int m = mine / heads, h = mine % heads;       // of this lane's next row
-    for (int r0 = 0; r0 < rows; r0 += AT * BATCH) {
-      uint4 x[BATCH];
-      int64_t at[BATCH];
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int64_t f = __shfl_sync(0xffffffffu, from, m & 31);
-        at[k] = __shfl_sync(0xffffffffu, to, m & 31);
-        const int64_t off = (int64_t)h * a.cache.head_stride + col;
-        if (r0 + k * AT + mine >= rows || at[k] < 0)
-          at[k] = -1;
-        else
-          at[k] += off;
-        if (at[k] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(pool + f + off));
-        for (h += AT; h >= heads; h -= heads) ++m;
-      }
-#pragma unroll
-      for (int k = 0; k < BATCH; ++k)
-        if (at[k] >= 0) *reinterpret_cast<uint4*>(pool + at[k]) = x[k];
-    }
-  }
+       m0 += (int64_t)gridDim.y * 8 * per)
+    move_rows<D, 8>(a, seg, m0, (int)min((int64_t)per, count - m0));
 }
 
 // Threads of a block and blocks of a segment's cluster.  Segments of up to 4,096
@@ -495,6 +519,7 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   a.src = reinterpret_cast<int32_t*>(ws + L.src);
   a.dst = reinterpret_cast<int32_t*>(ws + L.dst);
   a.status = reinterpret_cast<uint32_t*>(ws);
+  a.alone = L.moves <= kFewMoves;
   const int segs = g.batch * g.slot_heads;
   const Shape shape = shape_of(segs, a.cache.slots);
   const int cluster = shape.cluster, warps_of = shape.threads / 32;
@@ -524,7 +549,7 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a, room);
-  if (e != cudaSuccess || L.moves == 0) return e;
+  if (e != cudaSuccess || a.alone) return e;
   // moves of a warp at a time, and eight blocks an SM as far as there can be moves
   const int per = std::max(1, 32 / (g.slot_heads == 1 ? g.num_kv_heads : 1));
   const int64_t warps = (L.moves + per - 1) / per;
