@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "dev_common.cuh"
 #include "draft_cache.cuh"
@@ -50,6 +51,7 @@ struct RopeKArgs {
   int32_t n_rows, batch, hq, hkv, heads;   // heads = query + key (+ value) heads
   int32_t slot_heads, rotary, write;       // write: there is a cache
   int32_t per;                    // head groups of a warp
+  uint64_t heads_magic;           // 2^32 / heads, rounded up
   int32_t row_blocks;             // the blocks behind these look at the sequences
   float magnitude, sin_sign;
   unsigned long long turn[64];    // frequency j as a 64-bit fraction of a turn
@@ -57,6 +59,9 @@ struct RopeKArgs {
 
 constexpr int kRopeWarps = 4;             // warps of a block
 constexpr int kRopeBatch = 4;             // head groups of a warp, their loads together
+// Rows of few heads go several to a warp, when there are enough of them to fill
+// the machine all the same.
+constexpr int kFewHeads = 12, kManyRows = 16384, kMostRows = 65536;
 
 // The sequence before the first row_offsets[b] above row, by all lanes of a
 // warp, 32 at a time (offsets that are not monotone give some sequence; its own
@@ -119,6 +124,53 @@ DS_DEV void turn(uint4& u, uint4& v, const float4 (&cs)[4]) {
   v = make_uint4(vw[0], vw[1], vw[2], vw[3]);
 }
 
+// Kind (query, key, value) and number of a row's head hh.
+DS_DEV int head_of(const RopeKArgs& a, int hh, int& h) {
+  const int ty = hh < a.hq ? 0 : hh < a.hq + a.hkv ? 1 : 2;
+  h = hh - (ty > 0 ? a.hq : 0) - (ty > 1 ? a.hkv : 0);
+  return ty;
+}
+DS_DEV const uint16_t* head_row(const RopeKArgs& a, int ty, int64_t row, int off) {
+  return (ty == 0 ? a.x[0] : ty == 1 ? a.x[1] : a.x[2]) +
+         row * (ty == 0 ? a.stride[0] : ty == 1 ? a.stride[1] : a.stride[2]) + off;
+}
+// A lane's two vectors of a head to where they belong; at: the slot's place in
+// the pools, -1 for none.
+template <int D>
+DS_DEV void put_head(const RopeKArgs& a, int ty, int64_t row, int h, int64_t at, const uint4& u,
+                     const uint4& v, int e0, int e1) {
+  uint16_t* o = ty == 0 ? a.out[0] : ty == 1 ? a.out[1] : nullptr;
+  if (o) {
+    o += row * (ty == 0 ? a.out_stride[0] : a.out_stride[1]) + (int64_t)h * D;
+    *reinterpret_cast<uint4*>(o + e0) = u;
+    *reinterpret_cast<uint4*>(o + e1) = v;
+  }
+  if (ty > 0 && at >= 0) {
+    o = (ty == 1 ? a.cache.pool[0] : a.cache.pool[1]) + at + (int64_t)h * a.cache.head_stride;
+    *reinterpret_cast<uint4*>(o + e0) = u;
+    *reinterpret_cast<uint4*>(o + e1) = v;
+  }
+}
+// Cosine and sine at a position of a frequency, times the magnitude.  position *
+// frequency wraps modulo one turn in 64 bits; its upper half, read as a signed
+// number, is the angle in units of pi / 2^31.
+DS_DEV float2 turn_of(const RopeKArgs& a, int pos, unsigned long long frequency) {
+  const unsigned long long t = (unsigned long long)pos * frequency;
+  float sn, c;
+  sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &sn, &c);
+  return make_float2(c * a.magnitude, sn * a.magnitude * a.sin_sign);
+}
+// The last blocks have a thread per sequence, which checks its offsets and
+// length even when no row is mapped to it, and writes the new length.
+DS_DEV void check_sequences(const RopeKArgs& a) {
+  const int b = (blockIdx.x - a.row_blocks) * 32 * kRopeWarps + threadIdx.x;
+  if (b >= a.batch || blockIdx.y > 0) return;
+  int n0, n, from;
+  const bool usable = rope_rows_of(a, b, n0, n, from);
+  if (!usable) flag(a.status, DS_DEV_BAD_LENGTH);
+  if (a.new_lens) a.new_lens[b] = usable ? from + n : from;
+}
+
 template <int D, bool BF, bool HALVES>
 __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArgs a) {
   constexpr int LPH = D / 16;             // lanes of a head
@@ -127,15 +179,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // The last blocks have a thread per sequence, which checks its offsets and
-  // length even when no row is mapped to it, and writes the new length.
   if ((int)blockIdx.x >= a.row_blocks) {
-    const int b = (blockIdx.x - a.row_blocks) * 32 * kRopeWarps + threadIdx.x;
-    if (b >= a.batch || blockIdx.y > 0) return;
-    int n0, n, from;
-    const bool usable = rope_rows_of(a, b, n0, n, from);
-    if (!usable) flag(a.status, DS_DEV_BAD_LENGTH);
-    if (a.new_lens) a.new_lens[b] = usable ? from + n : from;
+    check_sequences(a);
     return;
   }
   const int64_t row64 = (int64_t)blockIdx.x * kRopeWarps + warp;
@@ -149,12 +194,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
   // the lane's two vectors of a head
   const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
   const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
-  // the heads of a row: query, key, value
-  auto which = [&](int hh, int& h) {
-    const int ty = hh < a.hq ? 0 : hh < a.hq + a.hkv ? 1 : 2;
-    h = hh - (ty > 0 ? a.hq : 0) - (ty > 1 ? a.hkv : 0);
-    return ty;
-  };
   uint4 u[kRopeBatch], v[kRopeBatch];
   auto load = [&](int gb) {
 #pragma unroll
@@ -162,11 +201,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
       const int hh = (gb + k) * HPW + sub;
       if (gb + k >= g1 || hh >= a.heads) continue;
       int h;
-      const int ty = which(hh, h);
+      const int ty = head_of(a, hh, h);
       // plain loads: with q_out = q the same bytes are written below
-      const uint16_t* p = (ty == 0 ? a.x[0] : ty == 1 ? a.x[1] : a.x[2]) +
-                          row * (ty == 0 ? a.stride[0] : ty == 1 ? a.stride[1] : a.stride[2]) +
-                          (int64_t)h * D;
+      const uint16_t* p = head_row(a, ty, row, h * D);
       u[k] = *reinterpret_cast<const uint4*>(p + e0);
       v[k] = *reinterpret_cast<const uint4*>(p + e1);
     }
@@ -193,15 +230,8 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
         if (a.slot_weights) a.slot_weights[i] = 0.f;
       }
   }
-  // position * frequency wraps modulo one turn in 64 bits; its upper half,
-  // read as a signed number, is the angle in units of pi / 2^31
   float2* const cs = s_cs[warp];
-  for (int j = lane; j < a.rotary / 2; j += 32) {
-    const unsigned long long t = (unsigned long long)pos * a.turn[j];
-    float sn, c;
-    sincospif((float)(int)(t >> 32) * 4.656612873077393e-10f, &sn, &c);
-    cs[j] = make_float2(c * a.magnitude, sn * a.magnitude * a.sin_sign);
-  }
+  for (int j = lane; j < a.rotary / 2; j += 32) cs[j] = turn_of(a, pos, a.turn[j]);
   __syncwarp();
   float4 rot[4];                          // of this lane's pairs, for all heads
 #pragma unroll
@@ -215,19 +245,110 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
       const int hh = (gb + k) * HPW + sub;
       if (gb + k >= g1 || hh >= a.heads) continue;
       int h;
-      const int ty = which(hh, h);
+      const int ty = head_of(a, hh, h);
       if (turned && ty < 2) turn<BF, HALVES>(u[k], v[k], rot);
-      uint16_t* o = ty == 0 ? a.out[0] : ty == 1 ? a.out[1] : nullptr;
-      if (o) {
-        o += row * (ty == 0 ? a.out_stride[0] : a.out_stride[1]) + (int64_t)h * D;
-        *reinterpret_cast<uint4*>(o + e0) = u[k];
-        *reinterpret_cast<uint4*>(o + e1) = v[k];
+      put_head<D>(a, ty, row, h, at, u[k], v[k], e0, e1);
+    }
+  }
+}
+
+// The same for rows of few heads: a warp takes R rows and their heads one behind
+// the other, so that a short last group of heads and what a row costs by itself
+// are shared; most of that is the table of frequencies, which lies in constant
+// memory, one address a cycle, and is read once for all rows here.  A lane looks
+// up a row; cosines and sines are kept by row, in an order in which eight lanes
+// read 128 bytes.  262,144 rows of 8 + 1 heads of 64: 178 us row by row, 125 by
+// fours, 108 by eights (floor 89); 16,384 rows 12.4, 10.9, 12.0; of 4,096 rows,
+// or of 16 heads and more, one at a time is as fast or faster (4.7, 5.5, 7.2;
+// 65,536 rows of 20 + 4 heads of 128: 121, 128, 136).
+template <int D, bool BF, bool HALVES, int R>
+__global__ void __launch_bounds__(32 * kRopeWarps, 6) rope_few_heads(const RopeKArgs a) {
+  constexpr int LPH = D / 16, HPW = 32 / LPH;
+  __shared__ __align__(16) float2 s_cs[kRopeWarps][R][D / 2];
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((int)blockIdx.x >= a.row_blocks) {
+    check_sequences(a);
+    return;
+  }
+  const int64_t row0 = ((int64_t)blockIdx.x * kRopeWarps + warp) * R;
+  if (row0 >= a.n_rows) return;
+  const int rows = (int)min((int64_t)R, a.n_rows - row0);
+  // ---- lane r: row r's position and place
+  int pos = 0;
+  int64_t at = -1;
+  bool use = false;
+  if (lane < rows) {
+    const int row = (int)row0 + lane;
+    pos = a.positions[row];
+    use = pos >= 0;
+    if (!use) flag(a.status, DS_DEV_BAD_LENGTH);
+    if (use && a.write) {
+      int lo = 0, hi = a.batch;           // before the first offset above the row
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.row_offsets[mid] <= row) lo = mid; else hi = mid;
       }
-      if (ty > 0 && at >= 0) {
-        o = (ty == 1 ? a.cache.pool[0] : a.cache.pool[1]) + at + (int64_t)h * a.cache.head_stride;
-        *reinterpret_cast<uint4*>(o + e0) = u[k];
-        *reinterpret_cast<uint4*>(o + e1) = v[k];
+      int n0, n, from;
+      use = rope_rows_of(a, lo, n0, n, from) && row >= n0 && row < n0 + n;
+      if (use) {
+        const int slot = from + (row - n0), pg = slot_page(a.cache, lo, slot);
+        if (pg >= 0) at = slot_at(a.cache, pg, slot);
+        else flag(a.status, DS_DEV_BAD_PAGE);
+        for (int h = 0; h < a.slot_heads; ++h) {
+          const int64_t i = ((int64_t)lo * a.slot_heads + h) * a.slot_stride + slot;
+          if (a.slot_positions) a.slot_positions[i] = pos;
+          if (a.slot_weights) a.slot_weights[i] = 0.f;
+        }
       }
+    }
+  }
+  const uint32_t used = __ballot_sync(0xffffffffu, use);
+#pragma unroll
+  for (int k = 0; k < D / 64; ++k) {      // (a lane's frequency is read once for all rows)
+    const int j = lane + 32 * k, to = (j % 8 / 2 * LPH + j / 8) * 2 + j % 2;
+    const unsigned long long f = a.turn[j];
+#pragma unroll 2
+    for (int r = 0; r < rows; ++r)
+      s_cs[warp][r][to] = turn_of(a, __shfl_sync(0xffffffffu, pos, r), f);
+  }
+  __syncwarp();
+  const int l = lane % LPH, sub = lane / LPH;
+  const bool turned = 16 * l < a.rotary;
+  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
+  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
+  const int items = rows * a.heads;
+  for (int g0 = 0; g0 < items; g0 += HPW * kRopeBatch) {
+    uint4 u[kRopeBatch], v[kRopeBatch];
+    int r[kRopeBatch], hh[kRopeBatch];
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int e = min(g0 + k * HPW + sub, items - 1);
+      r[k] = (int)(e * a.heads_magic >> 32);
+      hh[k] = e - r[k] * a.heads;
+      if (g0 + k * HPW + sub >= items || !(used >> r[k] & 1)) hh[k] = -1;
+      if (hh[k] < 0) continue;
+      int h;
+      const int ty = head_of(a, hh[k], h);
+      const uint16_t* p = head_row(a, ty, row0 + r[k], h * D);
+      u[k] = *reinterpret_cast<const uint4*>(p + e0);
+      v[k] = *reinterpret_cast<const uint4*>(p + e1);
+    }
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int64_t to = __shfl_sync(0xffffffffu, at, r[k]);
+      if (hh[k] < 0) continue;
+      int h;
+      const int ty = head_of(a, hh[k], h);
+      if (turned && ty < 2) {
+        float4 rot[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          rot[i] = *reinterpret_cast<const float4*>(&s_cs[warp][r[k]][(i * LPH + l) * 2]);
+        turn<BF, HALVES>(u[k], v[k], rot);
+      }
+      put_head<D>(a, ty, row0 + r[k], h, to, u[k], v[k], e0, e1);
     }
   }
 }
@@ -282,24 +403,40 @@ cudaError_t launch_rope_append(const ds_rope_args& g, cudaStream_t stream) {
     const double frac = turns - std::floor(turns);   // whole turns drop out
     a.turn[j] = frac < 1.0 ? (unsigned long long)(frac * 18446744073709551616.0) : 0ull;
   }
+  a.heads_magic = ((1ull << 32) + a.heads - 1) / a.heads;
   const int hpw = 32 / (g.head_dim / 16), groups = (a.heads + hpw - 1) / hpw;
   const int slices = (int)std::max<int64_t>(
       1, std::min<int64_t>(groups, 152 * 24 / std::max(1, g.n_rows)));
   a.per = (groups + slices - 1) / slices;
-  a.row_blocks = (int)(((int64_t)g.n_rows + kRopeWarps - 1) / kRopeWarps);
+  const bool few = a.heads <= kFewHeads && g.n_rows >= kManyRows;
+  const int64_t each = !few ? 1 : g.n_rows >= kMostRows ? 8 : 4, rows = kRopeWarps * each;   // of a warp, a block
+  a.row_blocks = (int)((g.n_rows + rows - 1) / rows);
   const dim3 grid((unsigned)(a.row_blocks + (a.batch + 32 * kRopeWarps - 1) / (32 * kRopeWarps)),
-                  (unsigned)((groups + a.per - 1) / a.per));
+                  few ? 1u : (unsigned)((groups + a.per - 1) / a.per));
   const dim3 block(32 * kRopeWarps);
   const bool bf = g.dtype == DS_KV_BF16, halves = g.layout == DS_ROPE_HALF;
-  auto go = [&](void (*k)(const RopeKArgs)) {
-    return launch_dependent(k, grid, block, 0, stream, a);
+  auto go = [&](void (*k)(const RopeKArgs), dim3 blocks) {
+    return launch_dependent(k, blocks, block, 0, stream, a);
   };
-  if (g.head_dim == 128) {
-    if (bf) return halves ? go(rope_append<128, true, true>) : go(rope_append<128, true, false>);
-    return halves ? go(rope_append<128, false, true>) : go(rope_append<128, false, false>);
-  }
-  if (bf) return halves ? go(rope_append<64, true, true>) : go(rope_append<64, true, false>);
-  return halves ? go(rope_append<64, false, true>) : go(rope_append<64, false, false>);
+  auto pick = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (each == 8)
+      return bf ? (halves ? go(rope_few_heads<D, true, true, 8>, grid)
+                          : go(rope_few_heads<D, true, false, 8>, grid))
+                : (halves ? go(rope_few_heads<D, false, true, 8>, grid)
+                          : go(rope_few_heads<D, false, false, 8>, grid));
+    if (each == 4)
+      return bf ? (halves ? go(rope_few_heads<D, true, true, 4>, grid)
+                          : go(rope_few_heads<D, true, false, 4>, grid))
+                : (halves ? go(rope_few_heads<D, false, true, 4>, grid)
+                          : go(rope_few_heads<D, false, false, 4>, grid));
+    return bf ? (halves ? go(rope_append<D, true, true>, grid)
+                        : go(rope_append<D, true, false>, grid))
+              : (halves ? go(rope_append<D, false, true>, grid)
+                        : go(rope_append<D, false, false>, grid));
+  };
+  return g.head_dim == 128 ? pick(std::integral_constant<int, 128>())
+                           : pick(std::integral_constant<int, 64>());
 }
 
 }  // namespace ds

@@ -164,6 +164,69 @@ def test_append(dtype, kv, page, d, hkv, hw):
     assert torch.equal(sp.cpu(), wp) and torch.equal(sw.cpu(), ww)
 
 
+@pytest.mark.parametrize("dtype,layout", [(torch.bfloat16, "half"), (torch.float16, "interleaved")])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 1), (128, 1, 1), (64, 0, 1), (128, 5, 3)])
+@pytest.mark.parametrize("rows", [16384 + 5, 65536 + 3])
+def test_many_rows_of_few_heads(dtype, layout, d, hq, hkv, rows):
+    """Several rows to a warp: the rotation alone, and into a cache with bad
+    sequences, a bad page, a negative position and rows of no sequence."""
+    g = torch.Generator(device=DEV).manual_seed(rows + d)
+    x = torch.randn(rows, hq + 2 * hkv, d, generator=g, device=DEV).to(dtype)
+    q, k, v = (x[:, :hq] if hq else None), x[:, hq:hq + hkv], x[:, hq + hkv:]
+    pos = torch.randint(0, 1 << 17, (rows,), generator=g, device=DEV, dtype=torch.int32)
+    new = lambda h: torch.full((rows, h, d), 7.0, dtype=dtype, device=DEV) if h else None
+    qo, ko = new(hq), new(hkv)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    kw = dict(layout=layout, rotary_dim=48, rope_base=10000.0, workspace=ws)
+    B.ds_rope_append(B.rope_append_args(q, k, None, pos, q_out=qo, k_out=ko, inverse=True, **kw))
+    freq = 10000.0 ** (-2.0 * np.arange(24) / 48)
+    inter = layout == "interleaved"
+    for got, y in ((qo, q), (ko, k)):
+        if y is not None:
+            check(got, y, pos.cpu().numpy(), freq, 1.0, inter, True)
+    assert B.ds_device_status(ws) == 0
+    # four sequences, the third one too long for its slots; 9 rows of none
+    n = [1000, rows // 2, 500, rows - 9 - rows // 2 - 1500, 0]
+    off = [0]
+    for m in n:
+        off.append(off[-1] + m)
+    per = -(-(rows + 64) // 128)
+    table = torch.arange(5 * per, dtype=torch.int32, device=DEV).view(5, per)
+    table[1, 2] = 5 * per
+    ctx, far = [3, 40, per * 128 - 499, 0, 17], 12345
+    pools = [torch.zeros(5 * per, 128, hkv, d, dtype=dtype, device=DEV) for _ in range(2)]
+    sp = torch.full((5, 1, per * 128), -5, dtype=torch.int32, device=DEV)
+    pos[1000 + far] = -1
+    qo, ko, lens = new(hq), new(hkv), i32([-9] * 5)
+    B.ds_rope_append(B.rope_append_args(
+        q, k, v, pos, q_out=qo, k_out=ko, k_cache=pools[0], v_cache=pools[1], page_table=table,
+        from_lens=i32(ctx), row_offsets=i32(off), slot_positions=sp, new_lens=lens, **kw))
+    assert B.ds_device_status(ws) == B.DS_DEV_BAD_LENGTH | B.DS_DEV_BAD_PAGE
+    assert lens.tolist() == [c + m if b != 2 else c for b, (c, m) in enumerate(zip(ctx, n))]
+    used = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    for b in (0, 1, 3):
+        used[off[b]:off[b + 1]] = True
+    used[1000 + far] = False
+    for got, y in ((qo, q), (ko, k)):
+        if y is not None:
+            assert bool((got[~used] == 7.0).all())
+            check(got[used], y[used], pos[used].cpu().numpy(), freq, 1.0, inter)
+    want = [torch.zeros_like(p) for p in pools]
+    wp = torch.full_like(sp, -5)
+    for b in (0, 1, 3):
+        t = torch.arange(ctx[b], ctx[b] + n[b], device=DEV)
+        r = torch.arange(off[b], off[b + 1], device=DEV)
+        t, r = t[used[r]], r[used[r]]
+        wp[b, 0, t] = pos[r]
+        ok = table[b].long()[t // 128] < 5 * per
+        t, r = t[ok], r[ok]
+        for w, y in zip(want, (ko, v)):
+            w[table[b].long()[t // 128], t % 128] = y[r]
+    for p, w in zip(pools, want):
+        assert torch.equal(p, w)
+    assert torch.equal(sp, wp)
+
+
 def test_append_leaves_bad_sequences_out():
     """Lengths and offsets that cannot be used, a page that is none and a
     negative position: told by status bits, everything else written."""
