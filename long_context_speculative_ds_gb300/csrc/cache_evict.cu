@@ -550,8 +550,12 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, a, room);
   if (e != cudaSuccess || a.alone) return e;
-  // moves of a warp at a time, and eight blocks an SM as far as there can be moves
-  const int per = std::max(1, 32 / (g.slot_heads == 1 ? g.num_kv_heads : 1));
+  // Rows of a warp at a time: 8, that go at once, up to 32 when there are enough to
+  // fill the machine with warps all the same; and eight blocks an SM as far as
+  // there can be moves.
+  const int heads = g.slot_heads == 1 ? g.num_kv_heads : 1;
+  const int64_t fill = (int64_t)segs * L.moves * heads / (152 * 24);
+  const int per = (int)std::max<int64_t>(1, std::min<int64_t>(32, std::max<int64_t>(8, fill)) / heads);
   const int64_t warps = (L.moves + per - 1) / per;
   const int rows = (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8,
                                                                152 * 8 / segs + 1));

@@ -10,21 +10,22 @@
 // Logits carry the factor log2 e, so that exponentials are powers of two.
 //
 // Bound by the stream of K and V.  With 32 query heads on 8 of 128: one token
-// over 128K 98 us, the split pass 87 of them (537 MB, 6.2 TB/s of the 6.8 that a
-// copy reaches; without weights the call takes 86); 96 ragged contexts of 33 to
-// 8K 75.5 us (457 MB, 6.1 TB/s); eight compact caches of 9K to 18K 83 us; 512
-// slots with 4 heads of 64 on 2 8.2 us, two launches of four dependent reads
+// over 128K 95 us, the split pass 86 of them (537 MB, 6.2 TB/s of the 6.8 that a
+// copy reaches; without weights the call takes 85); 96 ragged contexts of 33 to
+// 8K 74 us (457 MB, 6.2 TB/s); eight compact caches of 9K to 18K 82 us; 512
+// slots with 4 heads of 64 on 2 7.8 us, two launches of four dependent reads
 // each.  Logits cost 4 bytes a slot and query head, written and read: 3 % of the
-// bytes at 4 query heads a kv head, a quarter at 16 (128K: 121 us, 87 without
+// bytes at 4 query heads a kv head, a quarter at 16 (128K: 122 us, 87 without
 // weights).
 //
 // Split pass: blocks of four warps that compute and one that loads, two blocks
 // an SM, each with a ring of three (six at 64-wide heads) tiles of 64 slots.
 // The loader brings a tile's K and V as copies of 16 slots of one head through
-// the page table, and runs ahead over the ends of pieces, so that the stream
-// does not stop where one segment ends and the next begins; the other block's
-// ring covers what is left.  (One block of eight warps and six tiles an SM took
-// 88 us for the 96 ragged contexts, equal at 128K.)  A warp takes 16 slots of a
+// the page table, works out the pieces, and runs ahead over their ends, so that
+// the stream does not stop where one segment ends and the next begins; the other
+// block's ring covers what is left.  (One block of eight warps and six tiles an
+// SM took 88 us for the 96 ragged contexts; with pieces worked out by the
+// computing warps 206 sequences of up to 4 slots took 21.7 us, not 14.)  A warp takes 16 slots of a
 // tile, with the cache as the larger operand of m16n8k16 products and up to
 // eight query heads as the smaller (16 as two):
 //   S^T[16 slots, 8 heads] += K[16 slots, 16 channels] Q^T[16 channels, 8 heads]
@@ -130,9 +131,10 @@ DS_DEV int range_with(const Plan& p, int64_t u) {     // the last i with units i
 struct Piece {
   Range r;
   int b, h;
-  int t0, t1;                   // tiles
+  int t0, t1;                   // tiles; t1 0: no more pieces
   int64_t pos;                  // of the segment
 };
+constexpr int kPieces = 8;
 
 DS_DEV Range seq_range(const KArgs& a, int b, bool report) {
   return range_of(checked_len(a.lens[b], a.cache.slots, a.status, report), a.window,
@@ -279,6 +281,18 @@ DS_DEV void split2(float lo, float hi, uint32_t& big, uint32_t& rest) {
   rest = pack2<BF>(lo - b.x, hi - b.y);
 }
 
+// A barrier of the warps that compute; whether x holds for all of them.
+DS_DEV bool all_warps(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(32 * kWarps)
+      : "memory");
+  return r != 0;
+}
+
 template <int D>
 struct Cfg {
   static constexpr int kSubBytes = 16 * D * 2;          // 16 keys of K or V
@@ -294,12 +308,18 @@ struct Cfg {
 struct Shared {
   alignas(8) uint64_t full[6], empty[6];
   Plan plan;
-  Piece piece;                                // of the warps that compute
   int64_t sum[kWarps + 1][2];
   float m[kWarps][8], l[kWarps][8];
-  int abort, more;
+  // Pieces, from the loader to the warps that compute.  It is at most a ring of
+  // tiles ahead of them, and a piece has a tile or more: eight places are enough
+  // (a piece is copied out before its first tile is waited for).
+  uint64_t told[kPieces];
+  Piece piece[kPieces];
+  int abort;
 };
-static_assert(2 * (Cfg<128>::smem + sizeof(Shared) + 1024 + 16) <= 233472, "two blocks an SM");
+static_assert(sizeof(Shared) <= 1024 && 2 * (Cfg<128>::smem + 1024 + 1024) <= 233472,
+              "two blocks an SM (1 KB a block is the system's)");
+static_assert(Cfg<64>::kStages + 2 <= kPieces && Cfg<128>::kStages + 2 <= kPieces, "");
 
 template <int D, bool BF, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -318,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_init(smem_addr(&sh.full[i]), 1);
       mbar_init(smem_addr(&sh.empty[i]), 4);
     }
+    for (int i = 0; i < kPieces; ++i) mbar_init(smem_addr(&sh.told[i]), 1);
     sh.abort = 0;
     fence_mbar_init();
   }
@@ -340,8 +361,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int sub = lane & 3, kind = (lane >> 2) & 1;
     int64_t issued = 0;
     bool ok = true;
-    while (ok && next_piece(a, walk, pc)) {
+    for (int np = 0; ok; np = (np + 1) % kPieces) {
+      if (!next_piece(a, walk, pc)) pc.t1 = 0;
       const Range r = pc.r;
+      if (lane == 0) {
+        sh.piece[np] = pc;
+        mbar_arrive(smem_addr(&sh.told[np]));
+        if (pc.t1 > 0 && pc.t0 == 0) {        // numbered by range and segment, which never
+          const int64_t u = pc.pos + kLead, seg = (int64_t)pc.b * a.hkv + pc.h;
+          const int f = range_with(sh.plan, u);   // both stand still, pieces have places of
+          a.desc[seg] = make_int2((int)(f + seg),  // their own (u: the segment's first tile)
+                                  range_with(sh.plan, u + r.tiles - 1) - f + 1);
+        }
+      }
+      __syncwarp();
+      if (pc.t1 == 0) break;
       auto sub_visible = [&](int t, int s) {
         const int k0 = tile_slot(r, t) + 16 * s;
         return t < pc.t1 && k0 < r.n && (k0 < r.sinks || k0 + 16 > r.start);
@@ -406,14 +440,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto chunk_at = [&](uint32_t base, int row, int chunk) {
     return base + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
   };
-  // (one thread walks for all four warps, which meet at barriers a piece long)
-  if (tid == 0) sh.more = next_piece(a, walk, sh.piece);
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-  while (sh.more) {
-    pc = sh.piece;
-    const Range r = pc.r;
-    const int64_t seg = (int64_t)pc.b * a.hkv + pc.h;
-    uint32_t q[NT][D / 16][2];
+  // The next piece and its queries, which are read while the last one is joined.
+  uint32_t q[NT][D / 16][2];
+  int np = 0, told = 0;
+  auto fetch = [&] {
+    const bool ok = mbar_wait(smem_addr(&sh.told[np]), told, abort);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    pc = sh.piece[np];
+    if (++np == kPieces) { np = 0; told ^= 1; }
+    if (pc.t1 == 0) return false;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -426,6 +461,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           q[i][ks][1] = *reinterpret_cast<const uint32_t*>(p + 8);
         }
       }
+    return true;
+  };
+  // (a warp whose wait gave up takes the others with it: they meet at barriers)
+  bool more = all_warps(fetch());
+  while (more) {
+    const Range r = pc.r;
+    const int64_t seg = (int64_t)pc.b * a.hkv + pc.h;
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -546,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
     }
     // ---- the warps' outputs joined, eight rows at a time, into the piece's place
+    more = fetch();
     const int64_t piece = blockIdx.x + seg;
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1)
@@ -556,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* const mine = merge + warp * 8 * D;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
+      const bool all = all_warps(more);       // and the last rows have been read
+      if (i == 0) more = all;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = 2 * t4 + j;
@@ -592,15 +637,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<float4*>(a.part_o + ((piece * G + 8 * i + row) * D + c * 4)) = sum;
         if (c == 0) a.part_ml[piece * G + 8 * i + row] = make_float2(M, total);
       }
-      if (i == NT - 1 && tid == 0) {
-        if (pc.t0 == 0) {                     // numbered by range and segment, which never
-          const int64_t u = pc.pos + kLead;   // both stand still, pieces have places of their own
-          const int f = range_with(sh.plan, u);   // (u: the segment's first tile on the axis)
-          a.desc[seg] = make_int2((int)(f + seg), range_with(sh.plan, u + r.tiles - 1) - f + 1);
-        }
-        sh.more = next_piece(a, walk, sh.piece);
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     }
   }
   if (tid == 0 && *abort) flag(a.status, DS_DEV_TIMEOUT);
@@ -730,13 +766,54 @@ DS_DEV void load_logits(float (&s)[4], const float* p, int g0, int G) {
   }
 }
 
+// The weights of 128 slots of a (sequence, kv head) of up to four query heads, by
+// a warp: eight lanes join a row's sums.
+DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
+  const int lane = threadIdx.x & 31, G = a.group, l = lane % 8, row = lane / 8;
+  const int64_t spans = (a.cache.slots + 127) / 128, seg = item / spans;
+  const bool real = seg < (int64_t)a.batch * a.hkv;
+  const int n = real ? checked_len(a.lens[seg / a.hkv], a.cache.slots, nullptr, false) : 0;
+  const int t0 = (int)(item - seg * spans) * 128 + lane;
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  if (t0 - lane >= n) return;
+  const int2 d = a.desc[seg];
+  float s[4][4], old[4];
+  const int64_t at = seg * a.slot_stride;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int t = min(t0 + 32 * k, n - 1);
+    load_logits(s[k], a.logits + (seg * a.cache.slots + t) * G, 0, G);
+    old[k] = a.w_in ? a.w_in[at + t] : 0.f;
+  }
+  float2 ml = make_float2(-CUDART_INF_F, 0.f);
+  if (row < G)
+    for (int j = l; j < d.y; j += 8) ml = join_ml(ml, a.part_ml[(int64_t)(d.x + j) * G + row]);
+  ml = join_lanes<8>(ml);
+  const float ref = ml.x + log2f(ml.y);
+  const Range r = range_of(n, a.window, a.sinks);
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float rj = __shfl_sync(0xffffffffu, ref, 8 * j);
+    if (j < G) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sum[k] += visible(r, t0 + 32 * k) ? ptx::ex2(s[k][j] - rj) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (t0 + 32 * k < n) a.w_out[at + t0 + 32 * k] = fmaf(old[k], a.decay, sum[k]);
+}
+
 // Output rows (the first blocks), and the weights of SLOTS x 256 slots of a
 // (sequence, slot head) a time: the rows whose weights a slot sums go in chunks
 // of up to four of one kv head, CHUNKS at once, so that a thread has 16 loads
 // on its way beside the rows' own sums, which 8 to 32 lanes join a row.  With
-// CHUNKS 0 there are output rows only.
+// SLOTS 0 a warp works by itself (one chunk), or there are output rows only.
 template <int D, int SLOTS, int CHUNKS>
-__global__ void __launch_bounds__(kFinishThreads, CHUNKS == 0 || SLOTS * CHUNKS < 16 ? 4 : 2)
+__global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
     finish(const KArgs a, const int row_blocks, const int parts) {
   __shared__ float s_ref[32];
   __shared__ float s_o[kFinishWarps][D];
@@ -750,7 +827,10 @@ __global__ void __launch_bounds__(kFinishThreads, CHUNKS == 0 || SLOTS * CHUNKS 
     finish_row<D>(a, w / parts, w % parts, parts, s_o, s_ml);
     return;
   }
-  if constexpr (CHUNKS > 0) {
+  if constexpr (SLOTS == 0 && CHUNKS == 1) {              // short sequences
+    warp_weights(a, ((int64_t)blockIdx.x - row_blocks) * kFinishWarps + (tid >> 5));
+    return;
+  } else if constexpr (CHUNKS > 0) {
     constexpr int SPAN = SLOTS * kFinishThreads;
     constexpr int LPR = kFinishThreads / (4 * CHUNKS) < 32 ? kFinishThreads / (4 * CHUNKS) : 32;
     const int64_t spans = (a.cache.slots + SPAN - 1) / SPAN;
@@ -845,10 +925,16 @@ cudaError_t launch_finish(const KArgs& a, int pieces, cudaStream_t stream) {
   const int parts = pieces > 16 ? kFinishWarps : 1;
   const int row_blocks =
       (int)(((int64_t)a.batch * a.hq * parts + kFinishWarps - 1) / kFinishWarps);
-  const int span = std::max(1, SLOTS * kFinishThreads);
-  const int64_t items =
-      a.w_out ? (int64_t)a.batch * a.slot_heads * ((a.cache.slots + span - 1) / span) : 0;
-  const int grid = row_blocks + (int)std::min<int64_t>(items, 152 * 4 * 2);
+  int64_t items = 0;                      // blocks for the weights
+  if constexpr (CHUNKS > 0 && SLOTS > 0) {
+    const int span = SLOTS * kFinishThreads;
+    items = std::min<int64_t>(
+        (int64_t)a.batch * a.slot_heads * ((a.cache.slots + span - 1) / span), 152 * 4 * 2);
+  } else if constexpr (CHUNKS > 0) {
+    items = ((int64_t)a.batch * a.hkv * ((a.cache.slots + 127) / 128) + kFinishWarps - 1) /
+            kFinishWarps;
+  }
+  const int grid = (int)(row_blocks + items);
   return launch_dependent(finish<D, SLOTS, CHUNKS>, dim3(grid), dim3(kFinishThreads), 0, stream, a,
                           row_blocks, parts);
 }
@@ -951,17 +1037,17 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   // chunks of up to four rows whose weights a slot sums; pieces of a segment
   const int chunks = !a.w_out ? 0 : (a.group + 3) / 4 * (a.slot_heads == 1 ? a.hkv : 1);
   const int pieces = L.ranges / (a.batch * a.hkv) + 1;
-  // short sequences: fewer slots a block, and more blocks an SM (1,024 sequences
-  // of 512 slots, weights per head: 412 us instead of 505)
-  const bool few = chunks == 1 && a.cache.slots <= 1024;
+  // short sequences: a warp to 128 slots (1,024 sequences of 512 slots, weights
+  // per head: 385 us instead of 505)
+  const bool few = chunks == 1 && a.slot_heads == a.hkv && a.cache.slots <= 1024;
   if (g.head_dim == 128)
     return chunks == 0   ? launch_finish<128, 0, 0>(a, pieces, stream)
-           : few         ? launch_finish<128, 4, 1>(a, pieces, stream)
+           : few         ? launch_finish<128, 0, 1>(a, pieces, stream)
            : chunks == 1 ? launch_finish<128, 16, 1>(a, pieces, stream)
            : chunks < 8  ? launch_finish<128, 4, 4>(a, pieces, stream)
                          : launch_finish<128, 2, 8>(a, pieces, stream);
   return chunks == 0   ? launch_finish<64, 0, 0>(a, pieces, stream)
-         : few         ? launch_finish<64, 4, 1>(a, pieces, stream)
+         : few         ? launch_finish<64, 0, 1>(a, pieces, stream)
          : chunks == 1 ? launch_finish<64, 16, 1>(a, pieces, stream)
          : chunks < 8  ? launch_finish<64, 4, 4>(a, pieces, stream)
                        : launch_finish<64, 2, 8>(a, pieces, stream);
