@@ -32,8 +32,9 @@
 //   O^T[16 dims, 8 heads]  += V^T[16 dims, 16 slots]   P^T[16 slots, 8 heads]
 // P^T is S^T's fragment transposed (movmatrix), and enters as the sum of two
 // values of the cache's type, so that its rounding (2^-9 of a weight in bf16)
-// does not show beside the output's own.  The tensor pipe is at 13 % of its
-// rate, issue slots at 20 %.
+// does not show beside the output's own: 2^-17 of a weight is left, in f16 2^-22
+// of it or 2^-32 of the largest.  The tensor pipe is at 13 % of its rate, issue
+// slots at 20 %.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
@@ -440,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto chunk_at = [&](uint32_t base, int row, int chunk) {
     return base + (chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
   };
+  // m lies this far below the maximum that it follows (f16's range, see below).
+  constexpr float kBelow = BF ? 0.f : 7.f;
   // The next piece and its queries, which are read while the last one is joined.
   uint32_t q[NT][D / 16][2];
   int np = 0, told = 0;
@@ -521,19 +524,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               mx[i][j] = fmaxf(mx[i][j], __shfl_xor_sync(0xffffffffu, mx[i][j], x));
-        // the reference point follows the maximum only when that has grown by
-        // more than 2^8: weights reach at most 2^8, and outputs are rarely scaled
+        // the reference point m follows the maximum only when that has grown by
+        // more than 2^8, so that outputs are rarely scaled; in f16 it lies 2^7
+        // below: weights reach 2^15 of the 2^16 that there are, and those that
+        // the type's smallest step cuts short (2^-25 of its unit) lie 2^7 lower
         bool grow = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) grow |= mx[i][j] > m[i][j] + 8.f;
+          for (int j = 0; j < 2; ++j) grow |= mx[i][j] > m[i][j] + (8.f + kBelow);
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float now = fmaxf(m[i][j], mx[i][j]);
+              const float now = fmaxf(m[i][j], mx[i][j] - kBelow);
               const float f = m[i][j] == now ? 1.f : ex2(m[i][j] - now);
               m[i][j] = now;
               l[i][j] *= f;

@@ -347,3 +347,34 @@ def test_long_context():
     out, lse, w, ws, _ = run(q, pools, None, lens, hw=2)
     check(q, pools, None, lens, out, lse, w_out=w)
     assert B.ds_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rise", [0.0, 5.0])
+def test_light_weights_beside_a_heavy_one(dtype, rise):
+    """Channels where the heavy tokens have nothing: what the light ones give
+    there keeps its digits (a two-value weight is off by 2^-17 of itself in bf16;
+    in f16 by 2^-32 of the row's largest where its type ends).  With `rise` a
+    late logit is a little above the heavy ones before it, by less than it takes
+    for outputs to be scaled."""
+    d, n = 64, 150
+    g = torch.Generator().manual_seed(5)
+    q = torch.zeros(1, 3, d)
+    q[..., 0] = 1.0
+    k, v = torch.zeros(1, n, 1, d), torch.randn(1, n, 1, d, generator=g)
+    k[0, :, 0, 0] = -12.375                          # exact in both types: 2^-17.85
+    k[0, 6::16, 0, 0] = 0.0                          # one for each sixteen slots
+    k[0, 134, 0, 0] = rise
+    v[0, 6::16, 0, ::2] = 0.0
+    q, k, v = (x.to(dtype).to(DEV) for x in (q, k, v))
+    out, lse, _, ws, _ = run(q, [k, v], None, [n], out_dtype=torch.float32, scale=1.0)
+    o, l, p = draft.decode(f64(q[0]), f64(k[0]), f64(v[0]), 1.0, 0, 0)
+    a = np.abs(f64(v[0, :, 0]))
+    # logits are one product of exact values: off by 2^-22 of themselves at most
+    rel = 2.0 ** -22 * 16 * 2 + 2.0 ** -16 + 2.0 ** -18 + 2.0 ** -24 * n
+    tol = rel * (p[:, :] @ a)
+    if dtype == torch.float16:
+        tol = tol + p.max(1)[:, None] * 2.0 ** -32 * a.sum(0)
+    assert (np.abs(f64(out[0]) - o) <= tol).all()
+    assert (np.abs(f64(lse[0]) - l) <= 2.0 ** -21 + 2.0 ** -22 * np.abs(l)).all()
+    assert B.ds_device_status(ws) == 0
