@@ -771,10 +771,10 @@ DS_DEV void load_logits(float (&s)[4], const float* p, int g0, int G) {
   }
 }
 
-// The weights of 128 slots of a (sequence, kv head) of up to four query heads, by
-// a warp: eight lanes join a row's sums.
+// The weights of 128 slots of a (sequence, kv head), by a warp: four query heads
+// at a time, eight lanes to the sums of each.
 DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
-  const int lane = threadIdx.x & 31, G = a.group, l = lane % 8, row = lane / 8;
+  const int lane = threadIdx.x & 31, G = a.group, l = lane % 8;
   const int64_t spans = (a.cache.slots + 127) / 128, seg = item / spans;
   const bool real = seg < (int64_t)a.batch * a.hkv;
   const int n = real ? checked_len(a.lens[seg / a.hkv], a.cache.slots, nullptr, false) : 0;
@@ -783,28 +783,33 @@ DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
   grid_dep_launch_dependents();
   if (t0 - lane >= n) return;
   const int2 d = a.desc[seg];
-  float s[4][4], old[4];
+  const Range r = range_of(n, a.window, a.sinks);
   const int64_t at = seg * a.slot_stride;
+  float old[4], sum[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int t = min(t0 + 32 * k, n - 1);
-    load_logits(s[k], a.logits + (seg * a.cache.slots + t) * G, 0, G);
-    old[k] = a.w_in ? a.w_in[at + t] : 0.f;
+    old[k] = a.w_in ? a.w_in[at + min(t0 + 32 * k, n - 1)] : 0.f;
+    sum[k] = 0.f;
   }
-  float2 ml = make_float2(-CUDART_INF_F, 0.f);
-  if (row < G)
-    for (int j = l; j < d.y; j += 8) ml = join_ml(ml, a.part_ml[(int64_t)(d.x + j) * G + row]);
-  ml = join_lanes<8>(ml);
-  const float ref = ml.x + log2f(ml.y);
-  const Range r = range_of(n, a.window, a.sinks);
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int g0 = 0; g0 < G; g0 += 4) {
+    float s[4][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float rj = __shfl_sync(0xffffffffu, ref, 8 * j);
-    if (j < G) {
+    for (int k = 0; k < 4; ++k)
+      load_logits(s[k], a.logits + (seg * a.cache.slots + min(t0 + 32 * k, n - 1)) * G, g0, G);
+    const int row = g0 + lane / 8;
+    float2 ml = make_float2(-CUDART_INF_F, 0.f);
+    if (row < G)
+      for (int j = l; j < d.y; j += 8) ml = join_ml(ml, a.part_ml[(int64_t)(d.x + j) * G + row]);
+    ml = join_lanes<8>(ml);
+    const float ref = ml.x + log2f(ml.y);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sum[k] += visible(r, t0 + 32 * k) ? ptx::ex2(s[k][j] - rj) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const float rj = __shfl_sync(0xffffffffu, ref, 8 * j);
+      if (g0 + j < G) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sum[k] += visible(r, t0 + 32 * k) ? ptx::ex2(s[k][j] - rj) : 0.f;
+      }
     }
   }
 #pragma unroll
@@ -816,7 +821,7 @@ DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
 // (sequence, slot head) a time: the rows whose weights a slot sums go in chunks
 // of up to four of one kv head, CHUNKS at once, so that a thread has 16 loads
 // on its way beside the rows' own sums, which 8 to 32 lanes join a row.  With
-// SLOTS 0 a warp works by itself (one chunk), or there are output rows only.
+// SLOTS 0 a warp works by itself, or (CHUNKS 0) there are output rows only.
 template <int D, int SLOTS, int CHUNKS>
 __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
     finish(const KArgs a, const int row_blocks, const int parts) {
@@ -832,7 +837,7 @@ __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
     finish_row<D>(a, w / parts, w % parts, parts, s_o, s_ml);
     return;
   }
-  if constexpr (SLOTS == 0 && CHUNKS == 1) {              // short sequences
+  if constexpr (SLOTS == 0 && CHUNKS == 1) {
     warp_weights(a, ((int64_t)blockIdx.x - row_blocks) * kFinishWarps + (tid >> 5));
     return;
   } else if constexpr (CHUNKS > 0) {
@@ -1042,9 +1047,16 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   // chunks of up to four rows whose weights a slot sums; pieces of a segment
   const int chunks = !a.w_out ? 0 : (a.group + 3) / 4 * (a.slot_heads == 1 ? a.hkv : 1);
   const int pieces = L.ranges / (a.batch * a.hkv) + 1;
-  // short sequences: a warp to 128 slots (1,024 sequences of 512 slots, weights
-  // per head: 385 us instead of 505)
-  const bool few = chunks == 1 && a.slot_heads == a.hkv && a.cache.slots <= 1024;
+  // A warp to 128 slots, each with the rows' own sums (weights per head): 24
+  // sequences of 8,000 slots and eight heads of a group of 7 139 us instead of 150,
+  // 300 of 200 in room for 2,000 68 instead of 100, of a group of 4 59 instead of
+  // 88.  In long sequences these sums are many pieces (one head's token over 128K
+  // slots 87.7 instead of 84.3), and a few warps with many heads take longer than
+  // blocks that share them (16 heads of 1,000 slots 13.2 instead of 11.5).
+  const int64_t spans = (int64_t)((a.cache.slots + 127) / 128) * a.batch * a.hkv;
+  const bool few = a.w_out && a.slot_heads == a.hkv &&
+                   (a.group <= 4 ? a.cache.slots <= 16384
+                                 : a.cache.slots <= 65536 && spans >= 8 * 152);
   if (g.head_dim == 128)
     return chunks == 0   ? launch_finish<128, 0, 0>(a, pieces, stream)
            : few         ? launch_finish<128, 0, 1>(a, pieces, stream)
