@@ -258,12 +258,16 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
 // memory, one address a cycle, and is read once for all rows here.  A lane looks
 // up a row; cosines and sines are kept by row, in an order in which eight lanes
 // read 128 bytes.  262,144 rows of 8 + 1 heads of 64: 178 us row by row, 125 by
-// fours, 108 by eights (floor 89); 16,384 rows 12.4, 10.9, 12.0; of 4,096 rows,
+// fours, 104 by eights (floor 89); 16,384 rows 12.4, 10.6, 12.0; of 4,096 rows,
 // or of 16 heads and more, one at a time is as fast or faster (4.7, 5.5, 7.2;
-// 65,536 rows of 20 + 4 heads of 128: 121, 128, 136).
+// 65,536 rows of 20 + 4 heads of 128: 121, 128, 136).  By eights the first heads'
+// loads go out before the rows' places are known (730,000 rows of 2 + 1 heads into
+// a cache 176 us instead of 183); by fours that took longer (16,384 rows of 4 + 1
+// heads of 128 into 16 sequences 16.4 instead of 15.4).
 template <int D, bool BF, bool HALVES, int R>
 __global__ void __launch_bounds__(32 * kRopeWarps, 6) rope_few_heads(const RopeKArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
+  constexpr bool kEarly = R == 8;
   __shared__ __align__(16) float2 s_cs[kRopeWarps][R][D / 2];
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -275,13 +279,35 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 6) rope_few_heads(const RopeK
   const int64_t row0 = ((int64_t)blockIdx.x * kRopeWarps + warp) * R;
   if (row0 >= a.n_rows) return;
   const int rows = (int)min((int64_t)R, a.n_rows - row0);
+  const int l = lane % LPH, sub = lane / LPH;
+  const bool turned = 16 * l < a.rotary;
+  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
+  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
+  const int items = rows * a.heads;
+  uint4 u[kRopeBatch], v[kRopeBatch];
+  int r[kRopeBatch], hh[kRopeBatch];
+  auto load = [&](int g0) {
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const int e = min(g0 + k * HPW + sub, items - 1);
+      r[k] = (int)(e * a.heads_magic >> 32);
+      hh[k] = g0 + k * HPW + sub < items ? e - r[k] * a.heads : -1;
+      if (hh[k] < 0) continue;
+      int h;
+      const int ty = head_of(a, hh[k], h);
+      const uint16_t* p = head_row(a, ty, row0 + r[k], h * D);
+      u[k] = *reinterpret_cast<const uint4*>(p + e0);
+      v[k] = *reinterpret_cast<const uint4*>(p + e1);
+    }
+  };
   // ---- lane r: row r's position and place
   int pos = 0;
   int64_t at = -1;
   bool use = false;
+  if (lane < rows) pos = a.positions[row0 + lane];
+  if (kEarly) load(0);                    // beside what the positions ask for
   if (lane < rows) {
     const int row = (int)row0 + lane;
-    pos = a.positions[row];
     use = pos >= 0;
     if (!use) flag(a.status, DS_DEV_BAD_LENGTH);
     if (use && a.write) {
@@ -314,31 +340,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 6) rope_few_heads(const RopeK
       s_cs[warp][r][to] = turn_of(a, __shfl_sync(0xffffffffu, pos, r), f);
   }
   __syncwarp();
-  const int l = lane % LPH, sub = lane / LPH;
-  const bool turned = 16 * l < a.rotary;
-  const int e0 = !turned || !HALVES ? 16 * l : 8 * l;
-  const int e1 = !turned || !HALVES ? 16 * l + 8 : 8 * l + a.rotary / 2;
-  const int items = rows * a.heads;
   for (int g0 = 0; g0 < items; g0 += HPW * kRopeBatch) {
-    uint4 u[kRopeBatch], v[kRopeBatch];
-    int r[kRopeBatch], hh[kRopeBatch];
-#pragma unroll
-    for (int k = 0; k < kRopeBatch; ++k) {
-      const int e = min(g0 + k * HPW + sub, items - 1);
-      r[k] = (int)(e * a.heads_magic >> 32);
-      hh[k] = e - r[k] * a.heads;
-      if (g0 + k * HPW + sub >= items || !(used >> r[k] & 1)) hh[k] = -1;
-      if (hh[k] < 0) continue;
-      int h;
-      const int ty = head_of(a, hh[k], h);
-      const uint16_t* p = head_row(a, ty, row0 + r[k], h * D);
-      u[k] = *reinterpret_cast<const uint4*>(p + e0);
-      v[k] = *reinterpret_cast<const uint4*>(p + e1);
-    }
+    if (g0 > 0 || !kEarly) load(g0);
 #pragma unroll
     for (int k = 0; k < kRopeBatch; ++k) {
       const int64_t to = __shfl_sync(0xffffffffu, at, r[k]);
-      if (hh[k] < 0) continue;
+      if (hh[k] < 0 || !(used >> r[k] & 1)) continue;
       int h;
       const int ty = head_of(a, hh[k], h);
       if (turned && ty < 2) {
