@@ -6,16 +6,15 @@
 // finds the budget-th largest key of a segment (a sequence's slot head) digit
 // by digit, how many of that very key stay (the lower slots), and lists the
 // kept slots behind the budget and the free ones below it, both ascending;
-// `move` copies one to the other.  No move's source is another's target
-// (sources lie behind the budget, targets below it), so it works in place, and
-// moves no more than has to move.
+// `move` (or `select` itself, where there are few) copies one to the other.  No
+// move's source is another's target (sources lie behind the budget, targets below
+// it), so it works in place, and moves no more than has to move.
 //
 // The moves are bound by memory: 6.2 TB/s for rows of 256 bytes here and there
 // (heads by themselves), 6.5 where a token's heads move together.  The selection
 // is bound by the latency of its passes over the keys in shared memory and of the
-// cluster's barriers: 31 of 100 us for 16 segments of 128K slots cut to 32K, 13
-// of 66 for eight of 18K cut to half; one slot of 2,049 6.2 us in all, two
-// launches.
+// cluster's barriers: 32 of 101 us for 16 segments of 128K slots cut to 32K, 16
+// of 66 for eight of 18K cut to half; one slot of 2,049 4.1 us in all, one launch.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

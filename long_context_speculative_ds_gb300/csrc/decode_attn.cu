@@ -10,10 +10,10 @@
 // Logits carry the factor log2 e, so that exponentials are powers of two.
 //
 // Bound by the stream of K and V.  With 32 query heads on 8 of 128: one token
-// over 128K 95 us, the split pass 86 of them (537 MB, 6.2 TB/s of the 6.8 that a
+// over 128K 97 us, the split pass 86 of them (537 MB, 6.2 TB/s of the 6.8 that a
 // copy reaches; without weights the call takes 85); 96 ragged contexts of 33 to
-// 8K 74 us (457 MB, 6.2 TB/s); eight compact caches of 9K to 18K 82 us; 512
-// slots with 4 heads of 64 on 2 7.8 us, two launches of four dependent reads
+// 8K 75 us (457 MB, 6.1 TB/s); eight compact caches of 9K to 18K 82 us; 512
+// slots with 4 heads of 64 on 2 7.9 us, two launches of four dependent reads
 // each.  Logits cost 4 bytes a slot and query head, written and read: 3 % of the
 // bytes at 4 query heads a kv head, a quarter at 16 (128K: 122 us, 87 without
 // weights).
@@ -25,9 +25,9 @@
 // the stream does not stop where one segment ends and the next begins; the other
 // block's ring covers what is left.  (One block of eight warps and six tiles an
 // SM took 88 us for the 96 ragged contexts; with pieces worked out by the
-// computing warps 206 sequences of up to 4 slots took 21.7 us, not 14.)  A warp takes 16 slots of a
-// tile, with the cache as the larger operand of m16n8k16 products and up to
-// eight query heads as the smaller (16 as two):
+// computing warps 206 sequences of up to 4 slots took 21.7 us, not 14.)  A warp
+// takes 16 slots of a tile, with the cache as the larger operand of m16n8k16
+// products and up to eight query heads as the smaller (16 as two):
 //   S^T[16 slots, 8 heads] += K[16 slots, 16 channels] Q^T[16 channels, 8 heads]
 //   O^T[16 dims, 8 heads]  += V^T[16 dims, 16 slots]   P^T[16 slots, 8 heads]
 // P^T is S^T's fragment transposed (movmatrix), and enters as the sum of two
