@@ -378,3 +378,57 @@ def test_light_weights_beside_a_heavy_one(dtype, rise):
     assert (np.abs(f64(out[0]) - o) <= tol).all()
     assert (np.abs(f64(lse[0]) - l) <= 2.0 ** -21 + 2.0 ** -22 * np.abs(l)).all()
     assert B.ds_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,batch,top,room,window,dtype", [
+    (10, 2, 64, 150, 300, 700, 0, torch.float16),
+    (24, 3, 128, 90, 600, 640, 0, torch.bfloat16),
+    (24, 2, 64, 110, 129, 800, 40, torch.bfloat16),
+    (16, 1, 128, 160, 257, 1030, 0, torch.float16),
+    (7, 1, 64, 3, 9000, 65500, 0, torch.bfloat16),
+    (4, 1, 128, 5, 2000, 16384, 1000, torch.bfloat16),
+    (1, 1, 64, 4, 3000, 16385, 0, torch.float16)])
+def test_weights_per_head_of_many_short_sequences(hq, hkv, d, batch, top, room, window, dtype):
+    """Groups of every kind, much more room than slots, lengths at the ends of
+    128; weights summed in place, places behind the last slot left alone."""
+    rng = np.random.default_rng(batch)
+    lens = [0, 1, 127, 128, 129][:batch - 1] + \
+        [int(x) for x in rng.integers(0, top + 1, max(batch - 6, 0))] + [top]
+    q, pools, table = make(lens, hq, hkv, d, dtype, "HND", 0, batch, cap=room)
+    w_in = torch.rand(len(lens), hkv, room, device=DEV)
+    before = w_in.clone()
+    out, lse, w, ws, _ = run(q, pools, table, lens, kv="HND", hw=hkv, w_in=w_in, in_place=True,
+                             decay=0.75, window=window, sinks=2 if window else 0)
+    pools = [torch.nan_to_num(p) for p in pools]
+    check(q, pools, table, lens, out, lse, kv="HND", w_in=before, w_out=w, decay=0.75,
+          window=window, sinks=2 if window else 0)
+    for b, n in enumerate(lens):
+        assert torch.equal(w[b, :, n:], before[b, :, n:])
+    assert B.ds_device_status(ws) == 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, give the bits that
+    each gives alone."""
+    sets = []
+    for seed, lens, hw in ((1, [9000, 3, 700], 2), (2, [40, 5000], 1)):
+        q, pools, table = make(lens, 8, 2, 128, torch.bfloat16, "NHD", 16, seed)
+        out, lse, w, ws, a = run(q, pools, table, lens, hw=hw)
+        alone = [x.clone() for x in (out, lse, w)]
+        sets.append((a, (out, lse, w), alone, torch.cuda.Stream(), ws, (q, pools, table)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, got, _, stream, _, _ in sets:
+            for x in got:
+                x.fill_(4.0)
+        torch.cuda.synchronize()
+        for _ in range(6):
+            for a, _, _, stream, _, _ in sets:
+                B.ds_decode_attn(a, stream)
+        torch.cuda.synchronize()
+        for _, got, alone, _, ws, (q, pools, table) in sets:
+            assert torch.equal(got[0], alone[0]) and torch.equal(got[1], alone[1])
+            assert B.ds_device_status(ws) == 0
+    for (_, got, alone, _, _, _), lens in zip(sets, ([9000, 3, 700], [40, 5000])):
+        for b, n in enumerate(lens):
+            assert torch.equal(got[2][b, :, :n], alone[2][b, :, :n])

@@ -290,3 +290,30 @@ def test_many_sequences():
     pools, table, w, pos = make(lens, 1, 64, "NHD", 0, 1, 2, 90)
     for st in both(pools, table, lens, w, pos, [200] * 400, budget=33, recent=5):
         assert st == 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace and a cache of its own."""
+    sets = []
+    for lens, cap, budget, hkv in (([9000, 5000], 9000, 3000, 2), ([700, 90, 641], 700, 640, 3)):
+        pools, table, w, pos = make(lens, hkv, 128, "NHD", 0, hkv, cap, cap)
+        want = expect(pools, table, lens, w, pos, [10 ** 6] * len(lens), kv="NHD", budget=budget)
+        sets.append((pools, table, lens, w, pos, budget, want))
+    for _ in range(3):
+        running = []
+        for pools, table, lens, w, pos, budget, want in sets:
+            P, W, Q, s = [p.clone() for p in pools], w.clone(), pos.clone(), torch.cuda.Stream()
+            lens_dev = i32(lens)
+            new, _, _, ws, a = run(P, table, lens_dev, W, Q, [10 ** 6] * len(lens), budget=budget)
+            for x, y in zip((*P, W, Q), (*pools, w, pos)):      # the first state again
+                x.copy_(y)
+            running.append((a, s, P, W, Q, new, ws, want, lens_dev))
+        torch.cuda.synchronize()
+        for a, s, *_ in running:
+            B.ds_cache_evict(a, s)
+        torch.cuda.synchronize()
+        for _, _, P, W, Q, new, ws, want, _ in running:
+            assert new.tolist() == want[3] and B.ds_device_status(ws) == 0
+            assert all(same(g, x) for g, x in zip(P, want[0]))
+            assert np.array_equal(W.cpu().numpy(), want[1])
+            assert np.array_equal(Q.cpu().numpy(), want[2])
