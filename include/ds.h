@@ -818,7 +818,7 @@ ds_status ds_rope_append(const ds_rope_args* args, void* stream);
  *
  * Products are float32 sums of exact products; each weight enters the second
  * product as the sum of two values of the cache's type, which is exact to
- * 2^-16 of it (bf16; f16: 2^-22, or 2^-25 of the row's largest); maxima, sums,
+ * 2^-16 of it (bf16; f16: 2^-22, or 2^-32 of the row's largest); maxima, sums,
  * and what splits exchange are float32.
  * What lies in slots that are not attended to (NaN included) has no effect.
  * No state is kept in the workspace from call to call.

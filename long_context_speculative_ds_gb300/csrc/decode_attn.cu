@@ -528,11 +528,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         // more than 2^8, so that outputs are rarely scaled; in f16 it lies 2^7
         // below: weights reach 2^15 of the 2^16 that there are, and those that
         // the type's smallest step cuts short (2^-25 of its unit) lie 2^7 lower
+        // (the difference is exact where it is near the limit; of logits beyond
+        // 2^24 m plus the limit is not, and a weight of 2^16 has no value)
         bool grow = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) grow |= mx[i][j] > m[i][j] + (8.f + kBelow);
+          for (int j = 0; j < 2; ++j) grow |= mx[i][j] - m[i][j] > 8.f + kBelow;
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) {

@@ -432,3 +432,24 @@ def test_two_calls_at_once():
     for (_, got, alone, _, _, _), lens in zip(sets, ([9000, 3, 700], [40, 5000])):
         for b, n in enumerate(lens):
             assert torch.equal(got[2][b, :, :n], alone[2][b, :, :n])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("base", [2.0 ** 22, 2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 27])
+@pytest.mark.parametrize("step", [4.0, 8.0, 12.0, 16.0])
+def test_far_logits_that_grow_a_little(dtype, base, step):
+    """Logits so large that few bits are left below one, growing from tile to
+    tile by about what the running reference may lag behind: no weight leaves
+    the type's range, so the mean of equal values is that value."""
+    d, n = 64, 256
+    q, k = torch.zeros(1, 2, d), torch.zeros(1, n, 1, d)
+    q[..., 0], q[..., 1] = 4096.0, 1.0
+    k[..., 0] = base / 4096
+    k[0, :, 0, 1] = step * (torch.arange(n) // 64)
+    v = torch.ones(1, n, 1, d)
+    q, k, v = (x.to(dtype).to(DEV) for x in (q, k, v))
+    out, _, _, ws, _ = run(q, [k, v], None, [n], out_dtype=torch.float32, scale=0.6931472)
+    assert bool(torch.isfinite(out).all())
+    # weights and their sum: 2^-17 of each left out, 256 float32 sums of both
+    assert float((out - 1).abs().max()) <= 2.0 ** -17 + 2 * 256 * 2.0 ** -24 + 2.0 ** -22
+    assert B.ds_device_status(ws) == 0
