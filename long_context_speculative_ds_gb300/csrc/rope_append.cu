@@ -60,8 +60,10 @@ struct RopeKArgs {
 constexpr int kRopeWarps = 4;             // warps of a block
 constexpr int kRopeBatch = 4;             // head groups of a warp, their loads together
 // Rows of few heads go several to a warp, when there are enough of them to fill
-// the machine all the same.
-constexpr int kFewHeads = 12, kManyRows = 16384, kMostRows = 65536;
+// the machine all the same: up to 12 heads from kManyRows on, up to 20 of 64 or 16
+// of 128 from kMoreRows on, four rows, and eight from kMostRows on (of 1,536 values
+// and more from twice that).
+constexpr int kFewHeads = 12, kManyRows = 16384, kMoreRows = 32768, kMostRows = 65536;
 
 // The sequence before the first row_offsets[b] above row, by all lanes of a
 // warp, 32 at a time (offsets that are not monotone give some sequence; its own
@@ -258,9 +260,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
 // memory, one address a cycle, and is read once for all rows here.  A lane looks
 // up a row; cosines and sines are kept by row, in an order in which eight lanes
 // read 128 bytes.  262,144 rows of 8 + 1 heads of 64: 178 us row by row, 125 by
-// fours, 104 by eights (floor 89); 16,384 rows 12.4, 10.6, 12.0; of 4,096 rows,
-// or of 16 heads and more, one at a time is as fast or faster (4.7, 5.5, 7.2;
-// 65,536 rows of 20 + 4 heads of 128: 121, 128, 136).  By eights the first heads'
+// fours, 104 by eights (floor 89); 16,384 rows 12.4, 10.6, 12.0; of 4,096 rows one
+// at a time is faster (4.7, 5.5, 7.2).  Rows of 12 + 2 heads of 64: 48,000 39 and 34
+// (of 128 66 and 63), but 17,000 of 12 + 4 13.3 and 13.9, 48,000 of 20 + 4 50 and
+// 51.5 (of 16 + 4 of 128 81 and 83).  70,000 rows of 8 + 4 + 4 heads of 128 into a
+// cache 95 by fours, 100 by eights; 66,000 of 8 + 1 of 64 35 and 32.  By eights the first heads'
 // loads go out before the rows' places are known (730,000 rows of 2 + 1 heads into
 // a cache 176 us instead of 183); by fours that took longer (16,384 rows of 4 + 1
 // heads of 128 into 16 sequences 16.4 instead of 15.4).
@@ -415,8 +419,11 @@ cudaError_t launch_rope_append(const ds_rope_args& g, cudaStream_t stream) {
   const int slices = (int)std::max<int64_t>(
       1, std::min<int64_t>(groups, 152 * 24 / std::max(1, g.n_rows)));
   a.per = (groups + slices - 1) / slices;
-  const bool few = a.heads <= kFewHeads && g.n_rows >= kManyRows;
-  const int64_t each = !few ? 1 : g.n_rows >= kMostRows ? 8 : 4, rows = kRopeWarps * each;   // of a warp, a block
+  const int few_heads = g.n_rows < kMoreRows ? kFewHeads : g.head_dim == 64 ? 20 : 16;
+  const bool few = a.heads <= few_heads && g.n_rows >= kManyRows;
+  const int most = a.heads * g.head_dim >= 1536 ? 2 * kMostRows : kMostRows;
+  const int64_t each = !few ? 1 : g.n_rows >= most ? 8 : 4;   // rows of a warp
+  const int64_t rows = kRopeWarps * each;                     // of a block
   a.row_blocks = (int)((g.n_rows + rows - 1) / rows);
   const dim3 grid((unsigned)(a.row_blocks + (a.batch + 32 * kRopeWarps - 1) / (32 * kRopeWarps)),
                   few ? 1u : (unsigned)((groups + a.per - 1) / a.per));

@@ -227,6 +227,13 @@ def test_many_rows_of_few_heads(dtype, layout, d, hq, hkv, rows):
     assert torch.equal(sp, wp)
 
 
+@pytest.mark.parametrize("d,hq,hkv,rows", [(64, 14, 3, 32768 + 7), (64, 15, 3, 32768),
+                                           (128, 8, 4, 32767), (128, 8, 4, 32768 + 7)])
+def test_many_rows_of_more_heads(d, hq, hkv, rows):
+    """The same where more rows make room for rows of more heads."""
+    test_many_rows_of_few_heads(torch.bfloat16, "half", d, hq, hkv, rows)
+
+
 def test_append_leaves_bad_sequences_out():
     """Lengths and offsets that cannot be used, a page that is none and a
     negative position: told by status bits, everything else written."""
