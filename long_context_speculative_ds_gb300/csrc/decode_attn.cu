@@ -73,6 +73,7 @@ struct KArgs {
   int32_t slot_heads;
   int64_t slot_stride;
   int2* desc;
+  int32_t ranges;               // blocks of the split pass
   float2* part_ml;
   float* part_o;
   float* logits;                // NULL: no weights
@@ -667,6 +668,14 @@ DS_DEV float2 join_lanes(float2 x) {
 constexpr int kFinishWarps = 8;
 constexpr int kFinishThreads = 32 * kFinishWarps;
 
+// First piece and pieces of a segment with slots; none where the split pass gave up
+// before it told them (it has set the status bit), whose rows are 0 and whose slots
+// get no weight.
+DS_DEV int2 pieces_of(const KArgs& a, const int64_t seg) {
+  const int2 d = a.desc[seg];
+  return pieces_usable((int)seg, d.x, d.y, a.ranges) ? d : make_int2(0, 0);
+}
+
 // An output row by `parts` warps, which share its pieces: lane l has values 4 l ..
 // 4 l + 3 (2 l at D = 64) of eight pieces on their way at once.
 template <int D>
@@ -680,12 +689,13 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
   const int n = real ? checked_len(a.lens[b], a.cache.slots, nullptr, false) : 0;
   grid_dep_wait();
   grid_dep_launch_dependents();
-  const int2 d = a.desc[b * a.hkv + h];   // (not looked at without slots)
+  const int2 d = pieces_of(a, b * a.hkv + h);   // (not looked at without slots)
+  const bool some = n > 0 && d.y > 0;
   float o[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) o[k] = 0.f;
   float2 all = make_float2(-CUDART_INF_F, 0.f);
-  if (n > 0) {
+  if (some) {
     const int p0 = (int)((int64_t)d.y * part / parts), p1 = (int)((int64_t)d.y * (part + 1) / parts);
     const float2* ml = a.part_ml + (int64_t)d.x * G + g;
     const float* po = a.part_o + ((int64_t)d.x * G + g) * D + lane * V;
@@ -743,13 +753,13 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
     }
   }
   if (!real) return;
-  if (n > 0) {
+  if (some) {
     const float inv = 1.f / all.y;
 #pragma unroll
     for (int k = 0; k < V; ++k) o[k] *= inv;
   }
   if (a.lse && lane == 0)
-    a.lse[row] = n > 0 ? (all.x + log2f(all.y)) * 0.6931471805599453f : -CUDART_INF_F;
+    a.lse[row] = some ? (all.x + log2f(all.y)) * 0.6931471805599453f : -CUDART_INF_F;
   const int64_t at = row * D + lane * V;
 #pragma unroll
   for (int k = 0; k < V; k += 2) {
@@ -784,7 +794,7 @@ DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   if (t0 - lane >= n) return;
-  const int2 d = a.desc[seg];
+  const int2 d = pieces_of(a, seg);
   const Range r = range_of(n, a.window, a.sinks);
   const int64_t at = seg * a.slot_stride;
   float old[4], sum[4];
@@ -803,11 +813,12 @@ DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
     if (row < G)
       for (int j = l; j < d.y; j += 8) ml = join_ml(ml, a.part_ml[(int64_t)(d.x + j) * G + row]);
     ml = join_lanes<8>(ml);
-    const float ref = ml.x + log2f(ml.y);
+    // (no pieces: a sum of infinity, weights of zero)
+    const float ref = d.y > 0 ? ml.x + log2f(ml.y) : CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float rj = __shfl_sync(0xffffffffu, ref, 8 * j);
-      if (g0 + j < G) {
+      if (g0 + j < G && rj != CUDART_INF_F) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           sum[k] += visible(r, t0 + 32 * k) ? ptx::ex2(s[k][j] - rj) : 0.f;
@@ -884,7 +895,7 @@ __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
         for (int c0 = 0; c0 < chunks; c0 += CHUNKS) {
           const int mine = min(c0 + i / 4, chunks - 1), g = mine % per_head * 4 + i % 4;
           const bool row = i < 4 * CHUNKS && c0 + i / 4 < chunks && g < G;
-          const int2 d = a.desc[seg0 + mine / per_head];
+          const int2 d = pieces_of(a, seg0 + mine / per_head);
           float s[CHUNKS][SLOTS][4];
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c) {
@@ -903,8 +914,9 @@ __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
           if (row)
             for (int j = l + 2 * LPR; j < d.y; j += LPR) ml = join_ml(ml, p_ml[(int64_t)j * G]);
           ml = join_lanes<LPR>(ml);
-          // (no row: a sum of infinity, weights of zero)
-          if (i < 4 * CHUNKS && l == 0) s_ref[i] = row ? ml.x + log2f(ml.y) : CUDART_INF_F;
+          // (no row, no pieces: a sum of infinity, weights of zero)
+          if (i < 4 * CHUNKS && l == 0)
+            s_ref[i] = row && d.y > 0 ? ml.x + log2f(ml.y) : CUDART_INF_F;
           __syncthreads();
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c)
@@ -1029,6 +1041,7 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   a.slot_stride = g.slot_stride;
   unsigned char* ws = static_cast<unsigned char*>(g.workspace);
   a.desc = reinterpret_cast<int2*>(ws + L.desc);
+  a.ranges = L.ranges;
   a.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.part_o);
   a.logits = g.weights_out ? reinterpret_cast<float*>(ws + L.logits) : nullptr;

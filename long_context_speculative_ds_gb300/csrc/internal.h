@@ -131,6 +131,17 @@ struct EvictLayout {
   size_t total;
 };
 
+// Whether a segment can have these pieces: it has one of each of some ranges that
+// lie one behind the other, numbered by range and segment.  (A segment whose loader
+// gave up has what the workspace's earlier bytes say.)
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline bool pieces_usable(int32_t segment, int32_t first, int32_t count, int32_t ranges) {
+  const uint32_t range = (uint32_t)first - (uint32_t)segment;   // (wraps below the segment)
+  return range < (uint32_t)ranges && (uint32_t)count - 1u < (uint32_t)ranges - range;
+}
+
 DecodeLayout decode_layout(const ds_decode_args& a, int num_sms);
 EvictLayout evict_layout(const ds_evict_args& a);
 cudaError_t launch_rope_append(const ds_rope_args& a, cudaStream_t stream);
