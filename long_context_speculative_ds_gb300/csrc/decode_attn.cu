@@ -422,13 +422,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (++stage == S) { stage = 0; phase ^= 1; }
       }
     }
-    if (!ok) {                                // no copy may land behind the block's end
-      for (int i = 0; i < S && i < issued; ++i) {
-        if (--stage < 0) { stage = S - 1; phase ^= 1; }
-        drain_wait(smem_addr(&sh.full[stage]), phase);
-      }
-      if (lane == 0) flag(a.status, DS_DEV_TIMEOUT);
+    // No copy may land behind the block's end, whoever gave up: the loader stays
+    // until the last ones are here.
+    for (int i = 0; i < S && i < issued; ++i) {
+      if (--stage < 0) { stage = S - 1; phase ^= 1; }
+      drain_wait(smem_addr(&sh.full[stage]), phase);
     }
+    if (!ok && lane == 0) flag(a.status, DS_DEV_TIMEOUT);
     return;
   }
 
