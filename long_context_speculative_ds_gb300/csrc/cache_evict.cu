@@ -532,7 +532,9 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   const int64_t need = (a.cache.slots + 32 * cluster * warps_of - 1) / (32 * cluster * warps_of);
   const int room = (int)std::min<int64_t>(need, kMaxKeyBytes / (128 * warps_of));
   const size_t smem = (size_t)room * 128 * warps_of;
-  cudaError_t e = allow_smem(kernel, smem);
+  // (always the most, not this call's share: the permission is the kernel's, and
+  // another thread may be between its own and its launch)
+  cudaError_t e = allow_smem(kernel, kMaxKeyBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(segs * cluster));

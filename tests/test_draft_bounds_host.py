@@ -1,5 +1,6 @@
 """What the draft cache's launches and kernels may rely on, checked without a
-GPU: places read back from a workspace."""
+GPU: places read back from a workspace, and the shared memory that a kernel may
+use when calls of several threads meet."""
 import os
 import shutil
 import subprocess
@@ -20,6 +21,20 @@ def _run(tmp_path, source, *more):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([out], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def _run_library(tmp_path, source):
+    """The library's own objects over a runtime that only keeps account."""
+    objs = [os.path.join(build.OUT_DIR, "_obj", s + ".o") for s in build.SOURCES]
+    build.build(force=not all(os.path.exists(o) for o in objs))
+    libs = os.path.join(CUDA, "lib64")
+    if not os.path.exists(os.path.join(libs, "libcudart.so")):
+        pytest.skip("no shared CUDA runtime to take the kernels' registration")
+    _run(tmp_path, source, *objs, "-L" + libs, "-lcudart", "-Wl,-rpath," + libs)
+
+
+def test_no_call_takes_shared_memory_from_another(tmp_path):
+    _run_library(tmp_path, "draft_allowance.cpp")
 
 
 def test_pieces_that_a_workspace_can_name(tmp_path):
