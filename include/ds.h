@@ -747,7 +747,13 @@ ds_status ds_rope_frequencies(const ds_rope_scaling* scaling, double* inv_freq,
  * from_lens below 0, rows beyond the sequence's slots, or row offsets that
  * decrease or leave [0, n_rows] set DS_DEV_BAD_LENGTH and leave the sequence
  * out (new_lens[b] is from_lens[b] then); a page id outside [0, num_pages)
- * sets DS_DEV_BAD_PAGE, and that slot's key and value are not written.
+ * sets DS_DEV_BAD_PAGE, and that slot's key and value are not written
+ * (new_lens counts it).  Where offsets decrease or leave the rows,
+ * other sequences' rows can be in doubt: one that a search of the offsets does
+ * not find for each of its rows is left out too.  It finds every sequence of
+ * which no earlier offset lies above its first row and no later one below its
+ * end.  (A paged sequence of which no row has a page has nothing to write:
+ * new_lens counts its rows in that case.)
  *
  * Refused: head_dim not 64 or 128; rotary_dim not a multiple of 16 up to
  * head_dim; pointers not 16-byte aligned or strides not a multiple of 8 or

@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -65,10 +66,42 @@ constexpr int kRopeBatch = 4;             // head groups of a warp, their loads 
 // and more from twice that).
 constexpr int kFewHeads = 12, kManyRows = 16384, kMoreRows = 32768, kMostRows = 65536;
 
-// The sequence before the first row_offsets[b] above row, by all lanes of a
-// warp, 32 at a time (offsets that are not monotone give some sequence; its own
-// offsets are checked after).
-DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
+// A row's sequence is where a binary search of the offsets ends, the number's bits
+// from the highest down: a bit is set when the offset of the number with it lies at
+// or below the row.  Whatever the offsets are, the search finds sequence b for each
+// of its rows [n0, n1) just when, of the offsets on the way to b, those that set a
+// bit lie at or below n0 and the others at or above n1.  Offsets that decrease
+// somewhere can put that in doubt; such a sequence is left out like one whose own
+// offsets are wrong.
+struct Owner {
+  int b, low, high;               // sequence; the largest that set a bit, the least that did not
+};
+DS_DEV bool sure(const Owner& o, int n0, int n1) { return o.low <= n0 && o.high >= n1; }
+
+DS_DEV Owner row_owner(const int32_t* offs, int batch, int row) {
+  Owner o = {0, INT_MIN, INT_MAX};
+  for (int bit = 1 << (31 - __clz(max(batch - 1, 1))); bit > 0; bit >>= 1) {
+    if (o.b + bit >= batch) continue;
+    const int at = offs[o.b + bit];
+    if (at <= row) {
+      o.b += bit;
+      o.low = max(o.low, at);
+    } else {
+      o.high = min(o.high, at);
+    }
+  }
+  return o;
+}
+// Bit i's part of the way to sequence b.
+DS_DEV Owner way_to(const int32_t* offs, int batch, int b, int i) {
+  const uint32_t node = ((uint32_t)b >> i | 1u) << i;
+  const bool set = (uint32_t)b >> i & 1, there = node < (uint32_t)batch;
+  const int at = there ? offs[node] : 0;
+  return {b, set ? at : INT_MIN, there && !set ? at : INT_MAX};
+}
+// The sequence before the first of 32 offsets at a time that lies above the row, by
+// all lanes of a warp: where the search ends too when offsets increase.
+DS_DEV int guess_owner(const int32_t* offs, int batch, int row) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = batch;
   while (n > 1) {
@@ -81,7 +114,8 @@ DS_DEV int row_owner(const int32_t* offs, int batch, int row) {
   return lo;
 }
 
-// Rows [n0, n0 + n) and first slot of sequence b; false when they cannot be used.
+// Rows [n0, n0 + n) and first slot of sequence b; false when they cannot be used
+// (whatever the other offsets are).
 DS_DEV bool rope_rows_of(const RopeKArgs& a, int b, int& n0, int& n, int& from) {
   n0 = a.row_offsets[b];
   const int n1 = a.row_offsets[b + 1];
@@ -168,8 +202,21 @@ DS_DEV void check_sequences(const RopeKArgs& a) {
   const int b = (blockIdx.x - a.row_blocks) * 32 * kRopeWarps + threadIdx.x;
   if (b >= a.batch || blockIdx.y > 0) return;
   int n0, n, from;
-  const bool usable = rope_rows_of(a, b, n0, n, from);
+  bool usable = rope_rows_of(a, b, n0, n, from);
   if (!usable) flag(a.status, DS_DEV_BAD_LENGTH);
+  bool all_found = true;
+#pragma unroll 4
+  for (int i = 0; (a.batch - 1) >> i > 0; ++i)
+    all_found &= sure(way_to(a.row_offsets, a.batch, b, i), n0, n0 + n);
+  if (usable && n > 0 && !all_found) {
+    // left out (rows whose slots have no page go nowhere and count all the same)
+    flag(a.status, DS_DEV_BAD_LENGTH);
+    const int64_t page = a.cache.page_size;
+    usable = a.cache.page_table != nullptr;
+    for (int64_t t = from; usable && t < (int64_t)from + n; t = (t / page + 1) * page)
+      usable = slot_page(a.cache, b, (int)t) < 0;
+    if (usable) flag(a.status, DS_DEV_BAD_PAGE);
+  }
   if (a.new_lens) a.new_lens[b] = usable ? from + n : from;
 }
 
@@ -218,9 +265,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 7) rope_append(const RopeKArg
   }
   int64_t at = -1;                        // the slot's place in the pools
   if (a.write) {
-    const int b = row_owner(a.row_offsets, a.batch, row);
-    int n0, n, from;
-    if (!rope_rows_of(a, b, n0, n, from) || row < n0 || row >= n0 + n) return;
+    int b = guess_owner(a.row_offsets, a.batch, row), n0, n, from;
+    bool use = rope_rows_of(a, b, n0, n, from);
+    const Owner way = way_to(a.row_offsets, a.batch, b, lane);
+    if (!__all_sync(0xffffffffu, row >= n0 && row < n0 + n && sure(way, n0, n0 + n))) {
+      const Owner o = row_owner(a.row_offsets, a.batch, row);
+      b = o.b;
+      use = rope_rows_of(a, b, n0, n, from) && row >= n0 && row < n0 + n && sure(o, n0, n0 + n);
+    }
+    if (!use) return;
     const int slot = from + (row - n0);
     const int pg = slot_page(a.cache, b, slot);
     if (pg >= 0) at = slot_at(a.cache, pg, slot);
@@ -315,19 +368,15 @@ __global__ void __launch_bounds__(32 * kRopeWarps, 6) rope_few_heads(const RopeK
     use = pos >= 0;
     if (!use) flag(a.status, DS_DEV_BAD_LENGTH);
     if (use && a.write) {
-      int lo = 0, hi = a.batch;           // before the first offset above the row
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.row_offsets[mid] <= row) lo = mid; else hi = mid;
-      }
+      const Owner o = row_owner(a.row_offsets, a.batch, row);
       int n0, n, from;
-      use = rope_rows_of(a, lo, n0, n, from) && row >= n0 && row < n0 + n;
+      use = rope_rows_of(a, o.b, n0, n, from) && row >= n0 && row < n0 + n && sure(o, n0, n0 + n);
       if (use) {
-        const int slot = from + (row - n0), pg = slot_page(a.cache, lo, slot);
+        const int slot = from + (row - n0), pg = slot_page(a.cache, o.b, slot);
         if (pg >= 0) at = slot_at(a.cache, pg, slot);
         else flag(a.status, DS_DEV_BAD_PAGE);
         for (int h = 0; h < a.slot_heads; ++h) {
-          const int64_t i = ((int64_t)lo * a.slot_heads + h) * a.slot_stride + slot;
+          const int64_t i = ((int64_t)o.b * a.slot_heads + h) * a.slot_stride + slot;
           if (a.slot_positions) a.slot_positions[i] = pos;
           if (a.slot_weights) a.slot_weights[i] = 0.f;
         }
