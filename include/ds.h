@@ -827,6 +827,10 @@ ds_status ds_rope_append(const ds_rope_args* args, void* stream);
  * 2^-16 of it (bf16; f16: 2^-22, or 2^-32 of the row's largest); maxima, sums,
  * and what splits exchange are float32.
  * What lies in slots that are not attended to (NaN included) has no effect.
+ * An infinite value that is attended to makes its channel's output infinite,
+ * however small its weight; NaN, both signs, or a logit of -inf beside it make
+ * it NaN.  Outputs are divided by the sum of weights at the end: in bf16, |v|
+ * times that sum over the largest weight must stay below 2^119.
  * No state is kept in the workspace from call to call.
  *
  * Checked on the device: a length below 0 or beyond the sequence's slots sets

@@ -66,6 +66,7 @@ struct KArgs {
   float scale;                  // softmax scale times log2 e
   void* out;
   int32_t out_type;             // 0 bf16, 1 f16, 2 f32
+  int32_t f16;                  // of q and the cache; 0: bf16
   float* lse;
   const float* w_in;
   float* w_out;
@@ -676,6 +677,115 @@ DS_DEV int2 pieces_of(const KArgs& a, const int64_t seg) {
   return pieces_usable((int)seg, d.x, d.y, a.ranges) ? d : make_int2(0, 0);
 }
 
+// Lane l's values of a row of the cache or of q, 4 l .. 4 l + 3 or 2 l and 2 l + 1,
+template <int V>
+DS_DEV void row_words(uint32_t (&w)[V / 2], const uint16_t* row) {
+  if constexpr (V == 4) {
+    const uint2 y = *reinterpret_cast<const uint2*>(row + (threadIdx.x & 31) * V);
+    w[0] = y.x;
+    w[1] = y.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(row + (threadIdx.x & 31) * V);
+  }
+}
+// as float32.
+DS_DEV float2 word_values(uint32_t w, int f16) {
+  return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+             : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// The signs' bits of the values that are infinite or NaN (an exponent of ones
+// carries into the sign).
+DS_DEV uint32_t not_finite(uint32_t w, int f16) {
+  return ((w & 0x7fff7fffu) + (f16 ? 0x04000400u : 0x00800080u)) & 0x80008000u;
+}
+
+// An output row with NaN, looked at once more by its `parts` warps.  A weight is
+// above 0 and an infinite value times it infinite, but the split pass multiplies V
+// with the two values that make up a weight: the second, what rounding left, may be
+// 0 or below, and either too small for its type, and inf - inf and 0 inf are NaN.
+// So what the infinite and NaN values that the row attends to add up to by
+// themselves takes the output's place, each times 1, or times 0 where its logit is
+// -inf.  Only a row with NaN pays for it (32 rows of 128K slots 2.8 ms in all), the
+// others a vote, 0.1 to 0.2 us a call.  (Taken out of the products tile by tile
+// they cost every call: 128K 0.5 % more, with 16 query heads a kv head 1.8.)
+template <int D>
+DS_DEV void put_endless(const KArgs& a, int64_t row, int part, int parts, float (*s_o)[D]) {
+  constexpr int V = D / 32;
+  const int b = (int)(row / a.hq), hq = (int)(row % a.hq), lane = threadIdx.x & 31;
+  const int n = checked_len(a.lens[b], a.cache.slots, nullptr, false);
+  const Range r = range_of(n, a.window, a.sinks);
+  const int64_t head = (int64_t)(hq / a.group) * a.cache.head_stride;
+  const int t1 = (int)((int64_t)n * (part + 1) / parts);
+  float sum[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) sum[k] = 0.f;
+  // 16 bytes a lane of as many rows as that gives a warp, four times, are looked
+  // through; only rows that have something are gone into
+  constexpr int LPR = D / 8, AT = 32 / LPR;
+#pragma unroll 1
+  for (int t0 = (int)((int64_t)n * part / parts); t0 < t1; t0 += 4 * AT) {
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = min(t0 + j * AT + lane / LPR, t1 - 1);
+      const int pg = visible(r, t) ? slot_page(a.cache, b, t) : -1;
+      w[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (pg >= 0)
+        w[j] = *reinterpret_cast<const uint4*>(a.cache.pool[1] + slot_at(a.cache, pg, t) + head +
+                                               lane % LPR * 8);
+    }
+    uint32_t any = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      any |= not_finite(w[j].x, a.f16) | not_finite(w[j].y, a.f16) | not_finite(w[j].z, a.f16) |
+             not_finite(w[j].w, a.f16);
+    if (!__any_sync(0xffffffffu, any != 0u)) continue;
+#pragma unroll 1
+    for (int t = t0; t < min(t0 + 4 * AT, t1); ++t) {
+      const int pg = visible(r, t) ? slot_page(a.cache, b, t) : -1;
+      if (pg < 0) continue;
+      const int64_t at = slot_at(a.cache, pg, t) + head;
+      uint32_t q[V / 2], x[V / 2], v[V / 2];
+      row_words<V>(q, a.q + (int64_t)b * a.q_stride + (int64_t)hq * D);
+      row_words<V>(x, a.cache.pool[0] + at);
+      row_words<V>(v, a.cache.pool[1] + at);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 y = word_values(q[i], a.f16), z = word_values(x[i], a.f16);
+        s = fmaf(y.x, z.x, fmaf(y.y, z.y, s));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float p = s * a.scale == -CUDART_INF_F ? 0.f : 1.f;
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const float2 y = word_values(v[i], a.f16);
+        const uint32_t bad = not_finite(v[i], a.f16);
+        if (bad & 0xffffu) sum[2 * i] = fmaf(p, y.x, sum[2 * i]);
+        if (bad >> 16) sum[2 * i + 1] = fmaf(p, y.y, sum[2 * i + 1]);
+      }
+    }
+  }
+  if (parts > 1) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) s_o[part][lane * V + k] = sum[k];
+    __syncthreads();
+    if (part > 0) return;
+    for (int w = 1; w < parts; ++w)
+#pragma unroll
+      for (int k = 0; k < V; ++k) sum[k] += s_o[w][lane * V + k];
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const int64_t at = row * D + lane * V + k;
+    if (sum[k] == 0.f) continue;          // (nothing infinite here)
+    if (a.out_type == 2) static_cast<float*>(a.out)[at] = sum[k];
+    else static_cast<uint16_t*>(a.out)[at] =
+        (uint16_t)(a.out_type == 0 ? ptx::pack_bf16x2(sum[k], 0.f) : ptx::pack_f16x2(sum[k], 0.f));
+  }
+}
+
 // An output row by `parts` warps, which share its pieces: lane l has values 4 l ..
 // 4 l + 3 (2 l at D = 64) of eight pieces on their way at once.
 template <int D>
@@ -742,8 +852,7 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
     for (int k = 0; k < V; ++k) s_o[warp][lane * V + k] = o[k];
     if (lane == 0) s_ml[warp] = all;
     __syncthreads();
-    if (part > 0) return;
-    for (int w = 1; w < parts; ++w) {
+    for (int w = 1; part == 0 && w < parts; ++w) {
       const float2 x = s_ml[w], now = join_ml(all, x);
       const float ref = now.x == -CUDART_INF_F ? 0.f : now.x;
       const float f = ptx::ex2(x.x - ref), old = ptx::ex2(all.x - ref);
@@ -752,23 +861,31 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
       all = now;
     }
   }
-  if (!real) return;
-  if (some) {
-    const float inv = 1.f / all.y;
+  bool nan = false;                       // in the row, but not in its sum of weights
+  if (real && part == 0) {
+    if (some) {
+      const float inv = 1.f / all.y;
 #pragma unroll
-    for (int k = 0; k < V; ++k) o[k] *= inv;
-  }
-  if (a.lse && lane == 0)
-    a.lse[row] = some ? (all.x + log2f(all.y)) * 0.6931471805599453f : -CUDART_INF_F;
-  const int64_t at = row * D + lane * V;
+      for (int k = 0; k < V; ++k) o[k] *= inv;
+    }
+    if (a.lse && lane == 0)
+      a.lse[row] = some ? (all.x + log2f(all.y)) * 0.6931471805599453f : -CUDART_INF_F;
+    const int64_t at = row * D + lane * V;
 #pragma unroll
-  for (int k = 0; k < V; k += 2) {
-    if (a.out_type == 2)
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + k) = make_float2(o[k], o[k + 1]);
-    else
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + k) =
-          a.out_type == 0 ? ptx::pack_bf16x2(o[k], o[k + 1]) : ptx::pack_f16x2(o[k], o[k + 1]);
+    for (int k = 0; k < V; k += 2) {
+      if (a.out_type == 2)
+        *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + k) =
+            make_float2(o[k], o[k + 1]);
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + k) =
+            a.out_type == 0 ? ptx::pack_bf16x2(o[k], o[k + 1]) : ptx::pack_f16x2(o[k], o[k + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) nan |= o[k] != o[k];
+    nan &= all.y == all.y;
   }
+  nan = parts > 1 ? __syncthreads_or(nan) : __any_sync(0xffffffffu, nan);
+  if (nan) put_endless<D>(a, row, part, parts, s_o);
 }
 
 // Logits of rows g0 .. g0 + 3 of a slot's G, in a piece as wide as G allows;
@@ -1032,6 +1149,7 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   a.sinks = g.sinks;
   a.scale = (g.scale > 0.f ? g.scale : 1.f / std::sqrt((float)g.head_dim)) * kLog2e;
   a.out = g.out;
+  a.f16 = g.dtype == DS_KV_F16;
   a.out_type = g.out_f32 ? 2 : g.dtype == DS_KV_BF16 ? 0 : 1;
   a.lse = g.lse;
   a.w_in = g.weights_in;
