@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "dev_common.cuh"
@@ -481,13 +482,45 @@ __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
 struct Shape {
   int threads, cluster;
 };
-Shape shape_of(int segs, int64_t slots) {
+Shape shape_of(int segs, int64_t slots, bool sixteen) {
   if (slots <= 4096) return {256, 1};
-  if (slots > 65536 && segs <= 16) return {256, 16};
+  if (slots > 65536 && segs <= 16 && sixteen) return {256, 16};
   int c = 1;
   while (c < 8 && (int64_t)segs * 2 * c <= 152 && slots / (2 * c) >= 2048) c *= 2;
   while (c < 8 && slots * 4 > (int64_t)c * kMaxKeyBytes / 3) c *= 2;
   return {512, c};
+}
+
+// Whether the current device can place a cluster of 16 blocks with all the shared
+// memory that they may ask for: not every one has 16 SMs side by side.  What a
+// device has does not change, so it is asked once for each.
+bool sixteen_fit() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];              // 0: not yet, 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (dev < kDevices && known[dev].load(std::memory_order_relaxed))
+    return known[dev].load(std::memory_order_relaxed) == 2;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 16;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(16);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = kMaxKeyBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void (*const kernel)(KArgs, int) = select<256, 16>;
+  int clusters = 0;
+  const bool fit =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+          cudaSuccess &&
+      allow_smem(kernel, kMaxKeyBytes) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) == cudaSuccess && clusters >= 1;
+  if (!fit) cudaGetLastError();
+  if (dev < kDevices) known[dev].store(fit ? 2 : 1, std::memory_order_relaxed);
+  return fit;
 }
 
 }  // namespace evict
@@ -520,10 +553,10 @@ cudaError_t launch_cache_evict(const ds_evict_args& g, const EvictLayout& L,
   a.status = reinterpret_cast<uint32_t*>(ws);
   a.alone = L.moves <= kFewMoves;
   const int segs = g.batch * g.slot_heads;
-  const Shape shape = shape_of(segs, a.cache.slots);
+  const Shape shape = shape_of(segs, a.cache.slots, a.cache.slots > 65536 && sixteen_fit());
   const int cluster = shape.cluster, warps_of = shape.threads / 32;
   void (*const kernel)(KArgs, int) = shape.threads == 256 ? select<256, 16> : select<512, 8>;
-  if (cluster > 8) {                      // more than every device has to take
+  if (cluster > 8) {                      // more than every device has to take, sixteen_fit asked
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

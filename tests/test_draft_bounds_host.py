@@ -1,6 +1,6 @@
 """What the draft cache's launches and kernels may rely on, checked without a
 GPU: places read back from a workspace, and the shared memory that a kernel may
-use when calls of several threads meet."""
+use when calls of several threads meet, and the clusters that a device can place."""
 import os
 import shutil
 import subprocess
@@ -35,6 +35,10 @@ def _run_library(tmp_path, source):
 
 def test_no_call_takes_shared_memory_from_another(tmp_path):
     _run_library(tmp_path, "draft_allowance.cpp")
+
+
+def test_clusters_that_a_device_can_place(tmp_path):
+    _run_library(tmp_path, "draft_clusters.cpp")
 
 
 def test_pieces_that_a_workspace_can_name(tmp_path):
