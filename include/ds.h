@@ -822,6 +822,11 @@ ds_status ds_rope_append(const ds_rope_args* args, void* stream);
  * weights_in NULL counts as zeros; it may be weights_out.  Slots from n on
  * are left as they were.
  *
+ * `window` and `sinks` count slots here, not positions.  Where slots are not in
+ * order of position (a retrieved cache, or one that ds_cache_evict has cut) the
+ * last slots are not the last tokens, and a window is no sliding window of them;
+ * ds_cache_evict's `recent` and `sinks` go by position.
+ *
  * Products are float32 sums of exact products; each weight enters the second
  * product as the sum of two values of the cache's type, which is exact to
  * 2^-16 of it (bf16; f16: 2^-22, or 2^-32 of the row's largest); maxima, sums,
@@ -876,7 +881,8 @@ typedef struct ds_decode_args {
 
 void ds_decode_args_default(ds_decode_args* args);
 /* Depends on the sizes, on num_sms and on whether weights_out is given (then
- * it holds a float32 per query head and slot). */
+ * it holds a float32 per query head and slot that a sequence has room for,
+ * whatever the lengths: 604 MB for 256 sequences of 32 heads and 18,432 slots). */
 ds_status ds_decode_attn_workspace_size(const ds_decode_args* args, size_t* bytes);
 ds_status ds_decode_attn(const ds_decode_args* args, void* stream);
 
@@ -898,6 +904,12 @@ ds_status ds_decode_attn(const ds_decode_args* args, void* stream);
  * weights_out and positions_out, when given, receive the slots below new_lens
  * and leave the inputs as they were (they must not overlap them, or be the
  * inputs themselves, which is the same as NULL: in place).
+ *
+ * Rows move within a sequence's own pages: a page must belong to one sequence
+ * only, or another that shares it (a common prefix) loses its tokens.  What was
+ * given up is gone: tokens appended last can be taken back by a shorter length
+ * only while nothing has been evicted since, and what they added to the other
+ * slots' weights stays.
  *
  * Checked on the device: a length below 0 or beyond the sequence's slots sets
  * DS_DEV_BAD_LENGTH and the sequence is left alone (new_lens[b] = lens[b]); a

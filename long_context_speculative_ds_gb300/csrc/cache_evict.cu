@@ -51,6 +51,11 @@ struct KArgs {
 
 // Segments that can have no more moves than this are moved by `select`: a token
 // given up per call by a cache with a few slots above its budget saves a launch.
+// One slot of 2,049, in a graph: 4.1 us in one launch and 5.9 in two (heads that
+// move together 4.5 and 6.0), of 18,433 5.8 and 7.4, whatever the room.  But all the
+// moves that there is room for take, 32 of them, 8.0 and 9.6 us (together 11.3 and
+// 9.0), 64 8.7 and 9.8 (15.9 and 9.8), 128 9.8 and 10.0 (24 and 9.8), 256 11.9 and
+// 10.1 (38 and 10.0).  The room, not the length, is what the host knows.
 constexpr int kFewMoves = 64;
 
 // (without branches, so that the loads of many slots go out together)
@@ -475,9 +480,10 @@ __global__ void __launch_bounds__(256) move(const KArgs a, const int per) {
 // slots take one block of 256 threads, whose barriers cost less.  Longer ones
 // take up to eight blocks of 512, as many as fill the machine, but with 2,048
 // slots or more to each, and more while a block's keys do not fit beside two
-// others'.  Few segments beyond 65,536 slots take 16 blocks of 256 (16 segments
-// of 128K: 100 us instead of 105; but eight of 18K 69 instead of 66, and 64 of
-// 66K 168 instead of 148).  Blocks of which only one fits an SM leave no place
+// others'.  Few segments beyond 65,536 slots take 16 blocks of 256: cut to half,
+// 8 of 128K 48 us instead of 54, 16 77 instead of 82, 20 92 instead of 97, but 24
+// 121 instead of 110; 8 of 70,000 31 instead of 34, 16 48.6 instead of 49.3, 20 57.3
+// instead of 56.7, 32 89 instead of 80; 8 of 40,000 21.3 instead of 20.5.  Blocks of which only one fits an SM leave no place
 // for 16 clusters at once (two waves, 44 us for the selection instead of 35).
 struct Shape {
   int threads, cluster;

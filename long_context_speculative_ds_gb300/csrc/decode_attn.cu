@@ -34,7 +34,8 @@
 // values of the cache's type, so that its rounding (2^-9 of a weight in bf16)
 // does not show beside the output's own: 2^-17 of a weight is left, in f16 2^-22
 // of it or 2^-32 of the largest.  The tensor pipe is at 13 % of its rate, issue
-// slots at 20 %.
+// slots at 20 %.  The finish with 16 slots a thread spills 48 bytes of each, the one
+// by warps at 64-wide heads 8.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
@@ -1183,9 +1184,14 @@ cudaError_t launch_decode_attn(const ds_decode_args& g, const DecodeLayout& L,
   // A warp to 128 slots, each with the rows' own sums (weights per head): 24
   // sequences of 8,000 slots and eight heads of a group of 7 139 us instead of 150,
   // 300 of 200 in room for 2,000 68 instead of 100, of a group of 4 59 instead of
-  // 88.  In long sequences these sums are many pieces (one head's token over 128K
-  // slots 87.7 instead of 84.3), and a few warps with many heads take longer than
-  // blocks that share them (16 heads of 1,000 slots 13.2 instead of 11.5).
+  // 88.  A segment of many pieces makes these sums long (one head's token over
+  // 16,384 slots, 257 pieces, 15.3 instead of 10.7; four sequences of it, 77 pieces,
+  // 13.1 instead of 12.8), and a few warps with many heads take longer than blocks
+  // that share them (16 heads of 1,000 slots 13.2 instead of 11.5).  The rule goes
+  // by the capacity all the same, and where pieces are few it stops too early: one
+  // sequence of 18,432 slots and eight heads of a group of 4 (39 pieces) 21.5 where a
+  // warp to 128 slots takes 20.0, eight of them 107 and 104, one of 32,768 31.2 and
+  // 29.6, two of 70,000 of a group of 7 120 and 111.
   const int64_t spans = (int64_t)((a.cache.slots + 127) / 128) * a.batch * a.hkv;
   const bool few = a.w_out && a.slot_heads == a.hkv &&
                    (a.group <= 4 ? a.cache.slots <= 16384

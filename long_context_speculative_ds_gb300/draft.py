@@ -35,7 +35,11 @@ class DraftCache:
 
     Eviction cuts a sequence of more than `trigger` slots (0: budget) to
     `budget`; `sinks` first and `recent` last positions always stay.  So that
-    the next token fits, max(budget, trigger) must be below the capacity."""
+    the next token fits, max(budget, trigger) must be below the capacity.
+
+    Tokens that are not accepted can be taken back (lens, token_positions and
+    next_positions made smaller) only while nothing has been evicted since they
+    came; what they added to the other tokens' weights stays."""
 
     def __init__(self, qkv: List[torch.Tensor], k_cache: List[torch.Tensor],
                  v_cache: List[torch.Tensor], lens: torch.Tensor, *, num_q_heads: int,
@@ -96,8 +100,8 @@ class DraftCache:
                 weights: Optional[torch.Tensor] = None, stream=None):
         """The caches and `lens` hold new rows: their slots' positions
         ([batch, capacity], or None where slot i is position i) and weights
-        ([batch, capacity], None: 0) in every layer, and the position of the
-        next token.  A sequence over max(budget, trigger) slots is cut at once."""
+        ([batch, capacity]; None: 0, for retrieval carries none over) in every
+        layer, and the position of the next token.  A sequence over max(budget, trigger) slots is cut at once."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.restart(next_positions, positions, weights)
