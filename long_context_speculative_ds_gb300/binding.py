@@ -675,7 +675,8 @@ def _typed_rows(t: Optional[torch.Tensor], dtype, what: str):
     n, h, d = t.shape
     if t.numel() and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d)):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return C.c_void_p(t.data_ptr()), max(t.stride(0), h * d) if n <= 1 else t.stride(0), (n, h, d)
+    # (a row by itself has no next one, whatever its buffer's stride)
+    return C.c_void_p(t.data_ptr()), h * d if n <= 1 else t.stride(0), (n, h, d)
 
 
 def _int32(t: Optional[torch.Tensor], n: Optional[int], what: str):

@@ -6,7 +6,9 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
+from long_context_speculative_ds_gb300 import binding as B
 from long_context_speculative_ds_gb300 import build
 
 HERE = os.path.join(os.path.dirname(os.path.abspath(__file__)), "native")
@@ -43,3 +45,16 @@ def test_clusters_that_a_device_can_place(tmp_path):
 
 def test_pieces_that_a_workspace_can_name(tmp_path):
     _run(tmp_path, "draft_pieces.cpp")
+
+
+def test_one_row_of_any_stride():
+    """A row by itself has no next one: its buffer's stride does not matter."""
+    wide = torch.zeros(3, 8 * 64 + 4, dtype=torch.bfloat16)
+    pos, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
+    row = wide[:1, :4 * 64].view(1, 4, 64)
+    a = B.rope_append_args(row, None, None, pos, q_out=row, rope_base=1e4, workspace=ws)
+    assert (a.q_row_stride, a.q_out_row_stride) == (256, 256)
+    two = wide[:2, :4 * 64].unflatten(1, (4, 64))
+    pos = torch.zeros(2, dtype=torch.int32)
+    a = B.rope_append_args(two, None, None, pos, q_out=two, rope_base=1e4, workspace=ws)
+    assert (a.q_row_stride, a.q_out_row_stride) == (516, 516)
