@@ -51,7 +51,7 @@ def test_one_row_of_any_stride():
     """A row by itself has no next one: its buffer's stride does not matter."""
     wide = torch.zeros(3, 8 * 64 + 4, dtype=torch.bfloat16)
     pos, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(256, dtype=torch.uint8)
-    row = wide[:1, :4 * 64].view(1, 4, 64)
+    row = wide[:1].as_strided((1, 4, 64), (516, 64, 1))
     a = B.rope_append_args(row, None, None, pos, q_out=row, rope_base=1e4, workspace=ws)
     assert (a.q_row_stride, a.q_out_row_stride) == (256, 256)
     two = wide[:2, :4 * 64].unflatten(1, (4, 64))
