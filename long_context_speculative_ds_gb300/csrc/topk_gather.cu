@@ -381,9 +381,7 @@ DS_DEV void put_row(const GatherKArgs& a, const int b, const int i, const int pg
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) gather_rows(GatherKArgs a) {
-  __shared__ __align__(16) float2 s_cs[8][D / 2];
-  grid_dep_launch_dependents();
+DS_DEV void gather_row(const GatherKArgs& a, float2 (*s_cs)[D / 2]) {
   const int b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.x * 8 + warp;
@@ -422,6 +420,16 @@ __global__ void __launch_bounds__(256) gather_rows(GatherKArgs a) {
     pg = -1;
   }
   put_row<D>(a, b, i, pg, t % a.page_size, s_cs[warp]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) gather_rows(GatherKArgs a) {
+  __shared__ __align__(16) float2 s_cs[8][D / 2];
+  grid_dep_launch_dependents();
+  gather_row<D>(a, s_cs);
+  // Also where no row asked for the selection, one block ends behind topk_select:
+  // what comes next waits for this kernel, and takes lengths and ids from that one.
+  if (blockIdx.x == 0 && blockIdx.y == 0) grid_dep_wait();
 }
 
 cudaError_t launch_topk_gather(const ds_gather_args& g, cudaStream_t stream) {
