@@ -34,7 +34,7 @@
 // values of the cache's type, so that its rounding (2^-9 of a weight in bf16)
 // does not show beside the output's own: 2^-17 of a weight is left, in f16 2^-22
 // of it or 2^-32 of the largest.  The tensor pipe is at 13 % of its rate, issue
-// slots at 20 %.  The finish with 16 slots a thread spills 48 bytes of each, the one
+// slots at 20 %.  The finish with 16 slots a thread spills 32 bytes of each, the one
 // by warps at 64-wide heads 8.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -797,7 +797,7 @@ DS_DEV void finish_row(const KArgs& a, const int64_t row, const int part, const 
   const bool real = row < (int64_t)a.batch * a.hq;
   const int b = real ? (int)(row / a.hq) : 0, hq = real ? (int)(row % a.hq) : 0;
   const int h = hq / G, g = hq % G;
-  const int n = real ? checked_len(a.lens[b], a.cache.slots, nullptr, false) : 0;
+  const int n = real ? checked_len(__ldcg(a.lens + b), a.cache.slots, nullptr, false) : 0;
   grid_dep_wait();
   grid_dep_launch_dependents();
   const int2 d = pieces_of(a, b * a.hkv + h);   // (not looked at without slots)
@@ -907,7 +907,7 @@ DS_DEV void warp_weights(const KArgs& a, const int64_t item) {
   const int lane = threadIdx.x & 31, G = a.group, l = lane % 8;
   const int64_t spans = (a.cache.slots + 127) / 128, seg = item / spans;
   const bool real = seg < (int64_t)a.batch * a.hkv;
-  const int n = real ? checked_len(a.lens[seg / a.hkv], a.cache.slots, nullptr, false) : 0;
+  const int n = real ? checked_len(__ldcg(a.lens + seg / a.hkv), a.cache.slots, nullptr, false) : 0;
   const int t0 = (int)(item - seg * spans) * 128 + lane;
   grid_dep_wait();
   grid_dep_launch_dependents();
@@ -962,7 +962,8 @@ __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
   const int tid = threadIdx.x, G = a.group;
   // Every block of the split pass has waited for what came before it when it lets
   // this kernel's blocks start, so lengths and input weights are read, and places
-  // worked out, before this kernel's own wait.
+  // worked out, before this kernel's own wait.  These reads go past the L1, which the
+  // wait alone promises to hold nothing older than the kernels in front.
   if (CHUNKS == 0 || (int)blockIdx.x < row_blocks) {      // `parts` warps per output row
     const int w = blockIdx.x * kFinishWarps + (tid >> 5);
     finish_row<D>(a, w / parts, w % parts, parts, s_o, s_ml);
@@ -990,13 +991,13 @@ __global__ void __launch_bounds__(kFinishThreads, SLOTS == 0 ? 4 : 2)
       const int b = (int)(bw / a.slot_heads);
       seg0 = (int64_t)b * a.hkv + (a.slot_heads == 1 ? 0 : (int)(bw % a.slot_heads));
       at = bw * a.slot_stride;
-      n = checked_len(a.lens[b], a.cache.slots, nullptr, false);
+      n = checked_len(__ldcg(a.lens + b), a.cache.slots, nullptr, false);
       const int64_t start = (it - bw * spans) * SPAN;
       t0 = (int)start + tid;
       if (start >= n) return false;
       const float* p = a.w_in + at + min(t0, n - 1);
 #pragma unroll
-      for (int k = 0; k < SLOTS; ++k) old[k] = a.w_in ? p[slot(k)] : 0.f;
+      for (int k = 0; k < SLOTS; ++k) old[k] = a.w_in ? __ldcg(p + slot(k)) : 0.f;
       return true;
     };
     int64_t it = blockIdx.x - row_blocks;

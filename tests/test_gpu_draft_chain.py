@@ -71,3 +71,39 @@ def test_append_behind_retrieval(window, top_k, captured):
     for i in range(batch):
         assert torch.equal(out[1][i, want[i]], rows[i, 2 * hkv:])
     assert B.ds_device_status(ws[0]) == 0 and B.ds_device_status(ws[1]) == 0
+
+
+@pytest.mark.parametrize("hw", [1, 4])
+def test_weights_in_place_beside_other_work(hw):
+    """Each call's sums are the next one's input while another stream's work
+    moves the blocks from one SM to another."""
+    lens, calls = [2500, 700, 64, 9000], 120
+    g = torch.Generator(device=DEV).manual_seed(1)
+    bf = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()
+    batch, cap, hkv, d = len(lens), 9000, 4, 128
+    q, k, v = bf(batch, 8, d), bf(batch, cap, hkv, d), bf(batch, cap, hkv, d)
+    out = torch.empty_like(q)
+    w = torch.zeros(batch, hw, cap, device=DEV)
+    args = lambda ws: B.decode_attn_args(q, k, v, None, i32(lens), out=out, weights_in=w,
+                                         weights_out=w, decay=0.875, workspace=ws)
+    ws = torch.zeros(B.ds_decode_attn_workspace_size(args(None)), dtype=torch.uint8, device=DEV)
+    a = args(ws)
+    B.ds_decode_attn(a)                              # from zeros: the sum of one call
+    once, w0 = w.double(), torch.rand(w.shape, generator=g, device=DEV)
+    w.copy_(w0)
+    side, noise = torch.cuda.Stream(), torch.rand(300, 300, device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(calls):
+        with torch.cuda.stream(side):
+            for _ in range(1 + i % 3):
+                noise = (noise @ noise).clamp_(0, 1)
+        B.ds_decode_attn(a)
+    torch.cuda.synchronize()
+    f = 0.875 ** calls
+    for b, n in enumerate(lens):
+        want = w0[b, :, :n].double() * f + once[b, :, :n] * (1 - f) / 0.125
+        # a product and a sum a call, each off by half a step of the result
+        err = (w[b, :, :n].double() - want).abs()
+        assert bool((err <= calls * 2.0 ** -23 * (want + 1)).all())
+        assert torch.equal(w[b, :, n:], w0[b, :, n:])
+    assert B.ds_device_status(ws) == 0
