@@ -752,8 +752,8 @@ ds_status ds_rope_frequencies(const ds_rope_scaling* scaling, double* inv_freq,
  * other sequences' rows can be in doubt: one that a search of the offsets does
  * not find for each of its rows is left out too.  It finds every sequence of
  * which no earlier offset lies above its first row and no later one below its
- * end.  (A paged sequence of which no row has a page has nothing to write:
- * new_lens counts its rows in that case.)
+ * end.  (A paged sequence of which no row has a page has nothing to write when
+ * slot_positions and slot_weights are NULL: new_lens counts its rows then.)
  *
  * Refused: head_dim not 64 or 128; rotary_dim not a multiple of 16 up to
  * head_dim; pointers not 16-byte aligned or strides not a multiple of 8 or

@@ -209,10 +209,11 @@ DS_DEV void check_sequences(const RopeKArgs& a) {
   for (int i = 0; (a.batch - 1) >> i > 0; ++i)
     all_found &= sure(way_to(a.row_offsets, a.batch, b, i), n0, n0 + n);
   if (usable && n > 0 && !all_found) {
-    // left out (rows whose slots have no page go nowhere and count all the same)
+    // left out (rows whose slots have neither a page nor a position or weight to be
+    // noted go nowhere and count all the same)
     flag(a.status, DS_DEV_BAD_LENGTH);
     const int64_t page = a.cache.page_size;
-    usable = a.cache.page_table != nullptr;
+    usable = a.cache.page_table != nullptr && a.slot_heads == 0;
     for (int64_t t = from; usable && t < (int64_t)from + n; t = (t / page + 1) * page)
       usable = slot_page(a.cache, b, (int)t) < 0;
     if (usable) flag(a.status, DS_DEV_BAD_PAGE);

@@ -118,3 +118,28 @@ def test_offsets_of_every_kind(batch, rows, hq, hkv, d):
         seen |= set(check(off, ctx, slots, rows, hq, hkv, d, 16 * (turn & 1), 1 + (hkv - 1) *
                           (turn >> 1), turn))
     assert seen == {True, False}
+
+
+@pytest.mark.parametrize("rows", [12, 16384 + 12])
+@pytest.mark.parametrize("arrays", [False, True])
+def test_sequence_in_doubt_without_a_page(arrays, rows):
+    """Nothing of it could be written: its rows count, unless positions or weights
+    of its slots are kept, which would be those of earlier tokens."""
+    off = [0, 2, 4, 8, 10, 9, 12]
+    x = torch.randn(rows, 3, 64, device=DEV).bfloat16()
+    pools = [torch.zeros(8, 16, 1, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(6, 1)
+    table[5, 0] = -1
+    sp = torch.full((6, 1, 16), -5, dtype=torch.int32, device=DEV)
+    sw = torch.full((6, 1, 16), 2.5, device=DEV)
+    lens, ws = i32([-9] * 6), torch.zeros(256, dtype=torch.uint8, device=DEV)
+    qo = torch.full((rows, 1, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.ds_rope_append(B.rope_append_args(
+        x[:, :1], x[:, 1:2], x[:, 2:], torch.arange(rows, dtype=torch.int32, device=DEV),
+        q_out=qo, rope_base=10000.0, k_cache=pools[0], v_cache=pools[1], page_table=table,
+        from_lens=i32([0] * 6), row_offsets=i32(off), slot_positions=sp if arrays else None,
+        slot_weights=sw if arrays else None, new_lens=lens, workspace=ws))
+    assert lens.tolist() == [2, 2, 4, 2, 0, 0 if arrays else 3]
+    assert B.ds_device_status(ws) == B.DS_DEV_BAD_LENGTH | (0 if arrays else B.DS_DEV_BAD_PAGE)
+    assert bool((qo[10:] == 7.0).all()) and not bool((qo[:10] == 7.0).all(-1).any())
+    assert bool((sp[5] == -5).all()) and bool((sw[5] == 2.5).all())
