@@ -13,7 +13,7 @@
 // over 128K 97 us, the split pass 86 of them (537 MB, 6.2 TB/s of the 6.8 that a
 // copy reaches; without weights the call takes 85); 96 ragged contexts of 33 to
 // 8K 75 us (457 MB, 6.1 TB/s); eight compact caches of 9K to 18K 82 us; 512
-// slots with 4 heads of 64 on 2 7.9 us, two launches of four dependent reads
+// slots with 4 heads of 64 on 2 8.0 us, two launches of four dependent reads
 // each.  Logits cost 4 bytes a slot and query head, written and read: 3 % of the
 // bytes at 4 query heads a kv head, a quarter at 16 (128K: 122 us, 87 without
 // weights).
